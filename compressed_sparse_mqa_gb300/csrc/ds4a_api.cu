@@ -407,6 +407,142 @@ int ds4a_compress_attn_decode_batched(int B, const float *score_w, int ratio, fl
                                                       nullptr, 0, ratio, scale, out, score_w, state, c));
 }
 
+// ---- paged token cache and drafted-token trees ---------------------------------------------
+
+static int check_paged(const ds4a_paged_kv_t *kv) {
+    if (!kv || kv->B < 0 || kv->page < 1 || kv->max_pages < 1 || kv->n_pages < 1) return DS4A_ERR_ARG;
+    if (kv->B > 65535 || (kv->D != 64 && kv->D != 128) || kv->page % 16 != 0 || kv->page > 65536)
+        return DS4A_ERR_UNSUPPORTED;
+    if (static_cast<long long>(kv->max_pages) * kv->page > 0x7fffffffLL || kv->n_pages > 0x7fffffffLL / kv->page)
+        return DS4A_ERR_UNSUPPORTED;
+    if (kv->B > 0 && (!kv->k || !kv->v || !kv->table || !kv->len)) return DS4A_ERR_ARG;
+    if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->table, 4) || !aligned(kv->len, 8))
+        return DS4A_ERR_ARG;
+    return DS4A_OK;
+}
+
+static int check_tree(int N, const int32_t *n_node, const int32_t *parent) {
+    if (N < 1) return DS4A_ERR_ARG;
+    if (N > 64) return DS4A_ERR_UNSUPPORTED;
+    if (!n_node || !aligned(n_node, 4) || !aligned(parent, 4)) return DS4A_ERR_ARG;
+    return DS4A_OK;
+}
+
+static ds4a::PagedKV paged_view(const ds4a_paged_kv_t *kv) {
+    return ds4a::PagedKV{kv->k, kv->v, kv->table, kv->len, kv->n_pages, kv->page, kv->max_pages, kv->D};
+}
+
+int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16_t *v, int N, const int32_t *n_tok,
+                      const int32_t *parent, const float *inv_freq, int rot, int rot_off, int interleaved,
+                      const uint16_t *q, int H, uint16_t *q_out, void *stream) {
+    int rc = check_paged(kv);
+    if (rc != DS4A_OK) return rc;
+    if (N < 0 || rot < 0 || rot_off < 0 || (q == nullptr) != (q_out == nullptr)) return DS4A_ERR_ARG;
+    if ((parent && N > 64) || rot % 16 != 0 || rot_off % 8 != 0 || rot > kv->D || rot_off > kv->D - rot)
+        return DS4A_ERR_UNSUPPORTED;
+    if (q) {
+        rc = check_heads(H, kv->D);
+        if (rc != DS4A_OK) return rc;
+    }
+    if (kv->B == 0 || N == 0) return DS4A_OK;
+    if (!k || !v || !n_tok || (rot > 0 && !inv_freq)) return DS4A_ERR_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(n_tok, 4) ||
+        !aligned(parent, 4) || !aligned(inv_freq, 4))
+        return DS4A_ERR_ARG;
+    if (q && q_out != q) {   // in place, or apart
+        const uintptr_t a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(q_out);
+        const uintptr_t n = static_cast<uintptr_t>(kv->B) * N * H * kv->D * 2;
+        if (a < b + n && b < a + n) return DS4A_ERR_ARG;
+    }
+    ds4a::Ctx c;
+    rc = make_ctx(stream, c);
+    if (rc != DS4A_OK) return rc;
+    const ds4a::AppendArgs a{paged_view(kv), k, v, q, q_out, n_tok, parent, inv_freq, c.err, N, q ? H : 0, rot, rot_off,
+                             interleaved != 0};
+    return from_cuda(ds4a::launch_paged_append(a, kv->B, c));
+}
+
+int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, const int32_t *parent,
+                       const float *score_w, int ratio, const float *state, uint16_t *comp_k, uint16_t *comp_v,
+                       long long cap, void *stream) {
+    int rc = check_paged(kv);
+    if (rc != DS4A_OK) return rc;
+    rc = check_tree(N, n_node, parent);
+    if (rc != DS4A_OK) return rc;
+    if (ratio < 1 || cap < 0) return DS4A_ERR_ARG;
+    if (ratio > 1024 || cap > 0x7fffffffLL) return DS4A_ERR_UNSUPPORTED;
+    if (kv->B == 0) return DS4A_OK;
+    if (!score_w || !state || !comp_k || !comp_v) return DS4A_ERR_ARG;
+    if (!aligned(score_w, 4) || !aligned(state, 4) || !aligned(comp_k, 16) || !aligned(comp_v, 16)) return DS4A_ERR_ARG;
+    if (cap < N) return DS4A_ERR_CAPACITY;
+    ds4a::Ctx c;
+    rc = make_ctx(stream, c);
+    if (rc != DS4A_OK) return rc;
+    const ds4a::CompressTreeArgs a{paged_view(kv), n_node, parent, score_w, state, comp_k, comp_v, cap, c.err, N, ratio};
+    return from_cuda(ds4a::launch_compress_tree(a, kv->B, c));
+}
+
+size_t ds4a_attn_tree_workspace_bytes(int B, int N, int H, int D) {
+    if (B < 0 || N < 1 || N > 64 || check_heads(H, D) != DS4A_OK) return 0;
+    return ds4a::attn_tree_ws_bytes(B, N, H, D);
+}
+
+int ds4a_attn_tree(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, const int32_t *n_node,
+                   const int32_t *parent, long long window, const uint16_t *comp_k, const uint16_t *comp_v,
+                   long long cap, int ratio, const int32_t *sel, int n_sel, float scale, uint16_t *out, void *ws,
+                   size_t ws_bytes, void *stream) {
+    int rc = check_paged(kv);
+    if (rc != DS4A_OK) return rc;
+    rc = check_heads(H, kv->D);
+    if (rc != DS4A_OK) return rc;
+    rc = check_tree(N, n_node, parent);
+    if (rc != DS4A_OK) return rc;
+    if (window < 1 || ratio < 0 || cap < 0 || n_sel < 0 || (sel && (ratio == 0 || n_sel < 1))) return DS4A_ERR_ARG;
+    if (ratio > 1024 || cap > 0x7fffffffLL || n_sel > 0x3fffffff) return DS4A_ERR_UNSUPPORTED;
+    if (kv->B == 0) return DS4A_OK;
+    if (!q || !out || (ratio > 0 && (!comp_k || !comp_v))) return DS4A_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(comp_k, 16) || !aligned(comp_v, 16) || !aligned(sel, 4))
+        return DS4A_ERR_ARG;
+    if (ratio > 0 && cap < N) return DS4A_ERR_CAPACITY;
+    if (ratio > 0 && cap * kv->B > 0x7fffffffLL) return DS4A_ERR_UNSUPPORTED;
+    if (!ws || !aligned(ws, 256) || ws_bytes < ds4a_attn_tree_workspace_bytes(kv->B, N, H, kv->D))
+        return DS4A_ERR_WORKSPACE;
+    ds4a::Ctx c;
+    rc = make_ctx(stream, c);
+    if (rc != DS4A_OK) return rc;
+    const ds4a::AttnTreeArgs a{paged_view(kv), q, comp_k, comp_v, n_node, parent, sel, out, ws, c.err,
+                               window, cap, N, H, ratio, sel ? n_sel : 0, scale, 0.f};
+    return from_cuda(ds4a::launch_attn_tree(a, kv->B, c));
+}
+
+int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, const int32_t *parent,
+                     const int32_t *leaf, long long *len_out, const float *score_w, int ratio, const float *state,
+                     float *state_out, uint16_t *comp_k, uint16_t *comp_v, long long cap, uint16_t *k_idx, int d_idx,
+                     void *stream) {
+    int rc = check_paged(kv);
+    if (rc != DS4A_OK) return rc;
+    rc = check_tree(N, n_node, parent);
+    if (rc != DS4A_OK) return rc;
+    if (ratio < 0 || cap < 0 || (k_idx && ratio == 0)) return DS4A_ERR_ARG;
+    if (ratio > 1024 || cap > 0x7fffffffLL) return DS4A_ERR_UNSUPPORTED;
+    if (k_idx && (d_idx < 8 || d_idx > 256 || d_idx % 8 != 0)) return DS4A_ERR_UNSUPPORTED;
+    if (kv->B == 0) return DS4A_OK;
+    if (!leaf || !len_out || !aligned(leaf, 4) || !aligned(len_out, 8)) return DS4A_ERR_ARG;
+    if (ratio > 0) {
+        if (!score_w || !state || !state_out || !comp_k || !comp_v) return DS4A_ERR_ARG;
+        if (!aligned(score_w, 4) || !aligned(state, 4) || !aligned(state_out, 4) || !aligned(comp_k, 16) ||
+            !aligned(comp_v, 16) || !aligned(k_idx, 16))
+            return DS4A_ERR_ARG;
+        if (cap < N) return DS4A_ERR_CAPACITY;
+    }
+    ds4a::Ctx c;
+    rc = make_ctx(stream, c);
+    if (rc != DS4A_OK) return rc;
+    const ds4a::CommitTreeArgs a{paged_view(kv), n_node, parent, leaf, len_out, score_w, state, state_out, comp_k, comp_v,
+                                 k_idx, cap, c.err, N, ratio, k_idx ? d_idx : 0};
+    return from_cuda(ds4a::launch_commit_tree(a, kv->B, c));
+}
+
 // ---- one decode step of one layer from host memory ------------------------------------------
 
 // Every check that the calls ds4a_decode_layer_step makes would make, done before

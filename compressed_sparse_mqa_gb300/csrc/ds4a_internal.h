@@ -102,6 +102,62 @@ struct IngestArgs {
 };
 cudaError_t launch_ingest(const IngestArgs &a, const Ctx &c);
 
+// ---- paged token cache and drafted-token trees ----
+// one layer's cache: pools of n_pages pages of `page` token rows, the sessions' page
+// tables [B, max_pages] and committed lengths [B]
+struct PagedKV {
+    uint16_t *k, *v;
+    const int32_t *table;
+    const long long *len;
+    long long n_pages;
+    int page, max_pages, D;
+};
+struct AppendArgs {
+    PagedKV kv;
+    const uint16_t *k, *v, *q;   // [B, N, D], [B, N, H, D] (q may be nullptr)
+    uint16_t *q_out;
+    const int32_t *n_tok, *parent;
+    const float *inv_freq;
+    unsigned int *err;
+    int N, H, rot, rot_off, interleaved;
+};
+struct CompressTreeArgs {
+    PagedKV kv;
+    const int32_t *n_node, *parent;
+    const float *w, *state;
+    uint16_t *comp_k, *comp_v;
+    long long cap;
+    unsigned int *err;
+    int N, ratio;
+};
+struct CommitTreeArgs {
+    PagedKV kv;
+    const int32_t *n_node, *parent, *leaf;
+    long long *len_out;
+    const float *w, *state;
+    float *state_out;
+    uint16_t *comp_k, *comp_v, *k_idx;
+    long long cap;
+    unsigned int *err;
+    int N, ratio, d_idx;
+};
+struct AttnTreeArgs {
+    PagedKV kv;
+    const uint16_t *q, *comp_k, *comp_v;
+    const int32_t *n_node, *parent, *sel;
+    uint16_t *out;
+    void *ws;
+    unsigned int *err;
+    long long window, cap;
+    int N, H, ratio, n_sel;
+    float scale, scale_log2;
+};
+cudaError_t launch_paged_append(const AppendArgs &a, int B, const Ctx &c);
+cudaError_t launch_compress_tree(const CompressTreeArgs &a, int B, const Ctx &c);
+cudaError_t launch_commit_tree(const CommitTreeArgs &a, int B, const Ctx &c);
+size_t attn_tree_ws_bytes(int B, int N, int H, int D);
+cudaError_t launch_attn_tree(const AttnTreeArgs &a, int B, const Ctx &c);
+
 // measurement kernel: gather n_idx rows table[idx[i]] (D fp16 each) into shared memory
 cudaError_t launch_gather_probe(const uint16_t *table, long long n_table, int D, const int32_t *idx, long long n_idx,
                                 unsigned int *sink, const Ctx &c);

@@ -32,7 +32,8 @@ EXPORTED = ["ds4a_status_str", "ds4a_last_device_error", "ds4a_compress_append",
             "ds4a_indexer_topk_noalloc", "ds4a_test_set_wait_limit", "ds4a_compress_append_keys",
             "ds4a_decode_batched_workspace_bytes", "ds4a_indexer_topk_compress_batched", "ds4a_attn_decode_batched",
             "ds4a_compress_attn_decode_batched", "ds4a_probe_gather", "ds4a_decode_layer_step",
-            "ds4a_indexer_topk_compress_keys"]
+            "ds4a_indexer_topk_compress_keys", "ds4a_paged_append", "ds4a_compress_tree", "ds4a_attn_tree",
+            "ds4a_attn_tree_workspace_bytes", "ds4a_commit_tree"]
 
 
 class Ds4aError(RuntimeError):
@@ -71,8 +72,16 @@ def lib() -> ctypes.CDLL:
         L.ds4a_attn_prefill.argtypes = [P, I, I, I, P, P, I, I, P, P, LL, P, I, LL, I, F, P, P, SZ, P]
         L.ds4a_decode_layer_step.argtypes = [ctypes.POINTER(DecodeLayerDesc), LL, ctypes.POINTER(DecodeHostInputs),
                                              P, P]
+        KV = ctypes.POINTER(PagedKVDesc)
+        L.ds4a_paged_append.argtypes = [KV, P, P, I, P, P, P, I, I, I, P, I, P, P]
+        L.ds4a_compress_tree.argtypes = [KV, I, P, P, P, I, P, P, P, LL, P]
+        L.ds4a_attn_tree.argtypes = [KV, P, I, I, P, P, LL, P, P, LL, I, P, I, F, P, P, SZ, P]
+        L.ds4a_attn_tree_workspace_bytes.argtypes = [I, I, I, I]
+        L.ds4a_attn_tree_workspace_bytes.restype = SZ
+        L.ds4a_commit_tree.argtypes = [KV, I, P, P, P, P, P, I, P, P, P, P, LL, P, I, P]
         for name in EXPORTED:
-            if name not in ("ds4a_status_str", "ds4a_indexer_workspace_bytes", "ds4a_decode_batched_workspace_bytes"):
+            if name not in ("ds4a_status_str", "ds4a_indexer_workspace_bytes", "ds4a_decode_batched_workspace_bytes",
+                            "ds4a_attn_tree_workspace_bytes"):
                 getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -489,6 +498,177 @@ def ds4a_decode_layer_step(desc: DecodeLayerDesc, pos: int, k=None, v=None, q=No
     _check(lib().ds4a_decode_layer_step(*args), "ds4a_decode_layer_step")
 
 
+# ---- drafted tokens over a paged cache -----------------------------------------------------------
+
+class PagedKVDesc(ctypes.Structure):
+    """ds4a_paged_kv_t: one layer's paged token cache (see paged_kv_desc)."""
+    _fields_ = [("B", ctypes.c_int), ("D", ctypes.c_int), ("page", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("n_pages", ctypes.c_longlong), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("len", ctypes.c_void_p)]
+
+
+def paged_kv_desc(pool_k, pool_v, table, length) -> PagedKVDesc:
+    """The ds4a_paged_kv_t of pools [n_pages, page, D] fp16, page tables [B, max_pages] int32
+    and committed lengths [B] int64.  The descriptor keeps the tensors alive; it holds their
+    addresses, so their contents may change and they may not be resized."""
+    if pool_k.dim() != 3 or pool_v.shape != pool_k.shape or table.dim() != 2 or length.shape != (table.shape[0],):
+        raise ValueError("paged_kv_desc: pools [n_pages, page, D], table [B, max_pages], length [B]")
+    n_pages, page, D = pool_k.shape
+    desc = PagedKVDesc(B=table.shape[0], D=D, page=page, max_pages=table.shape[1], n_pages=n_pages,
+                       k=_ptr(pool_k, torch.float16, "pool_k"), v=_ptr(pool_v, torch.float16, "pool_v"),
+                       table=_ptr(table, torch.int32, "table"), len=_ptr(length, torch.int64, "length"))
+    desc.tensors = (pool_k, pool_v, table, length)
+    _one_device("paged_kv_desc", *desc.tensors)
+    return desc
+
+
+def _one_device(where, *tensors):
+    """Every tensor on the current device: the library launches there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{where}: a tensor on {t.device}, the current device is cuda:{cur}")
+
+
+def _tree_ptrs(where, kv, N, n_node, parent):
+    if n_node.shape != (kv.B,) or (parent is not None and parent.shape != (kv.B, N)):
+        raise ValueError(f"{where}: n_node [B], parent [B, N] (or None)")
+    return _ptr(n_node, torch.int32, "n_node"), _ptr(parent, torch.int32, "parent", optional=True)
+
+
+def _draft_rows(where, kv, N, comp_k, comp_v):
+    if comp_k.dim() != 3 or comp_k.shape[0] != kv.B or comp_k.shape[2] != kv.D or comp_v.shape != comp_k.shape:
+        raise ValueError(f"{where}: compressed rows [B, cap, D]")
+    return _ptr(comp_k, torch.float16, "comp_k"), _ptr(comp_v, torch.float16, "comp_v"), comp_k.shape[1]
+
+
+def _marshal_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, rot_off: int = 0,
+                          interleaved: bool = True, q=None, q_out=None, stream=None):
+    if k.dim() != 3 or k.shape[0] != kv.B or k.shape[2] != kv.D or v.shape != k.shape:
+        raise ValueError("paged_append: k, v [B, N, D]")
+    N, H = k.shape[1], 0
+    if (q is None) != (q_out is None):
+        raise ValueError("paged_append: q and q_out come together")
+    if q is not None:
+        if q.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != kv.D or q_out.shape != q.shape:
+            raise ValueError("paged_append: q, q_out [B, N, H, D]")
+        H = q.shape[2]
+    _one_device("paged_append", *kv.tensors, k, v, n_tok, parent, inv_freq, q, q_out)
+    pn, pp = _tree_ptrs("paged_append", kv, N, n_tok, parent)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return (ctypes.byref(kv), _ptr(k, torch.float16, "k"), _ptr(v, torch.float16, "v"), N, pn, pp,
+            _ptr(inv_freq, torch.float32, "inv_freq", optional=True), rot, rot_off, int(interleaved),
+            _ptr(q, torch.float16, "q", optional=True), H, _ptr(q_out, torch.float16, "q_out", optional=True),
+            _stream(stream))
+
+
+def ds4a_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, rot_off: int = 0,
+                      interleaved: bool = True, q=None, q_out=None, stream=None):
+    """Tokens k, v [B, N, D] (the first n_tok[s] of each session) into slots len + i of the
+    cache; keys, and queries q [B, N, H, D] into q_out, rotated to their positions with
+    inv_freq [rot/2] (None: as they are).  parent [B, N] int32 or None (a chain)."""
+    args = _marshal_paged_append(kv, k, v, n_tok, parent, inv_freq, rot_off, interleaved, q, q_out, stream)
+    _check(lib().ds4a_paged_append(*args), "ds4a_paged_append")
+
+
+def _marshal_compress_tree(kv: PagedKVDesc, n_node, parent, score_w, ratio: int, state, comp_k, comp_v, N=None,
+                           stream=None):
+    N = _nodes("compress_tree", parent, N)
+    if state.shape != (kv.B, 2 + 2 * kv.D) or score_w.numel() != kv.D:
+        raise ValueError("compress_tree: state [B, 2 + 2D], score_w [D]")
+    _one_device("compress_tree", *kv.tensors, n_node, parent, score_w, state, comp_k, comp_v)
+    pn, pp = _tree_ptrs("compress_tree", kv, N, n_node, parent)
+    ck, cv, cap = _draft_rows("compress_tree", kv, N, comp_k, comp_v)
+    return (ctypes.byref(kv), N, pn, pp, _ptr(score_w, torch.float32, "score_w"), ratio,
+            _ptr(state, torch.float32, "state"), ck, cv, cap, _stream(stream))
+
+
+def _nodes(where, parent, N):
+    """Nodes per session: parent's width, or N for a chain (parent None)."""
+    if N is None:
+        if parent is None:
+            raise ValueError(f"{where}: a chain (parent None) needs N")
+        return parent.shape[1]
+    return N
+
+
+def ds4a_compress_tree(kv: PagedKVDesc, n_node, parent, score_w, ratio: int, state, comp_k, comp_v, N=None,
+                       stream=None):
+    """The compressed rows that drafted nodes complete on their own paths, into rows
+    cap - N + node of comp_k, comp_v [B, cap, D]; state [B, 2 + 2D] is read only.  N: nodes
+    per session when parent is None."""
+    args = _marshal_compress_tree(kv, n_node, parent, score_w, ratio, state, comp_k, comp_v, N, stream)
+    _check(lib().ds4a_compress_tree(*args), "ds4a_compress_tree")
+
+
+def ds4a_attn_tree_workspace_bytes(B: int, N: int, H: int, D: int) -> int:
+    return int(lib().ds4a_attn_tree_workspace_bytes(B, N, H, D))
+
+
+def _marshal_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, comp_v, ratio: int, sel, scale: float,
+                       out, ws, stream=None):
+    if q.dim() != 4 or q.shape[0] != kv.B or q.shape[3] != kv.D or out.shape != q.shape:
+        raise ValueError("attn_tree: q, out [B, N, H, D]")
+    N, H = q.shape[1:3]
+    n_sel = 0
+    if sel is not None:
+        if sel.dim() != 3 or sel.shape[:2] != q.shape[:2]:
+            raise ValueError("attn_tree: sel [B, N, n_sel]")
+        n_sel = sel.shape[2]
+    _one_device("attn_tree", *kv.tensors, q, n_node, parent, comp_k, comp_v, sel, out, ws)
+    pn, pp = _tree_ptrs("attn_tree", kv, N, n_node, parent)
+    ck, cv, cap = _draft_rows("attn_tree", kv, N, comp_k, comp_v) if ratio else (None, None, 0)
+    return (ctypes.byref(kv), _ptr(q, torch.float16, "q"), N, H, pn, pp, window, ck, cv, cap, ratio,
+            _ptr(sel, torch.int32, "sel", optional=True), n_sel, scale, _ptr(out, torch.float16, "out"),
+            _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+
+
+def ds4a_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, comp_v, ratio: int, sel, scale: float, out,
+                   ws, stream=None):
+    """Attention of every drafted node: q, out [B, N, H, D]; its path's raw tokens inside the
+    window and, with ratio > 0, the compressed rows of comp_k, comp_v [B, cap, D] listed in
+    sel [B, N, n_sel] int32 or (sel None) every row complete at its position.  ws: uint8,
+    ds4a_attn_tree_workspace_bytes(B, N, H, D) bytes, zeroed once."""
+    args = _marshal_attn_tree(kv, q, n_node, parent, window, comp_k, comp_v, ratio, sel, scale, out, ws, stream)
+    _check(lib().ds4a_attn_tree(*args), "ds4a_attn_tree")
+
+
+def _marshal_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w=None, ratio: int = 0, state=None,
+                         state_out=None, comp_k=None, comp_v=None, k_idx=None, N=None, stream=None):
+    N = _nodes("commit_tree", parent, N)
+    if leaf.shape != (kv.B,) or len_out.shape != (kv.B,):
+        raise ValueError("commit_tree: leaf, len_out [B]")
+    _one_device("commit_tree", *kv.tensors, n_node, parent, leaf, len_out, score_w, state, state_out, comp_k, comp_v,
+                k_idx)
+    pn, pp = _tree_ptrs("commit_tree", kv, N, n_node, parent)
+    ck = cv = None
+    cap = d_idx = 0
+    if ratio:
+        if state.shape != (kv.B, 2 + 2 * kv.D) or state_out.shape != state.shape or score_w.numel() != kv.D:
+            raise ValueError("commit_tree: state, state_out [B, 2 + 2D], score_w [D]")
+        ck, cv, cap = _draft_rows("commit_tree", kv, N, comp_k, comp_v)
+    if k_idx is not None:
+        if k_idx.dim() != 3 or k_idx.shape[:2] != (kv.B, cap):
+            raise ValueError("commit_tree: k_idx [B, cap, d_idx], rows as comp_k")
+        d_idx = k_idx.shape[2]
+    return (ctypes.byref(kv), N, pn, pp, _ptr(leaf, torch.int32, "leaf"), _ptr(len_out, torch.int64, "len_out"),
+            _ptr(score_w, torch.float32, "score_w", optional=True) if ratio else None, ratio,
+            _ptr(state, torch.float32, "state") if ratio else None,
+            _ptr(state_out, torch.float32, "state_out") if ratio else None, ck, cv, cap,
+            _ptr(k_idx, torch.float16, "k_idx", optional=True), d_idx, _stream(stream))
+
+
+def ds4a_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w=None, ratio: int = 0, state=None,
+                     state_out=None, comp_k=None, comp_v=None, k_idx=None, N=None, stream=None):
+    """Accept the path ending in node leaf[s] (-1: none): its tokens move to slots len and up,
+    its compressed rows (and, with k_idx [B, cap, d_idx], their indexer keys) from the draft's
+    rows to their place; state_out and len_out are those after the path.  N: nodes per
+    session when parent is None."""
+    args = _marshal_commit_tree(kv, n_node, parent, leaf, len_out, score_w, ratio, state, state_out, comp_k, comp_v,
+                                k_idx, N, stream)
+    _check(lib().ds4a_commit_tree(*args), "ds4a_commit_tree")
+
+
 _MARSHAL = {"ds4a_attn_decode": _marshal_attn_decode,
             "ds4a_indexer_topk_compress_batched": _marshal_indexer_topk_compress_batched,
             "ds4a_attn_decode_batched": _marshal_attn_decode_batched,
@@ -498,7 +678,9 @@ _MARSHAL = {"ds4a_attn_decode": _marshal_attn_decode,
             "ds4a_compress_attn_decode": _marshal_compress_attn_decode,
             "ds4a_indexer_topk_compress": _marshal_indexer_topk_compress,
             "ds4a_decode_layer_step": _marshal_decode_layer_step,
-            "ds4a_indexer_topk_compress_keys": _marshal_indexer_topk_compress_keys}
+            "ds4a_indexer_topk_compress_keys": _marshal_indexer_topk_compress_keys,
+            "ds4a_paged_append": _marshal_paged_append, "ds4a_compress_tree": _marshal_compress_tree,
+            "ds4a_attn_tree": _marshal_attn_tree, "ds4a_commit_tree": _marshal_commit_tree}
 
 
 def bind(name: str, *args, **kwargs):

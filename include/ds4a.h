@@ -41,7 +41,8 @@
  *     waits for the kernel ahead to finish before it reads anything else or
  *     writes anything.  So the kernel directly ahead on the stream must not
  *     write those early inputs.  The calls of this library never write another
- *     call's early inputs; a kernel that does not use programmatic launch
+ *     call's early inputs (the drafted-token calls below excepted: they say which
+ *     arrays that concerns); a kernel that does not use programmatic launch
  *     finishes before the next call starts.  With the environment variable
  *     DS4A_PDL=0 (read once per process) every kernel waits for the kernel
  *     ahead before it starts.
@@ -486,6 +487,136 @@ typedef struct ds4a_decode_host_inputs {
  */
 int ds4a_decode_layer_step(const ds4a_decode_layer_t *layer, long long pos, const ds4a_decode_host_inputs_t *in,
                            uint16_t *out_host, void *stream);
+
+/*
+ * Drafted tokens: B sessions over a paged token cache.
+ * ("ds4 antirez DeepSeek V4 Flash local engine 2026 guide" and "DwarfStar (ds4)
+ * Deep Dive" name speculative decoding with a draft; the pages give no cache layout
+ * for it.)  A draft proposes a tree of tokens per session; one pass scores every node,
+ * and the accepted path is committed.  For each node the results are those of
+ * decoding its path token by token, so checking a draft loses nothing.
+ *
+ * One step of a layer is ds4a_paged_append (the drafted tokens into the pages, keys and
+ * queries rotated), ds4a_compress_tree (the compressed rows that nodes complete; layers
+ * with ratio > 0), ds4a_attn_tree, and, once a path is accepted, ds4a_commit_tree.
+ * ds4a_paged_append alone also fills the cache for a prompt.
+ *
+ * ds4a_paged_kv_t names one layer's cache: pages of `page` token rows in a pool that the
+ * sessions share.  The token in slot t of session s is row table[s][t / page] * page +
+ * t % page of k and v.  Slots 0 .. len[s]-1 hold the committed tokens (slot = position);
+ * drafted node i sits in slot len[s] + i.  Pages that calls write to (those of slots
+ * len[s] and up) belong to one session; others may be shared.  Page entries of slots that
+ * a call does not touch are not read.
+ *
+ * A tree: n_node [B] int32 nodes per session, 0 .. N (rows behind the last node are left
+ * as they were); parent [B, N] int32: an earlier node, or -1 for a node that continues the
+ * last committed token; parent NULL: node i continues node i-1.  A node's depth counts its
+ * ancestors and its position is len + depth.  Positions and tree shapes are device
+ * memory, so a captured step replays with new ones.
+ *
+ * Compressed rows: comp_k, comp_v (and k_idx) [B, cap, ...] whose last N rows are the
+ * draft's: row cap - N + i belongs to node i.  Committed rows are rows 0 .. cap-N-1.
+ *
+ * What is in device memory is checked by the kernels.  A session with len < 0, n_node
+ * outside 0 .. N or a bad parent or leaf is left alone (DS4A_ERR_DEVICE_INDEX in the device
+ * error word); so is one whose tokens pass max_pages * page or whose committed rows pass
+ * cap - N (DS4A_ERR_CAPACITY).  A page id outside the pool: the token is not written, not
+ * attended and not pooled (DS4A_ERR_DEVICE_INDEX); a commit then leaves the session alone.
+ * Early reads: none.  These calls write arrays that other calls read early when the
+ * caller passes them there (q_out as a query, committed key rows as k_idx): do not
+ * put such a call directly behind the call that writes them.
+ */
+typedef struct ds4a_paged_kv {
+    int B;                       /* sessions, 0 .. 65535 */
+    int D;                       /* head dim, 64 or 128 */
+    int page;                    /* token rows per page, a multiple of 16, 16 .. 65536 */
+    int max_pages;               /* page table entries per session; max_pages * page < 2^31 */
+    long long n_pages;           /* pages of the pool; n_pages * page < 2^31 */
+    uint16_t *k, *v;             /* [n_pages, page, D] fp16 */
+    const int32_t *table;        /* [B, max_pages] */
+    const long long *len;        /* [B] int64: committed tokens */
+} ds4a_paged_kv_t;
+
+/*
+ * ds4a_paged_append -- token i < n_tok[s] of session s into slot len[s] + i, with the
+ * rotation of its position applied to its key and, with q, to its query heads.
+ *
+ *   k, v       [B, N, D] fp16; N >= 0 (up to 64 with parent).
+ *   n_tok      [B] int32.
+ *   parent     [B, N] int32: positions len + depth; NULL: positions len + i.
+ *   inv_freq   [rot/2] float: radians per position of each rotated pair (>= 0, finite);
+ *              NULL with rot = 0: keys and queries are copied as they are.
+ *   rot, rot_off  the rotated dims rot_off .. rot_off+rot-1: rot a multiple of 16, 0 .. D,
+ *              rot_off a multiple of 8, rot_off + rot <= D.
+ *   interleaved  1: pair j is dims (2j, 2j+1) of the rotated dims; 0: dims (j, j + rot/2).
+ *   q, q_out   [B, N, H, D] fp16, or both NULL (H is then ignored); q_out may be q, and may
+ *              not overlap it otherwise.  H multiple of 8, 8 .. 64.
+ * The angle is position * inv_freq taken modulo one turn exactly; sine, cosine and the
+ * products are binary32, rounded once to fp16.  len is not changed.
+ */
+int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16_t *v, int N, const int32_t *n_tok,
+                      const int32_t *parent, const float *inv_freq, int rot, int rot_off, int interleaved,
+                      const uint16_t *q, int H, uint16_t *q_out, void *stream);
+
+/*
+ * ds4a_compress_tree -- the compressed row of every drafted node whose position p ends a
+ * block ((p+1) % ratio == 0), over the block's tokens on the node's own path, into row
+ * cap - N + node of comp_k and comp_v (rows of other nodes are left as they were).  The
+ * tokens are read from the pages; state is the state of ds4a_compress_append at len
+ * (read when len % ratio != 0, not changed).  The rows are, bit for bit, those that
+ * ds4a_compress_append writes when fed the path one token at a time.
+ *   N          1 .. 64;  ratio 1 .. 1024;  score_w [D] float;  state [B, 2 + 2D] float.
+ *   cap        rows per session, >= N (DS4A_ERR_CAPACITY).
+ */
+int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, const int32_t *parent,
+                       const float *score_w, int ratio, const float *state, uint16_t *comp_k, uint16_t *comp_v,
+                       long long cap, void *stream);
+
+/*
+ * ds4a_attn_tree -- for every node at position p and head h one softmax over: the raw
+ * tokens of its path at positions max(0, p-window+1) .. p (committed ones, then its
+ * ancestors and itself); and, with ratio > 0, the compressed rows in its sel row, or with
+ * sel = NULL every row j with (j+1)*ratio <= p+1.  Row j >= len/ratio is the row that the
+ * ancestor at position (j+1)*ratio-1 completed (ds4a_compress_tree wrote it).
+ *
+ *   q          [B, N, H, D] fp16; N 1 .. 64; H multiple of 8, 8 .. 64.
+ *   window     >= 1; a window past every length attends the whole cache.
+ *   comp_k, comp_v [B, cap, D] fp16, cap >= N; may be NULL when ratio == 0.
+ *   sel        [B, N, n_sel] int32 (as ds4a_indexer_topk writes them: negative entries are
+ *              skipped; entries not yet complete at p are skipped and recorded as
+ *              DS4A_ERR_DEVICE_INDEX), or NULL.
+ *   out        [B, N, H, D] fp16.
+ *   ws         ds4a_attn_tree_workspace_bytes(B, N, H, D) bytes, 256-byte aligned, zero-filled
+ *              once by the caller; the calls leave it ready for the next.  Calls that share one
+ *              workspace must be stream-ordered (two captured graphs that may replay at
+ *              the same time need one each).
+ * q, comp_k, comp_v, out and the pools are 16-byte aligned.  A node none of whose rows can be
+ * read (bad page ids) gets zeros.
+ */
+int ds4a_attn_tree(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, const int32_t *n_node,
+                   const int32_t *parent, long long window, const uint16_t *comp_k, const uint16_t *comp_v,
+                   long long cap, int ratio, const int32_t *sel, int n_sel, float scale, uint16_t *out, void *ws,
+                   size_t ws_bytes, void *stream);
+
+size_t ds4a_attn_tree_workspace_bytes(int B, int N, int H, int D);
+
+/*
+ * ds4a_commit_tree -- accepts the path that ends in node leaf[s] (-1: nothing): its tokens
+ * move to slots len .. len+a-1 in path order, the compressed rows they completed move
+ * from the draft's rows to rows len/ratio and up (with k_idx, their indexer keys too, laid
+ * out the same way), state_out gets the compressor state after the path and len_out[s] =
+ * len[s] + a.  A path token's state update and rows are those of ds4a_compress_append fed
+ * one token at a time.
+ *   leaf       [B] int32.
+ *   len_out    [B] int64; may be kv->len's array.
+ *   score_w, state, state_out, comp_k, comp_v, cap: as ds4a_compress_tree (state_out may be
+ *              state; it is written when (len + a) % ratio != 0); all NULL with ratio = 0.
+ *   k_idx      [B, cap, d_idx] fp16, 16-byte aligned, d_idx multiple of 8, 8 .. 256; or NULL.
+ */
+int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, const int32_t *parent,
+                     const int32_t *leaf, long long *len_out, const float *score_w, int ratio, const float *state,
+                     float *state_out, uint16_t *comp_k, uint16_t *comp_v, long long cap, uint16_t *k_idx, int d_idx,
+                     void *stream);
 
 /*
  * ds4a_probe_gather -- MEASUREMENT CALL, not a step of the attention path; the
