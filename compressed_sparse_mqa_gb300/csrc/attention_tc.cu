@@ -45,14 +45,25 @@
 // All hand-offs are mbarriers with time-bounded waits; a wait that gives up
 // records DS4A_ERR_TIMEOUT.  Warps that share a named barrier never leave their
 // loops early: after a failed wait they skip the work but keep the structure.
-#include <cuda.h>
-
 #include "ds4a_common.cuh"
 #include "ds4a_internal.h"
 #include "tcgen05.cuh"
+#include "tma.cuh"
 
 namespace ds4a {
 namespace {
+
+using tc::encode_tiled;
+using tc::expect_tx;
+using tc::ld_x32;
+using tc::mbar_arrive;
+using tc::prefetch_map;
+using tc::setmaxnreg_dec;
+using tc::setmaxnreg_inc;
+using tc::st_x16;
+using tc::tma_gather4;
+using tc::tma_load_2d;
+using tc::wait_st;
 
 constexpr int kH = 64;                      // heads (MMA N)
 constexpr int kD = 128;                     // head dim
@@ -123,28 +134,6 @@ struct Args {
     float scale_log2;
 };
 
-DS4A_DEVINL void ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-DS4A_DEVINL void st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
-}
-DS4A_DEVINL void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-
-DS4A_DEVINL void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(bar)) : "memory");
-}
 // named barriers 1 and 2: the four softmax warps of one head half (128 threads)
 DS4A_DEVINL void half_barrier(int half) { asm volatile("bar.sync %0, 128;\n" ::"r"(1 + half) : "memory"); }
 // the same barrier, returning whether any of the 128 threads passed pred = true
@@ -157,9 +146,6 @@ DS4A_DEVINL bool half_any(int half, bool pred) {
         : "memory");
     return r != 0;
 }
-template <int N> DS4A_DEVINL void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
-template <int N> DS4A_DEVINL void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
-
 // 2^x with the hardware approximation (flush-to-zero): the softmax numerators
 // are rounded to fp16 right after, far coarser than its error
 DS4A_DEVINL float ex2(float x) {
@@ -197,28 +183,6 @@ DS4A_DEVINL float transpose_sum32(float (&v)[32], int lane) {
         }
     }
     return v[0];
-}
-
-DS4A_DEVINL void expect_tx(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(tc::smem_u32(bar)), "r"(bytes)
-                 : "memory");
-}
-// 2-D TMA tile load (x = column, y = row) completing on bar
-DS4A_DEVINL void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(tc::smem_u32(dst)),
-                 "l"(map), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
-                 : "memory");
-}
-// four rows r.x .. r.w, columns x .. x+63, to 4 consecutive 128-byte rows at dst
-DS4A_DEVINL void tma_gather4(uint32_t dst, const CUtensorMap *map, int x, int4 r, uint64_t *bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(dst),
-                 "l"(map), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(tc::smem_u32(bar))
-                 : "memory");
-}
-DS4A_DEVINL void prefetch_map(const CUtensorMap *map) {
-    asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }
 
 // The key list of query i: its window rows padded to whole tiles, then its
@@ -695,32 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_tc_kernel(const __gr
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// the driver's tensor-map encoder, looked up once through the runtime
-EncodeTiledFn encode_tiled() {
-    static const EncodeTiledFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
-// rows x 128 fp16 values, row-major; boxes of 64 columns x box_rows rows, 128-byte swizzle
 bool encode_rows(CUtensorMap *m, const uint16_t *ptr, long long rows, uint32_t box_rows) {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
-    const cuuint32_t box[2] = {64, box_rows}, es[2] = {1, 1};
-    return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint16_t *>(ptr), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return tc::encode_map(m, ptr, kD, rows, box_rows);
 }
 
 }  // namespace

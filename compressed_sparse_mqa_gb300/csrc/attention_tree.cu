@@ -1,4 +1,5 @@
-// attention_tree.cu -- attention of a tree of drafted tokens over a paged cache.
+// attention_tree.cu -- attention of a tree of drafted tokens over a paged cache, on the
+// 5th-generation tensor cores.
 //
 // For node i at position p of session s and head h,
 //   o_h = sum_j softmax_j(scale * q_h . K_j) V_j
@@ -7,137 +8,990 @@
 // row complete at p.  A row j >= len / ratio is the one completed by the ancestor at
 // position (j+1) * ratio - 1; it is read from the draft's rows (cap - N + that node).
 //
-// One CTA per node; its keys are a list (raw positions in order, then compressed rows).
+// All heads of all nodes of a session share its keys (multi-query attention), so the
+// rows of one product are (node, head) pairs: 128 rows on the M side of tcgen05.mma, 128
+// keys on the N side.  Nodes differ only in a few keys (the tree, the window's edge): those
+// are masked in the scores.  With sel every node has its own key list and its heads are a
+// tile of their own.
+//
+// Keys.  A session's keys are runs of 16 rows: the raw slots from its window's edge to the
+// last drafted node (pages are multiples of 16 rows, so a run is inside one page), the
+// committed compressed rows, the draft's rows.  A key tile is 8 runs, one TMA box each per 64
+// columns (sel: tile::gather4 loads of 4 rows).  Runs past the end load zeros.
+//
+// Work item: a row tile (one or two 128-row blocks of a session, or one node's heads) and
+// a range of its key tiles; n_split ranges per row tile when there are few row tiles, joined
+// by combine_kernel.  CTAs are persistent, one per SM.  Roles:
+//   warps 0-3, 4-7  softmax of side 0 / 1: thread = row.  With two row blocks a side is a
+//                row block and both use the same key tiles; with one block the sides take
+//                alternate key tiles and are joined at the end (both accumulators have
+//                the row in the same tensor-memory lane).
+//   warp 8       work set-up: counts, ancestor masks, tile range of the next item.
+//   warp 9       MMA issuer: S = Q K^T into the side's score columns, O += P V with P in
+//                16 bits read from tensor memory, over the scores it came from.
+//   warps 10-11  checkers (below).
+//   warps 12-15  TMA producers: K (12, 13) and V (14, 15).
+// The two sides keep the tensor core busy in turn: while one computes its softmax, the
+// other's products run.  The softmax reference of a row is raised (and O rescaled) only when
+// a score exceeds it by 2^8; p <= 256 fits 16 bits, sums are binary32.
+//
+// Masked keys get weight 0, but 0 * V is not 0 where V is infinite or NaN: slots never
+// written, or another branch's values.  The checkers scan the V rows of runs that some row
+// masks: values that are not finite are set to 0, and where the key is valid for some
+// rows, noted, so that exactly those rows get them in the end.
 #include "paged_dev.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
 
 namespace ds4a {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 32;          // keys per tile, one per lane
-constexpr int kMaxHeadsPerWarp = 8;
+constexpr int kTK = 128;                   // keys per tile, rows per block
+constexpr int kRun = 16, kRuns = kTK / kRun;
+constexpr int kNS = 2;                     // K stages, and V stages
+constexpr int kSoftWarps = 8, kSetupWarp = 8, kMmaWarp = 9, kChkWarp0 = 10, kChkWarps = 2, kProdWarp0 = 12;
+constexpr int kProd = 2;                   // producer warps for K, and for V
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kSoftRegs = 200, kOtherRegs = 56;
+constexpr int kLaunchRegs = 65536 / kThreads;
+static_assert(kSoftWarps * kSoftRegs + (kWarps - kSoftWarps) * kOtherRegs <= kWarps * kLaunchRegs,
+              "the register split exceeds what the block is launched with");
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescale = 8.f;            // lazy rescale threshold (log2 units)
+constexpr int kEdge = 2 * kMaxNodes;       // first window-edge entry of the poison table
+constexpr int kPoison = 3 * kMaxNodes;     // keys that only some rows attend: nodes, their rows, the window's edge
+
+// One work item, made by the set-up warp.  Slots, rows and counts are below 2^31.
+struct alignas(16) Work {
+    unsigned long long raw[kMaxNodes];     // drafted tokens that node i attends
+    unsigned long long cmp[kMaxNodes];     // drafted nodes whose completed row node i attends (sel: its whole path)
+    int lo[kMaxNodes];                     // first committed slot that node i attends
+    unsigned long long any_raw, all_raw, any_cmp, all_cmp;   // over the item's nodes
+    int lo_min, lo_max;
+    int s, len, n, t0;                     // session; first slot of the key runs
+    int raw_runs, comp_runs, n_runs;       // runs of raw slots, of committed compressed rows (sel: of the list), in all
+    int n_vis0;                            // committed compressed rows (sel: list entries)
+    int node, depth;                       // sel: the node and its depth
+    int row0, rows;                        // first row in the session, valid rows (<= 256)
+    int sides2;                            // two row blocks
+    int tile0, tile1;                      // key tiles of this item
+    int active, split;                     // splits that have tiles; this one
+    int slot;                              // index of the row tile among all
+    int dirty;                             // poison entries exist
+    uint32_t poison[kPoison][12];          // per key: NaN, +inf, -inf bits of its 128 values
+};
+
+struct Bars {
+    uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_ok[kNS], v_empty[kNS];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t w_full[2], w_empty[2], chk[2];
+    uint64_t join;                         // side 1 has posted its sums
+};
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_tree_kernel(AttnTreeArgs a) {
-    __shared__ unsigned long long s_mask[kMaxNodes];
-    __shared__ int s_ptr[kMaxNodes];
-    __shared__ __align__(16) uint16_t s_k[kTile][D + 8], s_v[kTile][D + 8];
-    __shared__ const uint16_t *s_src[2][kTile];
-    __shared__ __align__(16) uint16_t s_q[64][D];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.x, s = blockIdx.y;
+struct Layout {
+    static constexpr int tile = kTK * D * 2;
+    static constexpr int q = 0;                               // 2 row blocks
+    static constexpr int k = q + 2 * tile;
+    static constexpr int v = k + kNS * tile;
+    static constexpr int work = v + kNS * tile;
+    // uint16 [4][8]: readable keys per run of the CTA's tile number & 3, once from the K and once from the V
+    // producers (a slot is written again four tiles on, when the products two tiles on have been issued and the
+    // readers of this one are therefore done)
+    static constexpr int info = work + 2 * static_cast<int>(sizeof(Work));
+    static constexpr int ml = info + 2 * 4 * kRuns * 2;                          // float2 [128] side 1's (max, sum)
+    static constexpr int bars = ml + kTK * 8;
+    static constexpr int end = bars + static_cast<int>(sizeof(Bars));
+    static constexpr size_t bytes = end + 1024;
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    static_assert(work % 16 == 0 && bars % 8 == 0 && sizeof(Work) % 16 == 0, "alignment");
+};
+
+struct Args {
+    CUtensorMap map_q, map_k, map_v;               // 128-row boxes; 16-row boxes over the pools
+    CUtensorMap map_ck, map_cv;                    // compressed rows: 16-row boxes (sel: one-row, gathers)
+    AttnTreeArgs a;
+    float *part;                                   // [slot * n_split + split][tile rows][D]
+    float2 *part_ml;                               // [...][tile rows] (max, sum)
+    int *active;                                   // [slots]
+    int B, n_split, min_tiles, row_tiles, tile_rows, n_work;
+    int pool_oob, comp_oob;                        // rows of the maps: the zero-fill rows
+};
+
+struct JoinArgs {
+    const float *part;
+    const float2 *part_ml;
+    const int *active;
+    const int32_t *n_node;
+    uint16_t *out;
+    int B, N, H, n_split, row_tiles, tile_rows, item_rows;
+};
+
+DS4A_DEVINL float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+DS4A_DEVINL int clamp16(int x) { return x < 0 ? 0 : (x > kRun ? kRun : x); }
+
+// Valid keys of run v for a row with first committed slot lo, drafted tokens raw and
+// completed rows cmp.  kSel: runs behind the raw ones are the list's, whose bits are in info.
+template <bool kSel>
+DS4A_DEVINL uint32_t run_bits(const Work &w, int v, int lo, unsigned long long raw, unsigned long long cmp,
+                              const uint16_t *info) {
+    if (v < w.raw_runs) {
+        const int t = w.t0 + v * kRun;
+        const int b = clamp16(lo - t), e = clamp16(w.len - t), d = t - w.len;
+        uint32_t bits = ((1u << e) - 1u) & ~((1u << b) - 1u);
+        if (d > -kRun && d < kMaxNodes) bits |= static_cast<uint32_t>(d >= 0 ? raw >> d : raw << -d);
+        return bits & info[v & (kRuns - 1)];
+    }
+    if (kSel) return info[v & (kRuns - 1)];   // behind the list: 0
+    v -= w.raw_runs;
+    if (v < w.comp_runs) return (1u << clamp16(w.n_vis0 - v * kRun)) - 1u;
+    v -= w.comp_runs;
+    return v * kRun < kMaxNodes ? static_cast<uint32_t>(cmp >> (v * kRun)) & 0xffffu : 0u;
+}
+// every key of tile t is valid for every row (with readable pages)
+DS4A_DEVINL bool tile_full(const Work &w, int t) {
+    const int v = t * kRuns;
+    if (v < w.raw_runs) {
+        const int slot = w.t0 + v * kRun;
+        return slot >= w.lo_max && slot + kTK <= w.len;
+    }
+    return (v - w.raw_runs + kRuns) * kRun <= w.n_vis0;
+}
+
+DS4A_DEVINL unsigned long long shfl64(unsigned long long v, int src) { return __shfl_sync(0xffffffffu, v, src); }
+
+// The set-up warp's item: lane holds nodes lane and lane + 32.
+template <bool kSel>
+__device__ void make_work(const Args &g, int item, Work &w, int lane) {
+    const AttnTreeArgs &a = g.a;
+    const int split = item % g.n_split, slot = item / g.n_split;
+    const int s = slot / g.row_tiles, rt = slot - s * g.row_tiles;
+    const Session ses = load_session(a.kv, a.n_node, a.N, s, lane == 0 ? a.err : nullptr);
+    bool ok = ses.ok;
+    if (ok && a.ratio > 0 && ses.len / a.ratio > a.cap - a.N) {
+        if (lane == 0) record_error(a.err, DS4A_ERR_CAPACITY);
+        ok = false;
+    }
+    const int row0 = kSel ? rt * a.H : rt * g.tile_rows;
+    const int n = ok ? ses.n : 0, len = ok ? static_cast<int>(ses.len) : 0;
+    int rows = n * a.H - row0;
+    rows = rows < 0 ? 0 : rows;
+    if (rows > (kSel ? a.H : g.tile_rows)) rows = kSel ? a.H : g.tile_rows;
+    // ancestors by pointer jumping: after round r a mask holds the nearest 2^r path members
+    unsigned long long m[2];
+    int p[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int i = lane + 32 * x;
+        p[x] = -1;
+        if (i < n) {
+            p[x] = a.parent ? __ldg(a.parent + static_cast<long long>(s) * a.N + i) : i - 1;
+            if (p[x] < -1 || p[x] >= i) {
+                record_error(a.err, DS4A_ERR_DEVICE_INDEX);
+                ok = false;
+                p[x] = -1;
+            }
+        }
+        m[x] = 1ull << i;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) rows = 0;
+    for (int round = 0; round < 6; ++round) {
+        unsigned long long nm[2];
+        int np[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int src = p[x] & 31;
+            const unsigned long long m0 = shfl64(m[0], src), m1 = shfl64(m[1], src);
+            const int p0 = __shfl_sync(0xffffffffu, p[0], src), p1 = __shfl_sync(0xffffffffu, p[1], src);
+            nm[x] = p[x] < 0 ? m[x] : m[x] | (p[x] < 32 ? m0 : m1);
+            np[x] = p[x] < 0 ? -1 : (p[x] < 32 ? p0 : p1);
+        }
+        m[0] = nm[0];
+        m[1] = nm[1];
+        p[0] = np[0];
+        p[1] = np[1];
+    }
+    // window: a drafted ancestor is in it if it is among the path's last `window` members
+    const int i0 = rows > 0 ? row0 / a.H : 0, i1 = rows > 0 ? (row0 + rows - 1) / a.H : -1;
+    unsigned long long done = 0;                     // nodes that complete a row
+    if (a.ratio > 0 && !kSel) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = lane + 32 * x;
+            const bool c = i < n && (len + __popcll(m[x])) % a.ratio == 0;
+            done |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, c)) << (32 * x);
+        }
+    }
+    unsigned long long any_raw = 0, all_raw = ~0ull, any_cmp = 0, all_cmp = ~0ull;
+    int lo_min = 0x7fffffff, lo_max = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int i = lane + 32 * x;
+        const int depth = __popcll(m[x]) - 1;
+        unsigned long long raw = m[x];
+        for (long long c = depth + 1; c > a.window; --c) raw &= raw - 1;   // the shallowest fall out of the window
+        const long long lo64 = static_cast<long long>(len) + depth - a.window + 1;
+        const int lo = lo64 < 0 ? 0 : static_cast<int>(lo64);
+        const unsigned long long cmp = kSel ? m[x] : m[x] & done;
+        w.raw[i] = raw;
+        w.cmp[i] = cmp;
+        w.lo[i] = lo;
+        if (i >= i0 && i <= i1) {
+            any_raw |= raw;
+            all_raw &= raw;
+            any_cmp |= cmp;
+            all_cmp &= cmp;
+            lo_min = min(lo_min, lo);
+            lo_max = max(lo_max, lo);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        any_raw |= __shfl_xor_sync(0xffffffffu, any_raw, o);
+        all_raw &= __shfl_xor_sync(0xffffffffu, all_raw, o);
+        any_cmp |= __shfl_xor_sync(0xffffffffu, any_cmp, o);
+        all_cmp &= __shfl_xor_sync(0xffffffffu, all_cmp, o);
+        lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
+        lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
+    }
+    if (w.dirty)
+        for (int x = lane; x < kPoison * 12; x += 32) (&w.poison[0][0])[x] = 0;
+    __syncwarp();
+    if (lane == 0) {
+        const int t0 = min(lo_min, len) & ~(kRun - 1);
+        w.any_raw = any_raw;
+        w.all_raw = all_raw;
+        w.any_cmp = any_cmp;
+        w.all_cmp = all_cmp;
+        w.lo_min = lo_min;
+        w.lo_max = lo_max;
+        w.s = s;
+        w.len = len;
+        w.n = n;
+        w.t0 = t0;
+        w.raw_runs = (len + n - t0 + kRun - 1) / kRun;
+        w.n_vis0 = kSel ? a.n_sel : (a.ratio > 0 ? len / a.ratio : 0);
+        w.comp_runs = (w.n_vis0 + kRun - 1) / kRun;
+        w.n_runs = w.raw_runs + w.comp_runs;
+        // the draft's rows, as far as one of the item's nodes attends any
+        if (!kSel && any_cmp) w.n_runs += (64 - __clzll(static_cast<long long>(any_cmp)) + kRun - 1) / kRun;
+        w.node = i0;
+        w.row0 = row0;
+        w.rows = rows;
+        w.sides2 = rows > kTK;
+        const int tiles = rows > 0 ? (w.n_runs + kRuns - 1) / kRuns : 0;
+        int chunk = (tiles + g.n_split - 1) / g.n_split;
+        if (chunk < g.min_tiles) chunk = g.min_tiles;
+        w.active = (tiles + chunk - 1) / chunk;
+        w.split = split;
+        w.slot = slot;
+        w.tile0 = min(tiles, split * chunk);
+        w.tile1 = min(tiles, w.tile0 + chunk);
+        w.dirty = 0;
+        if (split == 0 && g.n_split > 1) g.active[slot] = w.active;
+    }
+    __syncwarp();
+}
+
+// Row of entry j of a node's list in the session's compressed rows: -1 (skipped) if negative,
+// and recorded if not complete at the node's position.
+DS4A_DEVINL int sel_row(const AttnTreeArgs &a, int len, unsigned long long path, int j, bool record) {
+    if (j < 0) return -1;
+    if (j >= (len + __popcll(path)) / a.ratio) {
+        if (record) record_error(a.err, DS4A_ERR_DEVICE_INDEX);
+        return -1;
+    }
+    if (j < len / a.ratio) return j;
+    return static_cast<int>(a.cap) - a.N + path_node(path, (j + 1) * a.ratio - 1 - len);
+}
+
+template <int D, bool kSel>
+__global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_constant__ Args g) {
+    using L = Layout<D>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Work *works = reinterpret_cast<Work *>(smem + L::work);
+    uint16_t *info = reinterpret_cast<uint16_t *>(smem + L::info);
+    float2 *s_ml = reinterpret_cast<float2 *>(smem + L::ml);
+    Bars &bar = *reinterpret_cast<Bars *>(smem + L::bars);
+    __shared__ uint32_t s_tmem;
+    const AttnTreeArgs &a = g.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kAtoms = D / 64, kAtomBytes = kTK * 128;
+
+    if (tid == 0) {
+        for (int x = 0; x < kNS; ++x) {
+            tc::mbar_init(&bar.k_full[x], kProd);
+            tc::mbar_init(&bar.k_empty[x], 1);
+            tc::mbar_init(&bar.v_full[x], kProd);
+            tc::mbar_init(&bar.v_ok[x], kChkWarps);
+            tc::mbar_init(&bar.v_empty[x], 1);
+        }
+        tc::mbar_init(&bar.q_full, 1);
+        tc::mbar_init(&bar.q_empty, 1);
+        for (int x = 0; x < 2; ++x) {
+            tc::mbar_init(&bar.s_full[x], 1);
+            tc::mbar_init(&bar.p_full[x], 4);
+            tc::mbar_init(&bar.o_full[x], 1);
+            tc::mbar_init(&bar.o_empty[x], 4);
+            tc::mbar_init(&bar.w_full[x], 1);
+            tc::mbar_init(&bar.w_empty[x], kWarps - 1);
+            tc::mbar_init(&bar.chk[x], kChkWarps);
+        }
+        tc::mbar_init(&bar.join, 4);
+        tc::mbar_fence_init();
+    }
+    if (warp == kSetupWarp)
+        for (int x = lane; x < kPoison * 12; x += 32) {
+            (&works[0].poison[0][0])[x] = 0;
+            (&works[1].poison[0][0])[x] = 0;
+        }
+    if (warp == kSetupWarp && lane < 2) works[lane].dirty = 0;
+    if (warp == kMmaWarp) tc::tmem_alloc(&s_tmem, kTmemCols);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
     pdl_wait();
     pdl_trigger();
-    const Session ses = load_session(a.kv, a.n_node, a.N, s, a.err);
-    if (!ses.ok || i >= ses.n) return;
-    if (a.ratio > 0 && ses.len / a.ratio > a.cap - a.N) {
-        if (tid == 0) record_error(a.err, DS4A_ERR_CAPACITY);
-        return;
-    }
-    if (!tree_masks(a.parent ? a.parent + static_cast<long long>(s) * a.N : nullptr, ses.n, s_mask, s_ptr, a.err))
-        return;
-    const unsigned long long path = s_mask[i];
-    const long long p = ses.len + __popcll(path) - 1;
-    const long long first = p - a.window + 1 > 0 ? p - a.window + 1 : 0;
-    const long long n_raw = p - first + 1;
-    const long long n_vis0 = a.ratio > 0 ? ses.len / a.ratio : 0, n_vis = a.ratio > 0 ? (p + 1) / a.ratio : 0;
-    const long long n_comp = a.sel ? a.n_sel : n_vis;
-    const int32_t *sel = a.sel ? a.sel + (static_cast<long long>(s) * a.N + i) * a.n_sel : nullptr;
-    const int32_t *table = a.kv.table + static_cast<long long>(s) * a.kv.max_pages;
-    const long long node = static_cast<long long>(s) * a.N + i;
-    for (int w = tid; w < a.H * D / 8; w += kThreads)
-        reinterpret_cast<uint4 *>(&s_q[0][0])[w] = reinterpret_cast<const uint4 *>(a.q + node * a.H * D)[w];
-    float m[kMaxHeadsPerWarp], l[kMaxHeadsPerWarp], o[kMaxHeadsPerWarp][D / 32];
+    bool ok = true;
+    // a failed wait records the failure; later waits of this thread return at once
+    auto wait = [&](uint64_t *b, uint32_t parity) {
+        if (ok && !tc::mbar_wait(b, parity & 1u)) ok = false;
+        return ok;
+    };
+    // items of this CTA, and the shared copy of item number it
+    const int n_items = g.n_work > static_cast<int>(blockIdx.x) ? (g.n_work - blockIdx.x - 1) / gridDim.x + 1 : 0;
+
+    if (warp < kSoftWarps) {
+        tc::setmaxnreg_inc<kSoftRegs>();
+        const int side = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t col_s = tmem + lanes + kColS + side * kTK, col_o = tmem + lanes + kColO + side * kTK;
+        const float c2 = a.scale_log2;
+        uint32_t n_s = 0, n_o = 0, n_join = 0, n_t = 0;   // n_t: tiles of the items before
+        for (int it = 0; it < n_items; ++it) {
+            Work &w = works[it & 1];
+            if (!__all_sync(0xffffffffu, wait(&bar.w_full[it & 1], it >> 1))) break;
+            const int t0 = w.tile0, t1 = w.tile1, sides2 = w.sides2;
+            const int row = (sides2 ? side * kTK : 0) + r;        // row in the item
+            const int node = min(kMaxNodes - 1, (w.row0 + row) / a.H);
+            const int lo = w.lo[node];
+            const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
+            float m = -INFINITY, l = 0.f;
+            bool first = true;
+            for (int t = sides2 ? t0 : t0 + side; t < t1; t += sides2 ? 1 : 2) {
+                wait(&bar.s_full[side], n_s++);
+                tc::fence_after_sync();
+                uint32_t x[4][32];
 #pragma unroll
-    for (int x = 0; x < kMaxHeadsPerWarp; ++x) {
-        m[x] = -INFINITY;
-        l[x] = 0.f;
+                for (int c = 0; c < 4; ++c) tc::ld_x32(col_s + c * 32, x[c]);
+                tc::wait_ld();
+                const uint16_t *inf = info + ((n_t + t - t0) & 3) * kRuns;
+                const uint4 iw = *reinterpret_cast<const uint4 *>(inf);
+                if ((kSel ? t * kRuns < w.raw_runs : !tile_full(w, t)) || (iw.x & iw.y & iw.z & iw.w) != 0xffffffffu) {
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[x][e] = 0.f;
-    }
-    for (long long k0 = 0; k0 < n_raw + n_comp; k0 += kTile) {
-        if (tid < kTile) {
-            const long long kx = k0 + tid;
-            const uint16_t *ks = nullptr, *vs = nullptr;
-            if (kx < n_raw) {
-                const long long t = first + kx;
-                const long long slot = t < ses.len ? t : ses.len + path_node(path, static_cast<int>(t - ses.len));
-                const long long row = pool_row(a.kv, table, static_cast<unsigned>(slot), a.err);
-                if (row >= 0) {
-                    ks = a.kv.k + row * D;
-                    vs = a.kv.v + row * D;
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t bits = run_bits<kSel>(w, t * kRuns + 2 * c, lo, raw, cmp, inf) |
+                                              run_bits<kSel>(w, t * kRuns + 2 * c + 1, lo, raw, cmp, inf) << 16;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) x[c][e] = 0xff800000u;   // -inf
+                    }
                 }
-            } else if (kx < n_raw + n_comp) {
-                const long long j = sel ? sel[kx - n_raw] : kx - n_raw;
-                if (j >= n_vis) {
-                    record_error(a.err, DS4A_ERR_DEVICE_INDEX);
-                } else if (j >= 0) {
-                    const long long r = j < n_vis0 ? j : a.cap - a.N + path_node(path, static_cast<int>((j + 1) * a.ratio - 1 - ses.len));
-                    ks = a.comp_k + (static_cast<long long>(s) * a.cap + r) * D;
-                    vs = a.comp_v + (static_cast<long long>(s) * a.cap + r) * D;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[c][e]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;   // scale > 0
+                // raise the reference: at the first finite score, then only past the threshold
+                float alpha = 1.f;
+                if (top > m + kRescale || (m == -INFINITY && top > m)) {
+                    alpha = ex2(m - top);
+                    m = top;
+                    l *= alpha;
+                }
+                if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // the earlier product of this side is complete: it was issued before the scores just read
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t o[16];
+                        tc::ld_x16(col_o + c * 16, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tc::st_x16(col_o + c * 16, o);
+                    }
+                }
+                first = false;
+                const float ref = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float p0 = ex2(fmaf(__uint_as_float(x[c][2 * e]), c2, -ref));
+                        const float p1 = ex2(fmaf(__uint_as_float(x[c][2 * e + 1]), c2, -ref));
+                        sum[e & 1] += p0;
+                        sum[2 + (e & 1)] += p1;
+                        pk[e] = pack_half2(p0, p1);
+                    }
+                    tc::st_x16(col_s + c * 16, pk);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc::wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.p_full[side]);
+            }
+            n_t += t1 - t0;
+            // ---- end of the item ----
+            const bool have = !first;                              // this side has tiles
+            if (t1 > t0) {
+                if (have) {
+                    wait(&bar.o_full[side], n_o++);
+                    tc::fence_after_sync();
+                }
+                const bool joined = !sides2 && t1 - t0 > 1;        // side 1 holds part of the same rows
+                if (joined) {
+                    if (side == 1) {
+                        s_ml[r] = make_float2(m, l);
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&bar.join);
+                    } else {
+                        wait(&bar.join, n_join);
+                    }
+                    ++n_join;
+                }
+                if (have && (sides2 || side == 0)) {
+                    float wa = 1.f, wb = 0.f;
+                    if (joined) {
+                        const float2 o = s_ml[r];
+                        const float mm = fmaxf(m, o.x);
+                        const float rf = mm == -INFINITY ? 0.f : mm;
+                        wa = ex2(m - rf);
+                        wb = ex2(o.x - rf);
+                        l = l * wa + o.y * wb;
+                        m = mm;
+                    }
+                    wait(&bar.chk[it & 1], it >> 1);
+                    // values that are not finite, of the keys that this row attends
+                    uint32_t pz[12];
+#pragma unroll
+                    for (int e = 0; e < 12; ++e) pz[e] = 0;
+                    const int dirty = w.dirty;
+                    if (dirty) {
+                        for (int key = 0; key < kPoison; ++key) {
+                            bool hit;
+                            if (key < kMaxNodes) hit = (raw >> key) & 1ull;
+                            else if (key < kEdge) hit = (cmp >> (key - kMaxNodes)) & 1ull;
+                            else hit = w.lo_min + key - kEdge >= lo;
+                            if (!hit) continue;
+#pragma unroll
+                            for (int e = 0; e < 12; ++e) pz[e] |= w.poison[key][e];
+                        }
+                    }
+                    const bool valid = row < w.rows;
+                    const bool direct = w.active == 1;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    const long long qrow = (static_cast<long long>(w.s) * a.N) * a.H + w.row0 + row;
+                    const long long prow = (static_cast<long long>(w.slot) * g.n_split + w.split) * g.tile_rows + row;
+                    if (!direct && valid) g.part_ml[prow] = make_float2(m, l);
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tc::ld_x32(col_o + c * 32, o);
+                        if (joined) {
+                            uint32_t o2[32];
+                            tc::ld_x32(col_o + kTK + c * 32, o2);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * wa + __uint_as_float(o2[e]) * wb);
+                        } else {
+                            tc::wait_ld();
+                        }
+                        if (dirty) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const bool nan = (pz[c] >> e) & 1u, pi = (pz[4 + c] >> e) & 1u, ni = (pz[8 + c] >> e) & 1u;
+                                if (nan || (pi && ni)) o[e] = 0x7fffffffu;
+                                else if (pi) o[e] = 0x7f800000u;
+                                else if (ni) o[e] = 0xff800000u;
+                            }
+                        }
+                        if (valid && direct) {
+#pragma unroll
+                            for (int q4 = 0; q4 < 4; ++q4) {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    h[e] = pack_half2(__uint_as_float(o[q4 * 8 + 2 * e]) * inv,
+                                                      __uint_as_float(o[q4 * 8 + 2 * e + 1]) * inv);
+                                *reinterpret_cast<uint4 *>(a.out + qrow * D + c * 32 + q4 * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        } else if (valid) {
+#pragma unroll
+                            for (int q4 = 0; q4 < 8; ++q4)
+                                *reinterpret_cast<uint4 *>(g.part + prow * D + c * 32 + q4 * 4) =
+                                    make_uint4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]);
+                        }
+                    }
+                }
+                // the accumulators may be overwritten: side 0 has read both of a joined item
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (joined) {
+                        if (side == 0) {
+                            tc::mbar_arrive(&bar.o_empty[0]);
+                            tc::mbar_arrive(&bar.o_empty[1]);
+                        }
+                    } else if (have) {
+                        tc::mbar_arrive(&bar.o_empty[side]);
+                    }
                 }
             }
-            s_src[0][tid] = ks;
-            s_src[1][tid] = vs;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar.w_empty[it & 1]);
         }
-        __syncthreads();
-        for (int w = tid; w < kTile * D / 8; w += kThreads) {
-            const int r = w / (D / 8), ch = w % (D / 8);
-            const uint16_t *ks = s_src[0][r], *vs = s_src[1][r];
-            *reinterpret_cast<uint4 *>(&s_k[r][ch * 8]) = ks ? *reinterpret_cast<const uint4 *>(ks + ch * 8) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(&s_v[r][ch * 8]) = vs ? *reinterpret_cast<const uint4 *>(vs + ch * 8) : make_uint4(0, 0, 0, 0);
-        }
-        __syncthreads();
-        const bool valid = s_src[0][lane] != nullptr;
-#pragma unroll
-        for (int x = 0; x < kMaxHeadsPerWarp; ++x) {
-            const int h = warp + x * kWarps;
-            if (h >= a.H) continue;
-            float acc = 0.f;
-#pragma unroll 8
-            for (int d = 0; d < D; d += 2) {
-                const float2 qf = __half22float2(*reinterpret_cast<const __half2 *>(&s_q[h][d]));
-                const float2 kf = __half22float2(*reinterpret_cast<const __half2 *>(&s_k[lane][d]));
-                acc = fmaf(qf.x, kf.x, fmaf(qf.y, kf.y, acc));
+    } else {
+        tc::setmaxnreg_dec<kOtherRegs>();
+        // one lane waits for the warp, so that warp-wide steps stay converged
+        auto warp_wait = [&](uint64_t *b, uint32_t parity) {
+            bool good = true;
+            if (lane == 0) good = wait(b, parity);
+            good = __shfl_sync(0xffffffffu, good, 0);
+            __syncwarp();   // what lane 0 has waited for is visible to the warp
+            ok = ok && good;
+            return good;
+        };
+        if (warp == kSetupWarp) {
+            for (int it = 0; it < n_items; ++it) {
+                if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
+                make_work<kSel>(g, blockIdx.x + it * gridDim.x, works[it & 1], lane);
+                if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
+                __syncwarp();
             }
-            const float sc = valid ? acc * a.scale_log2 : -INFINITY;
-            const float mn = fmaxf(m[x], warp_max(sc));
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            const float pr = valid ? exp2f(sc - ref) : 0.f, al = exp2f(m[x] - ref);
-            l[x] = l[x] * al + warp_sum(pr);
-            m[x] = mn;
+        } else if (warp == kMmaWarp) {
+            if (lane == 0) {
+                constexpr uint32_t kIdS = tc::idesc_f16_f32(kTK, kTK, false, false);
+                constexpr uint32_t kIdO = tc::idesc_f16_f32(kTK, D, false, true);
+                uint32_t n_q = 0, n_k = 0, n_v = 0, n_p[2] = {0, 0}, n_o[2] = {0, 0};
+                for (int it = 0; it < n_items && ok; ++it) {
+                    const Work &w = works[it & 1];
+                    if (!wait(&bar.w_full[it & 1], it >> 1)) break;
+                    const int tiles = w.tile1 - w.tile0, sides2 = w.sides2;
+                    const int n = sides2 ? 2 * tiles : tiles;     // products: (side, tile) in turn
+                    if (n > 0) wait(&bar.q_full, n_q++);
+                    // S of product k: side k & 1, tile k / 2 or k
+                    auto issue_s = [&](int k) {
+                        const int side = k & 1;
+                        const uint32_t kt = n_k + (sides2 ? k >> 1 : k);
+                        const int st = kt % kNS;
+                        if (!sides2 || side == 0) wait(&bar.k_full[st], kt / kNS);
+                        if (!ok) return;
+                        tc::fence_after_sync();
+                        const uint32_t qa = tc::smem_u32(smem + L::q + (sides2 ? side : 0) * L::tile);
+                        const uint32_t kb = tc::smem_u32(smem + L::k + st * L::tile);
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) o[x][e] *= al;
-            for (int k = 0; k < kTile; ++k) {
-                const float pk = __shfl_sync(0xffffffffu, pr, k);
-                if (s_src[0][k] == nullptr) continue;
+                        for (int x = 0; x < D / 16; ++x)
+                            tc::mma_f16(tmem + kColS + side * kTK,
+                                        tc::desc_sw128(qa + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024),
+                                        tc::desc_sw128(kb + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024), kIdS, x > 0);
+                        tc::commit(&bar.s_full[side]);
+                        if (!sides2 || side == 1) tc::commit(&bar.k_empty[st]);
+                        if (k == n - 1) tc::commit(&bar.q_empty);
+                    };
+                    auto issue_pv = [&](int k) {
+                        const int side = k & 1;
+                        const uint32_t vt = n_v + (sides2 ? k >> 1 : k);
+                        const int st = vt % kNS;
+                        if (!sides2 || side == 0) wait(&bar.v_ok[st], vt / kNS);
+                        wait(&bar.p_full[side], n_p[side]++);
+                        if (k < 2 && n_o[side] > 0) wait(&bar.o_empty[side], n_o[side] - 1);
+                        if (!ok) return;
+                        tc::fence_after_sync();
+                        const uint32_t vb = tc::smem_u32(smem + L::v + st * L::tile);
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) o[x][e] = fmaf(pk, h2f(s_v[k][lane + e * 32]), o[x][e]);
+                        for (int x = 0; x < kTK / 16; ++x)
+                            tc::mma_f16_ts(tmem + kColO + side * kTK, tmem + kColS + side * kTK + x * 8,
+                                           tc::desc_sw128(vb + x * 2048, kAtomBytes, 1024), kIdO, k > 1 || x > 0);
+                        if (!sides2 || side == 1) tc::commit(&bar.v_empty[st]);
+                        if (k >= n - 2) {
+                            tc::commit(&bar.o_full[side]);
+                            ++n_o[side];
+                        }
+                    };
+                    if (n > 0) issue_s(0);
+                    if (n > 1 && ok) issue_s(1);
+                    for (int k = 0; k < n && ok; ++k) {
+                        issue_pv(k);
+                        if (k + 2 < n && ok) issue_s(k + 2);
+                    }
+                    n_k += tiles;
+                    n_v += tiles;
+                    tc::mbar_arrive(&bar.w_empty[it & 1]);
+                }
             }
+            __syncwarp();
+        } else if (warp < kProdWarp0) {
+            // ---------------- checkers ----------------
+            const int ct = (warp - kChkWarp0) * 32 + lane;
+            uint32_t n_v = 0;
+            for (int it = 0; it < n_items; ++it) {
+                Work &w = works[it & 1];
+                if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
+                for (int t = w.tile0; t < w.tile1; ++t, ++n_v) {
+                    const int st = n_v % kNS;
+                    if (!warp_wait(&bar.v_full[st], n_v / kNS)) break;
+                    if (kSel ? t * kRuns < w.raw_runs : !tile_full(w, t)) {
+                        const uint16_t *inf = info + (4 + (n_v & 3)) * kRuns;
+                        unsigned char *vt = smem + L::v + st * L::tile;
+                        bool wrote = false;
+                        for (int r = 0; r < kRuns; ++r) {
+                            const int v = t * kRuns + r;
+                            if (v >= w.n_runs) break;                                       // zeros
+                            const uint32_t any = run_bits<kSel>(w, v, w.lo_min, w.any_raw, w.any_cmp, inf);
+                            const uint32_t all = run_bits<kSel>(w, v, w.lo_max, w.all_raw, w.all_cmp, inf);
+                            if (all == 0xffffu || (kSel && v >= w.raw_runs)) continue;
+                            // 16-byte chunks of the run: 16 rows x 8 per atom
+#pragma unroll 1
+                            for (int x = ct; x < kRun * 8 * kAtoms; x += kChkWarps * 32) {
+                                const int atom = x / (kRun * 8), key = (x / 8) % kRun, ch = x % 8;
+                                uint4 *ptr = reinterpret_cast<uint4 *>(vt + atom * kAtomBytes +
+                                                                       tc::sw128_chunk(r * kRun + key, ch));
+                                const uint4 q = *ptr;
+                                auto odd = [](uint32_t u) {   // a half with all exponent bits set
+                                    const uint32_t z = (u & 0x7c007c00u) ^ 0x7c007c00u;
+                                    return (z - 0x00010001u) & ~z & 0x80008000u;
+                                };
+                                if (!(odd(q.x) | odd(q.y) | odd(q.z) | odd(q.w)) || ((all >> key) & 1u)) continue;
+                                uint16_t hv[8];
+                                *reinterpret_cast<uint4 *>(hv) = q;
+                                uint32_t nan = 0, pi = 0, ni = 0;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    if ((hv[e] & 0x7c00u) != 0x7c00u) continue;
+                                    if (hv[e] & 0x03ffu) nan |= 1u << e;
+                                    else if (hv[e] & 0x8000u) ni |= 1u << e;
+                                    else pi |= 1u << e;
+                                    hv[e] = 0;
+                                }
+                                *ptr = *reinterpret_cast<uint4 *>(hv);
+                                wrote = true;
+                                if (!((any >> key) & 1u)) continue;
+                                int slot;            // a key that some rows attend and some do not
+                                if (v < w.raw_runs) {
+                                    const int tk = w.t0 + v * kRun + key;
+                                    slot = tk >= w.len ? tk - w.len : kEdge + tk - w.lo_min;
+                                } else {
+                                    slot = kMaxNodes + (v - w.raw_runs - w.comp_runs) * kRun + key;
+                                }
+                                const int word = atom * 2 + ch / 4, sh = (ch % 4) * 8;
+                                if (nan) atomicOr(&w.poison[slot][word], nan << sh);
+                                if (pi) atomicOr(&w.poison[slot][4 + word], pi << sh);
+                                if (ni) atomicOr(&w.poison[slot][8 + word], ni << sh);
+                                w.dirty = 1;
+                            }
+                        }
+                        if (__any_sync(0xffffffffu, wrote)) tc::fence_proxy_async();
+                        __syncwarp();
+                    }
+                    if (lane == 0) tc::mbar_arrive(&bar.v_ok[st]);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(&bar.chk[it & 1]);
+                    tc::mbar_arrive(&bar.w_empty[it & 1]);
+                }
+            }
+        } else {
+            // ---------------- producers: warp pair K, warp pair V ----------------
+            const bool is_v = warp >= kProdWarp0 + kProd;
+            const int pw = (warp - kProdWarp0) % kProd;            // runs pw * 4 .. + 3 of each tile
+            constexpr int kRunsPer = kRuns / kProd;
+            uint64_t *full = is_v ? bar.v_full : bar.k_full, *empty = is_v ? bar.v_empty : bar.k_empty;
+            const CUtensorMap *map_raw = is_v ? &g.map_v : &g.map_k, *map_comp = is_v ? &g.map_cv : &g.map_ck;
+            unsigned char *ring = smem + (is_v ? L::v : L::k);
+            uint32_t n_t = 0, n_q = 0;
+            if (lane == 0) {
+                tc::prefetch_map(map_raw);
+                if (a.ratio > 0) tc::prefetch_map(map_comp);
+                if (!is_v && pw == 0) tc::prefetch_map(&g.map_q);
+            }
+            for (int it = 0; it < n_items; ++it) {
+                const Work &w = works[it & 1];
+                if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
+                const int32_t *table = a.kv.table + static_cast<long long>(w.s) * a.kv.max_pages;
+                if (!is_v && pw == 0 && w.tile1 > w.tile0) {
+                    if (n_q > 0 && !warp_wait(&bar.q_empty, n_q - 1)) break;
+                    if (lane == 0) {
+                        const int blocks = w.sides2 ? 2 : 1;
+                        tc::expect_tx(&bar.q_full, blocks * L::tile);
+                        const int qrow = w.s * a.N * a.H + w.row0;
+                        for (int b = 0; b < blocks; ++b)
+                            for (int at = 0; at < kAtoms; ++at)
+                                tc::tma_load_2d(smem + L::q + b * L::tile + at * kAtomBytes, &g.map_q, at * 64,
+                                                qrow + b * kTK, &bar.q_full);
+                    }
+                    __syncwarp();
+                    ++n_q;
+                }
+                for (int t = w.tile0; t < w.tile1; ++t, ++n_t) {
+                    const int st = n_t % kNS;
+                    // the rows of this warp's runs: lane = run (raw and dense), lane = group of 4 (list)
+                    const int run = pw * kRunsPer + (lane & (kRunsPer - 1));
+                    const int v = t * kRuns + run;
+                    int row = g.pool_oob;
+                    bool raw_run = true, readable = true;
+                    if (v < w.raw_runs) {
+                        const long long pr = pool_row(a.kv, table, static_cast<unsigned>(w.t0 + v * kRun),
+                                                      lane < kRunsPer ? a.err : nullptr);
+                        readable = pr >= 0;
+                        if (readable) row = static_cast<int>(pr);
+                    } else if (!kSel && v < w.n_runs) {
+                        raw_run = false;
+                        const int c = v - w.raw_runs;
+                        const long long base = static_cast<long long>(w.s) * a.cap;
+                        row = static_cast<int>(c < w.comp_runs ? base + c * kRun
+                                                               : base + a.cap - a.N + (c - w.comp_runs) * kRun);
+                    }
+                    int4 gr = make_int4(g.comp_oob, g.comp_oob, g.comp_oob, g.comp_oob);
+                    uint32_t gmask = 0;
+                    const int group = lane & (kRunsPer * 4 - 1);    // group of 4 rows among this warp's
+                    const int gv = t * kRuns + pw * kRunsPer + group / 4;
+                    if (kSel && gv >= w.raw_runs && gv < w.n_runs) {
+                        const long long nq = static_cast<long long>(w.s) * a.N + w.node;
+                        const int e0 = (gv - w.raw_runs) * kRun + (group & 3) * 4;
+                        int *rr = &gr.x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (e0 + e >= a.n_sel) continue;
+                            const int j = __ldg(a.sel + nq * a.n_sel + e0 + e);
+                            const int rrow = sel_row(a, w.len, w.cmp[w.node], j, lane < kRunsPer * 4 && !is_v);
+                            if (rrow >= 0) {
+                                rr[e] = static_cast<int>(static_cast<long long>(w.s) * a.cap + rrow);
+                                gmask |= 1u << e;
+                            }
+                        }
+                    }
+                    if (n_t >= kNS && !warp_wait(&empty[st], n_t / kNS - 1)) break;
+                    {   // readable keys per run, for the softmax (K) and the checkers (V)
+                        uint32_t m16 = readable ? 0xffffu : 0u;
+                        if (kSel) {
+                            uint32_t gm = gmask << ((group & 3) * 4);
+                            gm |= __shfl_xor_sync(0xffffffffu, gm, 1);
+                            gm |= __shfl_xor_sync(0xffffffffu, gm, 2);
+                            const uint32_t mine = __shfl_sync(0xffffffffu, gm, (lane & (kRunsPer - 1)) * 4);
+                            if (v >= w.raw_runs) m16 = mine;
+                        }
+                        if (lane < kRunsPer) info[(is_v * 4 + (n_t & 3)) * kRuns + run] = static_cast<uint16_t>(m16);
+                        __syncwarp();
+                    }
+                    if (lane == 0) tc::expect_tx(&full[st], L::tile / kProd);
+                    __syncwarp();
+                    const uint32_t dst = tc::smem_u32(ring + st * L::tile);
+                    if (!kSel || v < w.raw_runs || v >= w.n_runs) {
+                        if (lane < kRunsPer * kAtoms) {
+                            const int at = lane / kRunsPer;
+                            tc::tma_load_2d(dst + at * kAtomBytes + run * 2048, raw_run ? map_raw : map_comp, at * 64,
+                                               row, &full[st]);
+                        }
+                    }
+                    if (kSel) {
+                        if (gv >= w.raw_runs && gv < w.n_runs && lane < kRunsPer * 4)
+                            for (int at = 0; at < kAtoms; ++at)
+                                tc::tma_gather4(dst + at * kAtomBytes + (pw * kRunsPer * 4 + group) * 512, map_comp,
+                                                at * 64, gr, &full[st]);
+                    }
+                    __syncwarp();
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.w_empty[it & 1]);
+            }
+            // a wait gave up: the copies in flight land before the block may end
+            if (!ok && lane == 0) {
+                const uint32_t from = n_t > kNS ? n_t - kNS : 0;
+                for (uint32_t x = from; x < n_t; ++x) tc::mbar_wait(&full[x % kNS], (x / kNS) & 1u);
+                if (!is_v && pw == 0 && n_q > 0) tc::mbar_wait(&bar.q_full, (n_q - 1) & 1u);
+            }
+            __syncwarp();
         }
-        __syncthreads();
     }
+    if (!ok) record_error(a.err, DS4A_ERR_TIMEOUT);
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the splits of a row: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  One warp per
+// row; rows whose item was not split are already written.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
+    const int lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    if (row >= static_cast<long long>(g.B) * g.N * g.H) return;
+    const int s = static_cast<int>(row / (g.N * g.H)), r = static_cast<int>(row - static_cast<long long>(s) * g.N * g.H);
+    const int n = g.n_node[s];
+    if (n < 0 || n > g.N || r >= n * g.H) return;
+    const int rt = r / g.item_rows, slot = s * g.row_tiles + rt;
+    const int active = g.active[slot];
+    if (active <= 1) return;
+    const long long base = static_cast<long long>(slot) * g.n_split * g.tile_rows + (r - rt * g.item_rows);
+    float m = -INFINITY;
+    for (int i = lane; i < active; i += 32) m = fmaxf(m, g.part_ml[base + static_cast<long long>(i) * g.tile_rows].x);
+    m = warp_max(m);
+    const float ref = m == -INFINITY ? 0.f : m;
+    constexpr int kPer = D / 32;
+    float o[kPer] = {}, l = 0.f;
+    for (int i = 0; i < active; ++i) {
+        const long long at = base + static_cast<long long>(i) * g.tile_rows;
+        const float2 ml = g.part_ml[at];
+        if (ml.y == 0.f) continue;                 // no key of this split is this row's
+        const float w = ex2(ml.x - ref);
+        l += w * ml.y;
+        const float *src = g.part + at * D + lane * kPer;
 #pragma unroll
-    for (int x = 0; x < kMaxHeadsPerWarp; ++x) {
-        const int h = warp + x * kWarps;
-        if (h >= a.H) continue;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) a.out[(node * a.H + h) * D + lane + e * 32] =
-            f2h(l[x] == 0.f ? 0.f : o[x][e] / l[x]);   // no readable row (bad page ids, recorded): zeros
+        for (int e = 0; e < kPer; ++e) o[e] += w * src[e];
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t h[kPer / 2];
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) h[e] = pack_half2(o[2 * e] * inv, o[2 * e + 1] * inv);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(g.out + row * D) + lane * (kPer / 2);
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) dst[e] = h[e];
+}
+
+// Work items that a split launch may have: two for each of the 152 SMs.  Bounds the partial
+// results, and with them the workspace.
+constexpr int kMaxSplitItems = 304;
+
+struct Plan {
+    int tile_rows, item_rows, row_tiles, n_split, min_tiles;
+};
+
+size_t header_bytes(long long slots) { return (static_cast<size_t>(slots) * 4 + 255) / 256 * 256; }
+
+// How a call is cut.  Two row blocks per item (each K and V tile read once for 256 rows) when
+// that leaves at least four key tiles per SM; else one, with its two sides on alternate tiles.
+// Splits: the number with the least waves x (tiles + 4), the 4 being an item's fixed cost in
+// tiles, and 4 more for the join.
+Plan make_plan(const AttnTreeArgs &a, int B, int num_sms) {
+    Plan p{};
+    const long long tokens = static_cast<long long>(a.kv.max_pages) * a.kv.page;
+    const long long raw = (a.window < tokens ? a.window : tokens) + a.N + 2 * kRun;
+    const long long comp = a.sel ? a.n_sel : (a.ratio > 0 ? (a.cap < tokens / a.ratio ? a.cap : tokens / a.ratio) + kMaxNodes : 0);
+    const long long tiles = (raw + comp + kTK - 1) / kTK;
+    const long long rows = static_cast<long long>(a.N) * a.H;
+    if (a.sel) {
+        p.tile_rows = kTK;
+        p.item_rows = a.H;
+    } else {
+        const long long blocks = (rows + 2 * kTK - 1) / (2 * kTK) * B;
+        p.tile_rows = p.item_rows = rows > kTK && blocks * tiles >= 4LL * num_sms ? 2 * kTK : kTK;
+    }
+    p.row_tiles = static_cast<int>((rows + p.item_rows - 1) / p.item_rows);
+    p.min_tiles = p.tile_rows == kTK ? 2 : 1;
+    const long long slots = static_cast<long long>(p.row_tiles) * B;
+    p.n_split = 1;
+    long long best = -1;
+    for (long long ns = 1; ns == 1 || (ns * slots <= kMaxSplitItems && (ns - 1) * p.min_tiles < tiles); ++ns) {
+        long long chunk = (tiles + ns - 1) / ns;
+        if (chunk < p.min_tiles) chunk = p.min_tiles;
+        const long long cost = (slots * ns + num_sms - 1) / num_sms * (chunk + 4) + (ns > 1 ? 4 : 0);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.n_split = static_cast<int>(ns);
+        }
+    }
+    return p;
+}
+
+template <int D, bool kSel>
+cudaError_t launch_one(Args &g, const Ctx &c) {
+    static thread_local int configured_device = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_device != dev) {
+        cudaError_t e = cudaFuncSetAttribute(attn_tree_kernel<D, kSel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(Layout<D>::bytes));
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    const int grid = g.n_work < c.num_sms ? g.n_work : c.num_sms;
+    return launch(attn_tree_kernel<D, kSel>, dim3(grid), dim3(kThreads), Layout<D>::bytes, c, 1, g);
 }
 
 }  // namespace
 
-size_t attn_tree_ws_bytes(int, int, int, int) { return 256; }
+// The largest over the ways a call of these sizes may be cut.
+size_t attn_tree_ws_bytes(int B, int N, int H, int D) {
+    size_t most = 256;
+    const long long rows = static_cast<long long>(N) * H;
+    const long long item_rows[3] = {kTK, 2 * kTK, H};
+    for (long long ir : item_rows) {
+        const long long slots = (rows + ir - 1) / ir * B;
+        if (slots == 0 || 2 * slots > kMaxSplitItems) continue;
+        const long long tile_rows = ir == H ? kTK : ir;
+        const size_t bytes = header_bytes(slots) + static_cast<size_t>(kMaxSplitItems / slots * slots * tile_rows) *
+                                                       (static_cast<size_t>(D) * 4 + 8);
+        if (bytes > most) most = bytes;
+    }
+    return most;
+}
 
 cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
-    AttnTreeArgs a = args;
+    Args g{};
+    g.a = args;
+    AttnTreeArgs &a = g.a;
     a.scale_log2 = a.scale * kLog2e;
-    const dim3 grid(static_cast<unsigned>(a.N), static_cast<unsigned>(B));
-    return a.kv.D == 128 ? launch(attn_tree_kernel<128>, grid, dim3(kThreads), 0, c, 1, a)
-                         : launch(attn_tree_kernel<64>, grid, dim3(kThreads), 0, c, 1, a);
+    const Plan p = make_plan(a, B, c.num_sms);
+    const long long pool_rows = a.kv.n_pages * a.kv.page, comp_rows = a.ratio > 0 ? a.cap * B : 0;
+    const int D = a.kv.D;
+    const uint32_t comp_box = a.sel ? 1 : kRun;
+    if (!tc::encode_map(&g.map_q, a.q, D, static_cast<long long>(B) * a.N * a.H, kTK) ||
+        !tc::encode_map(&g.map_k, a.kv.k, D, pool_rows, kRun) || !tc::encode_map(&g.map_v, a.kv.v, D, pool_rows, kRun))
+        return cudaErrorInvalidValue;
+    if (a.ratio > 0 && (!tc::encode_map(&g.map_ck, a.comp_k, D, comp_rows, comp_box) ||
+                        !tc::encode_map(&g.map_cv, a.comp_v, D, comp_rows, comp_box)))
+        return cudaErrorInvalidValue;
+    const long long slots = static_cast<long long>(p.row_tiles) * B;
+    g.B = B;
+    g.n_split = p.n_split;
+    g.min_tiles = p.min_tiles;
+    g.row_tiles = p.row_tiles;
+    g.tile_rows = p.tile_rows;
+    g.n_work = static_cast<int>(slots * p.n_split);
+    g.pool_oob = static_cast<int>(pool_rows);
+    g.comp_oob = static_cast<int>(comp_rows);
+    unsigned char *ws = static_cast<unsigned char *>(a.ws);
+    const size_t part_rows = static_cast<size_t>(slots) * p.n_split * p.tile_rows;
+    g.active = reinterpret_cast<int *>(ws);
+    g.part = reinterpret_cast<float *>(ws + header_bytes(slots));
+    g.part_ml = reinterpret_cast<float2 *>(ws + header_bytes(slots) + part_rows * D * 4);
+    cudaError_t e = D == 128 ? (a.sel ? launch_one<128, true>(g, c) : launch_one<128, false>(g, c))
+                             : (a.sel ? launch_one<64, true>(g, c) : launch_one<64, false>(g, c));
+    if (e != cudaSuccess || p.n_split == 1) return e;
+    const JoinArgs j{g.part, g.part_ml, g.active, a.n_node, a.out, B, a.N, a.H, p.n_split, p.row_tiles, p.tile_rows, p.item_rows};
+    const long long rows = static_cast<long long>(B) * a.N * a.H;
+    const dim3 grid(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    return D == 128 ? launch(combine_kernel<128>, grid, dim3(kJoinThreads), 0, c, 1, j)
+                    : launch(combine_kernel<64>, grid, dim3(kJoinThreads), 0, c, 1, j);
 }
 
 }  // namespace ds4a

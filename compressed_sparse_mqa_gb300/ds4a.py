@@ -628,7 +628,7 @@ def ds4a_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, comp
     """Attention of every drafted node: q, out [B, N, H, D]; its path's raw tokens inside the
     window and, with ratio > 0, the compressed rows of comp_k, comp_v [B, cap, D] listed in
     sel [B, N, n_sel] int32 or (sel None) every row complete at its position.  ws: uint8,
-    ds4a_attn_tree_workspace_bytes(B, N, H, D) bytes, zeroed once."""
+    ds4a_attn_tree_workspace_bytes(B, N, H, D) bytes."""
     args = _marshal_attn_tree(kv, q, n_node, parent, window, comp_k, comp_v, ratio, sel, scale, out, ws, stream)
     _check(lib().ds4a_attn_tree(*args), "ds4a_attn_tree")
 

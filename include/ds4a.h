@@ -585,11 +585,12 @@ int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, 
  *   sel        [B, N, n_sel] int32 (as ds4a_indexer_topk writes them: negative entries are
  *              skipped; entries not yet complete at p are skipped and recorded as
  *              DS4A_ERR_DEVICE_INDEX), or NULL.
+ *   scale      softmax scale, > 0 and finite.
  *   out        [B, N, H, D] fp16.
- *   ws         ds4a_attn_tree_workspace_bytes(B, N, H, D) bytes, 256-byte aligned, zero-filled
- *              once by the caller; the calls leave it ready for the next.  Calls that share one
- *              workspace must be stream-ordered (two captured graphs that may replay at
- *              the same time need one each).
+ *   ws         ds4a_attn_tree_workspace_bytes(B, N, H, D) bytes, 256-byte aligned; its contents
+ *              need not be set or kept.  Calls that share one workspace must be
+ *              stream-ordered (two captured graphs that may replay at the same time need
+ *              one each).
  * q, comp_k, comp_v, out and the pools are 16-byte aligned.  A node none of whose rows can be
  * read (bad page ids) gets zeros.
  */

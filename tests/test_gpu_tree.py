@@ -327,6 +327,10 @@ ATTN = [
     ([333], [20], 20, 8, 64, 48, 17, 1, 40, "tree"),
     ([100, 700], [64, 2], 64, 32, 128, 16, 300, 2, 130, "chain"),
     ([70000], [2], 2, 8, 64, 256, 1 << 30, 0, 0, "tree"),
+    # more row tiles than SMs: several a CTA, of several sizes
+    ([40 + 37 * s for s in range(44)], [8 - s % 5 for s in range(44)], 8, 8, 128, 16, 64, 4, 100, "tree"),
+    ([1000 - 9 * s for s in range(60)], [10 - s % 9 for s in range(60)], 10, 64, 64, 16, 128, 8, 0, "tree"),
+    ([300 + s for s in range(200)], [1 + s % 2 for s in range(200)], 2, 8, 128, 32, 100, 0, 0, "roots"),
     ([900, 901, 902, 903, 904], [5, 4, 3, 2, 1], 5, 48, 128, 112, 64, 64, 1, "tree"),
 ]
 
