@@ -22,15 +22,15 @@
 // Work item: a row tile (one or two 128-row blocks of a session, or one node's heads) and
 // a range of its key tiles; n_split ranges per row tile when there are few row tiles, joined
 // by combine_kernel.  CTAs are persistent, one per SM.  Roles:
-//   warps 0-3, 4-7  softmax of side 0 / 1: thread = row.  With two row blocks a side is a
-//                row block and both use the same key tiles; with one block the sides take
-//                alternate key tiles and are joined at the end (both accumulators have
-//                the row in the same tensor-memory lane).
-//   warp 8       work set-up: counts, ancestor masks, tile range of the next item.
-//   warp 9       MMA issuer: S = Q K^T into the side's score columns, O += P V with P in
+//   warps 0-7, 8-15  softmax of side 0 / 1: two threads per row, 64 of a tile's keys each.
+//                With two row blocks a side is a row block and both use the same key tiles;
+//                with one block the sides take alternate key tiles and are joined at the end
+//                (both accumulators have the row in the same tensor-memory lane).
+//   warp 16      work set-up: counts, ancestor masks, tile range of the next item.
+//   warp 17      MMA issuer: S = Q K^T into the side's score columns, O += P V with P in
 //                16 bits read from tensor memory, over the scores it came from.
-//   warps 10-11  checkers (below).
-//   warps 12-15  TMA producers: K (12, 13) and V (14, 15).
+//   warps 18-19  checkers (below).
+//   warps 20-23  TMA producers: K (20, 21) and V (22, 23).
 // The two sides keep the tensor core busy in turn: while one computes its softmax, the
 // other's products run.  The softmax reference of a row is raised (and O rescaled) only when
 // a score exceeds it by 2^8; p <= 256 fits 16 bits, sums are binary32.
@@ -49,11 +49,14 @@ namespace {
 constexpr int kTK = 128;                   // keys per tile, rows per block
 constexpr int kRun = 16, kRuns = kTK / kRun;
 constexpr int kNS = 2;                     // K stages, and V stages
-constexpr int kSoftWarps = 8, kSetupWarp = 8, kMmaWarp = 9, kChkWarp0 = 10, kChkWarps = 2, kProdWarp0 = 12;
+constexpr int kSideWarps = 8, kSoftWarps = 2 * kSideWarps;
+constexpr int kSetupWarp = kSoftWarps, kMmaWarp = kSetupWarp + 1, kChkWarp0 = kMmaWarp + 1, kChkWarps = 2;
+constexpr int kProdWarp0 = kChkWarp0 + kChkWarps;
 constexpr int kProd = 2;                   // producer warps for K, and for V
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int kSoftRegs = 200, kOtherRegs = 56;
-constexpr int kLaunchRegs = 65536 / kThreads;
+constexpr int kWarps = kProdWarp0 + 2 * kProd, kThreads = 32 * kWarps;
+constexpr int kSoftRegs = 96, kOtherRegs = 48;
+constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+static_assert(kWarps % 4 == 0 && kSoftWarps % 4 == 0, "the register split is per warpgroup");
 static_assert(kSoftWarps * kSoftRegs + (kWarps - kSoftWarps) * kOtherRegs <= kWarps * kLaunchRegs,
               "the register split exceeds what the block is launched with");
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
@@ -101,8 +104,10 @@ struct Layout {
     // producers (a slot is written again four tiles on, when the products two tiles on have been issued and the
     // readers of this one are therefore done)
     static constexpr int info = work + 2 * static_cast<int>(sizeof(Work));
-    static constexpr int ml = info + 2 * 4 * kRuns * 2;                          // float2 [128] side 1's (max, sum)
-    static constexpr int bars = ml + kTK * 8;
+    static constexpr int top = info + 2 * 4 * kRuns * 2;                     // float [2 sides][2 halves][128] row maxima
+    static constexpr int sums = top + 4 * kTK * 4;                           // float [2][2][128] sums
+    static constexpr int ref = sums + 4 * kTK * 4;                           // float [128] side 1's references
+    static constexpr int bars = ref + kTK * 4;
     static constexpr int end = bars + static_cast<int>(sizeof(Bars));
     static constexpr size_t bytes = end + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
@@ -170,8 +175,9 @@ DS4A_DEVINL unsigned long long shfl64(unsigned long long v, int src) { return __
 template <bool kSel>
 __device__ void make_work(const Args &g, int item, Work &w, int lane) {
     const AttnTreeArgs &a = g.a;
-    const int split = item % g.n_split, slot = item / g.n_split;
-    const int s = slot / g.row_tiles, rt = slot - s * g.row_tiles;
+    // row tiles outermost: the empty ones (of sessions with fewer nodes) are the last items
+    const int split = item % g.n_split, x_item = item / g.n_split;
+    const int rt = x_item / g.B, s = x_item - rt * g.B, slot = s * g.row_tiles + rt;
     const Session ses = load_session(a.kv, a.n_node, a.N, s, lane == 0 ? a.err : nullptr);
     bool ok = ses.ok;
     if (ok && a.ratio > 0 && ses.len / a.ratio > a.cap - a.N) {
@@ -312,6 +318,37 @@ DS4A_DEVINL int sel_row(const AttnTreeArgs &a, int len, unsigned long long path,
     return static_cast<int>(a.cap) - a.N + path_node(path, (j + 1) * a.ratio - 1 - len);
 }
 
+// Values that are not finite, of the keys that `node` attends: into columns col .. col+15 of
+// its accumulator.
+__device__ __noinline__ void add_poison_bits(const Work &w, int node, int col, uint32_t &nan, uint32_t &pi, uint32_t &ni) {
+    const int lo = w.lo[node], word = col / 32, sh = col % 32;
+    const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
+    nan = pi = ni = 0;
+    for (int key = 0; key < kPoison; ++key) {
+        bool hit;
+        if (key < kMaxNodes) hit = (raw >> key) & 1ull;
+        else if (key < kEdge) hit = (cmp >> (key - kMaxNodes)) & 1ull;
+        else hit = w.lo_min + key - kEdge >= lo;
+        if (!hit) continue;
+        nan |= w.poison[key][word];
+        pi |= w.poison[key][4 + word];
+        ni |= w.poison[key][8 + word];
+    }
+    nan = (nan | (pi & ni)) >> sh;
+    pi >>= sh;
+    ni >>= sh;
+}
+DS4A_DEVINL void add_poison(const Work &w, int node, int col, uint32_t (&o)[16]) {
+    uint32_t nan, pi, ni;
+    add_poison_bits(w, node, col, nan, pi, ni);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        if ((nan >> e) & 1u) o[e] = 0x7fffffffu;
+        else if ((pi >> e) & 1u) o[e] = 0x7f800000u;
+        else if ((ni >> e) & 1u) o[e] = 0xff800000u;
+    }
+}
+
 template <int D, bool kSel>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_constant__ Args g) {
     using L = Layout<D>;
@@ -320,7 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Work *works = reinterpret_cast<Work *>(smem + L::work);
     uint16_t *info = reinterpret_cast<uint16_t *>(smem + L::info);
-    float2 *s_ml = reinterpret_cast<float2 *>(smem + L::ml);
+    float *s_top = reinterpret_cast<float *>(smem + L::top);
+    float *s_sum = reinterpret_cast<float *>(smem + L::sums);
+    float *s_ref = reinterpret_cast<float *>(smem + L::ref);
     Bars &bar = *reinterpret_cast<Bars *>(smem + L::bars);
     __shared__ uint32_t s_tmem;
     const AttnTreeArgs &a = g.a;
@@ -339,14 +378,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         tc::mbar_init(&bar.q_empty, 1);
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(&bar.s_full[x], 1);
-            tc::mbar_init(&bar.p_full[x], 4);
+            tc::mbar_init(&bar.p_full[x], kSideWarps);
             tc::mbar_init(&bar.o_full[x], 1);
-            tc::mbar_init(&bar.o_empty[x], 4);
+            tc::mbar_init(&bar.o_empty[x], kSideWarps);
             tc::mbar_init(&bar.w_full[x], 1);
             tc::mbar_init(&bar.w_empty[x], kWarps - 1);
             tc::mbar_init(&bar.chk[x], kChkWarps);
         }
-        tc::mbar_init(&bar.join, 4);
+        tc::mbar_init(&bar.join, kSideWarps);
         tc::mbar_fence_init();
     }
     if (warp == kSetupWarp)
@@ -373,35 +412,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
 
     if (warp < kSoftWarps) {
         tc::setmaxnreg_inc<kSoftRegs>();
-        const int side = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+        const int side = warp / kSideWarps, half = (warp >> 2) & 1, quad = warp & 3, r = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t col_s = tmem + lanes + kColS + side * kTK, col_o = tmem + lanes + kColO + side * kTK;
+        const int pair = 1 + side * 4 + quad;                     // named barrier of the two warps of these rows
+        float *top_mine = s_top + (side * 2 + half) * kTK + r, *top_other = s_top + (side * 2 + (half ^ 1)) * kTK + r;
         const float c2 = a.scale_log2;
         uint32_t n_s = 0, n_o = 0, n_join = 0, n_t = 0;   // n_t: tiles of the items before
         for (int it = 0; it < n_items; ++it) {
             Work &w = works[it & 1];
-            if (!__all_sync(0xffffffffu, wait(&bar.w_full[it & 1], it >> 1))) break;
-            const int t0 = w.tile0, t1 = w.tile1, sides2 = w.sides2;
+            wait(&bar.w_full[it & 1], it >> 1);
+            if (tc::bar_any(pair, 64, !ok)) ok = false;   // the two warps of a barrier leave out the same items
+            const int t0 = w.tile0, t1 = ok ? w.tile1 : t0, sides2 = w.sides2;
             const int row = (sides2 ? side * kTK : 0) + r;        // row in the item
             const int node = min(kMaxNodes - 1, (w.row0 + row) / a.H);
-            const int lo = w.lo[node];
-            const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
             float m = -INFINITY, l = 0.f;
             bool first = true;
             for (int t = sides2 ? t0 : t0 + side; t < t1; t += sides2 ? 1 : 2) {
                 wait(&bar.s_full[side], n_s++);
                 tc::fence_after_sync();
-                uint32_t x[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc::ld_x32(col_s + c * 32, x[c]);
-                tc::wait_ld();
+                uint32_t x[2][32];
+                tc::ld_x32(col_s + half * 64, x[0]);
+                tc::ld_x32(col_s + half * 64 + 32, x[1]);
                 const uint16_t *inf = info + ((n_t + t - t0) & 3) * kRuns;
                 const uint4 iw = *reinterpret_cast<const uint4 *>(inf);
-                if ((kSel ? t * kRuns < w.raw_runs : !tile_full(w, t)) || (iw.x & iw.y & iw.z & iw.w) != 0xffffffffu) {
+                const bool partial = (kSel ? t * kRuns < w.raw_runs : !tile_full(w, t)) ||
+                                     (iw.x & iw.y & iw.z & iw.w) != 0xffffffffu;
+                tc::wait_ld();
+                if (partial) {
+                    const int lo = w.lo[node];
+                    const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t bits = run_bits<kSel>(w, t * kRuns + 2 * c, lo, raw, cmp, inf) |
-                                              run_bits<kSel>(w, t * kRuns + 2 * c + 1, lo, raw, cmp, inf) << 16;
+                    for (int c = 0; c < 2; ++c) {
+                        const int v = t * kRuns + half * 4 + 2 * c;
+                        const uint32_t bits = (run_bits<kSel>(w, v, lo, raw, cmp, inf) & 0xffffu) |
+                                              run_bits<kSel>(w, v + 1, lo, raw, cmp, inf) << 16;
+                        if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!((bits >> e) & 1u)) x[c][e] = 0xff800000u;   // -inf
@@ -409,46 +455,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[c][e]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;   // scale > 0
-                // raise the reference: at the first finite score, then only past the threshold
-                float alpha = 1.f;
-                if (top > m + kRescale || (m == -INFINITY && top > m)) {
-                    alpha = ex2(m - top);
-                    m = top;
-                    l *= alpha;
-                }
-                if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // the earlier product of this side is complete: it was issued before the scores just read
+                    for (int e = 0; e < 32; e += 2)
+                        mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(x[c][e])), __uint_as_float(x[c][e + 1]));
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;   // scale > 0
+                // Raise the reference at the first finite score, then only past the threshold.  The two
+                // threads of a row hold the same one; they look at each other's maximum only when one of
+                // the 64 rows and halves here asks for it.  (Behind this barrier both have read their scores,
+                // which the weights will overwrite.)
+                if (tc::bar_any(pair, 64, top > m + kRescale || (m == -INFINITY && top > m))) {
+                    *top_mine = top;
+                    tc::bar_sync(pair, 64);
+                    top = fmaxf(top, *top_other);
+                    float alpha = 1.f;
+                    if (top > m + kRescale || (m == -INFINITY && top > m)) {
+                        alpha = ex2(m - top);
+                        m = top;
+                        l *= alpha;
+                    }
+                    if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        // the earlier product of this side is complete: it was issued before the scores just read
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t o[16];
-                        tc::ld_x16(col_o + c * 16, o);
-                        tc::wait_ld();
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[16];
+                            tc::ld_x16(col_o + half * (D / 2) + c * 16, o);
+                            tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tc::st_x16(col_o + c * 16, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tc::st_x16(col_o + half * (D / 2) + c * 16, o);
+                        }
                     }
                 }
                 first = false;
                 const float ref = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c22 = tc::pack2(c2, c2), ref2 = tc::pack2(-ref, -ref);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = ex2(fmaf(__uint_as_float(x[c][2 * e]), c2, -ref));
-                        const float p1 = ex2(fmaf(__uint_as_float(x[c][2 * e + 1]), c2, -ref));
-                        sum[e & 1] += p0;
-                        sum[2 + (e & 1)] += p1;
+                        float y0, y1;
+                        tc::unpack2(tc::fma2(tc::pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), c22,
+                                             ref2), y0, y1);
+                        const float p0 = ex2(y0), p1 = ex2(y1);
+                        sum[e & 1] = tc::add2(sum[e & 1], tc::pack2(p0, p1));
                         pk[e] = pack_half2(p0, p1);
                     }
-                    tc::st_x16(col_s + c * 16, pk);
+                    tc::st_x16(col_s + half * 32 + c * 16, pk);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float s0, s1;
+                tc::unpack2(tc::add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
                 tc::wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -457,93 +516,68 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             n_t += t1 - t0;
             // ---- end of the item ----
             const bool have = !first;                              // this side has tiles
-            if (t1 > t0) {
-                if (have) {
-                    wait(&bar.o_full[side], n_o++);
-                    tc::fence_after_sync();
+            const bool joined = !sides2 && t1 - t0 > 1;            // side 1 holds part of the same rows
+            if (have) {
+                // the row's sum over both halves, and over both sides of a joined item (behind o_full: the product
+                // waited until the item before had been read, its sums with it)
+                wait(&bar.o_full[side], n_o++);
+                s_sum[(side * 2 + half) * kTK + r] = l;
+                if (joined && side == 1) {
+                    if (half == 0) s_ref[r] = m;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.join);
                 }
-                const bool joined = !sides2 && t1 - t0 > 1;        // side 1 holds part of the same rows
-                if (joined) {
-                    if (side == 1) {
-                        s_ml[r] = make_float2(m, l);
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&bar.join);
-                    } else {
-                        wait(&bar.join, n_join);
-                    }
-                    ++n_join;
-                }
-                if (have && (sides2 || side == 0)) {
+                tc::bar_sync(pair, 64);
+                l += s_sum[(side * 2 + (half ^ 1)) * kTK + r];
+                if (joined && side == 0) wait(&bar.join, n_join);
+                tc::fence_after_sync();
+                if (joined) ++n_join;
+                if (sides2 || side == 0) {
                     float wa = 1.f, wb = 0.f;
                     if (joined) {
-                        const float2 o = s_ml[r];
-                        const float mm = fmaxf(m, o.x);
-                        const float rf = mm == -INFINITY ? 0.f : mm;
+                        const float mb = s_ref[r], mm = fmaxf(m, mb), rf = mm == -INFINITY ? 0.f : mm;
                         wa = ex2(m - rf);
-                        wb = ex2(o.x - rf);
-                        l = l * wa + o.y * wb;
+                        wb = ex2(mb - rf);
+                        l = l * wa + (s_sum[2 * kTK + r] + s_sum[3 * kTK + r]) * wb;
                         m = mm;
                     }
                     wait(&bar.chk[it & 1], it >> 1);
-                    // values that are not finite, of the keys that this row attends
-                    uint32_t pz[12];
-#pragma unroll
-                    for (int e = 0; e < 12; ++e) pz[e] = 0;
+                    const bool valid = row < w.rows, direct = w.active == 1;
                     const int dirty = w.dirty;
-                    if (dirty) {
-                        for (int key = 0; key < kPoison; ++key) {
-                            bool hit;
-                            if (key < kMaxNodes) hit = (raw >> key) & 1ull;
-                            else if (key < kEdge) hit = (cmp >> (key - kMaxNodes)) & 1ull;
-                            else hit = w.lo_min + key - kEdge >= lo;
-                            if (!hit) continue;
-#pragma unroll
-                            for (int e = 0; e < 12; ++e) pz[e] |= w.poison[key][e];
-                        }
-                    }
-                    const bool valid = row < w.rows;
-                    const bool direct = w.active == 1;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     const long long qrow = (static_cast<long long>(w.s) * a.N) * a.H + w.row0 + row;
                     const long long prow = (static_cast<long long>(w.slot) * g.n_split + w.split) * g.tile_rows + row;
-                    if (!direct && valid) g.part_ml[prow] = make_float2(m, l);
+                    if (!direct && valid && half == 0) g.part_ml[prow] = make_float2(m, l);
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tc::ld_x32(col_o + c * 32, o);
+                    for (int c = 0; c < D / 32; ++c) {             // 16 columns at a time
+                        const int col = half * (D / 2) + c * 16;
+                        uint32_t o[16];
+                        tc::ld_x16(col_o + col, o);
                         if (joined) {
-                            uint32_t o2[32];
-                            tc::ld_x32(col_o + kTK + c * 32, o2);
+                            uint32_t o2[16];
+                            tc::ld_x16(col_o + kTK + col, o2);
                             tc::wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                            for (int e = 0; e < 16; ++e)
                                 o[e] = __float_as_uint(__uint_as_float(o[e]) * wa + __uint_as_float(o2[e]) * wb);
                         } else {
                             tc::wait_ld();
                         }
-                        if (dirty) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const bool nan = (pz[c] >> e) & 1u, pi = (pz[4 + c] >> e) & 1u, ni = (pz[8 + c] >> e) & 1u;
-                                if (nan || (pi && ni)) o[e] = 0x7fffffffu;
-                                else if (pi) o[e] = 0x7f800000u;
-                                else if (ni) o[e] = 0xff800000u;
-                            }
-                        }
+                        if (dirty) add_poison(w, node, col, o);
                         if (valid && direct) {
 #pragma unroll
-                            for (int q4 = 0; q4 < 4; ++q4) {
+                            for (int q4 = 0; q4 < 2; ++q4) {
                                 uint32_t h[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     h[e] = pack_half2(__uint_as_float(o[q4 * 8 + 2 * e]) * inv,
                                                       __uint_as_float(o[q4 * 8 + 2 * e + 1]) * inv);
-                                *reinterpret_cast<uint4 *>(a.out + qrow * D + c * 32 + q4 * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+                                *reinterpret_cast<uint4 *>(a.out + qrow * D + col + q4 * 8) = make_uint4(h[0], h[1], h[2], h[3]);
                             }
                         } else if (valid) {
 #pragma unroll
-                            for (int q4 = 0; q4 < 8; ++q4)
-                                *reinterpret_cast<uint4 *>(g.part + prow * D + c * 32 + q4 * 4) =
+                            for (int q4 = 0; q4 < 4; ++q4)
+                                *reinterpret_cast<uint4 *>(g.part + prow * D + col + q4 * 4) =
                                     make_uint4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]);
                         }
                     }
@@ -552,13 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if (joined) {
-                        if (side == 0) {
-                            tc::mbar_arrive(&bar.o_empty[0]);
-                            tc::mbar_arrive(&bar.o_empty[1]);
-                        }
-                    } else if (have) {
+                    if (!joined) {
                         tc::mbar_arrive(&bar.o_empty[side]);
+                    } else if (side == 0) {
+                        tc::mbar_arrive(&bar.o_empty[0]);
+                        tc::mbar_arrive(&bar.o_empty[1]);
                     }
                 }
             }
