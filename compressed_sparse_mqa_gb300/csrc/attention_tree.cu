@@ -616,65 +616,78 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 __syncwarp();
             }
         } else if (warp == kMmaWarp) {
-            if (lane == 0) {
-                constexpr uint32_t kIdS = tc::idesc_f16_f32(kTK, kTK, false, false);
-                constexpr uint32_t kIdO = tc::idesc_f16_f32(kTK, D, false, true);
-                uint32_t n_q = 0, n_k = 0, n_v = 0, n_p[2] = {0, 0}, n_o[2] = {0, 0};
-                for (int it = 0; it < n_items && ok; ++it) {
-                    const Work &w = works[it & 1];
-                    if (!wait(&bar.w_full[it & 1], it >> 1)) break;
-                    const int tiles = w.tile1 - w.tile0, sides2 = w.sides2;
-                    const int n = sides2 ? 2 * tiles : tiles;     // products: (side, tile) in turn
-                    if (n > 0) wait(&bar.q_full, n_q++);
-                    // S of product k: side k & 1, tile k / 2 or k
-                    auto issue_s = [&](int k) {
-                        const int side = k & 1;
-                        const uint32_t kt = n_k + (sides2 ? k >> 1 : k);
-                        const int st = kt % kNS;
-                        if (!sides2 || side == 0) wait(&bar.k_full[st], kt / kNS);
-                        if (!ok) return;
-                        tc::fence_after_sync();
-                        const uint32_t qa = tc::smem_u32(smem + L::q + (sides2 ? side : 0) * L::tile);
-                        const uint32_t kb = tc::smem_u32(smem + L::k + st * L::tile);
+            // The whole warp runs this, converged, and one elected lane issues: the operands are then
+            // warp-uniform registers, which the instruction wants (issued from a lane == 0 branch, eight
+            // products took 570 cycles to issue, about as long as the tensor core needs for them).
+            constexpr uint32_t kIdS = tc::idesc_f16_f32(kTK, kTK, false, false);
+            constexpr uint32_t kIdO = tc::idesc_f16_f32(kTK, D, false, true);
+            uint32_t n_q = 0, n_k = 0, n_p[2] = {0, 0}, n_o[2] = {0, 0};
+            auto wait_all = [&](uint64_t *b, uint32_t parity) {
+                ok = __all_sync(0xffffffffu, wait(b, parity));
+                return ok;
+            };
+            const uint32_t q_s = tc::smem_u32(smem + L::q), k_s = tc::smem_u32(smem + L::k), v_s = tc::smem_u32(smem + L::v);
+            for (int it = 0; it < n_items && ok; ++it) {
+                const Work &w = works[it & 1];
+                if (!wait_all(&bar.w_full[it & 1], it >> 1)) break;
+                const int tiles = __shfl_sync(0xffffffffu, w.tile1 - w.tile0, 0);
+                const bool sides2 = __shfl_sync(0xffffffffu, w.sides2, 0) != 0;
+                const int n = sides2 ? 2 * tiles : tiles;         // products: sides in turn
+                if (n > 0) wait_all(&bar.q_full, n_q++);
+                // S of product k: side k & 1, tile k / 2 or k
+                auto issue_s = [&](int k) {
+                    const uint32_t side = k & 1;
+                    const uint32_t kt = n_k + (sides2 ? k >> 1 : k), st = kt % kNS;
+                    if (!sides2 || side == 0) wait_all(&bar.k_full[st], kt / kNS);
+                    if (!ok) return;
+                    tc::fence_after_sync();
+                    const uint32_t qa = q_s + (sides2 ? side : 0) * L::tile, kb = k_s + st * L::tile;
+                    const uint32_t d = tmem + kColS + side * kTK;
+                    const bool release = !sides2 || side == 1, last = k == n - 1;
+                    if (tc::elect()) {
 #pragma unroll
                         for (int x = 0; x < D / 16; ++x)
-                            tc::mma_f16(tmem + kColS + side * kTK,
-                                        tc::desc_sw128(qa + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024),
+                            tc::mma_f16(d, tc::desc_sw128(qa + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024),
                                         tc::desc_sw128(kb + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024), kIdS, x > 0);
                         tc::commit(&bar.s_full[side]);
-                        if (!sides2 || side == 1) tc::commit(&bar.k_empty[st]);
-                        if (k == n - 1) tc::commit(&bar.q_empty);
-                    };
-                    auto issue_pv = [&](int k) {
-                        const int side = k & 1;
-                        const uint32_t vt = n_v + (sides2 ? k >> 1 : k);
-                        const int st = vt % kNS;
-                        if (!sides2 || side == 0) wait(&bar.v_ok[st], vt / kNS);
-                        wait(&bar.p_full[side], n_p[side]++);
-                        if (k < 2 && n_o[side] > 0) wait(&bar.o_empty[side], n_o[side] - 1);
-                        if (!ok) return;
-                        tc::fence_after_sync();
-                        const uint32_t vb = tc::smem_u32(smem + L::v + st * L::tile);
+                        if (release) tc::commit(&bar.k_empty[st]);
+                        if (last) tc::commit(&bar.q_empty);
+                    }
+                    __syncwarp();
+                };
+                auto issue_pv = [&](int k) {
+                    const uint32_t side = k & 1;
+                    const uint32_t vt = n_k + (sides2 ? k >> 1 : k), st = vt % kNS;
+                    if (!sides2 || side == 0) wait_all(&bar.v_ok[st], vt / kNS);
+                    wait_all(&bar.p_full[side], side ? n_p[1]++ : n_p[0]++);
+                    const uint32_t items = side ? n_o[1] : n_o[0];
+                    if (k < 2 && items > 0) wait_all(&bar.o_empty[side], items - 1);
+                    if (!ok) return;
+                    tc::fence_after_sync();
+                    const uint32_t vb = v_s + st * L::tile;
+                    const uint32_t d = tmem + kColO + side * kTK, pa = tmem + kColS + side * kTK;
+                    const bool release = !sides2 || side == 1, last = k >= n - 2, more = k > 1;
+                    if (tc::elect()) {
 #pragma unroll
                         for (int x = 0; x < kTK / 16; ++x)
-                            tc::mma_f16_ts(tmem + kColO + side * kTK, tmem + kColS + side * kTK + x * 8,
-                                           tc::desc_sw128(vb + x * 2048, kAtomBytes, 1024), kIdO, k > 1 || x > 0);
-                        if (!sides2 || side == 1) tc::commit(&bar.v_empty[st]);
-                        if (k >= n - 2) {
-                            tc::commit(&bar.o_full[side]);
-                            ++n_o[side];
-                        }
-                    };
-                    if (n > 0) issue_s(0);
-                    if (n > 1 && ok) issue_s(1);
-                    for (int k = 0; k < n && ok; ++k) {
-                        issue_pv(k);
-                        if (k + 2 < n && ok) issue_s(k + 2);
+                            tc::mma_f16_ts(d, pa + x * 8, tc::desc_sw128(vb + x * 2048, kAtomBytes, 1024), kIdO, more || x > 0);
+                        if (release) tc::commit(&bar.v_empty[st]);
+                        if (last) tc::commit(&bar.o_full[side]);
                     }
-                    n_k += tiles;
-                    n_v += tiles;
-                    tc::mbar_arrive(&bar.w_empty[it & 1]);
+                    __syncwarp();
+                    if (last) {
+                        if (side) ++n_o[1];
+                        else ++n_o[0];
+                    }
+                };
+                if (n > 0) issue_s(0);
+                if (n > 1 && ok) issue_s(1);
+                for (int k = 0; k < n && ok; ++k) {
+                    issue_pv(k);
+                    if (k + 2 < n && ok) issue_s(k + 2);
                 }
+                n_k += tiles;
+                if (lane == 0) tc::mbar_arrive(&bar.w_empty[it & 1]);
             }
             __syncwarp();
         } else if (warp < kProdWarp0) {

@@ -47,6 +47,13 @@ DS4A_DEVINL void mma_f16(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t ide
         "l"(da), "l"(db), "r"(idesc), "r"(accumulate));
 }
 
+// true in one lane of a converged warp, the same one every time
+DS4A_DEVINL bool elect() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
 // A from tensor memory: row = lane, two consecutive K values per 32-bit column
 DS4A_DEVINL void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
