@@ -518,48 +518,82 @@ def paged_kv_desc(pool_k, pool_v, table, length) -> PagedKVDesc:
                        k=_ptr(pool_k, torch.float16, "pool_k"), v=_ptr(pool_v, torch.float16, "pool_v"),
                        table=_ptr(table, torch.int32, "table"), len=_ptr(length, torch.int64, "length"))
     desc.tensors = (pool_k, pool_v, table, length)
-    _one_device("paged_kv_desc", *desc.tensors)
+    desc.device = pool_k.get_device()
+    if any(t.get_device() != desc.device for t in desc.tensors):
+        raise ValueError("paged_kv_desc: the tensors are on different devices")
+    desc.ref = ctypes.byref(desc)
     return desc
 
 
-def _one_device(where, *tensors):
-    """Every tensor on the current device: the library launches there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"{where}: a tensor on {t.device}, the current device is cuda:{cur}")
+_F16, _F32, _I32, _I64, _U8 = torch.float16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
-def _tree_ptrs(where, kv, N, n_node, parent):
+def _arg(t, dtype, dev, name):
+    """The address of a contiguous tensor of this dtype on device dev (None: NULL)."""
+    if t is None:
+        return None
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, dtype, name)          # raises, unless it is the device that is wrong
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{dev}")
+    return p
+
+
+def _launch_on(where, kv, stream):
+    """The stream's handle; the cache must be on the current device, where the library launches."""
+    dev = torch._C._cuda_getDevice()
+    if dev != kv.device:
+        raise ValueError(f"{where}: the cache is on cuda:{kv.device}, the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _tree_args(where, kv, N, n_node, parent):
     if n_node.shape != (kv.B,) or (parent is not None and parent.shape != (kv.B, N)):
         raise ValueError(f"{where}: n_node [B], parent [B, N] (or None)")
-    return _ptr(n_node, torch.int32, "n_node"), _ptr(parent, torch.int32, "parent", optional=True)
+    return _arg(n_node, _I32, kv.device, "n_node"), _arg(parent, _I32, kv.device, "parent")
 
 
-def _draft_rows(where, kv, N, comp_k, comp_v):
-    if comp_k.dim() != 3 or comp_k.shape[0] != kv.B or comp_k.shape[2] != kv.D or comp_v.shape != comp_k.shape:
+def _draft_rows(where, kv, comp_k, comp_v):
+    shape = comp_k.shape
+    if len(shape) != 3 or shape[0] != kv.B or shape[2] != kv.D or comp_v.shape != shape:
         raise ValueError(f"{where}: compressed rows [B, cap, D]")
-    return _ptr(comp_k, torch.float16, "comp_k"), _ptr(comp_v, torch.float16, "comp_v"), comp_k.shape[1]
+    return _arg(comp_k, _F16, kv.device, "comp_k"), _arg(comp_v, _F16, kv.device, "comp_v"), shape[1]
+
+
+def _nodes(where, parent, N):
+    """Nodes per session: parent's width, or N for a chain (parent None)."""
+    if N is None:
+        if parent is None:
+            raise ValueError(f"{where}: a chain (parent None) needs N")
+        return parent.shape[1]
+    return N
+
+
+def _required(where, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{where}: {name} is required")
 
 
 def _marshal_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, rot_off: int = 0,
                           interleaved: bool = True, q=None, q_out=None, stream=None):
-    if k.dim() != 3 or k.shape[0] != kv.B or k.shape[2] != kv.D or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 3 or shape[0] != kv.B or shape[2] != kv.D or v.shape != shape:
         raise ValueError("paged_append: k, v [B, N, D]")
-    N, H = k.shape[1], 0
+    N, H = shape[1], 0
     if (q is None) != (q_out is None):
         raise ValueError("paged_append: q and q_out come together")
     if q is not None:
-        if q.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != kv.D or q_out.shape != q.shape:
+        qs = q.shape
+        if len(qs) != 4 or qs[0] != kv.B or qs[1] != N or qs[3] != kv.D or q_out.shape != qs:
             raise ValueError("paged_append: q, q_out [B, N, H, D]")
-        H = q.shape[2]
-    _one_device("paged_append", *kv.tensors, k, v, n_tok, parent, inv_freq, q, q_out)
-    pn, pp = _tree_ptrs("paged_append", kv, N, n_tok, parent)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    return (ctypes.byref(kv), _ptr(k, torch.float16, "k"), _ptr(v, torch.float16, "v"), N, pn, pp,
-            _ptr(inv_freq, torch.float32, "inv_freq", optional=True), rot, rot_off, int(interleaved),
-            _ptr(q, torch.float16, "q", optional=True), H, _ptr(q_out, torch.float16, "q_out", optional=True),
-            _stream(stream))
+        H = qs[2]
+    st, dev = _launch_on("paged_append", kv, stream), kv.device
+    pn, pp = _tree_args("paged_append", kv, N, n_tok, parent)
+    return (kv.ref, _arg(k, _F16, dev, "k"), _arg(v, _F16, dev, "v"), N, pn, pp, _arg(inv_freq, _F32, dev, "inv_freq"),
+            0 if inv_freq is None else 2 * inv_freq.numel(), rot_off, 1 if interleaved else 0,
+            _arg(q, _F16, dev, "q"), H, _arg(q_out, _F16, dev, "q_out"), st)
 
 
 def ds4a_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, rot_off: int = 0,
@@ -576,20 +610,11 @@ def _marshal_compress_tree(kv: PagedKVDesc, n_node, parent, score_w, ratio: int,
     N = _nodes("compress_tree", parent, N)
     if state.shape != (kv.B, 2 + 2 * kv.D) or score_w.numel() != kv.D:
         raise ValueError("compress_tree: state [B, 2 + 2D], score_w [D]")
-    _one_device("compress_tree", *kv.tensors, n_node, parent, score_w, state, comp_k, comp_v)
-    pn, pp = _tree_ptrs("compress_tree", kv, N, n_node, parent)
-    ck, cv, cap = _draft_rows("compress_tree", kv, N, comp_k, comp_v)
-    return (ctypes.byref(kv), N, pn, pp, _ptr(score_w, torch.float32, "score_w"), ratio,
-            _ptr(state, torch.float32, "state"), ck, cv, cap, _stream(stream))
-
-
-def _nodes(where, parent, N):
-    """Nodes per session: parent's width, or N for a chain (parent None)."""
-    if N is None:
-        if parent is None:
-            raise ValueError(f"{where}: a chain (parent None) needs N")
-        return parent.shape[1]
-    return N
+    st, dev = _launch_on("compress_tree", kv, stream), kv.device
+    pn, pp = _tree_args("compress_tree", kv, N, n_node, parent)
+    ck, cv, cap = _draft_rows("compress_tree", kv, comp_k, comp_v)
+    return (kv.ref, N, pn, pp, _arg(score_w, _F32, dev, "score_w"), ratio, _arg(state, _F32, dev, "state"), ck, cv, cap,
+            st)
 
 
 def ds4a_compress_tree(kv: PagedKVDesc, n_node, parent, score_w, ratio: int, state, comp_k, comp_v, N=None,
@@ -607,20 +632,20 @@ def ds4a_attn_tree_workspace_bytes(B: int, N: int, H: int, D: int) -> int:
 
 def _marshal_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, comp_v, ratio: int, sel, scale: float,
                        out, ws, stream=None):
-    if q.dim() != 4 or q.shape[0] != kv.B or q.shape[3] != kv.D or out.shape != q.shape:
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != kv.B or shape[3] != kv.D or out.shape != shape:
         raise ValueError("attn_tree: q, out [B, N, H, D]")
-    N, H = q.shape[1:3]
-    n_sel = 0
+    N, H, n_sel = shape[1], shape[2], 0
     if sel is not None:
-        if sel.dim() != 3 or sel.shape[:2] != q.shape[:2]:
+        ss = sel.shape
+        if len(ss) != 3 or ss[0] != kv.B or ss[1] != N:
             raise ValueError("attn_tree: sel [B, N, n_sel]")
-        n_sel = sel.shape[2]
-    _one_device("attn_tree", *kv.tensors, q, n_node, parent, comp_k, comp_v, sel, out, ws)
-    pn, pp = _tree_ptrs("attn_tree", kv, N, n_node, parent)
-    ck, cv, cap = _draft_rows("attn_tree", kv, N, comp_k, comp_v) if ratio else (None, None, 0)
-    return (ctypes.byref(kv), _ptr(q, torch.float16, "q"), N, H, pn, pp, window, ck, cv, cap, ratio,
-            _ptr(sel, torch.int32, "sel", optional=True), n_sel, scale, _ptr(out, torch.float16, "out"),
-            _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+        n_sel = ss[2]
+    st, dev = _launch_on("attn_tree", kv, stream), kv.device
+    pn, pp = _tree_args("attn_tree", kv, N, n_node, parent)
+    ck, cv, cap = _draft_rows("attn_tree", kv, comp_k, comp_v) if ratio else (None, None, 0)
+    return (kv.ref, _arg(q, _F16, dev, "q"), N, H, pn, pp, window, ck, cv, cap, ratio, _arg(sel, _I32, dev, "sel"), n_sel,
+            scale, _arg(out, _F16, dev, "out"), _arg(ws, _U8, dev, "ws"), 0 if ws is None else ws.numel(), st)
 
 
 def ds4a_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, comp_v, ratio: int, sel, scale: float, out,
@@ -638,24 +663,24 @@ def _marshal_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w
     N = _nodes("commit_tree", parent, N)
     if leaf.shape != (kv.B,) or len_out.shape != (kv.B,):
         raise ValueError("commit_tree: leaf, len_out [B]")
-    _one_device("commit_tree", *kv.tensors, n_node, parent, leaf, len_out, score_w, state, state_out, comp_k, comp_v,
-                k_idx)
-    pn, pp = _tree_ptrs("commit_tree", kv, N, n_node, parent)
+    st, dev = _launch_on("commit_tree", kv, stream), kv.device
+    pn, pp = _tree_args("commit_tree", kv, N, n_node, parent)
     ck = cv = None
     cap = d_idx = 0
     if ratio:
+        _required("commit_tree", score_w=score_w, state=state, state_out=state_out, comp_k=comp_k, comp_v=comp_v)
         if state.shape != (kv.B, 2 + 2 * kv.D) or state_out.shape != state.shape or score_w.numel() != kv.D:
             raise ValueError("commit_tree: state, state_out [B, 2 + 2D], score_w [D]")
-        ck, cv, cap = _draft_rows("commit_tree", kv, N, comp_k, comp_v)
+        ck, cv, cap = _draft_rows("commit_tree", kv, comp_k, comp_v)
+    else:
+        score_w = state = state_out = None
     if k_idx is not None:
         if k_idx.dim() != 3 or k_idx.shape[:2] != (kv.B, cap):
             raise ValueError("commit_tree: k_idx [B, cap, d_idx], rows as comp_k")
         d_idx = k_idx.shape[2]
-    return (ctypes.byref(kv), N, pn, pp, _ptr(leaf, torch.int32, "leaf"), _ptr(len_out, torch.int64, "len_out"),
-            _ptr(score_w, torch.float32, "score_w", optional=True) if ratio else None, ratio,
-            _ptr(state, torch.float32, "state") if ratio else None,
-            _ptr(state_out, torch.float32, "state_out") if ratio else None, ck, cv, cap,
-            _ptr(k_idx, torch.float16, "k_idx", optional=True), d_idx, _stream(stream))
+    return (kv.ref, N, pn, pp, _arg(leaf, _I32, dev, "leaf"), _arg(len_out, _I64, dev, "len_out"),
+            _arg(score_w, _F32, dev, "score_w"), ratio, _arg(state, _F32, dev, "state"),
+            _arg(state_out, _F32, dev, "state_out"), ck, cv, cap, _arg(k_idx, _F16, dev, "k_idx"), d_idx, st)
 
 
 def ds4a_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w=None, ratio: int = 0, state=None,

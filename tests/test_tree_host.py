@@ -123,7 +123,7 @@ def test_binding_refuses_host_tensors_and_shapes(ds4a_lib):
     with pytest.raises(ValueError, match="pools"):
         ds4a_lib.paged_kv_desc(pool, pool, tab, torch.zeros(2, dtype=torch.int64))
     desc = ds4a_lib.PagedKVDesc(B=1, D=64, page=16, max_pages=3, n_pages=4)
-    desc.tensors = ()
+    desc.tensors, desc.device, desc.ref = (), 0, None
     q = torch.zeros(1, 4, 8, 64, dtype=torch.float16)
     n, par = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 4, dtype=torch.int32)
     with pytest.raises(ValueError, match="attn_tree: q, out"):
