@@ -27,6 +27,8 @@ DS4A_DEVINL uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
+DS4A_DEVINL float2 unpack_half2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2 *>(&u)); }
+
 // ---- order-preserving binary32 -> u32 key (larger float -> larger key) -------------
 DS4A_DEVINL uint32_t float_key(float f) {
     uint32_t b = __float_as_uint(f);

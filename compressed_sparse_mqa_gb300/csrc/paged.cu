@@ -16,92 +16,135 @@ namespace ds4a {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kItems = 3;       // work items a thread, all loaded before the first is stored
+constexpr int kMaxTokens = 16;  // tokens of one CTA
 constexpr int kMaxPairs = 64;   // rotated pairs: head_dim / 2
 
-// One CTA per token.  Work items, 16 bytes x 2 each: unit u of a head holds the 8 pairs
-// 8u .. 8u+7 of its rotated dims (two adjacent 16-byte chunks when interleaved, chunks u
-// and u + rot/16 otherwise); the dims outside the rotation and V are copied in 16-byte
-// chunks.
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs a) {
-    __shared__ float2 s_cs[kMaxPairs];
+// A CTA takes t_cta consecutive tokens of a session.  A token's rows are its query heads, its
+// key and its value; a row is D / 16 items of 32 bytes: unit u of the rotated dims holds the 8
+// pairs 8u .. 8u+7 (two adjacent 16-byte chunks when interleaved, chunks u and u + rot/16
+// otherwise), the other items two of the remaining chunks.  Bound by memory: a 2048-token
+// chunk with 64 heads moves 69 MB.  The inputs do not depend on the session's counts, so a
+// thread's loads are in flight while length, angle and page are looked up.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs a, int t_cta, int d_shift) {
+    __shared__ __align__(16) float2 s_cs[kMaxTokens][kMaxPairs];
     __shared__ unsigned long long s_mask[kMaxNodes];
     __shared__ int s_ptr[kMaxNodes];
-    const int tid = threadIdx.x, i = blockIdx.x, s = blockIdx.y;
+    __shared__ long long s_row[kMaxTokens];
+    const int tid = threadIdx.x, i0 = blockIdx.x * t_cta, s = blockIdx.y;
+    const int rot = a.rot, D = a.kv.D, units = rot / 16, rows = a.H + 2;
+    const int n_items = t_cta * rows << d_shift;
+    const long long tok0 = static_cast<long long>(s) * a.N + i0;
     pdl_wait();
     pdl_trigger();
-    const Session ses = load_session(a.kv, a.n_tok, a.N, s, a.err);
-    if (!ses.ok || i >= ses.n) return;
-    long long pos = ses.len + i;
-    if (a.parent) {
-        if (!tree_masks(a.parent + static_cast<long long>(s) * a.N, ses.n, s_mask, s_ptr, a.err)) return;
-        pos = ses.len + __popcll(s_mask[i]) - 1;
+    struct Item {
+        int tt, row, u, o1, o2;   // token, row (heads, then key, then value), unit (-1: copied), the two chunks
+    };
+    auto item = [&](int k) {
+        const int w = tid + k * blockDim.x;
+        Item t;
+        const int r = w >> d_shift, c = w & ((1 << d_shift) - 1);
+        t.tt = r / rows;
+        t.row = r - t.tt * rows;
+        if (w >= n_items || i0 + t.tt >= a.N) t.tt = -1;
+        if (t.row == a.H + 1 || c >= units) {
+            t.u = -1;
+            const int base = t.row == a.H + 1 ? c * 16 : (c - units) * 16;
+            t.o1 = base;
+            t.o2 = base + 8;
+            if (t.row <= a.H) {
+                if (t.o1 >= a.rot_off) t.o1 += rot;
+                if (t.o2 >= a.rot_off) t.o2 += rot;
+            }
+        } else {
+            t.u = c;
+            t.o1 = a.rot_off + (kInterleaved ? c * 16 : c * 8);
+            t.o2 = kInterleaved ? t.o1 + 8 : t.o1 + rot / 2;
+        }
+        return t;
+    };
+    uint4 x1[kItems], x2[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const Item t = item(k);
+        if (t.tt < 0) continue;
+        const long long tok = tok0 + t.tt;
+        const uint16_t *src = t.row < a.H ? a.q + (tok * a.H + t.row) * D : (t.row == a.H ? a.k : a.v) + tok * D;
+        x1[k] = *reinterpret_cast<const uint4 *>(src + t.o1);
+        x2[k] = *reinterpret_cast<const uint4 *>(src + t.o2);
     }
-    const int rot = a.rot, D = a.kv.D;
-    if (tid < rot / 2) {
-        const double turns = static_cast<double>(a.inv_freq[tid]) * 0.15915494309189533577;   // 1 / (2 pi)
+    const Session ses = load_session(a.kv, a.n_tok, a.N, s, tid == 0 ? a.err : nullptr);
+    if (!ses.ok || i0 >= ses.n) return;
+    if (a.parent && !tree_masks(a.parent + static_cast<long long>(s) * a.N, ses.n, s_mask, s_ptr, a.err)) return;
+    const int count = min(t_cta, ses.n - i0);
+    if (tid < count)
+        s_row[tid] = pool_row(a.kv, a.kv.table + static_cast<long long>(s) * a.kv.max_pages,
+                              static_cast<unsigned>(ses.len + i0 + tid), a.err);
+    for (int w = tid; w < count * (rot / 2); w += blockDim.x) {
+        const int tt = w / (rot / 2), j = w - tt * (rot / 2);
+        const long long pos = ses.len + (a.parent ? __popcll(s_mask[i0 + tt]) - 1 : i0 + tt);
+        const double turns = static_cast<double>(a.inv_freq[j]) * 0.15915494309189533577;   // 1 / (2 pi)
         const double frac = turns - floor(turns);
         const unsigned long long step = __double2ull_rn(frac * 18446744073709551616.0);
         const int ang = static_cast<int>((step * static_cast<unsigned long long>(pos)) >> 32);
         float sn, cs;
         sincospif(static_cast<float>(ang) * 4.656612873077392578125e-10f, &sn, &cs);   // half-turns: 2^-31
-        s_cs[tid] = make_float2(cs, sn);
+        s_cs[tt][j] = make_float2(cs, sn);
     }
     __syncthreads();
-    const long long row = pool_row(a.kv, a.kv.table + static_cast<long long>(s) * a.kv.max_pages,
-                                   static_cast<unsigned>(ses.len + i), a.err);
-    const long long tok = static_cast<long long>(s) * a.N + i;
-    const int units = rot / 16, plain = (D - rot) / 8;
-    const int heads = (a.q ? a.H : 0) + 1;               // the key is the last head
-    const int per_head = units + plain;
-    auto head_ptrs = [&](int h, const uint16_t *&src, uint16_t *&dst) {
-        if (h == heads - 1) {
-            src = a.k + tok * D;
-            dst = row >= 0 ? a.kv.k + row * D : nullptr;
-        } else {
-            src = a.q + (tok * a.H + h) * D;
-            dst = a.q_out + (tok * a.H + h) * D;
-        }
-    };
-    for (int w = tid; w < heads * per_head; w += kAppendThreads) {
-        const int h = w / per_head, u = w - h * per_head;
-        const uint16_t *src;
-        uint16_t *dst;
-        head_ptrs(h, src, dst);
-        if (dst == nullptr) continue;
-        if (u >= units) {                                // a chunk outside the rotation
-            int off = (u - units) * 8;
-            if (off >= a.rot_off) off += rot;
-            *reinterpret_cast<uint4 *>(dst + off) = *reinterpret_cast<const uint4 *>(src + off);
-            continue;
-        }
-        const int o1 = a.rot_off + (a.interleaved ? u * 16 : u * 8);
-        const int o2 = a.interleaved ? o1 + 8 : o1 + rot / 2;
-        uint4 r1 = *reinterpret_cast<const uint4 *>(src + o1), r2 = *reinterpret_cast<const uint4 *>(src + o2);
-        uint16_t x[16], y[16];
-        *reinterpret_cast<uint4 *>(x) = r1;
-        *reinterpret_cast<uint4 *>(x + 8) = r2;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 cs = s_cs[u * 8 + e];
-            const int i1 = a.interleaved ? 2 * e : e, i2 = a.interleaved ? 2 * e + 1 : e + 8;
-            const float x1 = h2f(x[i1]), x2 = h2f(x[i2]);
-            y[i1] = f2h(x1 * cs.x - x2 * cs.y);
-            y[i2] = f2h(x1 * cs.y + x2 * cs.x);
+    for (int k = 0; k < kItems; ++k) {
+        const Item t = item(k);
+        if (t.tt < 0 || t.tt >= count) continue;
+        const long long tok = tok0 + t.tt;
+        uint16_t *dst;
+        if (t.row < a.H) {
+            dst = a.q_out + (tok * a.H + t.row) * D;
+        } else {
+            if (s_row[t.tt] < 0) continue;
+            dst = (t.row == a.H ? a.kv.k : a.kv.v) + s_row[t.tt] * D;
         }
-        *reinterpret_cast<uint4 *>(dst + o1) = *reinterpret_cast<uint4 *>(y);
-        *reinterpret_cast<uint4 *>(dst + o2) = *reinterpret_cast<uint4 *>(y + 8);
+        if (t.u >= 0) {
+            const float4 *cs4 = reinterpret_cast<const float4 *>(&s_cs[t.tt][t.u * 8]);
+            uint32_t w[8] = {x1[k].x, x1[k].y, x1[k].z, x1[k].w, x2[k].x, x2[k].y, x2[k].z, x2[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 cs = cs4[e];   // cos, sin of pairs 2e and 2e + 1
+                if (kInterleaved) {
+                    const float2 p = unpack_half2(w[2 * e]), q = unpack_half2(w[2 * e + 1]);
+                    w[2 * e] = pack_half2(p.x * cs.x - p.y * cs.y, p.x * cs.y + p.y * cs.x);
+                    w[2 * e + 1] = pack_half2(q.x * cs.z - q.y * cs.w, q.x * cs.w + q.y * cs.z);
+                } else {
+                    const float2 p = unpack_half2(w[e]), q = unpack_half2(w[e + 4]);
+                    w[e] = pack_half2(p.x * cs.x - q.x * cs.y, p.y * cs.z - q.y * cs.w);
+                    w[e + 4] = pack_half2(p.x * cs.y + q.x * cs.x, p.y * cs.w + q.y * cs.z);
+                }
+            }
+            x1[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            x2[k] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        *reinterpret_cast<uint4 *>(dst + t.o1) = x1[k];
+        *reinterpret_cast<uint4 *>(dst + t.o2) = x2[k];
     }
-    if (row >= 0)
-        for (int ch = tid; ch < D / 8; ch += kAppendThreads)
-            *reinterpret_cast<uint4 *>(a.kv.v + row * D + ch * 8) =
-                *reinterpret_cast<const uint4 *>(a.v + tok * D + ch * 8);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendArgs &a, int B, const Ctx &c) {
-    return launch(paged_append_kernel, dim3(static_cast<unsigned>(a.N), static_cast<unsigned>(B)),
-                  dim3(kAppendThreads), 0, c, 1, a);
+    // as many tokens a CTA as its threads have items for, but no fewer CTAs than SMs
+    const int d_shift = a.kv.D == 128 ? 3 : 2;
+    long long t = kItems * kAppendThreads / ((a.H + 2) << d_shift);
+    const long long spread = (static_cast<long long>(a.N) * B + c.num_sms - 1) / c.num_sms;
+    if (t > spread) t = spread;
+    if (t > kMaxTokens) t = kMaxTokens;
+    if (t < 1) t = 1;
+    const dim3 grid(static_cast<unsigned>((a.N + t - 1) / t), static_cast<unsigned>(B));
+    long long threads = ((t * (a.H + 2) << d_shift) + kItems - 1) / kItems;
+    threads = threads <= 64 ? 64 : (threads + 31) / 32 * 32;
+    const dim3 block(static_cast<unsigned>(threads));
+    return a.interleaved ? launch(paged_append_kernel<true>, grid, block, 0, c, 1, a, static_cast<int>(t), d_shift)
+                         : launch(paged_append_kernel<false>, grid, block, 0, c, 1, a, static_cast<int>(t), d_shift);
 }
 
 }  // namespace ds4a
