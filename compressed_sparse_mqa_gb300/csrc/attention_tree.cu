@@ -22,21 +22,26 @@
 // Work item: a row tile (one or two 128-row blocks of a session, or one node's heads) and
 // a range of its key tiles; n_split ranges per row tile when there are few row tiles, joined
 // by combine_kernel.  CTAs are persistent, one per SM.  Roles:
-//   warps 0-7, 8-15  softmax of side 0 / 1: two threads per row, 64 of a tile's keys each.
-//                With two row blocks a side is a row block and both use the same key tiles;
-//                with one block the sides take alternate key tiles and are joined at the end
-//                (both accumulators have the row in the same tensor-memory lane).
-//   warp 16      work set-up: counts, ancestor masks, tile range of the next item.
-//   warp 17      MMA issuer: S = Q K^T into the side's score columns, O += P V with P in
-//                16 bits read from tensor memory, over the scores it came from.
-//   warps 18-19  checkers (below).
-//   warps 20-23  TMA producers: K (20, 21) and V (22, 23).
-// The two sides keep the tensor core busy in turn: while one computes its softmax, the
-// other's products run.  The softmax reference of a row is raised (and O rescaled) only when
-// a score exceeds it by 2^8; p <= 256 fits 16 bits, sums are binary32.
+//   warps 0-3, 4-7  softmax of side 0 / 1: thread = row.  With two row blocks a side is a
+//                row block and both use the same key tiles; with one block the sides take
+//                alternate key tiles and are joined at the end (both accumulators have
+//                the row in the same tensor-memory lane).
+//   warp 8       work set-up: counts, ancestor masks, tile range of the next item.
+//   warps 9-10   MMA issuers of side 0 / 1: S = Q K^T into the side's score columns, O += P V
+//                with P in 16 bits read from tensor memory, over the scores it came from.  One
+//                warp's waits pass behind the other's products.
+//   warp 11      checker (below).
+//   warps 12-15  TMA producers: K (12, 13) and V (14, 15).
+// A tile is scored in two chunks of 64 keys, and each side has two score buffers, so the
+// scores of the next chunk are computed while the softmax of this one runs (with one buffer
+// of 128 keys per side the two sides fell into step, both in their softmax, then both waiting
+// for products: 4200 cycles a 256-row tile, of which the tensor core worked 2050).  The price is
+// that a product with N = 64 is bound by reading Q from shared memory, 48 cycles instead of 32.
+// The softmax reference of a row is raised (and O rescaled) only when a score exceeds it
+// by 2^8; p <= 256 fits 16 bits, sums are binary32.
 //
 // Masked keys get weight 0, but 0 * V is not 0 where V is infinite or NaN: slots never
-// written, or another branch's values.  The checkers scan the V rows of runs that some row
+// written, or another branch's values.  The checker scans the V rows of runs that some row
 // masks: values that are not finite are set to 0, and where the key is valid for some
 // rows, noted, so that exactly those rows get them in the end.
 #include "paged_dev.cuh"
@@ -48,13 +53,15 @@ namespace {
 
 constexpr int kTK = 128;                   // keys per tile, rows per block
 constexpr int kRun = 16, kRuns = kTK / kRun;
-constexpr int kNS = 2;                     // K stages, and V stages
-constexpr int kSideWarps = 8, kSoftWarps = 2 * kSideWarps;
-constexpr int kSetupWarp = kSoftWarps, kMmaWarp = kSetupWarp + 1, kChkWarp0 = kMmaWarp + 1, kChkWarps = 2;
+constexpr int kCK = 64, kChunkRuns = kCK / kRun;   // keys and runs of a chunk: two a tile
+constexpr int kNS = 2;                     // K stages, and V stages: with one row block, one for each side
+constexpr int kInfo = 8;                   // tiles whose run information is kept
+constexpr int kSideWarps = 4, kSoftWarps = 2 * kSideWarps;
+constexpr int kSetupWarp = kSoftWarps, kMmaWarp = kSetupWarp + 1, kChkWarp0 = kMmaWarp + 2, kChkWarps = 1;
 constexpr int kProdWarp0 = kChkWarp0 + kChkWarps;
 constexpr int kProd = 2;                   // producer warps for K, and for V
 constexpr int kWarps = kProdWarp0 + 2 * kProd, kThreads = 32 * kWarps;
-constexpr int kSoftRegs = 96, kOtherRegs = 48;
+constexpr int kSoftRegs = 160, kOtherRegs = 96;
 constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
 static_assert(kWarps % 4 == 0 && kSoftWarps % 4 == 0, "the register split is per warpgroup");
 static_assert(kSoftWarps * kSoftRegs + (kWarps - kSoftWarps) * kOtherRegs <= kWarps * kLaunchRegs,
@@ -75,39 +82,40 @@ struct alignas(16) Work {
     int s, len, n, t0;                     // session; first slot of the key runs
     int raw_runs, comp_runs, n_runs;       // runs of raw slots, of committed compressed rows (sel: of the list), in all
     int n_vis0;                            // committed compressed rows (sel: list entries)
-    int node, depth;                       // sel: the node and its depth
+    int node;                              // sel: the node
     int row0, rows;                        // first row in the session, valid rows (<= 256)
     int sides2;                            // two row blocks
     int tile0, tile1;                      // key tiles of this item
     int active, split;                     // splits that have tiles; this one
     int slot;                              // index of the row tile among all
     int dirty;                             // poison entries exist
-    uint32_t poison[kPoison][12];          // per key: NaN, +inf, -inf bits of its 128 values
+    int n_vis, n_done;                     // sel: rows complete at the node's position, and at the draft's start
+    alignas(16) uint32_t poison[kPoison][12];          // per key: NaN, +inf, -inf bits of its 128 values
 };
 
 struct Bars {
     uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_ok[kNS], v_empty[kNS];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t s_full[2][2], p_full[2][2];   // [side][score buffer]
+    uint64_t pv[2];                        // a product with V is done
+    uint64_t o_full[2], o_empty[2];        // the item's last one; the accumulator has been read
     uint64_t w_full[2], w_empty[2], chk[2];
     uint64_t join;                         // side 1 has posted its sums
 };
 
-template <int D>
+template <int D, bool kSel>
 struct Layout {
     static constexpr int tile = kTK * D * 2;
-    static constexpr int q = 0;                               // 2 row blocks
-    static constexpr int k = q + 2 * tile;
+    static constexpr int q = 0;                               // row blocks
+    static constexpr int k = q + (kSel ? 1 : 2) * tile;
     static constexpr int v = k + kNS * tile;
     static constexpr int work = v + kNS * tile;
-    // uint16 [4][8]: readable keys per run of the CTA's tile number & 3, once from the K and once from the V
-    // producers (a slot is written again four tiles on, when the products two tiles on have been issued and the
-    // readers of this one are therefore done)
+    // uint16 [8][8]: readable keys per run of the CTA's tile number & 7, once from the K and once from the V
+    // producers.  A slot is written again eight tiles on, two stages ahead of the products; those two tiles
+    // on are issued only when the softmax of this one is done.
     static constexpr int info = work + 2 * static_cast<int>(sizeof(Work));
-    static constexpr int top = info + 2 * 4 * kRuns * 2;                     // float [2 sides][2 halves][128] row maxima
-    static constexpr int sums = top + 4 * kTK * 4;                           // float [2][2][128] sums
-    static constexpr int ref = sums + 4 * kTK * 4;                           // float [128] side 1's references
-    static constexpr int bars = ref + kTK * 4;
+    static constexpr int ml = info + 2 * kInfo * kRuns * 2;                  // float2 [128] side 1's (reference, sum)
+    static constexpr int bars = ml + kTK * 8;
     static constexpr int end = bars + static_cast<int>(sizeof(Bars));
     static constexpr size_t bytes = end + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
@@ -121,7 +129,7 @@ struct Args {
     float *part;                                   // [slot * n_split + split][tile rows][D]
     float2 *part_ml;                               // [...][tile rows] (max, sum)
     int *active;                                   // [slots]
-    int B, n_split, min_tiles, row_tiles, tile_rows, n_work;
+    int B, n_split, min_tiles, row_tiles, tile_rows, item_rows, n_work;
     int pool_oob, comp_oob;                        // rows of the maps: the zero-fill rows
 };
 
@@ -169,15 +177,52 @@ DS4A_DEVINL bool tile_full(const Work &w, int t) {
     return (v - w.raw_runs + kRuns) * kRun <= w.n_vis0;
 }
 
+// some row masks keys of tile t whose V rows are read (not the list's: a skipped entry loads zeros)
+template <bool kSel>
+DS4A_DEVINL bool needs_check(const Work &w, int t) {
+    return kSel ? t * kRuns < w.raw_runs : !tile_full(w, t);
+}
+
+// chunks of tile t: the second has runs, or not
+DS4A_DEVINL int tile_chunks(int n_runs, int t) { return t * kRuns + kChunkRuns < n_runs ? 2 : 1; }
+
 DS4A_DEVINL unsigned long long shfl64(unsigned long long v, int src) { return __shfl_sync(0xffffffffu, v, src); }
+
+// Item number -> split, row tile, session.  Row tiles are outermost: the empty ones (of sessions
+// with fewer nodes) are the last items.
+struct ItemId {
+    int split, rt, s;
+};
+DS4A_DEVINL ItemId item_id(const Args &g, int item) {
+    ItemId id;
+    const int x = item / g.n_split;
+    id.split = item - x * g.n_split;
+    id.rt = x / g.B;
+    id.s = x - id.rt * g.B;
+    return id;
+}
+
+// or / and over the warp
+template <bool kOr>
+DS4A_DEVINL unsigned long long reduce64(unsigned long long v) {
+    const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
+    const uint32_t l = kOr ? __reduce_or_sync(0xffffffffu, lo) : __reduce_and_sync(0xffffffffu, lo);
+    const uint32_t h = kOr ? __reduce_or_sync(0xffffffffu, hi) : __reduce_and_sync(0xffffffffu, hi);
+    return static_cast<unsigned long long>(h) << 32 | l;
+}
 
 // The set-up warp's item: lane holds nodes lane and lane + 32.
 template <bool kSel>
 __device__ void make_work(const Args &g, int item, Work &w, int lane) {
     const AttnTreeArgs &a = g.a;
-    // row tiles outermost: the empty ones (of sessions with fewer nodes) are the last items
-    const int split = item % g.n_split, x_item = item / g.n_split;
-    const int rt = x_item / g.B, s = x_item - rt * g.B, slot = s * g.row_tiles + rt;
+    const ItemId id = item_id(g, item);
+    const int split = id.split, rt = id.rt, s = id.s, slot = s * g.row_tiles + rt;
+    int p[2];                                         // parents, loaded beside the session's counts
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int i = lane + 32 * x;
+        p[x] = a.parent && i < a.N ? __ldg(a.parent + static_cast<long long>(s) * a.N + i) : i - 1;
+    }
     const Session ses = load_session(a.kv, a.n_node, a.N, s, lane == 0 ? a.err : nullptr);
     bool ok = ses.ok;
     if (ok && a.ratio > 0 && ses.len / a.ratio > a.cap - a.N) {
@@ -191,24 +236,21 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
     if (rows > (kSel ? a.H : g.tile_rows)) rows = kSel ? a.H : g.tile_rows;
     // ancestors by pointer jumping: after round r a mask holds the nearest 2^r path members
     unsigned long long m[2];
-    int p[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int i = lane + 32 * x;
-        p[x] = -1;
-        if (i < n) {
-            p[x] = a.parent ? __ldg(a.parent + static_cast<long long>(s) * a.N + i) : i - 1;
-            if (p[x] < -1 || p[x] >= i) {
-                record_error(a.err, DS4A_ERR_DEVICE_INDEX);
-                ok = false;
-                p[x] = -1;
-            }
+        if (i >= n) {
+            p[x] = -1;
+        } else if (p[x] < -1 || p[x] >= i) {
+            record_error(a.err, DS4A_ERR_DEVICE_INDEX);
+            ok = false;
+            p[x] = -1;
         }
         m[x] = 1ull << i;
     }
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) rows = 0;
-    for (int round = 0; round < 6; ++round) {
+    for (int span = 1; span < n; span *= 2) {
         unsigned long long nm[2];
         int np[2];
 #pragma unroll
@@ -258,18 +300,15 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
             lo_max = max(lo_max, lo);
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        any_raw |= __shfl_xor_sync(0xffffffffu, any_raw, o);
-        all_raw &= __shfl_xor_sync(0xffffffffu, all_raw, o);
-        any_cmp |= __shfl_xor_sync(0xffffffffu, any_cmp, o);
-        all_cmp &= __shfl_xor_sync(0xffffffffu, all_cmp, o);
-        lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
-        lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
-    }
+    any_raw = reduce64<true>(any_raw);
+    all_raw = reduce64<false>(all_raw);
+    any_cmp = reduce64<true>(any_cmp);
+    all_cmp = reduce64<false>(all_cmp);
+    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
     if (w.dirty)
         for (int x = lane; x < kPoison * 12; x += 32) (&w.poison[0][0])[x] = 0;
-    __syncwarp();
+    __syncwarp();   // w.cmp is read below
     if (lane == 0) {
         const int t0 = min(lo_min, len) & ~(kRun - 1);
         w.any_raw = any_raw;
@@ -289,6 +328,11 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
         // the draft's rows, as far as one of the item's nodes attends any
         if (!kSel && any_cmp) w.n_runs += (64 - __clzll(static_cast<long long>(any_cmp)) + kRun - 1) / kRun;
         w.node = i0;
+        if (kSel) {
+            const int depth = __popcll(rows > 0 ? w.cmp[i0] : 1ull) - 1;
+            w.n_vis = (len + depth + 1) / a.ratio;
+            w.n_done = len / a.ratio;
+        }
         w.row0 = row0;
         w.rows = rows;
         w.sides2 = rows > kTK;
@@ -306,24 +350,24 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
     __syncwarp();
 }
 
-// Row of entry j of a node's list in the session's compressed rows: -1 (skipped) if negative,
+// Row of entry j of the node's list in the session's compressed rows: -1 (skipped) if negative,
 // and recorded if not complete at the node's position.
-DS4A_DEVINL int sel_row(const AttnTreeArgs &a, int len, unsigned long long path, int j, bool record) {
+DS4A_DEVINL int sel_row(const AttnTreeArgs &a, const Work &w, int j, bool record) {
     if (j < 0) return -1;
-    if (j >= (len + __popcll(path)) / a.ratio) {
+    if (j >= w.n_vis) {
         if (record) record_error(a.err, DS4A_ERR_DEVICE_INDEX);
         return -1;
     }
-    if (j < len / a.ratio) return j;
-    return static_cast<int>(a.cap) - a.N + path_node(path, (j + 1) * a.ratio - 1 - len);
+    if (j < w.n_done) return j;
+    return static_cast<int>(a.cap) - a.N + path_node(w.cmp[w.node], (j + 1) * a.ratio - 1 - w.len);
 }
 
-// Values that are not finite, of the keys that `node` attends: into columns col .. col+15 of
+// Values that are not finite, of the keys that `node` attends: into columns col .. col+31 of
 // its accumulator.
-__device__ __noinline__ void add_poison_bits(const Work &w, int node, int col, uint32_t &nan, uint32_t &pi, uint32_t &ni) {
-    const int lo = w.lo[node], word = col / 32, sh = col % 32;
+__device__ __noinline__ uint3 poison_bits(const Work &w, int node, int word) {
+    const int lo = w.lo[node];
     const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
-    nan = pi = ni = 0;
+    uint32_t nan = 0, pi = 0, ni = 0;
     for (int key = 0; key < kPoison; ++key) {
         bool hit;
         if (key < kMaxNodes) hit = (raw >> key) & 1ull;
@@ -334,32 +378,27 @@ __device__ __noinline__ void add_poison_bits(const Work &w, int node, int col, u
         pi |= w.poison[key][4 + word];
         ni |= w.poison[key][8 + word];
     }
-    nan = (nan | (pi & ni)) >> sh;
-    pi >>= sh;
-    ni >>= sh;
+    return make_uint3(nan | (pi & ni), pi, ni);
 }
-DS4A_DEVINL void add_poison(const Work &w, int node, int col, uint32_t (&o)[16]) {
-    uint32_t nan, pi, ni;
-    add_poison_bits(w, node, col, nan, pi, ni);
+DS4A_DEVINL void add_poison(const Work &w, int node, int col, uint32_t (&o)[32]) {
+    const uint3 p = poison_bits(w, node, col / 32);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        if ((nan >> e) & 1u) o[e] = 0x7fffffffu;
-        else if ((pi >> e) & 1u) o[e] = 0x7f800000u;
-        else if ((ni >> e) & 1u) o[e] = 0xff800000u;
+    for (int e = 0; e < 32; ++e) {
+        if ((p.x >> e) & 1u) o[e] = 0x7fffffffu;
+        else if ((p.y >> e) & 1u) o[e] = 0x7f800000u;
+        else if ((p.z >> e) & 1u) o[e] = 0xff800000u;
     }
 }
 
 template <int D, bool kSel>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_constant__ Args g) {
-    using L = Layout<D>;
+    using L = Layout<D, kSel>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Work *works = reinterpret_cast<Work *>(smem + L::work);
     uint16_t *info = reinterpret_cast<uint16_t *>(smem + L::info);
-    float *s_top = reinterpret_cast<float *>(smem + L::top);
-    float *s_sum = reinterpret_cast<float *>(smem + L::sums);
-    float *s_ref = reinterpret_cast<float *>(smem + L::ref);
+    float2 *s_ml = reinterpret_cast<float2 *>(smem + L::ml);
     Bars &bar = *reinterpret_cast<Bars *>(smem + L::bars);
     __shared__ uint32_t s_tmem;
     const AttnTreeArgs &a = g.a;
@@ -367,18 +406,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     constexpr int kAtoms = D / 64, kAtomBytes = kTK * 128;
 
     if (tid == 0) {
+        // a stage is released by two commits: one of each side, or two of the side whose tile it is
         for (int x = 0; x < kNS; ++x) {
             tc::mbar_init(&bar.k_full[x], kProd);
-            tc::mbar_init(&bar.k_empty[x], 1);
+            tc::mbar_init(&bar.k_empty[x], 2);
             tc::mbar_init(&bar.v_full[x], kProd);
             tc::mbar_init(&bar.v_ok[x], kChkWarps);
-            tc::mbar_init(&bar.v_empty[x], 1);
+            tc::mbar_init(&bar.v_empty[x], 2);
         }
         tc::mbar_init(&bar.q_full, 1);
-        tc::mbar_init(&bar.q_empty, 1);
+        tc::mbar_init(&bar.q_empty, 2);
         for (int x = 0; x < 2; ++x) {
-            tc::mbar_init(&bar.s_full[x], 1);
-            tc::mbar_init(&bar.p_full[x], kSideWarps);
+            for (int y = 0; y < 2; ++y) {
+                tc::mbar_init(&bar.s_full[x][y], 1);
+                tc::mbar_init(&bar.p_full[x][y], kSideWarps);
+            }
+            tc::mbar_init(&bar.pv[x], 1);
             tc::mbar_init(&bar.o_full[x], 1);
             tc::mbar_init(&bar.o_empty[x], kSideWarps);
             tc::mbar_init(&bar.w_full[x], 1);
@@ -388,11 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         tc::mbar_init(&bar.join, kSideWarps);
         tc::mbar_fence_init();
     }
-    if (warp == kSetupWarp)
-        for (int x = lane; x < kPoison * 12; x += 32) {
-            (&works[0].poison[0][0])[x] = 0;
-            (&works[1].poison[0][0])[x] = 0;
-        }
+    for (int x = tid; x < kPoison * 3; x += kThreads) {
+        reinterpret_cast<uint4 *>(works[0].poison)[x] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4 *>(works[1].poison)[x] = make_uint4(0, 0, 0, 0);
+    }
     if (warp == kSetupWarp && lane < 2) works[lane].dirty = 0;
     if (warp == kMmaWarp) tc::tmem_alloc(&s_tmem, kTmemCols);
     tc::fence_before_sync();
@@ -412,62 +454,60 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
 
     if (warp < kSoftWarps) {
         tc::setmaxnreg_inc<kSoftRegs>();
-        const int side = warp / kSideWarps, half = (warp >> 2) & 1, quad = warp & 3, r = quad * 32 + lane;
+        const int side = warp / kSideWarps, quad = warp & 3, r = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t col_s = tmem + lanes + kColS + side * kTK, col_o = tmem + lanes + kColO + side * kTK;
-        const int pair = 1 + side * 4 + quad;                     // named barrier of the two warps of these rows
-        float *top_mine = s_top + (side * 2 + half) * kTK + r, *top_other = s_top + (side * 2 + (half ^ 1)) * kTK + r;
         const float c2 = a.scale_log2;
-        uint32_t n_s = 0, n_o = 0, n_join = 0, n_t = 0;   // n_t: tiles of the items before
+        uint32_t n_c = 0, n_o = 0, n_join = 0, n_t = 0;   // this side's chunks and items, joined items, tiles so far
         for (int it = 0; it < n_items; ++it) {
             Work &w = works[it & 1];
-            wait(&bar.w_full[it & 1], it >> 1);
-            if (tc::bar_any(pair, 64, !ok)) ok = false;   // the two warps of a barrier leave out the same items
-            const int t0 = w.tile0, t1 = ok ? w.tile1 : t0, sides2 = w.sides2;
+            if (!__all_sync(0xffffffffu, wait(&bar.w_full[it & 1], it >> 1))) break;
+            const int t0 = w.tile0, t1 = w.tile1, sides2 = w.sides2, n_runs = w.n_runs;
             const int row = (sides2 ? side * kTK : 0) + r;        // row in the item
             const int node = min(kMaxNodes - 1, (w.row0 + row) / a.H);
             float m = -INFINITY, l = 0.f;
             bool first = true;
             for (int t = sides2 ? t0 : t0 + side; t < t1; t += sides2 ? 1 : 2) {
-                wait(&bar.s_full[side], n_s++);
-                tc::fence_after_sync();
-                uint32_t x[2][32];
-                tc::ld_x32(col_s + half * 64, x[0]);
-                tc::ld_x32(col_s + half * 64 + 32, x[1]);
-                const uint16_t *inf = info + ((n_t + t - t0) & 3) * kRuns;
-                const uint4 iw = *reinterpret_cast<const uint4 *>(inf);
-                const bool partial = (kSel ? t * kRuns < w.raw_runs : !tile_full(w, t)) ||
-                                     (iw.x & iw.y & iw.z & iw.w) != 0xffffffffu;
-                tc::wait_ld();
-                if (partial) {
-                    const int lo = w.lo[node];
-                    const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
+                const uint16_t *inf = info + ((n_t + t - t0) & (kInfo - 1)) * kRuns;
+                const int chunks = tile_chunks(n_runs, t);
+                const bool edge = needs_check<kSel>(w, t);
+                for (int c = 0; c < chunks; ++c, ++n_c) {
+                    const uint32_t sb = n_c & 1u, col = col_s + sb * kCK;
+                    wait(&bar.s_full[side][sb], n_c >> 1);
+                    tc::fence_after_sync();
+                    uint32_t x[2][32];
+                    tc::ld_x32(col, x[0]);
+                    tc::ld_x32(col + 32, x[1]);
+                    const uint2 iw = *reinterpret_cast<const uint2 *>(inf + c * kChunkRuns);
+                    const bool partial = edge || (iw.x & iw.y) != 0xffffffffu;
+                    uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+                    if (partial) {
+                        const int lo = w.lo[node], v = t * kRuns + c * kChunkRuns;
+                        const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int v = t * kRuns + half * 4 + 2 * c;
-                        const uint32_t bits = (run_bits<kSel>(w, v, lo, raw, cmp, inf) & 0xffffu) |
-                                              run_bits<kSel>(w, v + 1, lo, raw, cmp, inf) << 16;
-                        if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((bits >> e) & 1u)) x[c][e] = 0xff800000u;   // -inf
+                        for (int h = 0; h < 2; ++h)
+                            bits[h] = (run_bits<kSel>(w, v + 2 * h, lo, raw, cmp, inf) & 0xffffu) |
+                                      run_bits<kSel>(w, v + 2 * h + 1, lo, raw, cmp, inf) << 16;
                     }
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tc::wait_ld();
+                    if (partial) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                        for (int h = 0; h < 2; ++h) {
+                            if (__all_sync(0xffffffffu, bits[h] == 0xffffffffu)) continue;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(x[c][e])), __uint_as_float(x[c][e + 1]));
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;   // scale > 0
-                // Raise the reference at the first finite score, then only past the threshold.  The two
-                // threads of a row hold the same one; they look at each other's maximum only when one of
-                // the 64 rows and halves here asks for it.  (Behind this barrier both have read their scores,
-                // which the weights will overwrite.)
-                if (tc::bar_any(pair, 64, top > m + kRescale || (m == -INFINITY && top > m))) {
-                    *top_mine = top;
-                    tc::bar_sync(pair, 64);
-                    top = fmaxf(top, *top_other);
+                            for (int e = 0; e < 32; ++e)
+                                if (!((bits[h] >> e) & 1u)) x[h][e] = 0xff800000u;   // -inf
+                        }
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            mx[(e >> 1) & 3] =
+                                fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(x[h][e])), __uint_as_float(x[h][e + 1]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;   // scale > 0
+                    // raise the reference: at the first finite score, then only past the threshold
                     float alpha = 1.f;
                     if (top > m + kRescale || (m == -INFINITY && top > m)) {
                         alpha = ex2(m - top);
@@ -475,70 +515,70 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                         l *= alpha;
                     }
                     if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        // the earlier product of this side is complete: it was issued before the scores just read
+                        wait(&bar.pv[side], n_c - 1);   // the product before (the one before that is done: these scores came after it)
+                        tc::fence_after_sync();
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
+                        for (int d = 0; d < D / 16; ++d) {
                             uint32_t o[16];
-                            tc::ld_x16(col_o + half * (D / 2) + c * 16, o);
+                            tc::ld_x16(col_o + d * 16, o);
                             tc::wait_ld();
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tc::st_x16(col_o + half * (D / 2) + c * 16, o);
+                            tc::st_x16(col_o + d * 16, o);
                         }
                     }
-                }
-                first = false;
-                const float ref = m == -INFINITY ? 0.f : m;
-                const uint64_t c22 = tc::pack2(c2, c2), ref2 = tc::pack2(-ref, -ref);
-                uint64_t sum[2] = {0, 0};
+                    first = false;
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const uint64_t c22 = tc::pack2(c2, c2), ref2 = tc::pack2(-ref, -ref);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t pk[16];
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float y0, y1;
-                        tc::unpack2(tc::fma2(tc::pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), c22,
-                                             ref2), y0, y1);
-                        const float p0 = ex2(y0), p1 = ex2(y1);
-                        sum[e & 1] = tc::add2(sum[e & 1], tc::pack2(p0, p1));
-                        pk[e] = pack_half2(p0, p1);
+                        for (int e = 0; e < 16; ++e) {
+                            float y0, y1;
+                            tc::unpack2(tc::fma2(tc::pack2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1])),
+                                                 c22, ref2), y0, y1);
+                            const float p0 = ex2(y0), p1 = ex2(y1);
+                            sum[e & 1] = tc::add2(sum[e & 1], tc::pack2(p0, p1));
+                            pk[e] = pack_half2(p0, p1);
+                        }
+                        tc::st_x16(col + h * 16, pk);
                     }
-                    tc::st_x16(col_s + half * 32 + c * 16, pk);
+                    float s0, s1;
+                    tc::unpack2(tc::add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.p_full[side][sb]);
                 }
-                float s0, s1;
-                tc::unpack2(tc::add2(sum[0], sum[1]), s0, s1);
-                l += s0 + s1;
-                tc::wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar.p_full[side]);
             }
             n_t += t1 - t0;
             // ---- end of the item ----
             const bool have = !first;                              // this side has tiles
             const bool joined = !sides2 && t1 - t0 > 1;            // side 1 holds part of the same rows
             if (have) {
-                // the row's sum over both halves, and over both sides of a joined item (behind o_full: the product
-                // waited until the item before had been read, its sums with it)
                 wait(&bar.o_full[side], n_o++);
-                s_sum[(side * 2 + half) * kTK + r] = l;
-                if (joined && side == 1) {
-                    if (half == 0) s_ref[r] = m;
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar.join);
+                if (joined) {
+                    if (side == 1) {
+                        s_ml[r] = make_float2(m, l);
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&bar.join);
+                    } else {
+                        wait(&bar.join, n_join);
+                    }
+                    ++n_join;
                 }
-                tc::bar_sync(pair, 64);
-                l += s_sum[(side * 2 + (half ^ 1)) * kTK + r];
-                if (joined && side == 0) wait(&bar.join, n_join);
                 tc::fence_after_sync();
-                if (joined) ++n_join;
                 if (sides2 || side == 0) {
                     float wa = 1.f, wb = 0.f;
                     if (joined) {
-                        const float mb = s_ref[r], mm = fmaxf(m, mb), rf = mm == -INFINITY ? 0.f : mm;
+                        const float2 o = s_ml[r];
+                        const float mm = fmaxf(m, o.x), rf = mm == -INFINITY ? 0.f : mm;
                         wa = ex2(m - rf);
-                        wb = ex2(mb - rf);
-                        l = l * wa + (s_sum[2 * kTK + r] + s_sum[3 * kTK + r]) * wb;
+                        wb = ex2(o.x - rf);
+                        l = l * wa + o.y * wb;
                         m = mm;
                     }
                     wait(&bar.chk[it & 1], it >> 1);
@@ -547,46 +587,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     const long long qrow = (static_cast<long long>(w.s) * a.N) * a.H + w.row0 + row;
                     const long long prow = (static_cast<long long>(w.slot) * g.n_split + w.split) * g.tile_rows + row;
-                    if (!direct && valid && half == 0) g.part_ml[prow] = make_float2(m, l);
+                    if (!direct && valid) g.part_ml[prow] = make_float2(m, l);
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {             // 16 columns at a time
-                        const int col = half * (D / 2) + c * 16;
-                        uint32_t o[16];
-                        tc::ld_x16(col_o + col, o);
+                    for (int c = 0; c < D / 32; ++c) {             // 32 columns at a time
+                        uint32_t o[32];
+                        tc::ld_x32(col_o + c * 32, o);
                         if (joined) {
-                            uint32_t o2[16];
-                            tc::ld_x16(col_o + kTK + col, o2);
+                            uint32_t o2[32];
+                            tc::ld_x32(col_o + kTK + c * 32, o2);
                             tc::wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
+                            for (int e = 0; e < 32; ++e)
                                 o[e] = __float_as_uint(__uint_as_float(o[e]) * wa + __uint_as_float(o2[e]) * wb);
                         } else {
                             tc::wait_ld();
                         }
-                        if (dirty) add_poison(w, node, col, o);
+                        if (dirty) add_poison(w, node, c * 32, o);
                         if (valid && direct) {
 #pragma unroll
-                            for (int q4 = 0; q4 < 2; ++q4) {
+                            for (int q4 = 0; q4 < 4; ++q4) {
                                 uint32_t h[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     h[e] = pack_half2(__uint_as_float(o[q4 * 8 + 2 * e]) * inv,
                                                       __uint_as_float(o[q4 * 8 + 2 * e + 1]) * inv);
-                                *reinterpret_cast<uint4 *>(a.out + qrow * D + col + q4 * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+                                *reinterpret_cast<uint4 *>(a.out + qrow * D + c * 32 + q4 * 8) =
+                                    make_uint4(h[0], h[1], h[2], h[3]);
                             }
                         } else if (valid) {
 #pragma unroll
-                            for (int q4 = 0; q4 < 4; ++q4)
-                                *reinterpret_cast<uint4 *>(g.part + prow * D + col + q4 * 4) =
+                            for (int q4 = 0; q4 < 8; ++q4)
+                                *reinterpret_cast<uint4 *>(g.part + prow * D + c * 32 + q4 * 4) =
                                     make_uint4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]);
                         }
                     }
                 }
-                // the accumulators may be overwritten: side 0 has read both of a joined item
+                // the accumulators may be overwritten; with one row block side 0 has read both
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if (!joined) {
+                    if (sides2) {
                         tc::mbar_arrive(&bar.o_empty[side]);
                     } else if (side == 0) {
                         tc::mbar_arrive(&bar.o_empty[0]);
@@ -615,78 +655,103 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
                 __syncwarp();
             }
-        } else if (warp == kMmaWarp) {
+        } else if (warp < kChkWarp0) {
             // The whole warp runs this, converged, and one elected lane issues: the operands are then
             // warp-uniform registers, which the instruction wants (issued from a lane == 0 branch, eight
             // products took 570 cycles to issue, about as long as the tensor core needs for them).
-            constexpr uint32_t kIdS = tc::idesc_f16_f32(kTK, kTK, false, false);
+            constexpr uint32_t kIdS = tc::idesc_f16_f32(kTK, kCK, false, false);
             constexpr uint32_t kIdO = tc::idesc_f16_f32(kTK, D, false, true);
-            uint32_t n_q = 0, n_k = 0, n_p[2] = {0, 0}, n_o[2] = {0, 0};
+            const uint32_t side = warp - kMmaWarp;
+            uint32_t n_t = 0, n_c = 0, n_o = 0;                   // tiles; chunks of this side; items with tiles
             auto wait_all = [&](uint64_t *b, uint32_t parity) {
                 ok = __all_sync(0xffffffffu, wait(b, parity));
                 return ok;
             };
-            const uint32_t q_s = tc::smem_u32(smem + L::q), k_s = tc::smem_u32(smem + L::k), v_s = tc::smem_u32(smem + L::v);
+            const uint32_t k_s = tc::smem_u32(smem + L::k), v_s = tc::smem_u32(smem + L::v);
+            const uint32_t d_s = tmem + kColS + side * kTK, d_o = tmem + kColO + side * kTK;
             for (int it = 0; it < n_items && ok; ++it) {
                 const Work &w = works[it & 1];
                 if (!wait_all(&bar.w_full[it & 1], it >> 1)) break;
-                const int tiles = __shfl_sync(0xffffffffu, w.tile1 - w.tile0, 0);
+                const int tile0 = __shfl_sync(0xffffffffu, w.tile0, 0), n_runs = __shfl_sync(0xffffffffu, w.n_runs, 0);
+                const int tiles = __shfl_sync(0xffffffffu, w.tile1, 0) - tile0;
                 const bool sides2 = __shfl_sync(0xffffffffu, w.sides2, 0) != 0;
-                const int n = sides2 ? 2 * tiles : tiles;         // products: sides in turn
-                if (n > 0) wait_all(&bar.q_full, n_q++);
-                // S of product k: side k & 1, tile k / 2 or k
-                auto issue_s = [&](int k) {
-                    const uint32_t side = k & 1;
-                    const uint32_t kt = n_k + (sides2 ? k >> 1 : k), st = kt % kNS;
-                    if (!sides2 || side == 0) wait_all(&bar.k_full[st], kt / kNS);
+                const int first = sides2 ? 0 : static_cast<int>(side), by = sides2 ? 1 : 2;   // this side's tiles
+                const uint32_t qa = tc::smem_u32(smem + L::q) + (sides2 ? side : 0) * L::tile;
+                if (!wait_all(&bar.q_full, it)) break;
+                if (first >= tiles) {                             // nothing for this side: every phase is seen all the same
+                    if (lane == 0) tc::mbar_arrive(&bar.q_empty);
+                    if (tiles > 0 && n_o > 0) wait_all(&bar.o_empty[side], n_o - 1);
+                }
+                // the next chunk to score: tile st_t, half st_h, buffer st_n & 1
+                int st_t = first, st_h = 0;
+                uint32_t st_n = n_c;
+                auto issue_s = [&]() {
+                    if (st_t >= tiles || !ok) return;
+                    const uint32_t kt = n_t + st_t, stage = kt % kNS, buf = st_n & 1u;
+                    if (st_h == 0) wait_all(&bar.k_full[stage], kt / kNS);
                     if (!ok) return;
                     tc::fence_after_sync();
-                    const uint32_t qa = q_s + (sides2 ? side : 0) * L::tile, kb = k_s + st * L::tile;
-                    const uint32_t d = tmem + kColS + side * kTK;
-                    const bool release = !sides2 || side == 1, last = k == n - 1;
+                    const uint32_t kb = k_s + stage * L::tile + st_h * (kCK * 128), d = d_s + buf * kCK;
+                    const bool tile_end = st_h + 1 == tile_chunks(n_runs, tile0 + st_t);
+                    const bool last = tile_end && st_t + by >= tiles;
                     if (tc::elect()) {
 #pragma unroll
                         for (int x = 0; x < D / 16; ++x)
                             tc::mma_f16(d, tc::desc_sw128(qa + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024),
                                         tc::desc_sw128(kb + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024), kIdS, x > 0);
-                        tc::commit(&bar.s_full[side]);
-                        if (release) tc::commit(&bar.k_empty[st]);
+                        tc::commit(&bar.s_full[side][buf]);
+                        if (tile_end) {
+                            tc::commit(&bar.k_empty[stage]);
+                            if (!sides2) tc::commit(&bar.k_empty[stage]);
+                        }
                         if (last) tc::commit(&bar.q_empty);
                     }
                     __syncwarp();
+                    ++st_n;
+                    if (tile_end) {
+                        st_t += by;
+                        st_h = 0;
+                    } else {
+                        st_h = 1;
+                    }
                 };
-                auto issue_pv = [&](int k) {
-                    const uint32_t side = k & 1;
-                    const uint32_t vt = n_k + (sides2 ? k >> 1 : k), st = vt % kNS;
-                    if (!sides2 || side == 0) wait_all(&bar.v_ok[st], vt / kNS);
-                    wait_all(&bar.p_full[side], side ? n_p[1]++ : n_p[0]++);
-                    const uint32_t items = side ? n_o[1] : n_o[0];
-                    if (k < 2 && items > 0) wait_all(&bar.o_empty[side], items - 1);
-                    if (!ok) return;
-                    tc::fence_after_sync();
-                    const uint32_t vb = v_s + st * L::tile;
-                    const uint32_t d = tmem + kColO + side * kTK, pa = tmem + kColS + side * kTK;
-                    const bool release = !sides2 || side == 1, last = k >= n - 2, more = k > 1;
-                    if (tc::elect()) {
+                issue_s();
+                issue_s();
+                for (int t = first; t < tiles && ok; t += by) {
+                    const uint32_t vt = n_t + t, stage = vt % kNS;
+                    const int chunks = tile_chunks(n_runs, tile0 + t);
+                    for (int c = 0; c < chunks && ok; ++c, ++n_c) {
+                        const uint32_t buf = n_c & 1u;
+                        if (c == 0) {
+                            // The item before has been read: the accumulator is free, and every earlier V tile has
+                            // come, those that only the other side waited for too (so the parity below is the
+                            // right phase's).
+                            if (t == first && n_o > 0) wait_all(&bar.o_empty[side], n_o - 1);
+                            wait_all(&bar.v_ok[stage], vt / kNS);
+                        }
+                        const uint32_t vb = v_s + stage * L::tile + c * (kCK / 16 * 2048), pa = d_s + buf * kCK;
+                        wait_all(&bar.p_full[side][buf], n_c >> 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        const bool more = t != first || c != 0, tile_end = c + 1 == chunks;
+                        if (tc::elect()) {
 #pragma unroll
-                        for (int x = 0; x < kTK / 16; ++x)
-                            tc::mma_f16_ts(d, pa + x * 8, tc::desc_sw128(vb + x * 2048, kAtomBytes, 1024), kIdO, more || x > 0);
-                        if (release) tc::commit(&bar.v_empty[st]);
-                        if (last) tc::commit(&bar.o_full[side]);
+                            for (int x = 0; x < kCK / 16; ++x)
+                                tc::mma_f16_ts(d_o, pa + x * 8, tc::desc_sw128(vb + x * 2048, kAtomBytes, 1024), kIdO,
+                                               more || x > 0);
+                            if (tile_end) {
+                                tc::commit(&bar.v_empty[stage]);
+                                if (!sides2) tc::commit(&bar.v_empty[stage]);
+                            }
+                            tc::commit(&bar.pv[side]);
+                            if (tile_end && t + by >= tiles) tc::commit(&bar.o_full[side]);
+                        }
+                        __syncwarp();
+                        issue_s();
                     }
-                    __syncwarp();
-                    if (last) {
-                        if (side) ++n_o[1];
-                        else ++n_o[0];
-                    }
-                };
-                if (n > 0) issue_s(0);
-                if (n > 1 && ok) issue_s(1);
-                for (int k = 0; k < n && ok; ++k) {
-                    issue_pv(k);
-                    if (k + 2 < n && ok) issue_s(k + 2);
                 }
-                n_k += tiles;
+                if (tiles > 0) ++n_o;
+                n_t += tiles;
                 if (lane == 0) tc::mbar_arrive(&bar.w_empty[it & 1]);
             }
             __syncwarp();
@@ -700,8 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 for (int t = w.tile0; t < w.tile1; ++t, ++n_v) {
                     const int st = n_v % kNS;
                     if (!warp_wait(&bar.v_full[st], n_v / kNS)) break;
-                    if (kSel ? t * kRuns < w.raw_runs : !tile_full(w, t)) {
-                        const uint16_t *inf = info + (4 + (n_v & 3)) * kRuns;
+                    if (needs_check<kSel>(w, t)) {
+                        const uint16_t *inf = info + (kInfo + (n_v & (kInfo - 1))) * kRuns;
                         unsigned char *vt = smem + L::v + st * L::tile;
                         bool wrote = false;
                         for (int r = 0; r < kRuns; ++r) {
@@ -769,22 +834,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             uint64_t *full = is_v ? bar.v_full : bar.k_full, *empty = is_v ? bar.v_empty : bar.k_empty;
             const CUtensorMap *map_raw = is_v ? &g.map_v : &g.map_k, *map_comp = is_v ? &g.map_cv : &g.map_ck;
             unsigned char *ring = smem + (is_v ? L::v : L::k);
-            uint32_t n_t = 0, n_q = 0;
+            const int run = pw * kRunsPer + (lane & (kRunsPer - 1));          // lane = run (and atom)
+            const int group = lane & (kRunsPer * 4 - 1);                      // sel: lane = group of 4 entries
+            const int grun = pw * kRunsPer + group / 4;
             if (lane == 0) {
                 tc::prefetch_map(map_raw);
                 if (a.ratio > 0) tc::prefetch_map(map_comp);
                 if (!is_v && pw == 0) tc::prefetch_map(&g.map_q);
             }
+            // the rows of one tile: this lane's run, this lane's four list entries (the raw table entries and
+            // list entries of the next tile are loaded while this one waits for its stage)
+            struct Rows {
+                int v, gv, page;
+                int4 e;
+            };
+            int st = 0;
+            uint32_t ph = 0, n_t = 0, n_q = 0;
             for (int it = 0; it < n_items; ++it) {
                 const Work &w = works[it & 1];
-                if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
-                const int32_t *table = a.kv.table + static_cast<long long>(w.s) * a.kv.max_pages;
-                if (!is_v && pw == 0 && w.tile1 > w.tile0) {
+                if (!is_v && pw == 0) {
+                    // the query rows depend on nothing in device memory: loaded while the set-up runs
                     if (n_q > 0 && !warp_wait(&bar.q_empty, n_q - 1)) break;
                     if (lane == 0) {
-                        const int blocks = w.sides2 ? 2 : 1;
+                        const ItemId id = item_id(g, blockIdx.x + it * gridDim.x);
+                        constexpr int kBlocks = kSel ? 1 : 2;
+                        const int blocks = kBlocks == 2 && g.tile_rows > kTK ? 2 : 1;
+                        const int qrow = id.s * a.N * a.H + id.rt * g.item_rows;
                         tc::expect_tx(&bar.q_full, blocks * L::tile);
-                        const int qrow = w.s * a.N * a.H + w.row0;
                         for (int b = 0; b < blocks; ++b)
                             for (int at = 0; at < kAtoms; ++at)
                                 tc::tma_load_2d(smem + L::q + b * L::tile + at * kAtomBytes, &g.map_q, at * 64,
@@ -793,45 +869,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     __syncwarp();
                     ++n_q;
                 }
-                for (int t = w.tile0; t < w.tile1; ++t, ++n_t) {
-                    const int st = n_t % kNS;
-                    // the rows of this warp's runs: lane = run (raw and dense), lane = group of 4 (list)
-                    const int run = pw * kRunsPer + (lane & (kRunsPer - 1));
-                    const int v = t * kRuns + run;
+                if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
+                const int tile0 = w.tile0, tile1 = w.tile1, raw_runs = w.raw_runs, n_runs = w.n_runs;
+                const int32_t *table = a.kv.table + static_cast<long long>(w.s) * a.kv.max_pages;
+                const int32_t *list = kSel ? a.sel + (static_cast<long long>(w.s) * a.N + w.node) * a.n_sel : nullptr;
+                auto fetch = [&](int t) {
+                    Rows r;
+                    r.v = t * kRuns + run;
+                    r.gv = t * kRuns + grun;
+                    r.page = r.v < raw_runs ? __ldg(table + static_cast<unsigned>(w.t0 + r.v * kRun) / static_cast<unsigned>(a.kv.page)) : 0;
+                    r.e = make_int4(-1, -1, -1, -1);
+                    if (kSel && r.gv >= raw_runs && r.gv < n_runs) {
+                        const int e0 = (r.gv - raw_runs) * kRun + (group & 3) * 4;
+                        if (e0 < a.n_sel) r.e.x = __ldg(list + e0);
+                        if (e0 + 1 < a.n_sel) r.e.y = __ldg(list + e0 + 1);
+                        if (e0 + 2 < a.n_sel) r.e.z = __ldg(list + e0 + 2);
+                        if (e0 + 3 < a.n_sel) r.e.w = __ldg(list + e0 + 3);
+                    }
+                    return r;
+                };
+                Rows next{};
+                if (tile0 < tile1) next = fetch(tile0);
+                for (int t = tile0; t < tile1; ++t, ++n_t) {
+                    const Rows r = next;
+                    if (t + 1 < tile1) next = fetch(t + 1);
                     int row = g.pool_oob;
                     bool raw_run = true, readable = true;
-                    if (v < w.raw_runs) {
-                        const long long pr = pool_row(a.kv, table, static_cast<unsigned>(w.t0 + v * kRun),
-                                                      lane < kRunsPer ? a.err : nullptr);
-                        readable = pr >= 0;
-                        if (readable) row = static_cast<int>(pr);
-                    } else if (!kSel && v < w.n_runs) {
+                    if (r.v < raw_runs) {
+                        readable = r.page >= 0 && r.page < a.kv.n_pages;
+                        const unsigned slot = w.t0 + r.v * kRun;
+                        if (readable) row = r.page * a.kv.page + static_cast<int>(slot % static_cast<unsigned>(a.kv.page));
+                        else if (lane < kRunsPer) record_error(a.err, DS4A_ERR_DEVICE_INDEX);
+                    } else if (!kSel && r.v < n_runs) {
                         raw_run = false;
-                        const int c = v - w.raw_runs;
+                        const int c = r.v - raw_runs;
                         const long long base = static_cast<long long>(w.s) * a.cap;
                         row = static_cast<int>(c < w.comp_runs ? base + c * kRun
                                                                : base + a.cap - a.N + (c - w.comp_runs) * kRun);
                     }
                     int4 gr = make_int4(g.comp_oob, g.comp_oob, g.comp_oob, g.comp_oob);
                     uint32_t gmask = 0;
-                    const int group = lane & (kRunsPer * 4 - 1);    // group of 4 rows among this warp's
-                    const int gv = t * kRuns + pw * kRunsPer + group / 4;
-                    if (kSel && gv >= w.raw_runs && gv < w.n_runs) {
-                        const long long nq = static_cast<long long>(w.s) * a.N + w.node;
-                        const int e0 = (gv - w.raw_runs) * kRun + (group & 3) * 4;
-                        int *rr = &gr.x;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (e0 + e >= a.n_sel) continue;
-                            const int j = __ldg(a.sel + nq * a.n_sel + e0 + e);
-                            const int rrow = sel_row(a, w.len, w.cmp[w.node], j, lane < kRunsPer * 4 && !is_v);
-                            if (rrow >= 0) {
-                                rr[e] = static_cast<int>(static_cast<long long>(w.s) * a.cap + rrow);
-                                gmask |= 1u << e;
-                            }
-                        }
+                    if (kSel && r.gv >= raw_runs && r.gv < n_runs) {
+                        const bool record = lane < kRunsPer * 4 && !is_v;
+                        const int base = w.s * static_cast<int>(a.cap);
+                        const int e[4] = {sel_row(a, w, r.e.x, record), sel_row(a, w, r.e.y, record),
+                                          sel_row(a, w, r.e.z, record), sel_row(a, w, r.e.w, record)};
+                        if (e[0] >= 0) { gr.x = base + e[0]; gmask |= 1u; }
+                        if (e[1] >= 0) { gr.y = base + e[1]; gmask |= 2u; }
+                        if (e[2] >= 0) { gr.z = base + e[2]; gmask |= 4u; }
+                        if (e[3] >= 0) { gr.w = base + e[3]; gmask |= 8u; }
                     }
-                    if (n_t >= kNS && !warp_wait(&empty[st], n_t / kNS - 1)) break;
+                    if (n_t >= static_cast<uint32_t>(kNS) && !warp_wait(&empty[st], ph ^ 1u)) break;
                     {   // readable keys per run, for the softmax (K) and the checkers (V)
                         uint32_t m16 = readable ? 0xffffu : 0u;
                         if (kSel) {
@@ -839,36 +927,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                             gm |= __shfl_xor_sync(0xffffffffu, gm, 1);
                             gm |= __shfl_xor_sync(0xffffffffu, gm, 2);
                             const uint32_t mine = __shfl_sync(0xffffffffu, gm, (lane & (kRunsPer - 1)) * 4);
-                            if (v >= w.raw_runs) m16 = mine;
+                            if (r.v >= raw_runs) m16 = mine;
                         }
-                        if (lane < kRunsPer) info[(is_v * 4 + (n_t & 3)) * kRuns + run] = static_cast<uint16_t>(m16);
+                        if (lane < kRunsPer)
+                            info[((is_v ? kInfo : 0) + (n_t & (kInfo - 1))) * kRuns + run] = static_cast<uint16_t>(m16);
                         __syncwarp();
                     }
                     if (lane == 0) tc::expect_tx(&full[st], L::tile / kProd);
                     __syncwarp();
                     const uint32_t dst = tc::smem_u32(ring + st * L::tile);
-                    if (!kSel || v < w.raw_runs || v >= w.n_runs) {
-                        if (lane < kRunsPer * kAtoms) {
-                            const int at = lane / kRunsPer;
-                            tc::tma_load_2d(dst + at * kAtomBytes + run * 2048, raw_run ? map_raw : map_comp, at * 64,
-                                               row, &full[st]);
-                        }
+                    if (lane < kRunsPer * kAtoms && (!kSel || r.v < raw_runs || r.v >= n_runs)) {
+                        const int at = lane / kRunsPer;
+                        tc::tma_load_2d(dst + at * kAtomBytes + run * 2048, raw_run ? map_raw : map_comp, at * 64, row,
+                                        &full[st]);
                     }
-                    if (kSel) {
-                        if (gv >= w.raw_runs && gv < w.n_runs && lane < kRunsPer * 4)
-                            for (int at = 0; at < kAtoms; ++at)
-                                tc::tma_gather4(dst + at * kAtomBytes + (pw * kRunsPer * 4 + group) * 512, map_comp,
-                                                at * 64, gr, &full[st]);
+                    if (kSel && r.gv >= raw_runs && r.gv < n_runs && lane < kRunsPer * 4) {
+                        for (int at = 0; at < kAtoms; ++at)
+                            tc::tma_gather4(dst + at * kAtomBytes + (pw * kRunsPer * 4 + group) * 512, map_comp, at * 64,
+                                            gr, &full[st]);
                     }
                     __syncwarp();
+                    if (++st == kNS) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bar.w_empty[it & 1]);
             }
             // a wait gave up: the copies in flight land before the block may end
             if (!ok && lane == 0) {
-                const uint32_t from = n_t > kNS ? n_t - kNS : 0;
-                for (uint32_t x = from; x < n_t; ++x) tc::mbar_wait(&full[x % kNS], (x / kNS) & 1u);
+                const uint32_t ns = kNS, from = n_t > ns ? n_t - ns : 0;
+                for (uint32_t x = from; x < n_t; ++x) tc::mbar_wait(&full[x % ns], (x / ns) & 1u);
                 if (!is_v && pw == 0 && n_q > 0) tc::mbar_wait(&bar.q_full, (n_q - 1) & 1u);
             }
             __syncwarp();
@@ -974,12 +1064,12 @@ cudaError_t launch_one(Args &g, const Ctx &c) {
     cudaGetDevice(&dev);
     if (configured_device != dev) {
         cudaError_t e = cudaFuncSetAttribute(attn_tree_kernel<D, kSel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(Layout<D>::bytes));
+                                             static_cast<int>(Layout<D, kSel>::bytes));
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
     const int grid = g.n_work < c.num_sms ? g.n_work : c.num_sms;
-    return launch(attn_tree_kernel<D, kSel>, dim3(grid), dim3(kThreads), Layout<D>::bytes, c, 1, g);
+    return launch(attn_tree_kernel<D, kSel>, dim3(grid), dim3(kThreads), (Layout<D, kSel>::bytes), c, 1, g);
 }
 
 }  // namespace
@@ -1021,6 +1111,7 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
     g.min_tiles = p.min_tiles;
     g.row_tiles = p.row_tiles;
     g.tile_rows = p.tile_rows;
+    g.item_rows = p.item_rows;
     g.n_work = static_cast<int>(slots * p.n_split);
     g.pool_oob = static_cast<int>(pool_rows);
     g.comp_oob = static_cast<int>(comp_rows);
