@@ -402,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     Bars &bar = *reinterpret_cast<Bars *>(smem + L::bars);
     __shared__ uint32_t s_tmem;
     const AttnTreeArgs &a = g.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the shuffle tells the compiler that the warp's number is the same in all its lanes
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr int kAtoms = D / 64, kAtomBytes = kTK * 128;
 
     if (tid == 0) {
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     pdl_wait();
     pdl_trigger();
     bool ok = true;
