@@ -111,10 +111,11 @@ struct Layout {
     static constexpr int v = k + kNS * tile;
     static constexpr int work = v + kNS * tile;
     // uint16 [8][8]: readable keys per run of the CTA's tile number & 7, once from the K and once from the V
-    // producers.  A slot is written again eight tiles on, two stages ahead of the products; those two tiles
+    // producers; then uint8 [8][8]: every row of the item attends every key of the run.  A slot is written again eight tiles on, two stages ahead of the products; those two tiles
     // on are issued only when the softmax of this one is done.
     static constexpr int info = work + 2 * static_cast<int>(sizeof(Work));
-    static constexpr int ml = info + 2 * kInfo * kRuns * 2;                  // float2 [128] side 1's (reference, sum)
+    static constexpr int whole = info + 2 * kInfo * kRuns * 2;
+    static constexpr int ml = whole + kInfo * kRuns;                  // float2 [128] side 1's (reference, sum)
     static constexpr int bars = ml + kTK * 8;
     static constexpr int end = bars + static_cast<int>(sizeof(Bars));
     static constexpr size_t bytes = end + 1024;
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Work *works = reinterpret_cast<Work *>(smem + L::work);
     uint16_t *info = reinterpret_cast<uint16_t *>(smem + L::info);
+    uint8_t *whole = smem + L::whole;
     float2 *s_ml = reinterpret_cast<float2 *>(smem + L::ml);
     Bars &bar = *reinterpret_cast<Bars *>(smem + L::bars);
     __shared__ uint32_t s_tmem;
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             for (int t = sides2 ? t0 : t0 + side; t < t1; t += sides2 ? 1 : 2) {
                 const uint16_t *inf = info + ((n_t + t - t0) & (kInfo - 1)) * kRuns;
                 const int chunks = tile_chunks(n_runs, t);
-                const bool edge = needs_check<kSel>(w, t);
+                const uint8_t *wh = whole + ((n_t + t - t0) & (kInfo - 1)) * kRuns;
                 for (int c = 0; c < chunks; ++c, ++n_c) {
                     const uint32_t sb = n_c & 1u, col = col_s + sb * kCK;
                     wait(&bar.s_full[side][sb], n_c >> 1);
@@ -479,25 +481,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     uint32_t x[2][32];
                     tc::ld_x32(col, x[0]);
                     tc::ld_x32(col + 32, x[1]);
-                    const uint2 iw = *reinterpret_cast<const uint2 *>(inf + c * kChunkRuns);
-                    const bool partial = edge || (iw.x & iw.y) != 0xffffffffu;
-                    uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
-                    if (partial) {
-                        const int lo = w.lo[node], v = t * kRuns + c * kChunkRuns;
+                    const uint32_t full = *reinterpret_cast<const uint32_t *>(wh + c * kChunkRuns);   // a byte per run
+                    tc::wait_ld();
+                    if (full != 0x01010101u) {
+                        const int lo = w.lo[node];
                         const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            bits[h] = (run_bits<kSel>(w, v + 2 * h, lo, raw, cmp, inf) & 0xffffu) |
-                                      run_bits<kSel>(w, v + 2 * h + 1, lo, raw, cmp, inf) << 16;
-                    }
-                    tc::wait_ld();
-                    if (partial) {
+                        for (int u = 0; u < kChunkRuns; ++u) {
+                            if ((full >> (8 * u)) & 1u) continue;
+                            const uint32_t bits =
+                                run_bits<kSel>(w, t * kRuns + c * kChunkRuns + u, lo, raw, cmp, inf);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (__all_sync(0xffffffffu, bits[h] == 0xffffffffu)) continue;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((bits[h] >> e) & 1u)) x[h][e] = 0xff800000u;   // -inf
+                            for (int e = 0; e < kRun; ++e)
+                                if (!((bits >> e) & 1u)) x[u / 2][(u & 1) * kRun + e] = 0xff800000u;   // -inf
                         }
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -686,12 +682,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 // the next chunk to score: tile st_t, half st_h, buffer st_n & 1
                 int st_t = first, st_h = 0;
                 uint32_t st_n = n_c;
-                auto issue_s = [&]() {
-                    if (st_t >= tiles || !ok) return;
-                    const uint32_t kt = n_t + st_t, stage = kt % kNS, buf = st_n & 1u;
-                    if (st_h == 0) wait_all(&bar.k_full[stage], kt / kNS);
-                    if (!ok) return;
-                    tc::fence_after_sync();
+                auto wait_k = [&]() {
+                    if (st_t >= tiles || st_h != 0) return true;
+                    const uint32_t kt = n_t + st_t;
+                    return wait(&bar.k_full[kt % kNS], kt / kNS);
+                };
+                auto issue_s = [&]() {                            // behind wait_k
+                    if (st_t >= tiles) return;
+                    const uint32_t stage = (n_t + st_t) % kNS, buf = st_n & 1u;
                     const uint32_t kb = k_s + stage * L::tile + st_h * (kCK * 128), d = d_s + buf * kCK;
                     const bool tile_end = st_h + 1 == tile_chunks(n_runs, tile0 + st_t);
                     const bool last = tile_end && st_t + by >= tiles;
@@ -716,22 +714,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                         st_h = 1;
                     }
                 };
-                issue_s();
-                issue_s();
+                for (int x = 0; x < 2 && ok; ++x) {
+                    ok = __all_sync(0xffffffffu, wait_k());
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    issue_s();
+                }
                 for (int t = first; t < tiles && ok; t += by) {
                     const uint32_t vt = n_t + t, stage = vt % kNS;
                     const int chunks = tile_chunks(n_runs, tile0 + t);
                     for (int c = 0; c < chunks && ok; ++c, ++n_c) {
                         const uint32_t buf = n_c & 1u;
+                        // all this round's waits at once, so that nothing stands between its products
+                        bool good = wait_k();
                         if (c == 0) {
                             // The item before has been read: the accumulator is free, and every earlier V tile has
                             // come, those that only the other side waited for too (so the parity below is the
                             // right phase's).
-                            if (t == first && n_o > 0) wait_all(&bar.o_empty[side], n_o - 1);
-                            wait_all(&bar.v_ok[stage], vt / kNS);
+                            if (t == first && n_o > 0) good = wait(&bar.o_empty[side], n_o - 1) && good;
+                            good = wait(&bar.v_ok[stage], vt / kNS) && good;
                         }
                         const uint32_t vb = v_s + stage * L::tile + c * (kCK / 16 * 2048), pa = d_s + buf * kCK;
-                        wait_all(&bar.p_full[side][buf], n_c >> 1);
+                        good = wait(&bar.p_full[side][buf], n_c >> 1) && good;
+                        ok = __all_sync(0xffffffffu, good);
                         if (!ok) break;
                         tc::fence_after_sync();
                         const bool more = t != first || c != 0, tile_end = c + 1 == chunks;
@@ -930,8 +935,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                             const uint32_t mine = __shfl_sync(0xffffffffu, gm, (lane & (kRunsPer - 1)) * 4);
                             if (r.v >= raw_runs) m16 = mine;
                         }
-                        if (lane < kRunsPer)
-                            info[((is_v ? kInfo : 0) + (n_t & (kInfo - 1))) * kRuns + run] = static_cast<uint16_t>(m16);
+                        if (lane < kRunsPer) {
+                            uint16_t *inf = info + ((is_v ? kInfo : 0) + (n_t & (kInfo - 1))) * kRuns;
+                            inf[run] = static_cast<uint16_t>(m16);
+                            if (!is_v)
+                                whole[(n_t & (kInfo - 1)) * kRuns + run] =
+                                    (run_bits<kSel>(w, r.v, w.lo_max, w.all_raw, w.all_cmp, inf) & 0xffffu) == 0xffffu;
+                        }
                         __syncwarp();
                     }
                     if (lane == 0) tc::expect_tx(&full[st], L::tile / kProd);
