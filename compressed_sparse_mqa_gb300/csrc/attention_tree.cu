@@ -57,15 +57,11 @@ constexpr int kCK = 64, kChunkRuns = kCK / kRun;   // keys and runs of a chunk: 
 constexpr int kNS = 2;                     // K stages, and V stages: with one row block, one for each side
 constexpr int kInfo = 8;                   // tiles whose run information is kept
 constexpr int kSideWarps = 4, kSoftWarps = 2 * kSideWarps;
-constexpr int kSetupWarp = kSoftWarps, kMmaWarp = kSetupWarp + 1, kChkWarp0 = kMmaWarp + 2, kChkWarps = 1;
-constexpr int kProdWarp0 = kChkWarp0 + kChkWarps;
+constexpr int kSetupWarp = kSoftWarps, kMmaWarp = kSetupWarp + 1, kChkWarp = kMmaWarp + 2;
+constexpr int kProdWarp0 = kChkWarp + 1;
 constexpr int kProd = 2;                   // producer warps for K, and for V
-constexpr int kWarps = kProdWarp0 + 2 * kProd, kThreads = 32 * kWarps;
-constexpr int kSoftRegs = 160, kOtherRegs = 96;
-constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-static_assert(kWarps % 4 == 0 && kSoftWarps % 4 == 0, "the register split is per warpgroup");
-static_assert(kSoftWarps * kSoftRegs + (kWarps - kSoftWarps) * kOtherRegs <= kWarps * kLaunchRegs,
-              "the register split exceeds what the block is launched with");
+constexpr int kWarps = kProdWarp0 + 2 * kProd, kThreads = 32 * kWarps;   // 128 registers a thread, no split needed
+static_assert(kWarps == 16, "128 registers a thread");
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;            // lazy rescale threshold (log2 units)
@@ -226,12 +222,14 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
     }
     const Session ses = load_session(a.kv, a.n_node, a.N, s, lane == 0 ? a.err : nullptr);
     bool ok = ses.ok;
-    if (ok && a.ratio > 0 && ses.len / a.ratio > a.cap - a.N) {
+    const unsigned len_u = ok ? static_cast<unsigned>(ses.len) : 0u;       // below 2^31: it fits the pages
+    const int n_done = a.ratio > 0 ? static_cast<int>(len_u / static_cast<unsigned>(a.ratio)) : 0;
+    if (n_done > a.cap - a.N && a.ratio > 0) {
         if (lane == 0) record_error(a.err, DS4A_ERR_CAPACITY);
         ok = false;
     }
     const int row0 = kSel ? rt * a.H : rt * g.tile_rows;
-    const int n = ok ? ses.n : 0, len = ok ? static_cast<int>(ses.len) : 0;
+    const int n = ok ? ses.n : 0, len = static_cast<int>(len_u);
     int rows = n * a.H - row0;
     rows = rows < 0 ? 0 : rows;
     if (rows > (kSel ? a.H : g.tile_rows)) rows = kSel ? a.H : g.tile_rows;
@@ -274,7 +272,7 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int i = lane + 32 * x;
-            const bool c = i < n && (len + __popcll(m[x])) % a.ratio == 0;
+            const bool c = i < n && static_cast<unsigned>(len + __popcll(m[x])) % static_cast<unsigned>(a.ratio) == 0;
             done |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, c)) << (32 * x);
         }
     }
@@ -323,7 +321,7 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
         w.n = n;
         w.t0 = t0;
         w.raw_runs = (len + n - t0 + kRun - 1) / kRun;
-        w.n_vis0 = kSel ? a.n_sel : (a.ratio > 0 ? len / a.ratio : 0);
+        w.n_vis0 = kSel ? a.n_sel : n_done;
         w.comp_runs = (w.n_vis0 + kRun - 1) / kRun;
         w.n_runs = w.raw_runs + w.comp_runs;
         // the draft's rows, as far as one of the item's nodes attends any
@@ -332,7 +330,7 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
         if (kSel) {
             const int depth = __popcll(rows > 0 ? w.cmp[i0] : 1ull) - 1;
             w.n_vis = (len + depth + 1) / a.ratio;
-            w.n_done = len / a.ratio;
+            w.n_done = n_done;
         }
         w.row0 = row0;
         w.rows = rows;
@@ -363,6 +361,26 @@ DS4A_DEVINL int sel_row(const AttnTreeArgs &a, const Work &w, int j, bool record
     return static_cast<int>(a.cap) - a.N + path_node(w.cmp[w.node], (j + 1) * a.ratio - 1 - w.len);
 }
 
+// Sets the values of 16 bytes of a V row that are not finite to 0; notes them for key `slot` of
+// the poison table (-1: no row attends the key), at column col and up.
+__device__ __noinline__ void clean_chunk(Work &w, unsigned char *at, int slot, int col) {
+    uint32_t nan = 0, pi = 0, ni = 0;
+    for (int e = 0; e < 8; ++e) {
+        uint16_t &h = reinterpret_cast<uint16_t *>(at)[e];
+        if ((h & 0x7c00u) != 0x7c00u) continue;
+        if (h & 0x03ffu) nan |= 1u << e;
+        else if (h & 0x8000u) ni |= 1u << e;
+        else pi |= 1u << e;
+        h = 0;
+    }
+    if (slot < 0) return;
+    const int word = col / 32, sh = col % 32;
+    if (nan) atomicOr(&w.poison[slot][word], nan << sh);
+    if (pi) atomicOr(&w.poison[slot][4 + word], pi << sh);
+    if (ni) atomicOr(&w.poison[slot][8 + word], ni << sh);
+    w.dirty = 1;
+}
+
 // Values that are not finite, of the keys that `node` attends: into columns col .. col+31 of
 // its accumulator.
 __device__ __noinline__ uint3 poison_bits(const Work &w, int node, int word) {
@@ -391,6 +409,26 @@ DS4A_DEVINL void add_poison(const Work &w, int node, int col, uint32_t (&o)[32])
     }
 }
 
+// 4 x 4 pieces of 16 bytes among four neighbouring lanes: piece j of lane i goes to lane j's place i
+DS4A_DEVINL void transpose4(uint4 (&u)[4], int lane) {
+#pragma unroll
+    for (int b = 1; b <= 2; b <<= 1) {
+        const bool up = (lane & b) != 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & b) continue;
+            const uint4 send = up ? u[i] : u[i | b];
+            uint4 got;
+            got.x = __shfl_xor_sync(0xffffffffu, send.x, b);
+            got.y = __shfl_xor_sync(0xffffffffu, send.y, b);
+            got.z = __shfl_xor_sync(0xffffffffu, send.z, b);
+            got.w = __shfl_xor_sync(0xffffffffu, send.w, b);
+            if (up) u[i] = got;
+            else u[i | b] = got;
+        }
+    }
+}
+
 template <int D, bool kSel>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_constant__ Args g) {
     using L = Layout<D, kSel>;
@@ -414,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             tc::mbar_init(&bar.k_full[x], kProd);
             tc::mbar_init(&bar.k_empty[x], 2);
             tc::mbar_init(&bar.v_full[x], kProd);
-            tc::mbar_init(&bar.v_ok[x], kChkWarps);
+            tc::mbar_init(&bar.v_ok[x], 1);
             tc::mbar_init(&bar.v_empty[x], 2);
         }
         tc::mbar_init(&bar.q_full, 1);
@@ -429,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             tc::mbar_init(&bar.o_empty[x], kSideWarps);
             tc::mbar_init(&bar.w_full[x], 1);
             tc::mbar_init(&bar.w_empty[x], kWarps - 1);
-            tc::mbar_init(&bar.chk[x], kChkWarps);
+            tc::mbar_init(&bar.chk[x], 1);
         }
         tc::mbar_init(&bar.join, kSideWarps);
         tc::mbar_fence_init();
@@ -456,7 +494,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     const int n_items = g.n_work > static_cast<int>(blockIdx.x) ? (g.n_work - blockIdx.x - 1) / gridDim.x + 1 : 0;
 
     if (warp < kSoftWarps) {
-        tc::setmaxnreg_inc<kSoftRegs>();
         const int side = warp / kSideWarps, quad = warp & 3, r = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t col_s = tmem + lanes + kColS + side * kTK, col_o = tmem + lanes + kColO + side * kTK;
@@ -600,7 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                             tc::wait_ld();
                         }
                         if (dirty) add_poison(w, node, c * 32, o);
-                        if (valid && direct) {
+                        // With two row blocks four lanes trade 16-byte pieces, so that each writes its piece of
+                        // four rows and a store covers 64 contiguous bytes of 8 rows instead of 16 bytes of 32
+                        // (attn_r128_64x32 63 against 66 us); with one, where the item waits for it, each lane
+                        // writes its own row (attn_sel_16x16 32 against 34 us, attn_window_1x4 9.9 against 10.6).
+                        const int row4 = row - (lane & 3), piece = lane & 3;
+                        if (direct) {
+                            uint4 u[4];
 #pragma unroll
                             for (int q4 = 0; q4 < 4; ++q4) {
                                 uint32_t h[4];
@@ -608,14 +651,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                                 for (int e = 0; e < 4; ++e)
                                     h[e] = pack_half2(__uint_as_float(o[q4 * 8 + 2 * e]) * inv,
                                                       __uint_as_float(o[q4 * 8 + 2 * e + 1]) * inv);
-                                *reinterpret_cast<uint4 *>(a.out + qrow * D + c * 32 + q4 * 8) =
-                                    make_uint4(h[0], h[1], h[2], h[3]);
+                                u[q4] = make_uint4(h[0], h[1], h[2], h[3]);
                             }
-                        } else if (valid) {
+                            if (sides2) {
+                                transpose4(u, lane);
+                                uint16_t *dst = a.out + (qrow - (lane & 3)) * D + c * 32 + piece * 8;
 #pragma unroll
-                            for (int q4 = 0; q4 < 8; ++q4)
-                                *reinterpret_cast<uint4 *>(g.part + prow * D + c * 32 + q4 * 4) =
-                                    make_uint4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]);
+                                for (int q4 = 0; q4 < 4; ++q4)
+                                    if (row4 + q4 < w.rows) *reinterpret_cast<uint4 *>(dst + q4 * D) = u[q4];
+                            } else if (valid) {
+                                uint16_t *dst = a.out + qrow * D + c * 32;
+#pragma unroll
+                                for (int q4 = 0; q4 < 4; ++q4) *reinterpret_cast<uint4 *>(dst + q4 * 8) = u[q4];
+                            }
+                        } else {
+                            float *dst = g.part + (prow - (lane & 3)) * D + c * 32 + piece * 4;
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                uint4 u[4];
+#pragma unroll
+                                for (int q4 = 0; q4 < 4; ++q4)
+                                    u[q4] = make_uint4(o[hf * 16 + q4 * 4], o[hf * 16 + q4 * 4 + 1], o[hf * 16 + q4 * 4 + 2],
+                                                       o[hf * 16 + q4 * 4 + 3]);
+                                transpose4(u, lane);
+#pragma unroll
+                                for (int q4 = 0; q4 < 4; ++q4)
+                                    if (row4 + q4 < w.rows) *reinterpret_cast<uint4 *>(dst + q4 * D + hf * 16) = u[q4];
+                            }
                         }
                     }
                 }
@@ -635,15 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             if (lane == 0) tc::mbar_arrive(&bar.w_empty[it & 1]);
         }
     } else {
-        tc::setmaxnreg_dec<kOtherRegs>();
-        // one lane waits for the warp, so that warp-wide steps stay converged
+        // All lanes poll, so that the code around stays converged and its operands uniform (with one lane
+        // polling for the warp every hand-off was slower); the outcome is the same in every lane.
         auto warp_wait = [&](uint64_t *b, uint32_t parity) {
-            bool good = true;
-            if (lane == 0) good = wait(b, parity);
-            good = __shfl_sync(0xffffffffu, good, 0);
-            __syncwarp();   // what lane 0 has waited for is visible to the warp
-            ok = ok && good;
-            return good;
+            ok = __all_sync(0xffffffffu, wait(b, parity));
+            return ok;
         };
         if (warp == kSetupWarp) {
             for (int it = 0; it < n_items; ++it) {
@@ -652,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
                 __syncwarp();
             }
-        } else if (warp < kChkWarp0) {
+        } else if (warp < kChkWarp) {
             // The whole warp runs this, converged, and one elected lane issues: the operands are then
             // warp-uniform registers, which the instruction wants (issued from a lane == 0 branch, eight
             // products took 570 cycles to issue, about as long as the tensor core needs for them).
@@ -660,24 +718,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             constexpr uint32_t kIdO = tc::idesc_f16_f32(kTK, D, false, true);
             const uint32_t side = warp - kMmaWarp;
             uint32_t n_t = 0, n_c = 0, n_o = 0;                   // tiles; chunks of this side; items with tiles
-            auto wait_all = [&](uint64_t *b, uint32_t parity) {
-                ok = __all_sync(0xffffffffu, wait(b, parity));
-                return ok;
-            };
-            const uint32_t k_s = tc::smem_u32(smem + L::k), v_s = tc::smem_u32(smem + L::v);
+            // a descriptor holds the address in 16-byte units in its low bits: steps are additions
+            const uint64_t q_d = tc::desc_sw128(tc::smem_u32(smem + L::q), 16, 1024);
+            const uint64_t k_d = tc::desc_sw128(tc::smem_u32(smem + L::k), 16, 1024);
+            const uint64_t v_d = tc::desc_sw128(tc::smem_u32(smem + L::v), kAtomBytes, 1024);
+            constexpr int kTile16 = L::tile / 16;
             const uint32_t d_s = tmem + kColS + side * kTK, d_o = tmem + kColO + side * kTK;
             for (int it = 0; it < n_items && ok; ++it) {
                 const Work &w = works[it & 1];
-                if (!wait_all(&bar.w_full[it & 1], it >> 1)) break;
+                if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
                 const int tile0 = __shfl_sync(0xffffffffu, w.tile0, 0), n_runs = __shfl_sync(0xffffffffu, w.n_runs, 0);
                 const int tiles = __shfl_sync(0xffffffffu, w.tile1, 0) - tile0;
                 const bool sides2 = __shfl_sync(0xffffffffu, w.sides2, 0) != 0;
                 const int first = sides2 ? 0 : static_cast<int>(side), by = sides2 ? 1 : 2;   // this side's tiles
-                const uint32_t qa = tc::smem_u32(smem + L::q) + (sides2 ? side : 0) * L::tile;
-                if (!wait_all(&bar.q_full, it)) break;
+                const uint64_t qd = q_d + (sides2 ? side : 0) * kTile16;
+                if (!warp_wait(&bar.q_full, it)) break;
                 if (first >= tiles) {                             // nothing for this side: every phase is seen all the same
                     if (lane == 0) tc::mbar_arrive(&bar.q_empty);
-                    if (tiles > 0 && n_o > 0) wait_all(&bar.o_empty[side], n_o - 1);
+                    if (tiles > 0 && n_o > 0) warp_wait(&bar.o_empty[side], n_o - 1);
                 }
                 // the next chunk to score: tile st_t, half st_h, buffer st_n & 1
                 int st_t = first, st_h = 0;
@@ -690,14 +748,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 auto issue_s = [&]() {                            // behind wait_k
                     if (st_t >= tiles) return;
                     const uint32_t stage = (n_t + st_t) % kNS, buf = st_n & 1u;
-                    const uint32_t kb = k_s + stage * L::tile + st_h * (kCK * 128), d = d_s + buf * kCK;
+                    const uint64_t kd = k_d + stage * kTile16 + st_h * (kCK * 128 / 16);
+                    const uint32_t d = d_s + buf * kCK;
                     const bool tile_end = st_h + 1 == tile_chunks(n_runs, tile0 + st_t);
                     const bool last = tile_end && st_t + by >= tiles;
                     if (tc::elect()) {
 #pragma unroll
                         for (int x = 0; x < D / 16; ++x)
-                            tc::mma_f16(d, tc::desc_sw128(qa + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024),
-                                        tc::desc_sw128(kb + (x / 4) * kAtomBytes + (x % 4) * 32, 16, 1024), kIdS, x > 0);
+                            tc::mma_f16(d, qd + (x / 4) * (kAtomBytes / 16) + (x % 4) * 2,
+                                        kd + (x / 4) * (kAtomBytes / 16) + (x % 4) * 2, kIdS, x > 0);
                         tc::commit(&bar.s_full[side][buf]);
                         if (tile_end) {
                             tc::commit(&bar.k_empty[stage]);
@@ -734,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                             if (t == first && n_o > 0) good = wait(&bar.o_empty[side], n_o - 1) && good;
                             good = wait(&bar.v_ok[stage], vt / kNS) && good;
                         }
-                        const uint32_t vb = v_s + stage * L::tile + c * (kCK / 16 * 2048), pa = d_s + buf * kCK;
+                        const uint64_t vd = v_d + stage * kTile16 + c * (kCK / 16 * 128);
+                        const uint32_t pa = d_s + buf * kCK;
                         good = wait(&bar.p_full[side][buf], n_c >> 1) && good;
                         ok = __all_sync(0xffffffffu, good);
                         if (!ok) break;
@@ -743,8 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                         if (tc::elect()) {
 #pragma unroll
                             for (int x = 0; x < kCK / 16; ++x)
-                                tc::mma_f16_ts(d_o, pa + x * 8, tc::desc_sw128(vb + x * 2048, kAtomBytes, 1024), kIdO,
-                                               more || x > 0);
+                                tc::mma_f16_ts(d_o, pa + x * 8, vd + x * 128, kIdO, more || x > 0);
                             if (tile_end) {
                                 tc::commit(&bar.v_empty[stage]);
                                 if (!sides2) tc::commit(&bar.v_empty[stage]);
@@ -763,7 +822,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             __syncwarp();
         } else if (warp < kProdWarp0) {
             // ---------------- checkers ----------------
-            const int ct = (warp - kChkWarp0) * 32 + lane;
             uint32_t n_v = 0;
             for (int it = 0; it < n_items; ++it) {
                 Work &w = works[it & 1];
@@ -780,45 +838,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                             if (v >= w.n_runs) break;                                       // zeros
                             const uint32_t any = run_bits<kSel>(w, v, w.lo_min, w.any_raw, w.any_cmp, inf);
                             const uint32_t all = run_bits<kSel>(w, v, w.lo_max, w.all_raw, w.all_cmp, inf);
-                            if (all == 0xffffu || (kSel && v >= w.raw_runs)) continue;
-                            // 16-byte chunks of the run: 16 rows x 8 per atom
-#pragma unroll 1
-                            for (int x = ct; x < kRun * 8 * kAtoms; x += kChkWarps * 32) {
-                                const int atom = x / (kRun * 8), key = (x / 8) % kRun, ch = x % 8;
-                                uint4 *ptr = reinterpret_cast<uint4 *>(vt + atom * kAtomBytes +
-                                                                       tc::sw128_chunk(r * kRun + key, ch));
-                                const uint4 q = *ptr;
+                            if ((all & 0xffffu) == 0xffffu || (kSel && v >= w.raw_runs)) continue;
+                            // 16 rows x 8 chunks of 16 bytes per atom, the loads of a lane all in flight
+#pragma unroll
+                            for (int half = 0; half < kAtoms; ++half) {
+                                uint4 q[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    q[x] = *reinterpret_cast<const uint4 *>(
+                                        vt + half * kAtomBytes + tc::sw128_chunk(r * kRun + x * 4 + lane / 8, lane % 8));
                                 auto odd = [](uint32_t u) {   // a half with all exponent bits set
                                     const uint32_t z = (u & 0x7c007c00u) ^ 0x7c007c00u;
                                     return (z - 0x00010001u) & ~z & 0x80008000u;
                                 };
-                                if (!(odd(q.x) | odd(q.y) | odd(q.z) | odd(q.w)) || ((all >> key) & 1u)) continue;
-                                uint16_t hv[8];
-                                *reinterpret_cast<uint4 *>(hv) = q;
-                                uint32_t nan = 0, pi = 0, ni = 0;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    if ((hv[e] & 0x7c00u) != 0x7c00u) continue;
-                                    if (hv[e] & 0x03ffu) nan |= 1u << e;
-                                    else if (hv[e] & 0x8000u) ni |= 1u << e;
-                                    else pi |= 1u << e;
-                                    hv[e] = 0;
+                                for (int x = 0; x < 4; ++x) {
+                                    const int key = x * 4 + lane / 8, ch = lane % 8;
+                                    if (!(odd(q[x].x) | odd(q[x].y) | odd(q[x].z) | odd(q[x].w)) || ((all >> key) & 1u))
+                                        continue;
+                                    int slot = -1;   // a key that some rows attend and some do not
+                                    if ((any >> key) & 1u) {
+                                        if (v < w.raw_runs) {
+                                            const int tk = w.t0 + v * kRun + key;
+                                            slot = tk >= w.len ? tk - w.len : kEdge + tk - w.lo_min;
+                                        } else {
+                                            slot = kMaxNodes + (v - w.raw_runs - w.comp_runs) * kRun + key;
+                                        }
+                                    }
+                                    clean_chunk(w, vt + half * kAtomBytes + tc::sw128_chunk(r * kRun + key, ch), slot,
+                                                half * 64 + ch * 8);
+                                    wrote = true;
                                 }
-                                *ptr = *reinterpret_cast<uint4 *>(hv);
-                                wrote = true;
-                                if (!((any >> key) & 1u)) continue;
-                                int slot;            // a key that some rows attend and some do not
-                                if (v < w.raw_runs) {
-                                    const int tk = w.t0 + v * kRun + key;
-                                    slot = tk >= w.len ? tk - w.len : kEdge + tk - w.lo_min;
-                                } else {
-                                    slot = kMaxNodes + (v - w.raw_runs - w.comp_runs) * kRun + key;
-                                }
-                                const int word = atom * 2 + ch / 4, sh = (ch % 4) * 8;
-                                if (nan) atomicOr(&w.poison[slot][word], nan << sh);
-                                if (pi) atomicOr(&w.poison[slot][4 + word], pi << sh);
-                                if (ni) atomicOr(&w.poison[slot][8 + word], ni << sh);
-                                w.dirty = 1;
                             }
                         }
                         if (__any_sync(0xffffffffu, wrote)) tc::fence_proxy_async();
