@@ -96,7 +96,7 @@ struct Bars {
     uint64_t pv[2];                        // a product with V is done
     uint64_t o_full[2], o_empty[2];        // the item's last one; the accumulator has been read
     uint64_t w_full[2], w_empty[2], chk[2];
-    uint64_t join;                         // side 1 has posted its sums
+    uint64_t join[2];                      // side x has posted its references and sums
 };
 
 template <int D, bool kSel>
@@ -111,8 +111,8 @@ struct Layout {
     // on are issued only when the softmax of this one is done.
     static constexpr int info = work + 2 * static_cast<int>(sizeof(Work));
     static constexpr int whole = info + 2 * kInfo * kRuns * 2;
-    static constexpr int ml = whole + kInfo * kRuns;                  // float2 [128] side 1's (reference, sum)
-    static constexpr int bars = ml + kTK * 8;
+    static constexpr int ml = whole + kInfo * kRuns;           // float2 [2 sides][128] (reference, sum)
+    static constexpr int bars = ml + 2 * kTK * 8;
     static constexpr int end = bars + static_cast<int>(sizeof(Bars));
     static constexpr size_t bytes = end + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
@@ -128,6 +128,7 @@ struct Args {
     int *active;                                   // [slots]
     int B, n_split, min_tiles, row_tiles, tile_rows, item_rows, n_work;
     int pool_oob, comp_oob;                        // rows of the maps: the zero-fill rows
+    uint32_t h_mul;                                // node_of
 };
 
 struct JoinArgs {
@@ -138,6 +139,9 @@ struct JoinArgs {
     uint16_t *out;
     int B, N, H, n_split, row_tiles, tile_rows, item_rows;
 };
+
+// row / H of a session's row (below 64 * 64 + 256) without a division: h_mul = ceil(2^20 / H)
+DS4A_DEVINL int node_of(const Args &g, int row) { return static_cast<int>((static_cast<uint32_t>(row) * g.h_mul) >> 20); }
 
 DS4A_DEVINL float ex2(float x) {
     float y;
@@ -192,9 +196,9 @@ struct ItemId {
 };
 DS4A_DEVINL ItemId item_id(const Args &g, int item) {
     ItemId id;
-    const int x = item / g.n_split;
+    const unsigned x = g.n_split > 1 ? static_cast<unsigned>(item) / static_cast<unsigned>(g.n_split) : item;
     id.split = item - x * g.n_split;
-    id.rt = x / g.B;
+    id.rt = g.B > 1 ? x / static_cast<unsigned>(g.B) : x;
     id.s = x - id.rt * g.B;
     return id;
 }
@@ -266,7 +270,7 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
         p[1] = np[1];
     }
     // window: a drafted ancestor is in it if it is among the path's last `window` members
-    const int i0 = rows > 0 ? row0 / a.H : 0, i1 = rows > 0 ? (row0 + rows - 1) / a.H : -1;
+    const int i0 = rows > 0 ? node_of(g, row0) : 0, i1 = rows > 0 ? node_of(g, row0 + rows - 1) : -1;
     unsigned long long done = 0;                     // nodes that complete a row
     if (a.ratio > 0 && !kSel) {
 #pragma unroll
@@ -336,9 +340,13 @@ __device__ void make_work(const Args &g, int item, Work &w, int lane) {
         w.rows = rows;
         w.sides2 = rows > kTK;
         const int tiles = rows > 0 ? (w.n_runs + kRuns - 1) / kRuns : 0;
-        int chunk = (tiles + g.n_split - 1) / g.n_split;
-        if (chunk < g.min_tiles) chunk = g.min_tiles;
-        w.active = (tiles + chunk - 1) / chunk;
+        int chunk = tiles, active = tiles > 0;
+        if (g.n_split > 1) {
+            chunk = static_cast<unsigned>(tiles + g.n_split - 1) / static_cast<unsigned>(g.n_split);
+            if (chunk < g.min_tiles) chunk = g.min_tiles;
+            active = static_cast<unsigned>(tiles + chunk - 1) / static_cast<unsigned>(chunk);
+        }
+        w.active = active;
         w.split = split;
         w.slot = slot;
         w.tile0 = min(tiles, split * chunk);
@@ -464,12 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             }
             tc::mbar_init(&bar.pv[x], 1);
             tc::mbar_init(&bar.o_full[x], 1);
-            tc::mbar_init(&bar.o_empty[x], kSideWarps);
+            tc::mbar_init(&bar.o_empty[x], 2 * kSideWarps);
+            tc::mbar_init(&bar.join[x], kSideWarps);
             tc::mbar_init(&bar.w_full[x], 1);
             tc::mbar_init(&bar.w_empty[x], kWarps - 1);
             tc::mbar_init(&bar.chk[x], 1);
         }
-        tc::mbar_init(&bar.join, kSideWarps);
         tc::mbar_fence_init();
     }
     for (int x = tid; x < kPoison * 3; x += kThreads) {
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             if (!__all_sync(0xffffffffu, wait(&bar.w_full[it & 1], it >> 1))) break;
             const int t0 = w.tile0, t1 = w.tile1, sides2 = w.sides2, n_runs = w.n_runs;
             const int row = (sides2 ? side * kTK : 0) + r;        // row in the item
-            const int node = min(kMaxNodes - 1, (w.row0 + row) / a.H);
+            const int node = min(kMaxNodes - 1, node_of(g, w.row0 + row));
             float m = -INFINITY, l = 0.f;
             bool first = true;
             for (int t = sides2 ? t0 : t0 + side; t < t1; t += sides2 ? 1 : 2) {
@@ -595,40 +603,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             if (have) {
                 wait(&bar.o_full[side], n_o++);
                 if (joined) {
-                    if (side == 1) {
-                        s_ml[r] = make_float2(m, l);
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&bar.join);
-                    } else {
-                        wait(&bar.join, n_join);
-                    }
-                    ++n_join;
+                    s_ml[side * kTK + r] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.join[side]);
+                    wait(&bar.join[side ^ 1], n_join++);
                 }
                 tc::fence_after_sync();
-                if (sides2 || side == 0) {
+                {
+                    // a joined item's sides finish half of the columns each: the weights of this side's and the
+                    // other side's accumulator
                     float wa = 1.f, wb = 0.f;
                     if (joined) {
-                        const float2 o = s_ml[r];
+                        const float2 o = s_ml[(side ^ 1) * kTK + r];
                         const float mm = fmaxf(m, o.x), rf = mm == -INFINITY ? 0.f : mm;
                         wa = ex2(m - rf);
                         wb = ex2(o.x - rf);
                         l = l * wa + o.y * wb;
                         m = mm;
                     }
+                    const uint32_t col_other = tmem + lanes + kColO + (side ^ 1) * kTK;
+                    const int c0 = joined && side == 1 ? D / 64 : 0, c1 = joined && side == 0 ? D / 64 : D / 32;
                     wait(&bar.chk[it & 1], it >> 1);
                     const bool valid = row < w.rows, direct = w.active == 1;
                     const int dirty = w.dirty;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     const long long qrow = (static_cast<long long>(w.s) * a.N) * a.H + w.row0 + row;
                     const long long prow = (static_cast<long long>(w.slot) * g.n_split + w.split) * g.tile_rows + row;
-                    if (!direct && valid) g.part_ml[prow] = make_float2(m, l);
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {             // 32 columns at a time
+                    if (!direct && valid && c0 == 0) g.part_ml[prow] = make_float2(m, l);
+#pragma unroll 2
+                    for (int c = c0; c < c1; ++c) {                // 32 columns at a time
                         uint32_t o[32];
                         tc::ld_x32(col_o + c * 32, o);
                         if (joined) {
                             uint32_t o2[32];
-                            tc::ld_x32(col_o + kTK + c * 32, o2);
+                            tc::ld_x32(col_other + c * 32, o2);
                             tc::wait_ld();
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
@@ -681,15 +689,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                         }
                     }
                 }
-                // the accumulators may be overwritten; with one row block side 0 has read both
+                // Both accumulators may be overwritten when both sides' warps have read them, each warp counting
+                // once for each; a side that has an accumulator, or the item, to itself counts for the other too.
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if (sides2) {
+                    for (int x = 0; x < 2; ++x) {
                         tc::mbar_arrive(&bar.o_empty[side]);
-                    } else if (side == 0) {
-                        tc::mbar_arrive(&bar.o_empty[0]);
-                        tc::mbar_arrive(&bar.o_empty[1]);
+                        if (!sides2 && (!joined || x == 0)) tc::mbar_arrive(&bar.o_empty[side ^ 1]);
+                        if (joined) break;
                     }
                 }
             }
@@ -901,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             // the rows of one tile: this lane's run, this lane's four list entries (the raw table entries and
             // list entries of the next tile are loaded while this one waits for its stage)
             struct Rows {
-                int v, gv, page;
+                int v, gv, page, off;
                 int4 e;
             };
             int st = 0;
@@ -933,7 +941,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     Rows r;
                     r.v = t * kRuns + run;
                     r.gv = t * kRuns + grun;
-                    r.page = r.v < raw_runs ? __ldg(table + static_cast<unsigned>(w.t0 + r.v * kRun) / static_cast<unsigned>(a.kv.page)) : 0;
+                    r.page = r.off = 0;
+                    if (r.v < raw_runs) {
+                        const unsigned slot = w.t0 + r.v * kRun, pg = slot / static_cast<unsigned>(a.kv.page);
+                        r.page = __ldg(table + pg);
+                        r.off = static_cast<int>(slot - pg * a.kv.page);
+                    }
                     r.e = make_int4(-1, -1, -1, -1);
                     if (kSel && r.gv >= raw_runs && r.gv < n_runs) {
                         const int e0 = (r.gv - raw_runs) * kRun + (group & 3) * 4;
@@ -953,8 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     bool raw_run = true, readable = true;
                     if (r.v < raw_runs) {
                         readable = r.page >= 0 && r.page < a.kv.n_pages;
-                        const unsigned slot = w.t0 + r.v * kRun;
-                        if (readable) row = r.page * a.kv.page + static_cast<int>(slot % static_cast<unsigned>(a.kv.page));
+                        if (readable) row = r.page * a.kv.page + r.off;
                         else if (lane < kRunsPer) record_error(a.err, DS4A_ERR_DEVICE_INDEX);
                     } else if (!kSel && r.v < n_runs) {
                         raw_run = false;
@@ -1174,6 +1186,7 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
     g.tile_rows = p.tile_rows;
     g.item_rows = p.item_rows;
     g.n_work = static_cast<int>(slots * p.n_split);
+    g.h_mul = ((1u << 20) + static_cast<uint32_t>(a.H) - 1) / static_cast<uint32_t>(a.H);
     g.pool_oob = static_cast<int>(pool_rows);
     g.comp_oob = static_cast<int>(comp_rows);
     unsigned char *ws = static_cast<unsigned char *>(a.ws);
