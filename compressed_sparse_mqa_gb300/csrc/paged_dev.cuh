@@ -52,7 +52,7 @@ DS4A_DEVINL Session load_session(const PagedKV &kv, const int32_t *n_node, int N
 // Ancestor masks of a session's n nodes into mask[kMaxNodes] (shared memory), each node
 // with its own bit; every thread of the block calls this (blockDim.x >= 64).  parent
 // nullptr: a chain.  Pointer jumping: after round r a node's mask holds its nearest 2^r
-// members of the path and ptr its 2^r-th ancestor, so six rounds reach all 64.
+// members of the path and ptr its 2^r-th ancestor, so log2(n) rounds reach all.
 // Returns false (recorded) if a parent is not an earlier node or -1.
 DS4A_DEVINL bool tree_masks(const int32_t *parent, int n, unsigned long long *mask, int *ptr, unsigned int *err) {
     const int i = threadIdx.x;
@@ -71,7 +71,7 @@ DS4A_DEVINL bool tree_masks(const int32_t *parent, int n, unsigned long long *ma
         ptr[i] = p;
     }
     good = __syncthreads_and(good);
-    for (int round = 0; round < 6; ++round) {
+    for (int span = 1; span < n; span *= 2) {
         unsigned long long m = 0;
         int p = -1;
         if (i < kMaxNodes) {

@@ -16,91 +16,122 @@ namespace {
 constexpr int kTreeThreads = 256;
 constexpr int kTreeWarps = kTreeThreads / 32;
 
-// Weights of m path tokens, applied in order to a running state (max, sum): on return
-// s_e[t] is token t's exp(s_t - max after it), s_c[t] the factor that rescales what came
-// before it; max and sum are the state after the last.  resume: a state precedes them.
-DS4A_DEVINL void chain_weights(const float *s_score, int m, bool resume, float &mx, float &sum, float *s_e, float *s_c) {
-    for (int t = 0; t < m; ++t) {
-        const float m_new = fmaxf(mx, s_score[t]);
-        const bool first = !resume && t == 0;
-        const float c_old = first ? 0.f : __expf(mx - m_new);
-        const float e = __expf(s_score[t] - m_new);
-        sum = __fadd_rn(__fmul_rn(c_old, sum), e);
-        mx = m_new;
-        if (threadIdx.x == 0) {
-            s_e[t] = e;
-            s_c[t] = c_old;
-        }
-    }
-}
-
-// Scores w . k of the m path tokens at pool rows s_row (-1: unreadable, score 0): one
-// warp per token, the lanes over 8-dim chunks as in the compressor.
+// Scores w . k of the m path tokens at pool rows s_row (-1: unreadable, score 0): one warp per
+// token, the lanes over 8-dim chunks as in the compressor.  A warp's tokens (up to kMaxNodes /
+// kTreeWarps) are all loaded before the first is summed.
 DS4A_DEVINL void path_scores(const PagedKV &kv, const float *w, const long long *s_row, int m, float *s_score) {
+    constexpr int kPer = kMaxNodes / kTreeWarps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int t = warp; t < m; t += kTreeWarps) {
-        float acc = 0.f;
-        if (s_row[t] >= 0) {
-            for (int ch = lane; ch < kv.D / 8; ch += 32) {
-                const uint4 raw = *reinterpret_cast<const uint4 *>(kv.k + s_row[t] * kv.D + ch * 8);
-                const uint16_t *h = reinterpret_cast<const uint16_t *>(&raw);
+    uint4 raw[kPer];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc = fmaf(w[ch * 8 + e], h2f(h[e]), acc);
-            }
+    for (int x = 0; x < kPer; ++x) {
+        const int t = warp + x * kTreeWarps;
+        raw[x] = make_uint4(0, 0, 0, 0);
+        if (t < m && s_row[t] >= 0 && lane < kv.D / 8)
+            raw[x] = *reinterpret_cast<const uint4 *>(kv.k + s_row[t] * kv.D + lane * 8);
+    }
+    float wl[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wl[e] = lane < kv.D / 8 ? w[lane * 8 + e] : 0.f;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+        const int t = warp + x * kTreeWarps;
+        if (t >= m) break;
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(&raw[x]);
+        float acc = 0.f;
+        if (lane < kv.D / 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc = fmaf(wl[e], h2f(h[e]), acc);
         }
         acc = warp_sum(acc);
         if (lane == 0) s_score[t] = acc;
     }
 }
 
-// Applies the chain to column d (0 .. 2D-1: K dims, then V dims) of the weighted sums.
+// Weights of m path tokens, applied in order to a running state (max, sum): on return
+// s_e[t] is token t's exp(s_t - max after it), s_c[t] the factor that rescales what came
+// before it; mx and sum are the state after the last.  resume: a state precedes them.  The
+// maxima do not depend on the sums, so thread t takes token t; only the sum is a chain.
+DS4A_DEVINL void chain_weights(const float *s_score, int m, bool resume, float &mx, float &sum, float *s_e, float *s_c) {
+    const int t = threadIdx.x;
+    if (t < m) {
+        float before = mx;
+        for (int u = 0; u < t; ++u) before = fmaxf(before, s_score[u]);
+        const float after = fmaxf(before, s_score[t]);
+        s_c[t] = !resume && t == 0 ? 0.f : __expf(before - after);
+        s_e[t] = __expf(s_score[t] - after);
+    }
+    __syncthreads();
+    for (int u = 0; u < m; ++u) {
+        mx = fmaxf(mx, s_score[u]);
+        sum = __fadd_rn(__fmul_rn(s_c[u], sum), s_e[u]);
+    }
+}
+
+// Applies the chain to column d (0 .. 2D-1: K dims, then V dims) of the weighted sums, eight
+// tokens' loads at a time.
 DS4A_DEVINL float chain_column(const PagedKV &kv, const long long *s_row, const float *s_e, const float *s_c, int m,
                                int d, float acc) {
     const uint16_t *src = d < kv.D ? kv.k + d : kv.v + (d - kv.D);
-    for (int t = 0; t < m; ++t) {
-        const float x = s_row[t] >= 0 ? h2f(src[s_row[t] * kv.D]) : 0.f;
-        acc = fmaf(s_e[t], x, s_c[t] * acc);
+    for (int t0 = 0; t0 < m; t0 += 8) {
+        uint16_t x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = t0 + u < m && s_row[t0 + u] >= 0 ? src[s_row[t0 + u] * kv.D] : uint16_t(0);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (t0 + u < m) acc = fmaf(s_e[t0 + u], h2f(x[u]), s_c[t0 + u] * acc);
     }
     return acc;
 }
 
-// One CTA per node: completes a row or leaves.
+// gridDim.x CTAs per session take its completing nodes in turn.
 __global__ void __launch_bounds__(kTreeThreads) compress_tree_kernel(CompressTreeArgs a) {
     __shared__ unsigned long long s_mask[kMaxNodes];
     __shared__ int s_ptr[kMaxNodes];
     __shared__ long long s_row[kMaxNodes];
     __shared__ float s_score[kMaxNodes], s_e[kMaxNodes], s_c[kMaxNodes];
-    const int tid = threadIdx.x, i = blockIdx.x, s = blockIdx.y;
+    __shared__ uint32_t s_done[2];
+    const int tid = threadIdx.x, s = blockIdx.y;
     pdl_wait();
     pdl_trigger();
-    const Session ses = load_session(a.kv, a.n_node, a.N, s, a.err);
-    if (!ses.ok || i >= ses.n) return;
+    const Session ses = load_session(a.kv, a.n_node, a.N, s, tid == 0 ? a.err : nullptr);
+    if (!ses.ok) return;
     if (!tree_masks(a.parent ? a.parent + static_cast<long long>(s) * a.N : nullptr, ses.n, s_mask, s_ptr, a.err))
         return;
-    const unsigned long long path = s_mask[i];
-    const int cnt = __popcll(path);
-    const long long end = ses.len + cnt;
-    if (end % a.ratio != 0) return;
-    const long long start = end - a.ratio > ses.len ? end - a.ratio : ses.len;   // the block's first drafted token
-    const bool resume = start == ses.len && ses.len % a.ratio != 0;
-    const int d0 = static_cast<int>(start - ses.len), m = cnt - d0;
-    if (tid < m)
-        s_row[tid] = pool_row(a.kv, a.kv.table + static_cast<long long>(s) * a.kv.max_pages,
-                              static_cast<unsigned>(ses.len + path_node(path, d0 + tid)), a.err);
+    if (tid < kMaxNodes) {
+        const bool c = tid < ses.n && (ses.len + __popcll(s_mask[tid])) % a.ratio == 0;
+        const uint32_t b = __ballot_sync(0xffffffffu, c);
+        if ((tid & 31) == 0) s_done[tid / 32] = b;
+    }
     __syncthreads();
-    path_scores(a.kv, a.w, s_row, m, s_score);
-    __syncthreads();
-    const int D = a.kv.D;
-    const float *st = a.state + static_cast<long long>(s) * (2 + 2 * D);
-    float mx = -INFINITY, sum = 0.f;
-    if (resume) { mx = st[0]; sum = st[1]; }
-    chain_weights(s_score, m, resume, mx, sum, s_e, s_c);
-    __syncthreads();
-    const long long row = (static_cast<long long>(s) * a.cap + a.cap - a.N + i) * D;
-    for (int d = tid; d < 2 * D; d += kTreeThreads) {
-        const float acc = chain_column(a.kv, s_row, s_e, s_c, m, d, resume ? st[2 + d] : 0.f);
-        const float inv = 1.f / sum;
-        (d < D ? a.comp_k + row + d : a.comp_v + row + d - D)[0] = f2h(acc * inv);
+    const unsigned long long done = static_cast<unsigned long long>(s_done[1]) << 32 | s_done[0];
+    const int n_done = __popcll(done), D = a.kv.D;
+    for (int k = blockIdx.x; k < n_done; k += gridDim.x) {
+        const int i = path_node(done, k);                                            // the k-th completing node
+        const unsigned long long path = s_mask[i];
+        const int cnt = __popcll(path);
+        const long long end = ses.len + cnt;
+        const long long start = end - a.ratio > ses.len ? end - a.ratio : ses.len;   // the block's first drafted token
+        const bool resume = start == ses.len && ses.len % a.ratio != 0;
+        const int d0 = static_cast<int>(start - ses.len), m = cnt - d0;
+        if (tid < m)
+            s_row[tid] = pool_row(a.kv, a.kv.table + static_cast<long long>(s) * a.kv.max_pages,
+                                  static_cast<unsigned>(ses.len + path_node(path, d0 + tid)), a.err);
+        __syncthreads();
+        path_scores(a.kv, a.w, s_row, m, s_score);
+        __syncthreads();
+        const float *st = a.state + static_cast<long long>(s) * (2 + 2 * D);
+        float mx = -INFINITY, sum = 0.f;
+        if (resume) { mx = st[0]; sum = st[1]; }
+        chain_weights(s_score, m, resume, mx, sum, s_e, s_c);
+        __syncthreads();
+        const long long row = (static_cast<long long>(s) * a.cap + a.cap - a.N + i) * D;
+        for (int d = tid; d < 2 * D; d += kTreeThreads) {
+            const float acc = chain_column(a.kv, s_row, s_e, s_c, m, d, resume ? st[2 + d] : 0.f);
+            const float inv = 1.f / sum;
+            (d < D ? a.comp_k + row + d : a.comp_v + row + d - D)[0] = f2h(acc * inv);
+        }
+        __syncthreads();
     }
 }
 
@@ -138,8 +169,44 @@ __global__ void __launch_bounds__(kTreeThreads) commit_tree_kernel(CommitTreeArg
     }
     if (!__syncthreads_and(good)) return;
 
-    // the state of the block left open, from its committed state and its path tokens (read
-    // before any row moves)
+    // Path rows to consecutive slots: all of them are read (here, beside what follows) before the
+    // first is written, since a destination may be another path node's slot.
+    constexpr int kMove = kMaxNodes * 128 / 8 / kTreeThreads;   // 16-byte chunks a thread, D <= 128
+    const int chunks = D / 8, chunk_shift = D == 128 ? 4 : 3;
+    uint4 rk[kMove], rv[kMove];
+#pragma unroll
+    for (int m = 0; m < kMove; ++m) {
+        const int w = tid + m * kTreeThreads;
+        if (w < cnt * chunks) {
+            const long long at = s_src[w >> chunk_shift] * D + (w & (chunks - 1)) * 8;
+            rk[m] = *reinterpret_cast<const uint4 *>(a.kv.k + at);
+            rv[m] = *reinterpret_cast<const uint4 *>(a.kv.v + at);
+        }
+    }
+    // rows completed on the path, from the draft's rows to their place
+    if (a.ratio > 0) {
+        const long long base = static_cast<long long>(s) * a.cap, r0 = ses.len / a.ratio;
+        const int rows = static_cast<int>(end / a.ratio - r0);
+        for (int w = tid; w < rows << chunk_shift; w += kTreeThreads) {
+            const int r = w >> chunk_shift, ch = (w & (chunks - 1)) * 8;
+            const int node = path_node(path, static_cast<int>((r0 + r + 1) * a.ratio - 1 - ses.len));
+            const long long from = (base + a.cap - a.N + node) * D + ch, to = (base + r0 + r) * D + ch;
+            const uint4 k = *reinterpret_cast<const uint4 *>(a.comp_k + from);
+            const uint4 v = *reinterpret_cast<const uint4 *>(a.comp_v + from);
+            *reinterpret_cast<uint4 *>(a.comp_k + to) = k;
+            *reinterpret_cast<uint4 *>(a.comp_v + to) = v;
+        }
+        if (a.k_idx) {
+            const int ich = a.d_idx / 8;
+            for (int w = tid; w < rows * ich; w += kTreeThreads) {
+                const int r = w / ich, ch = (w - r * ich) * 8;
+                const int node = path_node(path, static_cast<int>((r0 + r + 1) * a.ratio - 1 - ses.len));
+                *reinterpret_cast<uint4 *>(a.k_idx + (base + r0 + r) * a.d_idx + ch) =
+                    *reinterpret_cast<const uint4 *>(a.k_idx + (base + a.cap - a.N + node) * a.d_idx + ch);
+            }
+        }
+    }
+    // the state of the block left open, from its committed state and its path tokens
     if (a.ratio > 0 && end % a.ratio != 0) {
         const long long blk = end - end % a.ratio;
         const long long start = blk > ses.len ? blk : ses.len;
@@ -161,43 +228,13 @@ __global__ void __launch_bounds__(kTreeThreads) commit_tree_kernel(CommitTreeArg
         }
     }
     __syncthreads();
-
-    // path rows to consecutive slots: all of them are read before the first is written,
-    // since a destination may be another path node's slot
-    constexpr int kMove = kMaxNodes * 128 / 8 / kTreeThreads;   // 16-byte chunks a thread, D <= 128
-    const int chunks = D / 8;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        uint16_t *pool = which ? a.kv.v : a.kv.k;
-        uint4 r[kMove];
-#pragma unroll
-        for (int m = 0; m < kMove; ++m) {
-            const int w = tid + m * kTreeThreads;
-            if (w < cnt * chunks) r[m] = *reinterpret_cast<const uint4 *>(pool + s_src[w / chunks] * D + w % chunks * 8);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int m = 0; m < kMove; ++m) {
-            const int w = tid + m * kTreeThreads;
-            if (w < cnt * chunks) *reinterpret_cast<uint4 *>(pool + s_dst[w / chunks] * D + w % chunks * 8) = r[m];
-        }
-    }
-    // rows completed on the path, from the draft's rows to their place
-    if (a.ratio > 0) {
-        const long long base = static_cast<long long>(s) * a.cap;
-        for (long long r = ses.len / a.ratio; r < end / a.ratio; ++r) {
-            const int node = path_node(path, static_cast<int>((r + 1) * a.ratio - 1 - ses.len));
-            const long long from = base + a.cap - a.N + node, to = base + r;
-            for (int ch = tid; ch < chunks; ch += kTreeThreads) {
-                *reinterpret_cast<uint4 *>(a.comp_k + to * D + ch * 8) =
-                    *reinterpret_cast<const uint4 *>(a.comp_k + from * D + ch * 8);
-                *reinterpret_cast<uint4 *>(a.comp_v + to * D + ch * 8) =
-                    *reinterpret_cast<const uint4 *>(a.comp_v + from * D + ch * 8);
-            }
-            if (a.k_idx)
-                for (int ch = tid; ch < a.d_idx / 8; ch += kTreeThreads)
-                    *reinterpret_cast<uint4 *>(a.k_idx + to * a.d_idx + ch * 8) =
-                        *reinterpret_cast<const uint4 *>(a.k_idx + from * a.d_idx + ch * 8);
+    for (int m = 0; m < kMove; ++m) {
+        const int w = tid + m * kTreeThreads;
+        if (w < cnt * chunks) {
+            const long long at = s_dst[w >> chunk_shift] * D + (w & (chunks - 1)) * 8;
+            *reinterpret_cast<uint4 *>(a.kv.k + at) = rk[m];
+            *reinterpret_cast<uint4 *>(a.kv.v + at) = rv[m];
         }
     }
     if (tid == 0) a.len_out[s] = end;                      // after the last read of len: it may be len itself
@@ -206,7 +243,10 @@ __global__ void __launch_bounds__(kTreeThreads) commit_tree_kernel(CommitTreeArg
 }  // namespace
 
 cudaError_t launch_compress_tree(const CompressTreeArgs &a, int B, const Ctx &c) {
-    return launch(compress_tree_kernel, dim3(static_cast<unsigned>(a.N), static_cast<unsigned>(B)),
+    // CTAs per session: up to one a node, about four per SM in all
+    int per = 4 * c.num_sms / B;
+    per = per < 1 ? 1 : (per > a.N ? a.N : per);
+    return launch(compress_tree_kernel, dim3(static_cast<unsigned>(per), static_cast<unsigned>(B)),
                   dim3(kTreeThreads), 0, c, 1, a);
 }
 
