@@ -487,3 +487,155 @@ class BatchedDecodeLayer:
             self.pos.add_(1)
         self.p_host = p_new
         return self.step(stream=stream)
+
+
+class TreeDecodeLayer:
+    """B sessions of one layer that check drafted tokens: a tree of up to `max_nodes` tokens
+    per session in one pass over a paged token cache, then the accepted path committed
+    (ds4a_paged_append, ds4a_compress_tree, ds4a_attn_tree, ds4a_commit_tree).
+
+    Built from one DecodeInstance per session, as BatchedDecodeLayer; the token at the
+    instance's position is committed, so a session starts with p + 1 tokens.  Every node's
+    output is that of decoding its path token by token.  `room` is how many tokens beyond the
+    longest session the pages and the compressed rows have place for (a draft counts
+    until it is committed or dropped).  rope = (inv_freq [rot/2] float32 tensor, first rotated
+    dim, interleaved) rotates keys and queries to their positions on the way in; None takes
+    them as already encoded.
+    """
+
+    def __init__(self, instances, max_nodes: int = 16, room: int = 256, page: int = 64, rope=None, device="cuda"):
+        for inst in instances[1:]:
+            if not np.array_equal(inst.w, instances[0].w):
+                raise ValueError("TreeDecodeLayer: the sessions of one layer share its compressor score weights")
+        if not 1 <= max_nodes <= 64 or room < max_nodes:
+            raise ValueError("TreeDecodeLayer: 1 .. 64 nodes, and room for at least one draft")
+        singles = [DecodeLayer(inst, device=device, cap_extra=1) for inst in instances]
+        L0 = singles[0]
+        for L in singles:
+            if (L.H, L.D, L.W, L.ratio, L.topk) != (L0.H, L0.D, L0.W, L0.ratio, L0.topk) or L.pooled_keys:
+                raise ValueError("TreeDecodeLayer: sessions must share the layer's shape and schedule")
+        self.B, self.N, self.page, self.rope = len(singles), max_nodes, page, rope
+        self.H, self.D, self.W, self.ratio, self.topk, self.scale = L0.H, L0.D, L0.W, L0.ratio, L0.topk, L0.scale
+        dev, B, N, D = torch.device(device), self.B, self.N, self.D
+        self.len_host = [L.p + 1 for L in singles]
+        self.max_tokens = max(self.len_host) + room
+        # pages from the one that holds the window's first token on; earlier ones are not kept
+        mp = (self.max_tokens + page - 1) // page
+        table = np.full((B, mp), -1, np.int32)
+        first = [max(0, n - self.W) // page for n in self.len_host]
+        n_pages = 0
+        for s in range(B):
+            table[s, first[s]:] = np.arange(n_pages, n_pages + mp - first[s])
+            n_pages += mp - first[s]
+        self.table = _dev(table, dev)
+        self.pool_k = torch.zeros(n_pages, page, D, dtype=torch.float16, device=dev)
+        self.pool_v = torch.zeros_like(self.pool_k)
+        self.length = torch.tensor(self.len_host, dtype=torch.int64, device=dev)
+        self.kv = ds4a.paged_kv_desc(self.pool_k, self.pool_v, self.table, self.length)
+        for s, inst in enumerate(instances):
+            pos = np.arange(max(0, self.len_host[s] - self.W), self.len_host[s])
+            rows = torch.from_numpy(table[s][pos // page].astype(np.int64) * page + pos % page).to(dev)
+            self.pool_k.view(-1, D)[rows] = _dev(inst.raw_k[pos - inst.raw_pos0], dev)
+            self.pool_v.view(-1, D)[rows] = _dev(inst.raw_v[pos - inst.raw_pos0], dev)
+        self.n_node = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.parent = torch.full((B, N), -1, dtype=torch.int32, device=dev)
+        self.parent_host, self.n_host = np.full((B, N), -1, np.int32), [0] * B
+        self.leaf = torch.full((B,), -1, dtype=torch.int32, device=dev)
+        self.q = torch.zeros(B, N, self.H, D, dtype=torch.float16, device=dev)
+        self.out = torch.zeros_like(self.q)
+        self.ws = torch.empty(ds4a.ds4a_attn_tree_workspace_bytes(B, N, self.H, D), dtype=torch.uint8, device=dev)
+        self.w = L0.w
+        self.cap, self.state, self.comp_k, self.comp_v, self.kidx, self.sel, self.sel_ws = 0, None, None, None, None, None, None
+        if self.ratio:
+            self.cap = self.max_tokens // self.ratio + N           # the last N rows are the draft's
+            self.state = torch.stack([L.state for L in singles])
+            self.comp_k = torch.zeros(B, self.cap, D, dtype=torch.float16, device=dev)
+            self.comp_v = torch.zeros_like(self.comp_k)
+            for s, L in enumerate(singles):
+                L.state = self.state[s]
+                ds4a.ds4a_compress_append(L.ring_k[L.slot:L.slot + 1], L.ring_v[L.slot:L.slot + 1], L.w, L.ratio, L.p,
+                                          L.state, L.comp_k, L.comp_v)
+                n = self.len_host[s] // self.ratio
+                self.comp_k[s, :n], self.comp_v[s, :n] = L.comp_k[:n], L.comp_v[:n]
+        if self.topk:
+            d_idx = L0.kidx.shape[1]
+            self.kidx = torch.zeros(B, self.cap, d_idx, dtype=torch.float16, device=dev)
+            for s, L in enumerate(singles):
+                n = self.len_host[s] // self.ratio
+                self.kidx[s, :n] = L.kidx[:n]
+            self.sel = torch.full((B, N, self.topk), -1, dtype=torch.int32, device=dev)
+            self.sel_ws = torch.zeros(ds4a.ds4a_indexer_workspace_bytes(N, self.cap, self.topk), dtype=torch.uint8,
+                                      device=dev)
+
+    def verify(self, k, v, q, parent, n_node, q_idx=None, kidx=None):
+        """Checks a draft: k, v [B, N, D] and q [B, N, H, D] fp16 device tensors of the drafted
+        tokens; parent [B, N] (int array-like on the host: an earlier node or -1) and n_node [B]
+        its shape; on an indexer layer q_idx [B, N, d_idx], and kidx [B, N, d_idx] holding the
+        indexer key of the row that each node completes (other nodes' are ignored).  Returns
+        out [B, N, H, D].  Replaces an earlier draft that was not accepted."""
+        par = np.ascontiguousarray(parent, dtype=np.int32)
+        n_host = [int(n) for n in n_node]
+        if par.shape != (self.B, self.N) or len(n_host) != self.B:
+            raise ValueError("verify: parent [B, N], n_node [B]")
+        for s, n in enumerate(n_host):
+            if not 0 <= n <= self.N or any(not -1 <= par[s, i] < i for i in range(n)):
+                raise ValueError(f"verify: session {s}: a parent is an earlier node or -1, at most {self.N} nodes")
+            if self.len_host[s] + n > self.max_tokens:
+                raise ValueError(f"verify: session {s} has no room for {n} more tokens")
+        if self.topk and (q_idx is None or kidx is None):
+            raise ValueError("verify: an indexer layer needs the nodes' indexer queries and keys")
+        self.parent_host, self.n_host = par, n_host
+        self.parent.copy_(torch.from_numpy(par))
+        self.n_node.copy_(torch.tensor(n_host, dtype=torch.int32))
+        inv, off, inter = self.rope if self.rope is not None else (None, 0, True)
+        qr = self.q if inv is not None else q
+        ds4a.ds4a_paged_append(self.kv, k, v, self.n_node, self.parent, inv, off, inter, q if inv is not None else None,
+                               self.q if inv is not None else None)
+        if self.ratio:
+            ds4a.ds4a_compress_tree(self.kv, self.n_node, self.parent, self.w, self.ratio, self.state, self.comp_k,
+                                    self.comp_v)
+        if self.topk:
+            self.kidx[:, self.cap - self.N:] = kidx
+            self._select(q_idx)
+        ds4a.ds4a_attn_tree(self.kv, qr, self.n_node, self.parent, self.W, self.comp_k, self.comp_v, self.ratio, self.sel,
+                            self.scale, self.out, self.ws)
+        return self.out
+
+    def _select(self, q_idx):
+        """Every node's kept rows.  The indexer ranks rows by position, so the nodes of one
+        root-to-leaf path are one call over the committed keys and that path's own (laid out
+        behind them, in rows that are free until the commit)."""
+        par, dev = self.parent_host, self.kidx.device
+        for s in range(self.B):
+            n, ln = self.n_host[s], self.len_host[s]
+            done = set()
+            for leaf in [i for i in range(n) if i not in set(par[s, :n])]:
+                path = [leaf]
+                while par[s, path[0]] >= 0:
+                    path.insert(0, int(par[s, path[0]]))
+                rows = [i for d, i in enumerate(path) if (ln + d + 1) % self.ratio == 0]
+                n_vis = ln // self.ratio
+                if rows:
+                    self.kidx[s, n_vis:n_vis + len(rows)] = self.kidx[s, self.cap - self.N:][torch.tensor(rows, device=dev)]
+                idx = torch.tensor(path, device=dev)
+                out = torch.empty(len(path), self.topk, dtype=torch.int32, device=dev)
+                ds4a.ds4a_indexer_topk(q_idx[s].index_select(0, idx), self.kidx[s], ln, self.ratio, self.topk, out, None,
+                                       self.sel_ws, n_rows=n_vis + len(rows))
+                new = [d for d, i in enumerate(path) if i not in done]
+                self.sel[s, idx[new[0]:]] = out[new[0]:]
+                done.update(path)
+
+    def accept(self, leaf):
+        """Commits the path that ends in node leaf[s] of the verified draft (host ints, -1: none)."""
+        leaf = [int(x) for x in leaf]
+        if len(leaf) != self.B or any(not -1 <= x < n for x, n in zip(leaf, self.n_host)):
+            raise ValueError("accept: one node of the draft, or -1, per session")
+        self.leaf.copy_(torch.tensor(leaf, dtype=torch.int32))
+        ds4a.ds4a_commit_tree(self.kv, self.n_node, self.parent, self.leaf, self.length, self.w, self.ratio, self.state,
+                              self.state, self.comp_k, self.comp_v, self.kidx)
+        for s, x in enumerate(leaf):
+            while x >= 0:
+                self.len_host[s] += 1
+                x = int(self.parent_host[s, x])
+        self.n_host = [0] * self.B                                  # the draft is used up
+        self.n_node.zero_()
