@@ -63,6 +63,7 @@ constexpr int kProd = 2;                   // producer warps for K, and for V
 constexpr int kWarps = kProdWarp0 + 2 * kProd, kThreads = 32 * kWarps;   // 128 registers a thread, no split needed
 static_assert(kWarps == 16, "128 registers a thread");
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
+constexpr uint64_t kWaitNs = 10000000000ull;   // some waits last an item, which over a cache of 10^8 tokens is a second
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;            // lazy rescale threshold (log2 units)
 constexpr int kEdge = 2 * kMaxNodes;       // first window-edge entry of the poison table
@@ -126,7 +127,7 @@ struct Args {
     float *part;                                   // [slot * n_split + split][tile rows][D]
     float2 *part_ml;                               // [...][tile rows] (max, sum)
     int *active;                                   // [slots]
-    int B, n_split, min_tiles, row_tiles, tile_rows, item_rows, n_work;
+    int B, n_split, min_tiles, row_tiles, tile_rows, item_rows, n_work, walk;
     int pool_oob, comp_oob;                        // rows of the maps: the zero-fill rows
     uint32_t h_mul;                                // node_of
 };
@@ -189,8 +190,8 @@ DS4A_DEVINL int tile_chunks(int n_runs, int t) { return t * kRuns + kChunkRuns <
 
 DS4A_DEVINL unsigned long long shfl64(unsigned long long v, int src) { return __shfl_sync(0xffffffffu, v, src); }
 
-// Item number -> split, row tile, session.  Row tiles are outermost: the empty ones (of sessions
-// with fewer nodes) are the last items.
+// Item number -> split, row tile, session.  When every CTA has one item at most the item is
+// known at once (row tiles of sessions with fewer nodes are empty items).
 struct ItemId {
     int split, rt, s;
 };
@@ -200,6 +201,51 @@ DS4A_DEVINL ItemId item_id(const Args &g, int item) {
     id.split = item - x * g.n_split;
     id.rt = g.B > 1 ? x / static_cast<unsigned>(g.B) : x;
     id.s = x - id.rt * g.B;
+    return id;
+}
+
+// With more items than CTAs only row tiles that have nodes are counted, session after session,
+// so that every CTA gets the same number to within one (64 sessions of 16 .. 32 nodes, 406 of 512
+// row tiles in use: 3 items at most instead of 4).  The set-up warp walks the sessions once,
+// 32 at a time, as its items' numbers grow.
+struct Walk {
+    int first, before, mine, incl;   // first session of the group; row tiles before it; this lane's; up to this lane
+};
+DS4A_DEVINL void walk_load(const Args &g, Walk &k, int first, int before, int lane) {
+    k.first = first;
+    k.before = before;
+    int n = first + lane < g.B ? g.a.n_node[first + lane] : 0;
+    if (n < 0 || n > g.a.N) {        // left alone; there are then fewer items than numbers, and the last CTA walks to the end
+        record_error(g.a.err, DS4A_ERR_DEVICE_INDEX);
+        n = 0;
+    }
+    k.mine = static_cast<int>(static_cast<unsigned>(n * g.a.H + g.item_rows - 1) / static_cast<unsigned>(g.item_rows));
+    k.incl = k.mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, k.incl, o);
+        if (lane >= o) k.incl += up;
+    }
+}
+// s = -1: no such item
+DS4A_DEVINL ItemId walk_item(const Args &g, Walk &k, int item, int lane) {
+    ItemId id;
+    const int t = g.n_split > 1 ? static_cast<unsigned>(item) / static_cast<unsigned>(g.n_split) : item;
+    id.split = item - t * g.n_split;
+    for (;;) {
+        const int total = __shfl_sync(0xffffffffu, k.incl, 31);
+        if (t < k.before + total) break;
+        if (k.first + 32 >= g.B) {
+            id.rt = 0;
+            id.s = -1;
+            return id;
+        }
+        walk_load(g, k, k.first + 32, k.before + total, lane);
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, k.before + k.incl > t);
+    const int l = __ffs(past) - 1;
+    id.s = k.first + l;
+    id.rt = t - k.before - __shfl_sync(0xffffffffu, k.incl - k.mine, l);
     return id;
 }
 
@@ -214,9 +260,16 @@ DS4A_DEVINL unsigned long long reduce64(unsigned long long v) {
 
 // The set-up warp's item: lane holds nodes lane and lane + 32.
 template <bool kSel>
-__device__ void make_work(const Args &g, int item, Work &w, int lane) {
+__device__ void make_work(const Args &g, const ItemId id, Work &w, int lane) {
     const AttnTreeArgs &a = g.a;
-    const ItemId id = item_id(g, item);
+    if (id.s < 0) {
+        if (lane == 0) {
+            w.tile0 = w.tile1 = w.n_runs = w.raw_runs = w.rows = w.s = w.node = w.sides2 = w.row0 = 0;
+            w.active = 0;
+        }
+        __syncwarp();
+        return;
+    }
     const int split = id.split, rt = id.rt, s = id.s, slot = s * g.row_tiles + rt;
     int p[2];                                         // parents, loaded beside the session's counts
 #pragma unroll
@@ -495,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     bool ok = true;
     // a failed wait records the failure; later waits of this thread return at once
     auto wait = [&](uint64_t *b, uint32_t parity) {
-        if (ok && !tc::mbar_wait(b, parity & 1u)) ok = false;
+        if (ok && !tc::mbar_wait(b, parity & 1u, kWaitNs)) ok = false;
         return ok;
     };
     // items of this CTA, and the shared copy of item number it
@@ -712,9 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             return ok;
         };
         if (warp == kSetupWarp) {
+            Walk walk{};
             for (int it = 0; it < n_items; ++it) {
                 if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
-                make_work<kSel>(g, blockIdx.x + it * gridDim.x, works[it & 1], lane);
+                const int item = blockIdx.x + it * gridDim.x;
+                if (g.walk && it == 0) walk_load(g, walk, 0, 0, lane);
+                make_work<kSel>(g, g.walk ? walk_item(g, walk, item, lane) : item_id(g, item), works[it & 1], lane);
                 if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
                 __syncwarp();
             }
@@ -725,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             constexpr uint32_t kIdS = tc::idesc_f16_f32(kTK, kCK, false, false);
             constexpr uint32_t kIdO = tc::idesc_f16_f32(kTK, D, false, true);
             const uint32_t side = warp - kMmaWarp;
-            uint32_t n_t = 0, n_c = 0, n_o = 0;                   // tiles; chunks of this side; items with tiles
+            uint32_t n_t = 0, n_c = 0, n_o = 0, n_q = 0;          // tiles; chunks of this side; items with tiles; query loads
             // a descriptor holds the address in 16-byte units in its low bits: steps are additions
             const uint64_t q_d = tc::desc_sw128(tc::smem_u32(smem + L::q), 16, 1024);
             const uint64_t k_d = tc::desc_sw128(tc::smem_u32(smem + L::k), 16, 1024);
@@ -740,9 +796,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 const bool sides2 = __shfl_sync(0xffffffffu, w.sides2, 0) != 0;
                 const int first = sides2 ? 0 : static_cast<int>(side), by = sides2 ? 1 : 2;   // this side's tiles
                 const uint64_t qd = q_d + (sides2 ? side : 0) * kTile16;
-                if (!warp_wait(&bar.q_full, it)) break;
+                if ((tiles > 0 || !g.walk) && !warp_wait(&bar.q_full, n_q++)) break;
                 if (first >= tiles) {                             // nothing for this side: every phase is seen all the same
-                    if (lane == 0) tc::mbar_arrive(&bar.q_empty);
+                    if (lane == 0 && (tiles > 0 || !g.walk)) tc::mbar_arrive(&bar.q_empty);
                     if (tiles > 0 && n_o > 0) warp_wait(&bar.o_empty[side], n_o - 1);
                 }
                 // the next chunk to score: tile st_t, half st_h, buffer st_n & 1
@@ -914,26 +970,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             };
             int st = 0;
             uint32_t ph = 0, n_t = 0, n_q = 0;
+            auto load_q = [&](int s, int row0) {
+                if (n_q > 0 && !warp_wait(&bar.q_empty, n_q - 1)) return false;
+                if (lane == 0) {
+                    const int blocks = !kSel && g.tile_rows > kTK ? 2 : 1;
+                    const int qrow = s * a.N * a.H + row0;
+                    tc::expect_tx(&bar.q_full, blocks * L::tile);
+                    for (int b = 0; b < blocks; ++b)
+                        for (int at = 0; at < kAtoms; ++at)
+                            tc::tma_load_2d(smem + L::q + b * L::tile + at * kAtomBytes, &g.map_q, at * 64,
+                                            qrow + b * kTK, &bar.q_full);
+                }
+                __syncwarp();
+                ++n_q;
+                return true;
+            };
             for (int it = 0; it < n_items; ++it) {
                 const Work &w = works[it & 1];
-                if (!is_v && pw == 0) {
-                    // the query rows depend on nothing in device memory: loaded while the set-up runs
-                    if (n_q > 0 && !warp_wait(&bar.q_empty, n_q - 1)) break;
-                    if (lane == 0) {
-                        const ItemId id = item_id(g, blockIdx.x + it * gridDim.x);
-                        constexpr int kBlocks = kSel ? 1 : 2;
-                        const int blocks = kBlocks == 2 && g.tile_rows > kTK ? 2 : 1;
-                        const int qrow = id.s * a.N * a.H + id.rt * g.item_rows;
-                        tc::expect_tx(&bar.q_full, blocks * L::tile);
-                        for (int b = 0; b < blocks; ++b)
-                            for (int at = 0; at < kAtoms; ++at)
-                                tc::tma_load_2d(smem + L::q + b * L::tile + at * kAtomBytes, &g.map_q, at * 64,
-                                                qrow + b * kTK, &bar.q_full);
-                    }
-                    __syncwarp();
-                    ++n_q;
+                // Without the walk the query rows are known from the item's number: loaded while the set-up runs.
+                const bool q_mine = !is_v && pw == 0;
+                if (q_mine && !g.walk) {
+                    const ItemId id = item_id(g, blockIdx.x + it * gridDim.x);
+                    if (!load_q(id.s, id.rt * g.item_rows)) break;
                 }
                 if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
+                if (q_mine && g.walk && w.tile1 > w.tile0 && !load_q(w.s, w.row0)) break;
                 const int tile0 = w.tile0, tile1 = w.tile1, raw_runs = w.raw_runs, n_runs = w.n_runs;
                 const int32_t *table = a.kv.table + static_cast<long long>(w.s) * a.kv.max_pages;
                 const int32_t *list = kSel ? a.sel + (static_cast<long long>(w.s) * a.N + w.node) * a.n_sel : nullptr;
@@ -1142,6 +1203,7 @@ cudaError_t launch_one(Args &g, const Ctx &c) {
         configured_device = dev;
     }
     const int grid = g.n_work < c.num_sms ? g.n_work : c.num_sms;
+    g.walk = g.n_work > grid;
     return launch(attn_tree_kernel<D, kSel>, dim3(grid), dim3(kThreads), (Layout<D, kSel>::bytes), c, 1, g);
 }
 

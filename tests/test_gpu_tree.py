@@ -451,6 +451,25 @@ def test_attn_tree_reports_bad_device_values():
     check_attn(c, par, q, ck, cv, sel, 64, 4, 0.1, out)
 
 
+def test_attn_tree_reports_bad_sessions_among_many():
+    """More row tiles than SMs: sessions with bad counts, lengths, parents or no nodes between others."""
+    rng = np.random.default_rng(6)
+    B, N = 70, 9
+    lens, n = [50 + s for s in range(B)], [1 + s % N for s in range(B)]
+    c, par, q, ck, cv, _ = attn_setup(rng, lens, n, N, 64, 64, 16, 40, 4, 0, "tree")
+    good = list(n)
+    for s, bad in ((0, 10), (33, -1), (69, 1 << 20), (40, 0)):
+        c.n[s], good[s] = bad, 0
+    c.lens[12], good[12] = -7, 0
+    par[50, 1], good[50] = 1, 0
+    c.n[50] = 3
+    out = run_attn(c, par, q, ck, cv, None, 40, 4, 0.1)
+    torch.cuda.synchronize()
+    assert ds4a.ds4a_last_device_error() == ds4a.DS4A_ERR_DEVICE_INDEX
+    c.n, par[50, 1] = good, 0
+    check_attn(c, par, q, ck, cv, None, 40, 4, 0.1, out)
+
+
 def test_attn_tree_without_a_readable_row_gives_zeros():
     c, par, q, ck, cv, sel = attn_setup(np.random.default_rng(1), [20, 20], [2, 2], 2, 8, 64, 16, 64, 0, 0, "chain")
     c.table[0, :] = -1
