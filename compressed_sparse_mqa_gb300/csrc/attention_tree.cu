@@ -20,8 +20,13 @@
 // columns (sel: tile::gather4 loads of 4 rows).  Runs past the end load zeros.
 //
 // Work item: a row tile (one or two 128-row blocks of a session, or one node's heads) and
-// a range of its key tiles; n_split ranges per row tile when there are few row tiles, joined
-// by combine_kernel.  CTAs are persistent, one per SM.  Roles:
+// its key tiles.  CTAs are persistent, one per SM, and take items in one of three ways:
+//   direct  no more row tiles than SMs: one each, known from the CTA's number;
+//   walk    more: the row tiles that have nodes, dealt out evenly;
+//   stream  few row tiles over many keys: all (row tile, key tile) pairs in one line, cut into equal
+//           pieces, one a CTA.  A row tile that two or more CTAs share is joined by
+//           combine_kernel (attn_full_4x64: 58 row tiles of 258 key tiles, 98.5 each).
+// Roles:
 //   warps 0-3, 4-7  softmax of side 0 / 1: thread = row.  With two row blocks a side is a
 //                row block and both use the same key tiles; with one block the sides take
 //                alternate key tiles and are joined at the end (both accumulators have
@@ -83,8 +88,8 @@ struct alignas(16) Work {
     int row0, rows;                        // first row in the session, valid rows (<= 256)
     int sides2;                            // two row blocks
     int tile0, tile1;                      // key tiles of this item
-    int active, split;                     // splits that have tiles; this one
-    int slot;                              // index of the row tile among all
+    int pieces, part;                      // CTAs that share the row tile; this one's place in the partial results
+    int stop;                              // no item: the CTA is done
     int dirty;                             // poison entries exist
     int n_vis, n_done;                     // sel: rows complete at the node's position, and at the draft's start
     alignas(16) uint32_t poison[kPoison][12];          // per key: NaN, +inf, -inf bits of its 128 values
@@ -124,21 +129,25 @@ struct Args {
     CUtensorMap map_q, map_k, map_v;               // 128-row boxes; 16-row boxes over the pools
     CUtensorMap map_ck, map_cv;                    // compressed rows: 16-row boxes (sel: one-row, gathers)
     AttnTreeArgs a;
-    float *part;                                   // [slot * n_split + split][tile rows][D]
-    float2 *part_ml;                               // [...][tile rows] (max, sum)
-    int *active;                                   // [slots]
-    int B, n_split, min_tiles, row_tiles, tile_rows, item_rows, n_work, walk;
+    float *part;                                   // stream: [2 per CTA][tile rows][D], a row tile's tail and head pieces
+    float2 *part_ml;                               // [2 per CTA][tile rows] (max, sum)
+    int2 *pieces;                                  // [row tiles] (CTAs that share it, the first of them)
+    int B, mode, min_tiles, row_tiles, tile_rows, item_rows, n_work;
     int pool_oob, comp_oob;                        // rows of the maps: the zero-fill rows
     uint32_t h_mul;                                // node_of
 };
 
+enum { kDirect, kWalk, kStream };
+
 struct JoinArgs {
     const float *part;
     const float2 *part_ml;
-    const int *active;
+    const int2 *pieces;
+    PagedKV kv;
     const int32_t *n_node;
     uint16_t *out;
-    int B, N, H, n_split, row_tiles, tile_rows, item_rows;
+    long long cap;
+    int B, N, H, ratio, row_tiles, tile_rows, item_rows;
 };
 
 // row / H of a session's row (below 64 * 64 + 256) without a division: h_mul = ceil(2^20 / H)
@@ -190,62 +199,129 @@ DS4A_DEVINL int tile_chunks(int n_runs, int t) { return t * kRuns + kChunkRuns <
 
 DS4A_DEVINL unsigned long long shfl64(unsigned long long v, int src) { return __shfl_sync(0xffffffffu, v, src); }
 
-// Item number -> split, row tile, session.  When every CTA has one item at most the item is
-// known at once (row tiles of sessions with fewer nodes are empty items).
-struct ItemId {
-    int split, rt, s;
+// An item: session (-1: none), row tile, its key tiles t0 .. t1-1 (as far as there are any);
+// stream: how many CTAs share the row tile, the first of them, this one's place.
+struct Item {
+    int s, rt, t0, t1, pieces, first, part;
 };
-DS4A_DEVINL ItemId item_id(const Args &g, int item) {
-    ItemId id;
-    const unsigned x = g.n_split > 1 ? static_cast<unsigned>(item) / static_cast<unsigned>(g.n_split) : item;
-    id.split = item - x * g.n_split;
-    id.rt = g.B > 1 ? x / static_cast<unsigned>(g.B) : x;
-    id.s = x - id.rt * g.B;
+DS4A_DEVINL Item direct_item(const Args &g) {
+    Item id{-1, 0, 0, 0x7fffffff, 1, 0, 0};
+    if (static_cast<int>(blockIdx.x) < g.n_work) {
+        const unsigned x = blockIdx.x;
+        id.rt = g.B > 1 ? x / static_cast<unsigned>(g.B) : x;
+        id.s = x - id.rt * g.B;
+    }
     return id;
 }
 
-// With more items than CTAs only row tiles that have nodes are counted, session after session,
-// so that every CTA gets the same number to within one (64 sessions of 16 .. 32 nodes, 406 of 512
-// row tiles in use: 3 items at most instead of 4).  The set-up warp walks the sessions once,
-// 32 at a time, as its items' numbers grow.
+// First slot of a session's key runs when every node's window is meant (the widest: depth 0)
+DS4A_DEVINL int session_t0(const AttnTreeArgs &a, int len) {
+    const long long lo = static_cast<long long>(len) - a.window + 1;
+    return (lo < 0 ? 0 : min(static_cast<int>(lo), len)) & ~(kRun - 1);
+}
+DS4A_DEVINL int runs_of(int rows) { return (rows + kRun - 1) / kRun; }
+
+// The set-up warp's walk over the sessions, 32 at a time.  A session counts its row tiles that
+// have nodes (64 sessions of 16 .. 32 nodes, 406 of 512 row tiles in use: 3 items a CTA at
+// most instead of 4), or in stream mode their key tiles; one that must be left alone counts none.
 struct Walk {
-    int first, before, mine, incl;   // first session of the group; row tiles before it; this lane's; up to this lane
+    int first, tiles;                // first session of the group; this lane's session's key tiles (stream)
+    long long before, mine, incl;    // counted before the group; this lane's session; up to and with it
 };
-DS4A_DEVINL void walk_load(const Args &g, Walk &k, int first, int before, int lane) {
+template <bool kSel>
+DS4A_DEVINL void walk_load(const Args &g, Walk &k, int first, long long before, int lane) {
+    const AttnTreeArgs &a = g.a;
     k.first = first;
     k.before = before;
-    int n = first + lane < g.B ? g.a.n_node[first + lane] : 0;
-    if (n < 0 || n > g.a.N) {        // left alone; there are then fewer items than numbers, and the last CTA walks to the end
-        record_error(g.a.err, DS4A_ERR_DEVICE_INDEX);
-        n = 0;
+    k.mine = 0;
+    k.tiles = 0;
+    if (first + lane < g.B) {
+        const Session ses = load_session(a.kv, a.n_node, a.N, first + lane, a.err);
+        const int done = ses.ok && a.ratio > 0 ? static_cast<int>(static_cast<unsigned>(ses.len) / static_cast<unsigned>(a.ratio)) : 0;
+        if (ses.ok && done > a.cap - a.N && a.ratio > 0) {
+            record_error(a.err, DS4A_ERR_CAPACITY);
+        } else if (ses.ok) {
+            k.mine = static_cast<int>(static_cast<unsigned>(ses.n * a.H + g.item_rows - 1) / static_cast<unsigned>(g.item_rows));
+            if (g.mode == kStream) {
+                const int len = static_cast<int>(ses.len);
+                int runs = runs_of(len + ses.n - session_t0(a, len)) + runs_of(kSel ? a.n_sel : done);
+                if (!kSel && a.ratio > 0) runs += runs_of(ses.n);
+                k.tiles = (runs + kRuns - 1) / kRuns;
+                k.mine *= k.tiles;
+            }
+        }
     }
-    k.mine = static_cast<int>(static_cast<unsigned>(n * g.a.H + g.item_rows - 1) / static_cast<unsigned>(g.item_rows));
     k.incl = k.mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, k.incl, o);
+        const long long up = __shfl_up_sync(0xffffffffu, k.incl, o);
         if (lane >= o) k.incl += up;
     }
 }
-// s = -1: no such item
-DS4A_DEVINL ItemId walk_item(const Args &g, Walk &k, int item, int lane) {
-    ItemId id;
-    const int t = g.n_split > 1 ? static_cast<unsigned>(item) / static_cast<unsigned>(g.n_split) : item;
-    id.split = item - t * g.n_split;
+DS4A_DEVINL long long walk_end(const Walk &k) { return k.before + __shfl_sync(0xffffffffu, k.incl, 31); }
+// Moves to the group of number t; the lane whose session has it, or -1 behind the last.
+template <bool kSel>
+DS4A_DEVINL int walk_to(const Args &g, Walk &k, long long t, int lane) {
     for (;;) {
-        const int total = __shfl_sync(0xffffffffu, k.incl, 31);
-        if (t < k.before + total) break;
-        if (k.first + 32 >= g.B) {
-            id.rt = 0;
-            id.s = -1;
-            return id;
-        }
-        walk_load(g, k, k.first + 32, k.before + total, lane);
+        const long long end = walk_end(k);
+        if (t < end) return __ffs(__ballot_sync(0xffffffffu, k.before + k.incl > t)) - 1;
+        if (k.first + 32 >= g.B) return -1;
+        walk_load<kSel>(g, k, k.first + 32, end, lane);
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, k.before + k.incl > t);
-    const int l = __ffs(past) - 1;
+}
+template <bool kSel>
+DS4A_DEVINL Item walk_item(const Args &g, Walk &k, int number, int lane) {
+    Item id{-1, 0, 0, 0x7fffffff, 1, 0, 0};
+    const int l = walk_to<kSel>(g, k, number, lane);
+    if (l >= 0) {
+        id.s = k.first + l;
+        id.rt = static_cast<int>(number - k.before - __shfl_sync(0xffffffffu, k.incl - k.mine, l));
+    }
+    return id;
+}
+// non-negative a / b; in 32 bits when they fit, as they do but for lines of millions of tiles
+DS4A_DEVINL long long quot(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+}
+
+// The line of key tiles is cut at units * c / ctas; piece u .. end of this CTA's share.
+struct Share {
+    long long units, u, end;
+    int ctas;
+};
+template <bool kSel>
+DS4A_DEVINL Share stream_share(const Args &g, Walk &k, int lane) {
+    walk_load<kSel>(g, k, 0, 0, lane);
+    while (k.first + 32 < g.B) walk_load<kSel>(g, k, k.first + 32, walk_end(k), lane);
+    Share h;
+    h.units = walk_end(k);
+    if (g.B > 32) walk_load<kSel>(g, k, 0, 0, lane);
+    const long long most = quot(h.units + g.min_tiles - 1, g.min_tiles);
+    h.ctas = most < static_cast<long long>(gridDim.x) ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+    const int c = blockIdx.x;
+    h.u = c < h.ctas ? quot(h.units * c, h.ctas) : 0;
+    h.end = c < h.ctas ? quot(h.units * (c + 1), h.ctas) : 0;
+    return h;
+}
+template <bool kSel>
+DS4A_DEVINL Item stream_item(const Args &g, Walk &k, Share &h, int lane) {
+    Item id{-1, 0, 0, 0, 1, 0, 0};
+    if (h.u >= h.end) return id;
+    const int l = walk_to<kSel>(g, k, h.u, lane);
+    if (l < 0) return id;
+    const int tiles = __shfl_sync(0xffffffffu, k.tiles, l);
+    const long long at = k.before + __shfl_sync(0xffffffffu, k.incl - k.mine, l);   // the session's first unit
     id.s = k.first + l;
-    id.rt = t - k.before - __shfl_sync(0xffffffffu, k.incl - k.mine, l);
+    id.rt = static_cast<int>(quot(h.u - at, tiles));
+    const long long lo = at + static_cast<long long>(id.rt) * tiles, hi = lo + tiles;
+    id.t0 = static_cast<int>(h.u - lo);
+    const long long end = hi < h.end ? hi : h.end;
+    id.t1 = static_cast<int>(end - lo);
+    // the CTA that has unit x: the largest c with units * c / ctas <= x
+    id.first = static_cast<int>(quot((lo + 1) * h.ctas - 1, h.units));
+    id.pieces = static_cast<int>(quot(hi * h.ctas - 1, h.units)) - id.first + 1;
+    id.part = 2 * static_cast<int>(blockIdx.x) + (id.first == static_cast<int>(blockIdx.x));   // a head or a tail of this CTA
+    h.u = end;
     return id;
 }
 
@@ -260,17 +336,14 @@ DS4A_DEVINL unsigned long long reduce64(unsigned long long v) {
 
 // The set-up warp's item: lane holds nodes lane and lane + 32.
 template <bool kSel>
-__device__ void make_work(const Args &g, const ItemId id, Work &w, int lane) {
+__device__ void make_work(const Args &g, const Item id, Work &w, int lane) {
     const AttnTreeArgs &a = g.a;
+    if (lane == 0) w.stop = id.s < 0;
     if (id.s < 0) {
-        if (lane == 0) {
-            w.tile0 = w.tile1 = w.n_runs = w.raw_runs = w.rows = w.s = w.node = w.sides2 = w.row0 = 0;
-            w.active = 0;
-        }
         __syncwarp();
         return;
     }
-    const int split = id.split, rt = id.rt, s = id.s, slot = s * g.row_tiles + rt;
+    const int rt = id.rt, s = id.s;
     int p[2];                                         // parents, loaded beside the session's counts
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -366,7 +439,7 @@ __device__ void make_work(const Args &g, const ItemId id, Work &w, int lane) {
         for (int x = lane; x < kPoison * 12; x += 32) (&w.poison[0][0])[x] = 0;
     __syncwarp();   // w.cmp is read below
     if (lane == 0) {
-        const int t0 = min(lo_min, len) & ~(kRun - 1);
+        const int t0 = g.mode == kStream ? session_t0(a, len) : min(lo_min, len) & ~(kRun - 1);
         w.any_raw = any_raw;
         w.all_raw = all_raw;
         w.any_cmp = any_cmp;
@@ -381,8 +454,9 @@ __device__ void make_work(const Args &g, const ItemId id, Work &w, int lane) {
         w.n_vis0 = kSel ? a.n_sel : n_done;
         w.comp_runs = (w.n_vis0 + kRun - 1) / kRun;
         w.n_runs = w.raw_runs + w.comp_runs;
-        // the draft's rows, as far as one of the item's nodes attends any
-        if (!kSel && any_cmp) w.n_runs += (64 - __clzll(static_cast<long long>(any_cmp)) + kRun - 1) / kRun;
+        // the draft's rows (stream: the session's all, as in the walk), as far as one of the item's nodes attends any
+        if (!kSel && a.ratio > 0 && g.mode == kStream) w.n_runs += runs_of(n);
+        else if (!kSel && any_cmp) w.n_runs += (64 - __clzll(static_cast<long long>(any_cmp)) + kRun - 1) / kRun;
         w.node = i0;
         if (kSel) {
             const int depth = __popcll(rows > 0 ? w.cmp[i0] : 1ull) - 1;
@@ -393,19 +467,13 @@ __device__ void make_work(const Args &g, const ItemId id, Work &w, int lane) {
         w.rows = rows;
         w.sides2 = rows > kTK;
         const int tiles = rows > 0 ? (w.n_runs + kRuns - 1) / kRuns : 0;
-        int chunk = tiles, active = tiles > 0;
-        if (g.n_split > 1) {
-            chunk = static_cast<unsigned>(tiles + g.n_split - 1) / static_cast<unsigned>(g.n_split);
-            if (chunk < g.min_tiles) chunk = g.min_tiles;
-            active = static_cast<unsigned>(tiles + chunk - 1) / static_cast<unsigned>(chunk);
-        }
-        w.active = active;
-        w.split = split;
-        w.slot = slot;
-        w.tile0 = min(tiles, split * chunk);
-        w.tile1 = min(tiles, w.tile0 + chunk);
+        w.tile0 = min(tiles, id.t0);
+        w.tile1 = min(tiles, id.t1);
+        w.pieces = id.pieces;
+        w.part = id.part;
         w.dirty = 0;
-        if (split == 0 && g.n_split > 1) g.active[slot] = w.active;
+        if (g.mode == kStream && id.first == static_cast<int>(blockIdx.x))
+            g.pieces[s * g.row_tiles + rt] = make_int2(rows > 0 ? id.pieces : 0, id.first);
     }
     __syncwarp();
 }
@@ -551,18 +619,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         if (ok && !tc::mbar_wait(b, parity & 1u, kWaitNs)) ok = false;
         return ok;
     };
-    // items of this CTA, and the shared copy of item number it
-    const int n_items = g.n_work > static_cast<int>(blockIdx.x) ? (g.n_work - blockIdx.x - 1) / gridDim.x + 1 : 0;
-
     if (warp < kSoftWarps) {
         const int side = warp / kSideWarps, quad = warp & 3, r = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t col_s = tmem + lanes + kColS + side * kTK, col_o = tmem + lanes + kColO + side * kTK;
         const float c2 = a.scale_log2;
         uint32_t n_c = 0, n_o = 0, n_join = 0, n_t = 0;   // this side's chunks and items, joined items, tiles so far
-        for (int it = 0; it < n_items; ++it) {
+        for (int it = 0;; ++it) {
             Work &w = works[it & 1];
-            if (!__all_sync(0xffffffffu, wait(&bar.w_full[it & 1], it >> 1))) break;
+            if (!__all_sync(0xffffffffu, wait(&bar.w_full[it & 1], it >> 1)) || w.stop) break;
             const int t0 = w.tile0, t1 = w.tile1, sides2 = w.sides2, n_runs = w.n_runs;
             const int row = (sides2 ? side * kTK : 0) + r;        // row in the item
             const int node = min(kMaxNodes - 1, node_of(g, w.row0 + row));
@@ -677,11 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     const uint32_t col_other = tmem + lanes + kColO + (side ^ 1) * kTK;
                     const int c0 = joined && side == 1 ? D / 64 : 0, c1 = joined && side == 0 ? D / 64 : D / 32;
                     wait(&bar.chk[it & 1], it >> 1);
-                    const bool valid = row < w.rows, direct = w.active == 1;
+                    const bool valid = row < w.rows, direct = w.pieces == 1;
                     const int dirty = w.dirty;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     const long long qrow = (static_cast<long long>(w.s) * a.N) * a.H + w.row0 + row;
-                    const long long prow = (static_cast<long long>(w.slot) * g.n_split + w.split) * g.tile_rows + row;
+                    const long long prow = static_cast<long long>(w.part) * g.tile_rows + row;
                     if (!direct && valid && c0 == 0) g.part_ml[prow] = make_float2(m, l);
 #pragma unroll 2
                     for (int c = c0; c < c1; ++c) {                // 32 columns at a time
@@ -766,13 +831,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         };
         if (warp == kSetupWarp) {
             Walk walk{};
-            for (int it = 0; it < n_items; ++it) {
+            Share share{};
+            if (g.mode == kWalk) walk_load<kSel>(g, walk, 0, 0, lane);
+            if (g.mode == kStream) share = stream_share<kSel>(g, walk, lane);
+            for (int it = 0;; ++it) {
                 if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
-                const int item = blockIdx.x + it * gridDim.x;
-                if (g.walk && it == 0) walk_load(g, walk, 0, 0, lane);
-                make_work<kSel>(g, g.walk ? walk_item(g, walk, item, lane) : item_id(g, item), works[it & 1], lane);
+                Item id{-1, 0, 0, 0, 0, 0, 0};
+                if (g.mode == kWalk) id = walk_item<kSel>(g, walk, blockIdx.x + it * gridDim.x, lane);
+                else if (g.mode == kStream) id = stream_item<kSel>(g, walk, share, lane);
+                else if (it == 0) id = direct_item(g);
+                make_work<kSel>(g, id, works[it & 1], lane);
                 if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
                 __syncwarp();
+                if (id.s < 0) break;
             }
         } else if (warp < kChkWarp) {
             // The whole warp runs this, converged, and one elected lane issues: the operands are then
@@ -788,17 +859,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             const uint64_t v_d = tc::desc_sw128(tc::smem_u32(smem + L::v), kAtomBytes, 1024);
             constexpr int kTile16 = L::tile / 16;
             const uint32_t d_s = tmem + kColS + side * kTK, d_o = tmem + kColO + side * kTK;
-            for (int it = 0; it < n_items && ok; ++it) {
+            for (int it = 0; ok; ++it) {
                 const Work &w = works[it & 1];
-                if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
+                if (!warp_wait(&bar.w_full[it & 1], it >> 1) || __shfl_sync(0xffffffffu, w.stop, 0)) break;
                 const int tile0 = __shfl_sync(0xffffffffu, w.tile0, 0), n_runs = __shfl_sync(0xffffffffu, w.n_runs, 0);
                 const int tiles = __shfl_sync(0xffffffffu, w.tile1, 0) - tile0;
                 const bool sides2 = __shfl_sync(0xffffffffu, w.sides2, 0) != 0;
                 const int first = sides2 ? 0 : static_cast<int>(side), by = sides2 ? 1 : 2;   // this side's tiles
                 const uint64_t qd = q_d + (sides2 ? side : 0) * kTile16;
-                if ((tiles > 0 || !g.walk) && !warp_wait(&bar.q_full, n_q++)) break;
+                if ((tiles > 0 || g.mode == kDirect) && !warp_wait(&bar.q_full, n_q++)) break;
                 if (first >= tiles) {                             // nothing for this side: every phase is seen all the same
-                    if (lane == 0 && (tiles > 0 || !g.walk)) tc::mbar_arrive(&bar.q_empty);
+                    if (lane == 0 && (tiles > 0 || g.mode == kDirect)) tc::mbar_arrive(&bar.q_empty);
                     if (tiles > 0 && n_o > 0) warp_wait(&bar.o_empty[side], n_o - 1);
                 }
                 // the next chunk to score: tile st_t, half st_h, buffer st_n & 1
@@ -887,9 +958,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         } else if (warp < kProdWarp0) {
             // ---------------- checkers ----------------
             uint32_t n_v = 0;
-            for (int it = 0; it < n_items; ++it) {
+            for (int it = 0;; ++it) {
                 Work &w = works[it & 1];
-                if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
+                if (!warp_wait(&bar.w_full[it & 1], it >> 1) || w.stop) break;
                 for (int t = w.tile0; t < w.tile1; ++t, ++n_v) {
                     const int st = n_v % kNS;
                     if (!warp_wait(&bar.v_full[st], n_v / kNS)) break;
@@ -985,16 +1056,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 ++n_q;
                 return true;
             };
-            for (int it = 0; it < n_items; ++it) {
+            for (int it = 0;; ++it) {
                 const Work &w = works[it & 1];
-                // Without the walk the query rows are known from the item's number: loaded while the set-up runs.
+                // in direct mode the query rows are known from the CTA's number: loaded while the set-up runs
                 const bool q_mine = !is_v && pw == 0;
-                if (q_mine && !g.walk) {
-                    const ItemId id = item_id(g, blockIdx.x + it * gridDim.x);
-                    if (!load_q(id.s, id.rt * g.item_rows)) break;
+                if (q_mine && it == 0 && g.mode == kDirect) {
+                    const Item id = direct_item(g);
+                    if (id.s >= 0 && !load_q(id.s, id.rt * g.item_rows)) break;
                 }
-                if (!warp_wait(&bar.w_full[it & 1], it >> 1)) break;
-                if (q_mine && g.walk && w.tile1 > w.tile0 && !load_q(w.s, w.row0)) break;
+                if (!warp_wait(&bar.w_full[it & 1], it >> 1) || w.stop) break;
+                if (q_mine && g.mode != kDirect && w.tile1 > w.tile0 && !load_q(w.s, w.row0)) break;
                 const int tile0 = w.tile0, tile1 = w.tile1, raw_runs = w.raw_runs, n_runs = w.n_runs;
                 const int32_t *table = a.kv.table + static_cast<long long>(w.s) * a.kv.max_pages;
                 const int32_t *list = kSel ? a.sel + (static_cast<long long>(w.s) * a.N + w.node) * a.n_sel : nullptr;
@@ -1104,36 +1175,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the splits of a row: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  One warp per
-// row; rows whose item was not split are already written.
+// Joins the pieces of a row: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  One warp per
+// row; rows of a row tile that one CTA had are already written.
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
     const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const unsigned row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);   // below 2^31: a row is 128 bytes or more
+    const unsigned per = g.N * g.H;
     pdl_wait();
     pdl_trigger();
-    if (row >= static_cast<long long>(g.B) * g.N * g.H) return;
-    const int s = static_cast<int>(row / (g.N * g.H)), r = static_cast<int>(row - static_cast<long long>(s) * g.N * g.H);
-    const int n = g.n_node[s];
-    if (n < 0 || n > g.N || r >= n * g.H) return;
-    const int rt = r / g.item_rows, slot = s * g.row_tiles + rt;
-    const int active = g.active[slot];
-    if (active <= 1) return;
-    const long long base = static_cast<long long>(slot) * g.n_split * g.tile_rows + (r - rt * g.item_rows);
+    if (row >= g.B * per) return;
+    const int s = row / per, r = row - s * per, rt = static_cast<unsigned>(r) / static_cast<unsigned>(g.item_rows);
+    const int2 p = g.pieces[s * g.row_tiles + rt];   // set if the session is in the line
+    const Session ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
+    if (!ses.ok || r >= ses.n * g.H) return;
+    if (g.ratio > 0 && static_cast<unsigned>(ses.len) / static_cast<unsigned>(g.ratio) > g.cap - g.N) return;
+    const int pieces = p.x, first = p.y;
+    if (pieces <= 1) return;
+    const int in_tile = r - rt * g.item_rows;
+    // the first CTA has the row tile as its tail, the others as their head
+    auto at = [&](int i) { return static_cast<long long>(2 * (first + i) + (i == 0)) * g.tile_rows + in_tile; };
     float m = -INFINITY;
-    for (int i = lane; i < active; i += 32) m = fmaxf(m, g.part_ml[base + static_cast<long long>(i) * g.tile_rows].x);
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, g.part_ml[at(i)].x);
     m = warp_max(m);
     const float ref = m == -INFINITY ? 0.f : m;
     constexpr int kPer = D / 32;
     float o[kPer] = {}, l = 0.f;
-    for (int i = 0; i < active; ++i) {
-        const long long at = base + static_cast<long long>(i) * g.tile_rows;
-        const float2 ml = g.part_ml[at];
-        if (ml.y == 0.f) continue;                 // no key of this split is this row's
+    for (int i = 0; i < pieces; ++i) {
+        const float2 ml = g.part_ml[at(i)];
+        if (ml.y == 0.f) continue;                 // no key of this piece is this row's
         const float w = ex2(ml.x - ref);
         l += w * ml.y;
-        const float *src = g.part + at * D + lane * kPer;
+        const float *src = g.part + at(i) * D + lane * kPer;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) o[e] += w * src[e];
     }
@@ -1141,25 +1215,26 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
     uint32_t h[kPer / 2];
 #pragma unroll
     for (int e = 0; e < kPer / 2; ++e) h[e] = pack_half2(o[2 * e] * inv, o[2 * e + 1] * inv);
-    uint32_t *dst = reinterpret_cast<uint32_t *>(g.out + row * D) + lane * (kPer / 2);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(g.out + static_cast<size_t>(row) * D) + lane * (kPer / 2);
 #pragma unroll
     for (int e = 0; e < kPer / 2; ++e) dst[e] = h[e];
 }
 
-// Work items that a split launch may have: two for each of the 152 SMs.  Bounds the partial
-// results, and with them the workspace.
-constexpr int kMaxSplitItems = 304;
+// CTAs that a stream launch may have, two partial results each: bounds the workspace.
+constexpr int kMaxCtas = 152;
 
 struct Plan {
-    int tile_rows, item_rows, row_tiles, n_split, min_tiles;
+    int mode, tile_rows, item_rows, row_tiles, min_tiles, ctas;
 };
 
-size_t header_bytes(long long slots) { return (static_cast<size_t>(slots) * 4 + 255) / 256 * 256; }
+size_t header_bytes(long long slots) { return (static_cast<size_t>(slots) * 8 + 255) / 256 * 256; }
 
-// How a call is cut.  Two row blocks per item (each K and V tile read once for 256 rows) when
-// that leaves at least four key tiles per SM; else one, with its two sides on alternate tiles.
-// Splits: the number with the least waves x (tiles + 4), the 4 being an item's fixed cost in
-// tiles, and 4 more for the join.
+// How a call is cut, from the sizes that the host knows (the most keys and nodes there may be).
+// Two row blocks per item (each K and V tile read once for 256 rows) when that leaves at least four
+// key tiles per SM; else one, with its two sides on alternate tiles.  Stream or not: the smaller of
+// the two costs, in key tiles: an item's fixed part counts 4, in a stream 6 (its pieces start and end
+// anywhere), and the join 4.  Measured, stream against whole items: attn_full_4x64 172 / 385 us,
+// attn_r128_1x16 17.7 / 19.3, attn_r128_64x32 90 / 53, attn_sel_16x16 45 / 32.
 Plan make_plan(const AttnTreeArgs &a, int B, int num_sms) {
     Plan p{};
     const long long tokens = static_cast<long long>(a.kv.max_pages) * a.kv.page;
@@ -1176,23 +1251,24 @@ Plan make_plan(const AttnTreeArgs &a, int B, int num_sms) {
     }
     p.row_tiles = static_cast<int>((rows + p.item_rows - 1) / p.item_rows);
     p.min_tiles = p.tile_rows == kTK ? 2 : 1;
-    const long long slots = static_cast<long long>(p.row_tiles) * B;
-    p.n_split = 1;
-    long long best = -1;
-    for (long long ns = 1; ns == 1 || (ns * slots <= kMaxSplitItems && (ns - 1) * p.min_tiles < tiles); ++ns) {
-        long long chunk = (tiles + ns - 1) / ns;
-        if (chunk < p.min_tiles) chunk = p.min_tiles;
-        const long long cost = (slots * ns + num_sms - 1) / num_sms * (chunk + 4) + (ns > 1 ? 4 : 0);
-        if (best < 0 || cost < best) {
-            best = cost;
-            p.n_split = static_cast<int>(ns);
-        }
+    const long long slots = static_cast<long long>(p.row_tiles) * B, units = slots * tiles;
+    const long long whole = (slots + num_sms - 1) / num_sms * (tiles + 4);
+    const long long sms = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+    long long ctas = (units + p.min_tiles - 1) / p.min_tiles;
+    if (ctas > sms) ctas = sms;
+    const long long share = (units + ctas - 1) / ctas, stream = share + 6 * (share / tiles + 1) + 4;
+    if (tiles > p.min_tiles && stream < whole) {
+        p.mode = kStream;
+        p.ctas = static_cast<int>(ctas);
+    } else {
+        p.mode = slots > num_sms ? kWalk : kDirect;
+        p.ctas = static_cast<int>(slots < num_sms ? slots : num_sms);
     }
     return p;
 }
 
 template <int D, bool kSel>
-cudaError_t launch_one(Args &g, const Ctx &c) {
+cudaError_t launch_one(Args &g, int ctas, const Ctx &c) {
     static thread_local int configured_device = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1202,27 +1278,15 @@ cudaError_t launch_one(Args &g, const Ctx &c) {
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
-    const int grid = g.n_work < c.num_sms ? g.n_work : c.num_sms;
-    g.walk = g.n_work > grid;
-    return launch(attn_tree_kernel<D, kSel>, dim3(grid), dim3(kThreads), (Layout<D, kSel>::bytes), c, 1, g);
+    return launch(attn_tree_kernel<D, kSel>, dim3(ctas), dim3(kThreads), (Layout<D, kSel>::bytes), c, 1, g);
 }
 
 }  // namespace
 
-// The largest over the ways a call of these sizes may be cut.
+// The largest over the ways a call of these sizes may be cut: one or two row blocks, or a node.
 size_t attn_tree_ws_bytes(int B, int N, int H, int D) {
-    size_t most = 256;
-    const long long rows = static_cast<long long>(N) * H;
-    const long long item_rows[3] = {kTK, 2 * kTK, H};
-    for (long long ir : item_rows) {
-        const long long slots = (rows + ir - 1) / ir * B;
-        if (slots == 0 || 2 * slots > kMaxSplitItems) continue;
-        const long long tile_rows = ir == H ? kTK : ir;
-        const size_t bytes = header_bytes(slots) + static_cast<size_t>(kMaxSplitItems / slots * slots * tile_rows) *
-                                                       (static_cast<size_t>(D) * 4 + 8);
-        if (bytes > most) most = bytes;
-    }
-    return most;
+    const long long rows = static_cast<long long>(N) * H, slots = (rows + (H < kTK ? H : kTK) - 1) / (H < kTK ? H : kTK) * B;
+    return header_bytes(slots) + static_cast<size_t>(2 * kMaxCtas) * (rows > kTK ? 2 * kTK : kTK) * (static_cast<size_t>(D) * 4 + 8);
 }
 
 cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
@@ -1242,24 +1306,25 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
         return cudaErrorInvalidValue;
     const long long slots = static_cast<long long>(p.row_tiles) * B;
     g.B = B;
-    g.n_split = p.n_split;
+    g.mode = p.mode;
     g.min_tiles = p.min_tiles;
     g.row_tiles = p.row_tiles;
     g.tile_rows = p.tile_rows;
     g.item_rows = p.item_rows;
-    g.n_work = static_cast<int>(slots * p.n_split);
+    g.n_work = static_cast<int>(slots);
     g.h_mul = ((1u << 20) + static_cast<uint32_t>(a.H) - 1) / static_cast<uint32_t>(a.H);
     g.pool_oob = static_cast<int>(pool_rows);
     g.comp_oob = static_cast<int>(comp_rows);
     unsigned char *ws = static_cast<unsigned char *>(a.ws);
-    const size_t part_rows = static_cast<size_t>(slots) * p.n_split * p.tile_rows;
-    g.active = reinterpret_cast<int *>(ws);
+    const size_t part_rows = static_cast<size_t>(2 * p.ctas) * p.tile_rows;
+    g.pieces = reinterpret_cast<int2 *>(ws);
     g.part = reinterpret_cast<float *>(ws + header_bytes(slots));
     g.part_ml = reinterpret_cast<float2 *>(ws + header_bytes(slots) + part_rows * D * 4);
-    cudaError_t e = D == 128 ? (a.sel ? launch_one<128, true>(g, c) : launch_one<128, false>(g, c))
-                             : (a.sel ? launch_one<64, true>(g, c) : launch_one<64, false>(g, c));
-    if (e != cudaSuccess || p.n_split == 1) return e;
-    const JoinArgs j{g.part, g.part_ml, g.active, a.n_node, a.out, B, a.N, a.H, p.n_split, p.row_tiles, p.tile_rows, p.item_rows};
+    cudaError_t e = D == 128 ? (a.sel ? launch_one<128, true>(g, p.ctas, c) : launch_one<128, false>(g, p.ctas, c))
+                             : (a.sel ? launch_one<64, true>(g, p.ctas, c) : launch_one<64, false>(g, p.ctas, c));
+    if (e != cudaSuccess || p.mode != kStream) return e;
+    const JoinArgs j{g.part, g.part_ml, g.pieces, a.kv, a.n_node, a.out, a.cap, B, a.N, a.H, a.ratio, p.row_tiles,
+                     p.tile_rows, p.item_rows};
     const long long rows = static_cast<long long>(B) * a.N * a.H;
     const dim3 grid(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
     return D == 128 ? launch(combine_kernel<128>, grid, dim3(kJoinThreads), 0, c, 1, j)
