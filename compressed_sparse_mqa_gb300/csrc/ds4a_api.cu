@@ -421,6 +421,11 @@ static int check_paged(const ds4a_paged_kv_t *kv) {
     return DS4A_OK;
 }
 
+static bool overlap(const void *a, const void *b, size_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bytes && y < x + bytes;
+}
+
 static int check_tree(int N, const int32_t *n_node, const int32_t *parent) {
     if (N < 1) return DS4A_ERR_ARG;
     if (N > 64) return DS4A_ERR_UNSUPPORTED;
@@ -449,11 +454,8 @@ int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(n_tok, 4) ||
         !aligned(parent, 4) || !aligned(inv_freq, 4))
         return DS4A_ERR_ARG;
-    if (q && q_out != q) {   // in place, or apart
-        const uintptr_t a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(q_out);
-        const uintptr_t n = static_cast<uintptr_t>(kv->B) * N * H * kv->D * 2;
-        if (a < b + n && b < a + n) return DS4A_ERR_ARG;
-    }
+    // queries in place, or apart
+    if (q && q_out != q && overlap(q, q_out, static_cast<size_t>(kv->B) * N * H * kv->D * 2)) return DS4A_ERR_ARG;
     ds4a::Ctx c;
     rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
@@ -504,6 +506,7 @@ int ds4a_attn_tree(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, c
     if (!q || !out || (ratio > 0 && (!comp_k || !comp_v))) return DS4A_ERR_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(comp_k, 16) || !aligned(comp_v, 16) || !aligned(sel, 4))
         return DS4A_ERR_ARG;
+    if (overlap(q, out, static_cast<size_t>(kv->B) * N * H * kv->D * 2)) return DS4A_ERR_ARG;
     if (ratio > 0 && cap < N) return DS4A_ERR_CAPACITY;
     if (ratio > 0 && cap * kv->B > 0x7fffffffLL) return DS4A_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256) || ws_bytes < ds4a_attn_tree_workspace_bytes(kv->B, N, H, kv->D))

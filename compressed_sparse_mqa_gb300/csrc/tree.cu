@@ -16,9 +16,9 @@ namespace {
 constexpr int kTreeThreads = 256;
 constexpr int kTreeWarps = kTreeThreads / 32;
 
-// Scores w . k of the m path tokens at pool rows s_row (-1: unreadable, score 0): one warp per
-// token, the lanes over 8-dim chunks as in the compressor.  A warp's tokens (up to kMaxNodes /
-// kTreeWarps) are all loaded before the first is summed.
+// Scores w . k of the m path tokens at pool rows s_row: one warp per token, the lanes over
+// 8-dim chunks as in the compressor.  A warp's tokens (up to kMaxNodes / kTreeWarps) are all
+// loaded before the first is summed.
 DS4A_DEVINL void path_scores(const PagedKV &kv, const float *w, const long long *s_row, int m, float *s_score) {
     constexpr int kPer = kMaxNodes / kTreeWarps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -27,7 +27,7 @@ DS4A_DEVINL void path_scores(const PagedKV &kv, const float *w, const long long 
     for (int x = 0; x < kPer; ++x) {
         const int t = warp + x * kTreeWarps;
         raw[x] = make_uint4(0, 0, 0, 0);
-        if (t < m && s_row[t] >= 0 && lane < kv.D / 8)
+        if (t < m && lane < kv.D / 8)
             raw[x] = *reinterpret_cast<const uint4 *>(kv.k + s_row[t] * kv.D + lane * 8);
     }
     float wl[8];
@@ -76,7 +76,7 @@ DS4A_DEVINL float chain_column(const PagedKV &kv, const long long *s_row, const 
     for (int t0 = 0; t0 < m; t0 += 8) {
         uint16_t x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = t0 + u < m && s_row[t0 + u] >= 0 ? src[s_row[t0 + u] * kv.D] : uint16_t(0);
+        for (int u = 0; u < 8; ++u) x[u] = t0 + u < m ? src[s_row[t0 + u] * kv.D] : uint16_t(0);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             if (t0 + u < m) acc = fmaf(s_e[t0 + u], h2f(x[u]), s_c[t0 + u] * acc);
@@ -114,10 +114,13 @@ __global__ void __launch_bounds__(kTreeThreads) compress_tree_kernel(CompressTre
         const long long start = end - a.ratio > ses.len ? end - a.ratio : ses.len;   // the block's first drafted token
         const bool resume = start == ses.len && ses.len % a.ratio != 0;
         const int d0 = static_cast<int>(start - ses.len), m = cnt - d0;
-        if (tid < m)
+        bool good = true;
+        if (tid < m) {
             s_row[tid] = pool_row(a.kv, a.kv.table + static_cast<long long>(s) * a.kv.max_pages,
                                   static_cast<unsigned>(ses.len + path_node(path, d0 + tid)), a.err);
-        __syncthreads();
+            good = s_row[tid] >= 0;
+        }
+        if (!__syncthreads_and(good)) continue;   // a token in a page outside the pool (recorded): no row
         path_scores(a.kv, a.w, s_row, m, s_score);
         __syncthreads();
         const float *st = a.state + static_cast<long long>(s) * (2 + 2 * D);

@@ -521,7 +521,6 @@ def paged_kv_desc(pool_k, pool_v, table, length) -> PagedKVDesc:
     desc.device = pool_k.get_device()
     if any(t.get_device() != desc.device for t in desc.tensors):
         raise ValueError("paged_kv_desc: the tensors are on different devices")
-    desc.ref = ctypes.byref(desc)
     return desc
 
 
@@ -591,7 +590,7 @@ def _marshal_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=No
         H = qs[2]
     st, dev = _launch_on("paged_append", kv, stream), kv.device
     pn, pp = _tree_args("paged_append", kv, N, n_tok, parent)
-    return (kv.ref, _arg(k, _F16, dev, "k"), _arg(v, _F16, dev, "v"), N, pn, pp, _arg(inv_freq, _F32, dev, "inv_freq"),
+    return (ctypes.byref(kv), _arg(k, _F16, dev, "k"), _arg(v, _F16, dev, "v"), N, pn, pp, _arg(inv_freq, _F32, dev, "inv_freq"),
             0 if inv_freq is None else 2 * inv_freq.numel(), rot_off, 1 if interleaved else 0,
             _arg(q, _F16, dev, "q"), H, _arg(q_out, _F16, dev, "q_out"), st)
 
@@ -613,7 +612,7 @@ def _marshal_compress_tree(kv: PagedKVDesc, n_node, parent, score_w, ratio: int,
     st, dev = _launch_on("compress_tree", kv, stream), kv.device
     pn, pp = _tree_args("compress_tree", kv, N, n_node, parent)
     ck, cv, cap = _draft_rows("compress_tree", kv, comp_k, comp_v)
-    return (kv.ref, N, pn, pp, _arg(score_w, _F32, dev, "score_w"), ratio, _arg(state, _F32, dev, "state"), ck, cv, cap,
+    return (ctypes.byref(kv), N, pn, pp, _arg(score_w, _F32, dev, "score_w"), ratio, _arg(state, _F32, dev, "state"), ck, cv, cap,
             st)
 
 
@@ -644,7 +643,7 @@ def _marshal_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, 
     st, dev = _launch_on("attn_tree", kv, stream), kv.device
     pn, pp = _tree_args("attn_tree", kv, N, n_node, parent)
     ck, cv, cap = _draft_rows("attn_tree", kv, comp_k, comp_v) if ratio else (None, None, 0)
-    return (kv.ref, _arg(q, _F16, dev, "q"), N, H, pn, pp, window, ck, cv, cap, ratio, _arg(sel, _I32, dev, "sel"), n_sel,
+    return (ctypes.byref(kv), _arg(q, _F16, dev, "q"), N, H, pn, pp, window, ck, cv, cap, ratio, _arg(sel, _I32, dev, "sel"), n_sel,
             scale, _arg(out, _F16, dev, "out"), _arg(ws, _U8, dev, "ws"), 0 if ws is None else ws.numel(), st)
 
 
@@ -678,7 +677,7 @@ def _marshal_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w
         if k_idx.dim() != 3 or k_idx.shape[:2] != (kv.B, cap):
             raise ValueError("commit_tree: k_idx [B, cap, d_idx], rows as comp_k")
         d_idx = k_idx.shape[2]
-    return (kv.ref, N, pn, pp, _arg(leaf, _I32, dev, "leaf"), _arg(len_out, _I64, dev, "len_out"),
+    return (ctypes.byref(kv), N, pn, pp, _arg(leaf, _I32, dev, "leaf"), _arg(len_out, _I64, dev, "len_out"),
             _arg(score_w, _F32, dev, "score_w"), ratio, _arg(state, _F32, dev, "state"),
             _arg(state_out, _F32, dev, "state_out"), ck, cv, cap, _arg(k_idx, _F16, dev, "k_idx"), d_idx, st)
 

@@ -520,8 +520,9 @@ int ds4a_decode_layer_step(const ds4a_decode_layer_t *layer, long long pos, cons
  * What is in device memory is checked by the kernels.  A session with len < 0, n_node
  * outside 0 .. N or a bad parent or leaf is left alone (DS4A_ERR_DEVICE_INDEX in the device
  * error word); so is one whose tokens pass max_pages * page or whose committed rows pass
- * cap - N (DS4A_ERR_CAPACITY).  A page id outside the pool: the token is not written, not
- * attended and not pooled (DS4A_ERR_DEVICE_INDEX); a commit then leaves the session alone.
+ * cap - N (DS4A_ERR_CAPACITY).  A page id outside the pool (DS4A_ERR_DEVICE_INDEX): the
+ * token is not written and not attended, a row that would pool it is not written, and a
+ * commit leaves the session alone.
  * Early reads: none.  These calls write arrays that other calls read early when the
  * caller passes them there (q_out as a query, committed key rows as k_idx): do not
  * put such a call directly behind the call that writes them.
@@ -544,13 +545,14 @@ typedef struct ds4a_paged_kv {
  *   k, v       [B, N, D] fp16; N >= 0 (up to 64 with parent).
  *   n_tok      [B] int32.
  *   parent     [B, N] int32: positions len + depth; NULL: positions len + i.
- *   inv_freq   [rot/2] float: radians per position of each rotated pair (>= 0, finite);
+ *   inv_freq   [rot/2] float: radians per position of each rotated pair (finite);
  *              NULL with rot = 0: keys and queries are copied as they are.
  *   rot, rot_off  the rotated dims rot_off .. rot_off+rot-1: rot a multiple of 16, 0 .. D,
  *              rot_off a multiple of 8, rot_off + rot <= D.
  *   interleaved  1: pair j is dims (2j, 2j+1) of the rotated dims; 0: dims (j, j + rot/2).
  *   q, q_out   [B, N, H, D] fp16, or both NULL (H is then ignored); q_out may be q, and may
  *              not overlap it otherwise.  H multiple of 8, 8 .. 64.
+ * k, v and q may not overlap the pools.
  * The angle is position * inv_freq taken modulo one turn exactly; sine, cosine and the
  * products are binary32, rounded once to fp16.  len is not changed.
  */
@@ -586,7 +588,7 @@ int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, 
  *              skipped; entries not yet complete at p are skipped and recorded as
  *              DS4A_ERR_DEVICE_INDEX), or NULL.
  *   scale      softmax scale, > 0 and finite.
- *   out        [B, N, H, D] fp16.
+ *   out        [B, N, H, D] fp16, not overlapping q (DS4A_ERR_ARG).
  *   ws         ds4a_attn_tree_workspace_bytes(B, N, H, D) bytes, 256-byte aligned; its contents
  *              need not be set or kept.  Calls that share one workspace must be
  *              stream-ordered (two captured graphs that may replay at the same time need

@@ -249,6 +249,130 @@ def test_commit_moves_the_path_and_continues_the_compressor(lens, n, N, D, page,
             assert torch.equal(state_out[s].view(torch.int32), want_s[s].view(torch.int32)), s
 
 
+def test_append_compress_commit_leave_bad_sessions_alone():
+    """A bad count, length, parent, leaf or page id: that session's arrays keep their bits, the
+    others' are served, and the error word says so."""
+    IDX, CAP = ds4a.DS4A_ERR_DEVICE_INDEX, ds4a.DS4A_ERR_CAPACITY
+    N, ratio, D = 6, 2, 64
+
+    def make(seed=3):
+        rng = np.random.default_rng(seed)
+        c = Cache(rng, [21, 34, 15], [6, 5, 4], D, 16, N)
+        c.draft()
+        x = comp_setup(rng, c, ratio, D)
+        par = R.random_parents(rng, 3, N)
+        return rng, c, x, par
+
+    def run(call, c, x, par, leaf=(5, 4, 3)):
+        ck, cv, w, state, dck, dcv, dw = x
+        kv = c.upload()
+        so, lo = state.clone(), torch.full((3,), -9, device="cuda")
+        before = [t.clone() for t in (c.dk, c.dv, dck, dcv, so, lo)]
+        kn = torch.ones(3, N, D, dtype=torch.float16, device="cuda")
+        if call == "append":
+            ds4a.ds4a_paged_append(kv, kn, kn, c.dn, dev(par))
+        elif call == "compress":
+            ds4a.ds4a_compress_tree(kv, c.dn, dev(par), dw, ratio, state, dck, dcv)
+        else:
+            ds4a.ds4a_commit_tree(kv, c.dn, dev(par), dev(np.array(leaf, np.int32)), lo, dw, ratio, state, so, dck, dcv)
+        torch.cuda.synchronize()
+        return ds4a.ds4a_last_device_error(), before, [c.dk, c.dv, dck, dcv, so, lo]
+
+    def rows_of(c, t, s):
+        return t.view(-1, D)[torch.from_numpy(c.rows(s, range(c.mp * c.page)).clip(0)).cuda()]
+    for call in ("append", "compress", "commit"):
+        for what in ("n_low", "n_high", "len", "cap", "parent", "leaf", "page"):
+            if what == "leaf" and call != "commit":
+                continue
+            rng, c, x, par = make()
+            good_table, code, leaf = c.table.copy(), IDX, (5, 4, 3)
+            if what == "n_low":
+                c.n[1] = -1
+            elif what == "n_high":
+                c.n[1] = N + 1
+            elif what == "len":
+                c.lens[1] = -4
+            elif what == "cap":
+                c.lens[1], code = c.mp * 16 - 2, CAP
+            elif what == "parent":
+                par[1, 3] = 3
+            elif what == "leaf":
+                leaf = (5, 5, 3)
+            else:                                   # every drafted token of session 1 in a page that is none
+                c.table[1, 34 // 16:] = 1 << 30
+            err, before, after = run(call, c, x, par, leaf)
+            assert err == code, (call, what)
+            c.table = good_table
+            for b, a in zip(before[:2], after[:2]):     # session 1's pages
+                assert torch.equal(rows_of(c, b, 1).view(torch.int16), rows_of(c, a, 1).view(torch.int16)), (call, what)
+            for b, a in zip(before[2:], after[2:]):
+                assert torch.equal(b[1].view(torch.uint8) if b.dim() > 1 else b[1], a[1].view(torch.uint8) if a.dim() > 1 else a[1]), (call, what)
+            # the others are served as without the fault
+            rng2, c2, x2, par2 = make()
+            err2, _, ok = run(call, c2, x2, par2)
+            assert err2 == 0
+            for s in (0, 2):
+                for b, a in zip(ok[:2], after[:2]):
+                    assert torch.equal(rows_of(c, b, s).view(torch.int16), rows_of(c, a, s).view(torch.int16)), (call, what, s)
+                for b, a in zip(ok[2:5], after[2:5]):
+                    assert torch.equal(b[s].view(torch.int16), a[s].view(torch.int16)), (call, what, s)
+                assert ok[5][s] == after[5][s]
+
+
+def test_commit_of_compressed_rows_past_the_capacity_is_refused():
+    rng = np.random.default_rng(8)
+    c = Cache(rng, [16, 4], [4, 4], 64, 16, 4)
+    c.draft()
+    ck, cv, w, state, dck, dcv, dw = comp_setup(rng, c, 4, 64)
+    keep = 4 + 4                                     # committed rows 0 .. 3: session 0's next row has no place
+    dck, dcv = dck[:, :keep].contiguous(), dcv[:, :keep].contiguous()
+    kv = c.upload()
+    lo = torch.full((2,), -9, device="cuda")
+    leaf = torch.tensor([3, 3], dtype=torch.int32, device="cuda")
+    ds4a.ds4a_commit_tree(kv, c.dn, None, leaf, lo, dw, 4, state, state, dck, dcv, N=4)
+    torch.cuda.synchronize()
+    assert ds4a.ds4a_last_device_error() == ds4a.DS4A_ERR_CAPACITY
+    assert lo.tolist() == [-9, 8]
+
+
+def test_pools_past_32_bit_offsets():
+    """Pages whose elements lie past 2^31: append, compress, attention and commit reach them."""
+    D, page, n_pages, N, ln = 128, 4096, 4200, 5, 8190           # 2.2e9 values a pool
+    pk = torch.empty(n_pages, page, D, dtype=torch.float16, device="cuda")
+    pv = torch.empty_like(pk)
+    ids = [n_pages - 1, n_pages - 3, n_pages - 2]
+    for i in ids:
+        pk[i].normal_()
+        pv[i].normal_()
+    table = torch.tensor([ids], dtype=torch.int32, device="cuda")
+    length = torch.tensor([ln], device="cuda")
+    kv = ds4a.paged_kv_desc(pk, pv, table, length)
+    rng = np.random.default_rng(0)
+    k, v = (rng.standard_normal((1, N, D)).astype(np.float16) for _ in range(2))
+    n = torch.tensor([N], dtype=torch.int32, device="cuda")
+    par = np.array([[-1, 0, 0, 1, 3]], np.int32)
+    ds4a.ds4a_paged_append(kv, dev(k), dev(v), n, dev(par))
+    q = rng.standard_normal((1, N, 8, D)).astype(np.float16)
+    out = torch.zeros(1, N, 8, D, dtype=torch.float16, device="cuda")
+    ws = torch.empty(ds4a.ds4a_attn_tree_workspace_bytes(1, N, 8, D), dtype=torch.uint8, device="cuda")
+    ds4a.ds4a_attn_tree(kv, dev(q), n, dev(par), 1 << 20, None, None, 0, None, 0.08, out, ws)
+    no_error()
+    # the three pages as a small pool of their own
+    small_k = pk[torch.tensor(ids).cuda()].cpu().numpy().reshape(-1, D)
+    small_v = pv[torch.tensor(ids).cuda()].cpu().numpy().reshape(-1, D)
+    assert np.array_equal(small_k[ln:ln + N], k[0]) and np.array_equal(small_v[ln:ln + N], v[0])
+    for i, path in enumerate(R.paths_of(par[0], N)):
+        kk, vv = R.node_keys(small_k, small_v, None, None, np.arange(3), page, ln, path, N, 1 << 20, 0, None)
+        want, tol = R.attend(q[0, i], kk, vv, 0.08)
+        assert (np.abs(out[0, i].cpu().numpy().astype(np.float64) - want) <= tol).all()
+    leaf = torch.tensor([4], dtype=torch.int32, device="cuda")
+    ds4a.ds4a_commit_tree(kv, n, dev(par), leaf, length)
+    no_error()
+    assert length.item() == ln + 4
+    got = pk[torch.tensor(ids).cuda()].cpu().numpy().reshape(-1, D)
+    assert np.array_equal(got[ln:ln + 4], k[0][[0, 1, 3, 4]])
+
+
 # ---- attention -----------------------------------------------------------------------------------
 
 def attn_setup(rng, lens, n, N, H, D, page, window, ratio, n_sel, kind):
@@ -332,6 +456,12 @@ ATTN = [
     ([1000 - 9 * s for s in range(60)], [10 - s % 9 for s in range(60)], 10, 64, 64, 16, 128, 8, 0, "tree"),
     ([300 + s for s in range(200)], [1 + s % 2 for s in range(200)], 2, 8, 128, 32, 100, 0, 0, "roots"),
     ([900, 901, 902, 903, 904], [5, 4, 3, 2, 1], 5, 48, 128, 112, 64, 64, 1, "tree"),
+    # few row tiles over many keys: one line of key tiles over the SMs, sessions without nodes in it
+    ([9000, 0, 4000, 77], [3, 2, 0, 3], 3, 64, 128, 64, 1 << 30, 0, 0, "tree"),
+    ([12000], [1], 1, 8, 128, 64, 1 << 30, 4, 0, "chain"),
+    ([7000 - 150 * s for s in range(40)], [s % 3 for s in range(40)], 2, 16, 64, 48, 1 << 30, 128, 0, "tree"),
+    ([20000, 3], [40, 2], 40, 64, 128, 128, 1 << 30, 128, 0, "tree"),
+    ([6000], [2], 2, 64, 128, 16, 128, 1, 2048, "chain"),
 ]
 
 

@@ -36,7 +36,7 @@ def compress(L, cache, **kw):
 
 def attn(L, cache, **kw):
     a = dict(q=FAKE, N=4, H=64, n=FAKE, parent=FAKE, window=128, ck=FAKE, cv=FAKE, cap=100, ratio=4, sel=None, n_sel=0,
-             out=FAKE, ws=FAKE, nb=None, scale=0.1)
+             out=FAKE + (1 << 24), ws=FAKE, nb=None, scale=0.1)
     a.update(kw)
     nb = L.ds4a_attn_tree_workspace_bytes(2, 4, 64, 128) if a["nb"] is None else a["nb"]
     return L.ds4a_attn_tree(cache, a["q"], a["N"], a["H"], a["n"], a["parent"], a["window"], a["ck"], a["cv"], a["cap"],
@@ -105,7 +105,7 @@ def test_attn_refusals(ds4a_lib):
                      (dict(H=12), UNSUP), (dict(H=72), UNSUP), (dict(window=0), ARG), (dict(window=-1), ARG),
                      (dict(sel=FAKE, n_sel=0), ARG), (dict(sel=FAKE, n_sel=8, ratio=0), ARG), (dict(n_sel=-1), ARG),
                      (dict(sel=FAKE + 2, n_sel=8), ARG), (dict(sel=FAKE, n_sel=1 << 30), UNSUP),
-                     (dict(cap=1 << 30), UNSUP), (dict(scale=0.0), ARG), (dict(scale=-1.0), ARG), (dict(scale=float("nan")), ARG),
+                     (dict(cap=1 << 30), UNSUP), (dict(out=FAKE), ARG), (dict(out=FAKE + 16), ARG), (dict(scale=0.0), ARG), (dict(scale=-1.0), ARG), (dict(scale=float("nan")), ARG),
                      (dict(scale=float("inf")), ARG), (dict(ws=None), WS), (dict(ws=FAKE + 128), WS), (dict(nb=nb - 1), WS)]:
         assert attn(L, c, **kw) == code, kw
     for bad in [(-1, 4, 64, 128), (2, 0, 64, 128), (2, 65, 64, 128), (2, 4, 12, 128), (2, 4, 64, 96)]:
@@ -123,7 +123,7 @@ def test_binding_refuses_host_tensors_and_shapes(ds4a_lib):
     with pytest.raises(ValueError, match="pools"):
         ds4a_lib.paged_kv_desc(pool, pool, tab, torch.zeros(2, dtype=torch.int64))
     desc = ds4a_lib.PagedKVDesc(B=1, D=64, page=16, max_pages=3, n_pages=4)
-    desc.tensors, desc.device, desc.ref = (), 0, None
+    desc.tensors, desc.device = (), 0
     q = torch.zeros(1, 4, 8, 64, dtype=torch.float16)
     n, par = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 4, dtype=torch.int32)
     with pytest.raises(ValueError, match="attn_tree: q, out"):
