@@ -1175,17 +1175,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the pieces of a row: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  One warp per
-// row; rows of a row tile that one CTA had are already written.
-constexpr int kJoinThreads = 256;
-template <int D>
+// Joins the pieces of a row: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  kPerRow warps per
+// row: one when a row has few pieces, eight when it has many (one row tile over 32768 keys has
+// 128; with one warp going through them one by one the join took 40 us).  Rows of a row tile that
+// one CTA had are already written.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+template <int D, int kPerRow>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
-    const int lane = threadIdx.x & 31;
-    const unsigned row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);   // below 2^31: a row is 128 bytes or more
+    constexpr int kPer = D / 32, kBatch = 8;
+    __shared__ float s_o[kPerRow > 1 ? kPerRow : 1][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kPerRow;
+    const unsigned row = blockIdx.x * (kJoinWarps / kPerRow) + warp / kPerRow;   // below 2^31: a row is 128 bytes or more
     const unsigned per = g.N * g.H;
     pdl_wait();
     pdl_trigger();
-    if (row >= g.B * per) return;
+    if (row >= g.B * per) return;                    // (with kPerRow > 1 a block has one row: it leaves as a whole)
     const int s = row / per, r = row - s * per, rt = static_cast<unsigned>(r) / static_cast<unsigned>(g.item_rows);
     const int2 p = g.pieces[s * g.row_tiles + rt];   // set if the session is in the line
     const Session ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
@@ -1200,16 +1204,57 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
     for (int i = lane; i < pieces; i += 32) m = fmaxf(m, g.part_ml[at(i)].x);
     m = warp_max(m);
     const float ref = m == -INFINITY ? 0.f : m;
-    constexpr int kPer = D / 32;
     float o[kPer] = {}, l = 0.f;
-    for (int i = 0; i < pieces; ++i) {
-        const float2 ml = g.part_ml[at(i)];
-        if (ml.y == 0.f) continue;                 // no key of this piece is this row's
-        const float w = ex2(ml.x - ref);
-        l += w * ml.y;
-        const float *src = g.part + at(i) * D + lane * kPer;
+    for (int c = 0; c < pieces; c += 32) {           // a lane has the weight of piece c + lane
+        float w = 0.f;
+        if (c + lane < pieces) {
+            const float2 ml = g.part_ml[at(c + lane)];
+            if (ml.y != 0.f) {                       // else: no key of this piece is this row's
+                w = ex2(ml.x - ref);
+                l += w * ml.y;
+            }
+        }
+        for (int k0 = sub; k0 < 32 && c + k0 < pieces; k0 += kBatch * kPerRow) {
+            float x[kBatch][kPer];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] += w * src[e];
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = k0 + u * kPerRow;
+                const bool in = k < 32 && c + k < pieces;
+                const float *src = g.part + at(c + k) * D + lane * kPer;
+                if (kPer == 4) {
+                    const float4 v = in ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[u][0] = v.x;
+                    x[u][1] = v.y;
+                    x[u][kPer - 2] = v.z;
+                    x[u][kPer - 1] = v.w;
+                } else {
+                    const float2 v = in ? *reinterpret_cast<const float2 *>(src) : make_float2(0.f, 0.f);
+                    x[u][0] = v.x;
+                    x[u][1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = k0 + u * kPerRow;
+                const float wk = __shfl_sync(0xffffffffu, w, k & 31);
+                if (k < 32 && c + k < pieces && wk != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) o[e] += wk * x[u][e];
+                }
+            }
+        }
+    }
+    l = warp_sum(l);
+    if (kPerRow > 1) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) s_o[sub][lane * kPer + e] = o[e];
+        __syncthreads();
+        if (sub != 0) return;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            o[e] = s_o[0][lane * kPer + e];
+            for (int x = 1; x < kPerRow; ++x) o[e] += s_o[x][lane * kPer + e];
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint32_t h[kPer / 2];
@@ -1326,9 +1371,14 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
     const JoinArgs j{g.part, g.part_ml, g.pieces, a.kv, a.n_node, a.out, a.cap, B, a.N, a.H, a.ratio, p.row_tiles,
                      p.tile_rows, p.item_rows};
     const long long rows = static_cast<long long>(B) * a.N * a.H;
-    const dim3 grid(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
-    return D == 128 ? launch(combine_kernel<128>, grid, dim3(kJoinThreads), 0, c, 1, j)
-                    : launch(combine_kernel<64>, grid, dim3(kJoinThreads), 0, c, 1, j);
+    if (p.ctas >= 8 * slots) {                           // eight pieces a row tile or more
+        const dim3 grid(static_cast<unsigned>(rows));
+        return D == 128 ? launch(combine_kernel<128, kJoinWarps>, grid, dim3(kJoinThreads), 0, c, 1, j)
+                        : launch(combine_kernel<64, kJoinWarps>, grid, dim3(kJoinThreads), 0, c, 1, j);
+    }
+    const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+    return D == 128 ? launch(combine_kernel<128, 1>, grid, dim3(kJoinThreads), 0, c, 1, j)
+                    : launch(combine_kernel<64, 1>, grid, dim3(kJoinThreads), 0, c, 1, j);
 }
 
 }  // namespace ds4a
