@@ -524,6 +524,121 @@ def test_attn_tree_keeps_other_nodes_values_out(bad, where):
             assert torch.equal(out[0, i], clean[0, i]), i
 
 
+@pytest.mark.parametrize("B,N,H,D,window,ratio,lens", [
+    (40, 10, 64, 128, 96, 4, lambda s: 130 + 11 * s),        # two row blocks an item, more items than SMs
+    (40, 10, 64, 64, 96, 4, lambda s: 130 + 11 * s),
+    (90, 6, 16, 128, 60, 0, lambda s: 100 + s),              # one row block
+    (3, 6, 64, 128, 1 << 30, 16, lambda s: 6000 - 900 * s),  # a line of key tiles, its pieces joined
+])
+def test_attn_tree_keeps_values_that_are_not_finite_to_their_nodes(B, N, H, D, window, ratio, lens):
+    """The same over many items: every third session has drafted tokens (and, with a window, a token
+    at its edge) with values that are not finite; nodes that do not attend them keep their bits,
+    the others get them in those columns and keep the rest within the tolerance."""
+    rng = np.random.default_rng(B + D)
+    ln, n = [lens(s) for s in range(B)], [N - s % 3 for s in range(B)]
+    c, par, q, ck, cv, _ = attn_setup(rng, ln, n, N, H, D, 16, window, ratio, 0, "tree")
+    clean = run_attn(c, par, q, ck, cv, None, window, ratio, 0.09).clone()
+    no_error()
+    bad = {}                                          # (session, node) -> {column: value}
+    for s in range(0, B, 3):
+        paths = R.paths_of(par[s], n[s])
+        marks = [(int(rng.integers(0, n[s])), int(rng.integers(0, D)), v) for v in (np.inf, -np.inf, np.nan)]
+        for j, col, val in marks:
+            r = c.rows(s, [ln[s] + j])[0]
+            c.v[r, col] = val
+            for i, path in enumerate(paths):
+                if j in path and len(path) - path.index(j) <= window:
+                    bad.setdefault((s, i), {}).setdefault(col, set()).add((j, str(val)))
+        if window < 1 << 20:
+            t, col = ln[s] - window + 2, int(rng.integers(0, D))   # attended up to depth 1
+            c.v[c.rows(s, [t])[0], col] = np.inf
+            for i, path in enumerate(paths):
+                if t >= ln[s] + len(path) - 1 - window + 1:
+                    bad.setdefault((s, i), {}).setdefault(col, set()).add((-1, "inf"))
+    # a later mark in one place replaces an earlier one: what the arrays hold counts
+    out = run_attn(c, par, q, ck, cv, None, window, ratio, 0.09)
+    no_error()
+    o, w = out.float().cpu().numpy(), clean.float().cpu().numpy()
+    for s in range(B):
+        paths = R.paths_of(par[s], n[s])
+        for i, path in enumerate(paths):
+            _, v = R.node_keys(c.k, c.v, None if ck is None else ck[s], None if cv is None else cv[s], c.table[s], 16, ln[s],
+                               path, N, window, ratio, None)
+            with np.errstate(invalid="ignore"):
+                total = np.where(np.isfinite(v), 0.0, v).sum(0)
+            odd = ~np.isfinite(v).all(0)
+            if not odd.any():
+                assert np.array_equal(o[s, i], w[s, i]), (s, i)
+                continue
+            assert (s, i) in bad
+            assert np.array_equal(o[s, i][:, ~odd], w[s, i][:, ~odd]), (s, i)
+            for col in np.flatnonzero(odd):
+                got = o[s, i][:, col]
+                if np.isnan(total[col]):
+                    assert np.isnan(got).all(), (s, i, col)
+                else:
+                    assert (got == total[col]).all(), (s, i, col)
+
+
+def test_attn_tree_two_streams_at_once():
+    """Two calls on two streams, each with its own workspace, give the bits that they give alone."""
+    rng = np.random.default_rng(13)
+    sets = [(attn_setup(rng, [9000, 40], [7, 5], 7, 64, 128, 64, 1 << 30, 16, 0, "tree"), 1 << 30, 16),
+            (attn_setup(rng, [900 - 5 * s for s in range(30)], [9] * 30, 9, 64, 128, 16, 128, 4, 0, "tree"), 128, 4)]
+    alone = [run_attn(*x, w, r, 0.1).clone() for x, w, r in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        outs = []
+        for (x, w, r), st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                outs.append(run_attn(*x, w, r, 0.1, stream=st))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, outs))
+    no_error()
+
+
+def test_attn_tree_same_row_twice_and_no_nodes():
+    rng = np.random.default_rng(14)
+    # a list that names rows twice attends them twice
+    c, par, q, ck, cv, sel = attn_setup(rng, [300, 70], [5, 4], 5, 16, 64, 16, 40, 4, 12, "tree")
+    sel[:, :, 7:] = sel[:, :, :5]
+    out = run_attn(c, par, q, ck, cv, sel, 40, 4, 0.1)
+    no_error()
+    check_attn(c, par, q, ck, cv, sel, 40, 4, 0.1, out)
+    # a list of nothing: the window alone
+    sel[:] = -1
+    out = run_attn(c, par, q, ck, cv, sel, 40, 4, 0.1)
+    no_error()
+    check_attn(c, par, q, ck, cv, sel, 40, 4, 0.1, out)
+    # no session has a node, in each way of cutting the work
+    for lens, window in (([30, 40], 16), ([9000], 1 << 30), ([20] * 200, 8)):
+        c, par, q, ck, cv, sel = attn_setup(rng, lens, [0] * len(lens), 3, 64, 64, 16, window, 0, 0, "tree")
+        out = run_attn(c, par, q, ck, cv, sel, window, 0, 0.1)
+        no_error()
+        assert (out == 7.0).all()
+
+
+def test_binding_refuses_other_layouts_and_devices():
+    c, par, q, ck, cv, sel = attn_setup(np.random.default_rng(0), [20], [2], 2, 8, 64, 16, 16, 0, 0, "chain")
+    kv = c.upload()
+    dq, dpar = dev(q), dev(par)
+    ws = torch.empty(ds4a.ds4a_attn_tree_workspace_bytes(1, 2, 8, 64), dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(dq)
+    wide = torch.zeros(1, 2, 8, 128, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        ds4a.ds4a_attn_tree(kv, wide[..., ::2], c.dn, dpar, 16, None, None, 0, None, 0.1, out, ws)
+    with pytest.raises(TypeError, match="float16"):
+        ds4a.ds4a_attn_tree(kv, dq.float(), c.dn, dpar, 16, None, None, 0, None, 0.1, out, ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        ds4a.ds4a_attn_tree(kv, dq, c.dn.cpu(), dpar, 16, None, None, 0, None, 0.1, out, ws)
+    with pytest.raises(ds4a.Ds4aError, match="workspace"):
+        ds4a.ds4a_attn_tree(kv, dq, c.dn, dpar, 16, None, None, 0, None, 0.1, out, ws[:-1])
+    kv.device = 1                                    # as if the cache were on another device than the current one
+    with pytest.raises(ValueError, match="current device"):
+        ds4a.ds4a_attn_tree(kv, dq, c.dn, dpar, 16, None, None, 0, None, 0.1, out, ws)
+
+
 def test_attn_tree_reports_bad_device_values():
     """Bad parents, counts, lengths, page ids and sel entries are skipped and recorded."""
     rng = np.random.default_rng(2)
