@@ -49,6 +49,8 @@
 // written, or another branch's values.  The checker scans the V rows of runs that some row
 // masks: values that are not finite are set to 0, and where the key is valid for some
 // rows, noted, so that exactly those rows get them in the end.
+#include <type_traits>
+
 #include "paged_dev.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"
@@ -59,7 +61,7 @@ namespace {
 constexpr int kTK = 128;                   // keys per tile, rows per block
 constexpr int kRun = 16, kRuns = kTK / kRun;
 constexpr int kCK = 64, kChunkRuns = kCK / kRun;   // keys and runs of a chunk: two a tile
-constexpr int kNS = 2;                     // K stages, and V stages: with one row block, one for each side
+constexpr int kNS = 2;                     // K stages, and V stages but with sel: with one row block, one for each side
 constexpr int kInfo = 8;                   // tiles whose run information is kept
 constexpr int kSideWarps = 4, kSoftWarps = 2 * kSideWarps;
 constexpr int kSetupWarp = kSoftWarps, kMmaWarp = kSetupWarp + 1, kChkWarp = kMmaWarp + 2;
@@ -75,7 +77,7 @@ constexpr int kEdge = 2 * kMaxNodes;       // first window-edge entry of the poi
 constexpr int kPoison = 3 * kMaxNodes;     // keys that only some rows attend: nodes, their rows, the window's edge
 
 // One work item, made by the set-up warp.  Slots, rows and counts are below 2^31.
-struct alignas(16) Work {
+struct alignas(16) WorkInfo {
     unsigned long long raw[kMaxNodes];     // drafted tokens that node i attends
     unsigned long long cmp[kMaxNodes];     // drafted nodes whose completed row node i attends (sel: its whole path)
     int lo[kMaxNodes];                     // first committed slot that node i attends
@@ -92,11 +94,13 @@ struct alignas(16) Work {
     int stop;                              // no item: the CTA is done
     int dirty;                             // poison entries exist
     int n_vis, n_done;                     // sel: rows complete at the node's position, and at the draft's start
+};
+struct Work : WorkInfo {                   // (with sel an item is one node: no key is some rows' only)
     alignas(16) uint32_t poison[kPoison][12];          // per key: NaN, +inf, -inf bits of its 128 values
 };
 
 struct Bars {
-    uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_ok[kNS], v_empty[kNS];
+    uint64_t k_full[kNS], k_empty[kNS], v_full[4], v_ok[4], v_empty[4];
     uint64_t q_full, q_empty;
     uint64_t s_full[2][2], p_full[2][2];   // [side][score buffer]
     uint64_t pv[2];                        // a product with V is done
@@ -105,28 +109,35 @@ struct Bars {
     uint64_t join[2];                      // side x has posted its references and sums
 };
 
+// With sel the query block is 64 rows (the products read 128: the other 64 are what follows in
+// shared memory, rows that nobody reads) and there is no poison table, which leaves room for two V
+// stages a side: listed rows come slowly, and a V stage is held until its product is done
+// (attn_sel_16x16 29.7 us, 32 with one a side).
 template <int D, bool kSel>
 struct Layout {
+    using W = std::conditional_t<kSel, WorkInfo, Work>;
     static constexpr int tile = kTK * D * 2;
+    static constexpr int nv = kSel ? 4 : kNS;                 // V stages
+    static constexpr int q_rows = kSel ? 64 : kTK;
     static constexpr int q = 0;                               // row blocks
-    static constexpr int k = q + (kSel ? 1 : 2) * tile;
+    static constexpr int k = q + (kSel ? tile / 2 : 2 * tile);
     static constexpr int v = k + kNS * tile;
-    static constexpr int work = v + kNS * tile;
+    static constexpr int work = v + nv * tile;
     // uint16 [8][8]: readable keys per run of the CTA's tile number & 7, once from the K and once from the V
     // producers; then uint8 [8][8]: every row of the item attends every key of the run.  A slot is written again eight tiles on, two stages ahead of the products; those two tiles
     // on are issued only when the softmax of this one is done.
-    static constexpr int info = work + 2 * static_cast<int>(sizeof(Work));
+    static constexpr int info = work + 2 * static_cast<int>(sizeof(W));
     static constexpr int whole = info + 2 * kInfo * kRuns * 2;
     static constexpr int ml = whole + kInfo * kRuns;           // float2 [2 sides][128] (reference, sum)
     static constexpr int bars = ml + 2 * kTK * 8;
     static constexpr int end = bars + static_cast<int>(sizeof(Bars));
     static constexpr size_t bytes = end + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
-    static_assert(work % 16 == 0 && bars % 8 == 0 && sizeof(Work) % 16 == 0, "alignment");
+    static_assert(work % 16 == 0 && bars % 8 == 0 && sizeof(W) % 16 == 0, "alignment");
 };
 
 struct Args {
-    CUtensorMap map_q, map_k, map_v;               // 128-row boxes; 16-row boxes over the pools
+    CUtensorMap map_q, map_k, map_v;               // 128-row (sel: 64-row) boxes; 16-row boxes over the pools
     CUtensorMap map_ck, map_cv;                    // compressed rows: 16-row boxes (sel: one-row, gathers)
     AttnTreeArgs a;
     float *part;                                   // stream: [2 per CTA][tile rows][D], a row tile's tail and head pieces
@@ -163,7 +174,7 @@ DS4A_DEVINL int clamp16(int x) { return x < 0 ? 0 : (x > kRun ? kRun : x); }
 // Valid keys of run v for a row with first committed slot lo, drafted tokens raw and
 // completed rows cmp.  kSel: runs behind the raw ones are the list's, whose bits are in info.
 template <bool kSel>
-DS4A_DEVINL uint32_t run_bits(const Work &w, int v, int lo, unsigned long long raw, unsigned long long cmp,
+DS4A_DEVINL uint32_t run_bits(const WorkInfo &w, int v, int lo, unsigned long long raw, unsigned long long cmp,
                               const uint16_t *info) {
     if (v < w.raw_runs) {
         const int t = w.t0 + v * kRun;
@@ -179,7 +190,7 @@ DS4A_DEVINL uint32_t run_bits(const Work &w, int v, int lo, unsigned long long r
     return v * kRun < kMaxNodes ? static_cast<uint32_t>(cmp >> (v * kRun)) & 0xffffu : 0u;
 }
 // every key of tile t is valid for every row (with readable pages)
-DS4A_DEVINL bool tile_full(const Work &w, int t) {
+DS4A_DEVINL bool tile_full(const WorkInfo &w, int t) {
     const int v = t * kRuns;
     if (v < w.raw_runs) {
         const int slot = w.t0 + v * kRun;
@@ -190,7 +201,7 @@ DS4A_DEVINL bool tile_full(const Work &w, int t) {
 
 // some row masks keys of tile t whose V rows are read (not the list's: a skipped entry loads zeros)
 template <bool kSel>
-DS4A_DEVINL bool needs_check(const Work &w, int t) {
+DS4A_DEVINL bool needs_check(const WorkInfo &w, int t) {
     return kSel ? t * kRuns < w.raw_runs : !tile_full(w, t);
 }
 
@@ -335,8 +346,8 @@ DS4A_DEVINL unsigned long long reduce64(unsigned long long v) {
 }
 
 // The set-up warp's item: lane holds nodes lane and lane + 32.
-template <bool kSel>
-__device__ void make_work(const Args &g, const Item id, Work &w, int lane) {
+template <bool kSel, typename W>
+__device__ void make_work(const Args &g, const Item id, W &w, int lane) {
     const AttnTreeArgs &a = g.a;
     if (lane == 0) w.stop = id.s < 0;
     if (id.s < 0) {
@@ -435,8 +446,9 @@ __device__ void make_work(const Args &g, const Item id, Work &w, int lane) {
     all_cmp = reduce64<false>(all_cmp);
     lo_min = __reduce_min_sync(0xffffffffu, lo_min);
     lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-    if (w.dirty)
-        for (int x = lane; x < kPoison * 12; x += 32) (&w.poison[0][0])[x] = 0;
+    if constexpr (!kSel)
+        if (w.dirty)
+            for (int x = lane; x < kPoison * 12; x += 32) (&w.poison[0][0])[x] = 0;
     __syncwarp();   // w.cmp is read below
     if (lane == 0) {
         const int t0 = g.mode == kStream ? session_t0(a, len) : min(lo_min, len) & ~(kRun - 1);
@@ -480,7 +492,7 @@ __device__ void make_work(const Args &g, const Item id, Work &w, int lane) {
 
 // Row of entry j of the node's list in the session's compressed rows: -1 (skipped) if negative,
 // and recorded if not complete at the node's position.
-DS4A_DEVINL int sel_row(const AttnTreeArgs &a, const Work &w, int j, bool record) {
+DS4A_DEVINL int sel_row(const AttnTreeArgs &a, const WorkInfo &w, int j, bool record) {
     if (j < 0) return -1;
     if (j >= w.n_vis) {
         if (record) record_error(a.err, DS4A_ERR_DEVICE_INDEX);
@@ -491,8 +503,8 @@ DS4A_DEVINL int sel_row(const AttnTreeArgs &a, const Work &w, int j, bool record
 }
 
 // Sets the values of 16 bytes of a V row that are not finite to 0; notes them for key `slot` of
-// the poison table (-1: no row attends the key), at column col and up.
-__device__ __noinline__ void clean_chunk(Work &w, unsigned char *at, int slot, int col) {
+// the item's poison table (-1: no row attends the key), at column col and up.
+__device__ __noinline__ void clean_chunk(Work *w, unsigned char *at, int slot, int col) {
     uint32_t nan = 0, pi = 0, ni = 0;
     for (int e = 0; e < 8; ++e) {
         uint16_t &h = reinterpret_cast<uint16_t *>(at)[e];
@@ -502,12 +514,12 @@ __device__ __noinline__ void clean_chunk(Work &w, unsigned char *at, int slot, i
         else pi |= 1u << e;
         h = 0;
     }
-    if (slot < 0) return;
+    if (slot < 0 || w == nullptr) return;
     const int word = col / 32, sh = col % 32;
-    if (nan) atomicOr(&w.poison[slot][word], nan << sh);
-    if (pi) atomicOr(&w.poison[slot][4 + word], pi << sh);
-    if (ni) atomicOr(&w.poison[slot][8 + word], ni << sh);
-    w.dirty = 1;
+    if (nan) atomicOr(&w->poison[slot][word], nan << sh);
+    if (pi) atomicOr(&w->poison[slot][4 + word], pi << sh);
+    if (ni) atomicOr(&w->poison[slot][8 + word], ni << sh);
+    w->dirty = 1;
 }
 
 // Values that are not finite, of the keys that `node` attends: into columns col .. col+31 of
@@ -564,7 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Work *works = reinterpret_cast<Work *>(smem + L::work);
+    using W = typename L::W;
+    W *works = reinterpret_cast<W *>(smem + L::work);
     uint16_t *info = reinterpret_cast<uint16_t *>(smem + L::info);
     uint8_t *whole = smem + L::whole;
     float2 *s_ml = reinterpret_cast<float2 *>(smem + L::ml);
@@ -580,6 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         for (int x = 0; x < kNS; ++x) {
             tc::mbar_init(&bar.k_full[x], kProd);
             tc::mbar_init(&bar.k_empty[x], 2);
+        }
+        for (int x = 0; x < L::nv; ++x) {
             tc::mbar_init(&bar.v_full[x], kProd);
             tc::mbar_init(&bar.v_ok[x], 1);
             tc::mbar_init(&bar.v_empty[x], 2);
@@ -601,10 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         }
         tc::mbar_fence_init();
     }
-    for (int x = tid; x < kPoison * 3; x += kThreads) {
-        reinterpret_cast<uint4 *>(works[0].poison)[x] = make_uint4(0, 0, 0, 0);
-        reinterpret_cast<uint4 *>(works[1].poison)[x] = make_uint4(0, 0, 0, 0);
-    }
+    if constexpr (!kSel)
+        for (int x = tid; x < kPoison * 3; x += kThreads) {
+            reinterpret_cast<uint4 *>(works[0].poison)[x] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(works[1].poison)[x] = make_uint4(0, 0, 0, 0);
+        }
     if (warp == kSetupWarp && lane < 2) works[lane].dirty = 0;
     if (warp == kMmaWarp) tc::tmem_alloc(&s_tmem, kTmemCols);
     tc::fence_before_sync();
@@ -626,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         const float c2 = a.scale_log2;
         uint32_t n_c = 0, n_o = 0, n_join = 0, n_t = 0;   // this side's chunks and items, joined items, tiles so far
         for (int it = 0;; ++it) {
-            Work &w = works[it & 1];
+            W &w = works[it & 1];
             if (!__all_sync(0xffffffffu, wait(&bar.w_full[it & 1], it >> 1)) || w.stop) break;
             const int t0 = w.tile0, t1 = w.tile1, sides2 = w.sides2, n_runs = w.n_runs;
             const int row = (sides2 ? side * kTK : 0) + r;        // row in the item
@@ -762,7 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                         } else {
                             tc::wait_ld();
                         }
-                        if (dirty) add_poison(w, node, c * 32, o);
+                        if constexpr (!kSel)
+                            if (dirty) add_poison(w, node, c * 32, o);
                         // With two row blocks four lanes trade 16-byte pieces, so that each writes its piece of
                         // four rows and a store covers 64 contiguous bytes of 8 rows instead of 16 bytes of 32
                         // (attn_r128_64x32 63 against 66 us); with one, where the item waits for it, each lane
@@ -860,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             constexpr int kTile16 = L::tile / 16;
             const uint32_t d_s = tmem + kColS + side * kTK, d_o = tmem + kColO + side * kTK;
             for (int it = 0; ok; ++it) {
-                const Work &w = works[it & 1];
+                const W &w = works[it & 1];
                 if (!warp_wait(&bar.w_full[it & 1], it >> 1) || __shfl_sync(0xffffffffu, w.stop, 0)) break;
                 const int tile0 = __shfl_sync(0xffffffffu, w.tile0, 0), n_runs = __shfl_sync(0xffffffffu, w.n_runs, 0);
                 const int tiles = __shfl_sync(0xffffffffu, w.tile1, 0) - tile0;
@@ -890,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     if (tc::elect()) {
 #pragma unroll
                         for (int x = 0; x < D / 16; ++x)
-                            tc::mma_f16(d, qd + (x / 4) * (kAtomBytes / 16) + (x % 4) * 2,
+                            tc::mma_f16(d, qd + (x / 4) * (L::q_rows * 8) + (x % 4) * 2,
                                         kd + (x / 4) * (kAtomBytes / 16) + (x % 4) * 2, kIdS, x > 0);
                         tc::commit(&bar.s_full[side][buf]);
                         if (tile_end) {
@@ -915,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     issue_s();
                 }
                 for (int t = first; t < tiles && ok; t += by) {
-                    const uint32_t vt = n_t + t, stage = vt % kNS;
+                    const uint32_t vt = n_t + t, stage = vt % L::nv;
                     const int chunks = tile_chunks(n_runs, tile0 + t);
                     for (int c = 0; c < chunks && ok; ++c, ++n_c) {
                         const uint32_t buf = n_c & 1u;
@@ -926,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                             // come, those that only the other side waited for too (so the parity below is the
                             // right phase's).
                             if (t == first && n_o > 0) good = wait(&bar.o_empty[side], n_o - 1) && good;
-                            good = wait(&bar.v_ok[stage], vt / kNS) && good;
+                            good = wait(&bar.v_ok[stage], vt / L::nv) && good;
                         }
                         const uint64_t vd = v_d + stage * kTile16 + c * (kCK / 16 * 128);
                         const uint32_t pa = d_s + buf * kCK;
@@ -959,11 +976,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             // ---------------- checkers ----------------
             uint32_t n_v = 0;
             for (int it = 0;; ++it) {
-                Work &w = works[it & 1];
+                W &w = works[it & 1];
                 if (!warp_wait(&bar.w_full[it & 1], it >> 1) || w.stop) break;
                 for (int t = w.tile0; t < w.tile1; ++t, ++n_v) {
-                    const int st = n_v % kNS;
-                    if (!warp_wait(&bar.v_full[st], n_v / kNS)) break;
+                    const int st = n_v % L::nv;
+                    if (!warp_wait(&bar.v_full[st], n_v / L::nv)) break;
                     if (needs_check<kSel>(w, t)) {
                         const uint16_t *inf = info + (kInfo + (n_v & (kInfo - 1))) * kRuns;
                         unsigned char *vt = smem + L::v + st * L::tile;
@@ -1000,7 +1017,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                                             slot = kMaxNodes + (v - w.raw_runs - w.comp_runs) * kRun + key;
                                         }
                                     }
-                                    clean_chunk(w, vt + half * kAtomBytes + tc::sw128_chunk(r * kRun + key, ch), slot,
+                                    Work *table = nullptr;
+                                    if constexpr (!kSel) table = &w;
+                                    clean_chunk(table, vt + half * kAtomBytes + tc::sw128_chunk(r * kRun + key, ch), slot,
                                                 half * 64 + ch * 8);
                                     wrote = true;
                                 }
@@ -1039,6 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 int v, gv, page, off;
                 int4 e;
             };
+            const int n_stages = is_v ? L::nv : kNS;
             int st = 0;
             uint32_t ph = 0, n_t = 0, n_q = 0;
             auto load_q = [&](int s, int row0) {
@@ -1046,10 +1066,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 if (lane == 0) {
                     const int blocks = !kSel && g.tile_rows > kTK ? 2 : 1;
                     const int qrow = s * a.N * a.H + row0;
-                    tc::expect_tx(&bar.q_full, blocks * L::tile);
+                    constexpr int kBlock = L::q_rows * D * 2;
+                    tc::expect_tx(&bar.q_full, blocks * kBlock);
                     for (int b = 0; b < blocks; ++b)
                         for (int at = 0; at < kAtoms; ++at)
-                            tc::tma_load_2d(smem + L::q + b * L::tile + at * kAtomBytes, &g.map_q, at * 64,
+                            tc::tma_load_2d(smem + L::q + b * kBlock + at * (L::q_rows * 128), &g.map_q, at * 64,
                                             qrow + b * kTK, &bar.q_full);
                 }
                 __syncwarp();
@@ -1057,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 return true;
             };
             for (int it = 0;; ++it) {
-                const Work &w = works[it & 1];
+                const W &w = works[it & 1];
                 // in direct mode the query rows are known from the CTA's number: loaded while the set-up runs
                 const bool q_mine = !is_v && pw == 0;
                 if (q_mine && it == 0 && g.mode == kDirect) {
@@ -1119,7 +1140,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                         if (e[2] >= 0) { gr.z = base + e[2]; gmask |= 4u; }
                         if (e[3] >= 0) { gr.w = base + e[3]; gmask |= 8u; }
                     }
-                    if (n_t >= static_cast<uint32_t>(kNS) && !warp_wait(&empty[st], ph ^ 1u)) break;
+                    if (n_t >= static_cast<uint32_t>(n_stages) && !warp_wait(&empty[st], ph ^ 1u)) break;
                     {   // readable keys per run, for the softmax (K) and the checkers (V)
                         uint32_t m16 = readable ? 0xffffu : 0u;
                         if (kSel) {
@@ -1152,7 +1173,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                                             gr, &full[st]);
                     }
                     __syncwarp();
-                    if (++st == kNS) {
+                    if (++st == n_stages) {
                         st = 0;
                         ph ^= 1u;
                     }
@@ -1162,7 +1183,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             }
             // a wait gave up: the copies in flight land before the block may end
             if (!ok && lane == 0) {
-                const uint32_t ns = kNS, from = n_t > ns ? n_t - ns : 0;
+                const uint32_t ns = n_stages, from = n_t > ns ? n_t - ns : 0;
                 for (uint32_t x = from; x < n_t; ++x) tc::mbar_wait(&full[x % ns], (x / ns) & 1u);
                 if (!is_v && pw == 0 && n_q > 0) tc::mbar_wait(&bar.q_full, (n_q - 1) & 1u);
             }
@@ -1343,7 +1364,7 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
     const long long pool_rows = a.kv.n_pages * a.kv.page, comp_rows = a.ratio > 0 ? a.cap * B : 0;
     const int D = a.kv.D;
     const uint32_t comp_box = a.sel ? 1 : kRun;
-    if (!tc::encode_map(&g.map_q, a.q, D, static_cast<long long>(B) * a.N * a.H, kTK) ||
+    if (!tc::encode_map(&g.map_q, a.q, D, static_cast<long long>(B) * a.N * a.H, a.sel ? 64 : kTK) ||
         !tc::encode_map(&g.map_k, a.kv.k, D, pool_rows, kRun) || !tc::encode_map(&g.map_v, a.kv.v, D, pool_rows, kRun))
         return cudaErrorInvalidValue;
     if (a.ratio > 0 && (!tc::encode_map(&g.map_ck, a.comp_k, D, comp_rows, comp_box) ||
