@@ -31,7 +31,7 @@
 //                row block and both use the same key tiles; with one block the sides take
 //                alternate key tiles and are joined at the end (both accumulators have
 //                the row in the same tensor-memory lane).
-//   warp 8       work set-up: counts, ancestor masks, tile range of the next item.
+//   warp 8       work set-up: counts, ancestor masks, tile range of the next item; its queries.
 //   warps 9-10   MMA issuers of side 0 / 1: S = Q K^T into the side's score columns, O += P V
 //                with P in 16 bits read from tensor memory, over the scores it came from.  One
 //                warp's waits pass behind the other's products.
@@ -847,21 +847,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             return ok;
         };
         if (warp == kSetupWarp) {
+            uint32_t n_q = 0;
+            auto load_q = [&](int s, int row0) {
+                if (n_q > 0 && !warp_wait(&bar.q_empty, n_q - 1)) return false;
+                if (lane == 0) {
+                    const int blocks = !kSel && g.tile_rows > kTK ? 2 : 1;
+                    const int qrow = s * a.N * a.H + row0;
+                    constexpr int kBlock = L::q_rows * D * 2;
+                    tc::expect_tx(&bar.q_full, blocks * kBlock);
+                    for (int b = 0; b < blocks; ++b)
+                        for (int at = 0; at < kAtoms; ++at)
+                            tc::tma_load_2d(smem + L::q + b * kBlock + at * (L::q_rows * 128), &g.map_q, at * 64,
+                                            qrow + b * kTK, &bar.q_full);
+                }
+                __syncwarp();
+                ++n_q;
+                return true;
+            };
             Walk walk{};
             Share share{};
+            if (lane == 0) tc::prefetch_map(&g.map_q);
+            if (g.mode == kDirect) {   // the query rows are known from the CTA's number
+                const Item id = direct_item(g);
+                if (id.s >= 0) load_q(id.s, id.rt * g.item_rows);
+            }
             if (g.mode == kWalk) walk_load<kSel>(g, walk, 0, 0, lane);
             if (g.mode == kStream) share = stream_share<kSel>(g, walk, lane);
             for (int it = 0;; ++it) {
                 if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
+                W &w = works[it & 1];
                 Item id{-1, 0, 0, 0, 0, 0, 0};
                 if (g.mode == kWalk) id = walk_item<kSel>(g, walk, blockIdx.x + it * gridDim.x, lane);
                 else if (g.mode == kStream) id = stream_item<kSel>(g, walk, share, lane);
                 else if (it == 0) id = direct_item(g);
-                make_work<kSel>(g, id, works[it & 1], lane);
+                make_work<kSel>(g, id, w, lane);
                 if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
                 __syncwarp();
                 if (id.s < 0) break;
+                // the queries, when the item before has made its last scores (its output, which frees the
+                // Work after next, comes later; the K producers do not wait here)
+                if (g.mode != kDirect && w.tile1 > w.tile0 && !load_q(w.s, w.row0)) break;
             }
+            if (!ok && lane == 0 && n_q > 0) tc::mbar_wait(&bar.q_full, (n_q - 1) & 1u);   // a wait gave up
+            __syncwarp();
         } else if (warp < kChkWarp) {
             // The whole warp runs this, converged, and one elected lane issues: the operands are then
             // warp-uniform registers, which the instruction wants (issued from a lane == 0 branch, eight
@@ -1050,7 +1078,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             if (lane == 0) {
                 tc::prefetch_map(map_raw);
                 if (a.ratio > 0) tc::prefetch_map(map_comp);
-                if (!is_v && pw == 0) tc::prefetch_map(&g.map_q);
             }
             // the rows of one tile: this lane's run, this lane's four list entries (the raw table entries and
             // list entries of the next tile are loaded while this one waits for its stage)
@@ -1060,33 +1087,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             };
             const int n_stages = is_v ? L::nv : kNS;
             int st = 0;
-            uint32_t ph = 0, n_t = 0, n_q = 0;
-            auto load_q = [&](int s, int row0) {
-                if (n_q > 0 && !warp_wait(&bar.q_empty, n_q - 1)) return false;
-                if (lane == 0) {
-                    const int blocks = !kSel && g.tile_rows > kTK ? 2 : 1;
-                    const int qrow = s * a.N * a.H + row0;
-                    constexpr int kBlock = L::q_rows * D * 2;
-                    tc::expect_tx(&bar.q_full, blocks * kBlock);
-                    for (int b = 0; b < blocks; ++b)
-                        for (int at = 0; at < kAtoms; ++at)
-                            tc::tma_load_2d(smem + L::q + b * kBlock + at * (L::q_rows * 128), &g.map_q, at * 64,
-                                            qrow + b * kTK, &bar.q_full);
-                }
-                __syncwarp();
-                ++n_q;
-                return true;
-            };
+            uint32_t ph = 0, n_t = 0;
             for (int it = 0;; ++it) {
                 const W &w = works[it & 1];
-                // in direct mode the query rows are known from the CTA's number: loaded while the set-up runs
-                const bool q_mine = !is_v && pw == 0;
-                if (q_mine && it == 0 && g.mode == kDirect) {
-                    const Item id = direct_item(g);
-                    if (id.s >= 0 && !load_q(id.s, id.rt * g.item_rows)) break;
-                }
                 if (!warp_wait(&bar.w_full[it & 1], it >> 1) || w.stop) break;
-                if (q_mine && g.mode != kDirect && w.tile1 > w.tile0 && !load_q(w.s, w.row0)) break;
                 const int tile0 = w.tile0, tile1 = w.tile1, raw_runs = w.raw_runs, n_runs = w.n_runs;
                 const int32_t *table = a.kv.table + static_cast<long long>(w.s) * a.kv.max_pages;
                 const int32_t *list = kSel ? a.sel + (static_cast<long long>(w.s) * a.N + w.node) * a.n_sel : nullptr;
@@ -1185,7 +1189,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             if (!ok && lane == 0) {
                 const uint32_t ns = n_stages, from = n_t > ns ? n_t - ns : 0;
                 for (uint32_t x = from; x < n_t; ++x) tc::mbar_wait(&full[x % ns], (x / ns) & 1u);
-                if (!is_v && pw == 0 && n_q > 0) tc::mbar_wait(&bar.q_full, (n_q - 1) & 1u);
             }
             __syncwarp();
         }
