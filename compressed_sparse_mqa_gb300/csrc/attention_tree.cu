@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     const long long qrow = (static_cast<long long>(w.s) * a.N) * a.H + w.row0 + row;
                     const long long prow = static_cast<long long>(w.part) * g.tile_rows + row;
                     if (!direct && valid && c0 == 0) g.part_ml[prow] = make_float2(m, l);
-#pragma unroll 2
+#pragma unroll 1
                     for (int c = c0; c < c1; ++c) {                // 32 columns at a time
                         uint32_t o[32];
                         tc::ld_x32(col_o + c * 32, o);

@@ -547,13 +547,15 @@ def _launch_on(where, kv, stream):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _tree_args(where, kv, N, n_node, parent):
-    if n_node.shape != (kv.B,) or (parent is not None and parent.shape != (kv.B, N)):
+def _tree_args(where, kv, B, N, n_node, parent):
+    if n_node.shape != (B,) or (parent is not None and parent.shape != (B, N)):
         raise ValueError(f"{where}: n_node [B], parent [B, N] (or None)")
     return _arg(n_node, _I32, kv.device, "n_node"), _arg(parent, _I32, kv.device, "parent")
 
 
 def _draft_rows(where, kv, comp_k, comp_v):
+    if comp_k is None or comp_v is None:
+        raise ValueError(f"{where}: comp_k and comp_v are required")
     shape = comp_k.shape
     if len(shape) != 3 or shape[0] != kv.B or shape[2] != kv.D or comp_v.shape != shape:
         raise ValueError(f"{where}: compressed rows [B, cap, D]")
@@ -569,30 +571,24 @@ def _nodes(where, parent, N):
     return N
 
 
-def _required(where, **tensors):
-    for name, t in tensors.items():
-        if t is None:
-            raise ValueError(f"{where}: {name} is required")
-
-
 def _marshal_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, rot_off: int = 0,
                           interleaved: bool = True, q=None, q_out=None, stream=None):
-    shape = k.shape
-    if len(shape) != 3 or shape[0] != kv.B or shape[2] != kv.D or v.shape != shape:
+    shape, B, D = k.shape, kv.B, kv.D
+    if len(shape) != 3 or shape[0] != B or shape[2] != D or v.shape != shape:
         raise ValueError("paged_append: k, v [B, N, D]")
     N, H = shape[1], 0
     if (q is None) != (q_out is None):
         raise ValueError("paged_append: q and q_out come together")
     if q is not None:
         qs = q.shape
-        if len(qs) != 4 or qs[0] != kv.B or qs[1] != N or qs[3] != kv.D or q_out.shape != qs:
+        if len(qs) != 4 or qs[0] != B or qs[1] != N or qs[3] != D or q_out.shape != qs:
             raise ValueError("paged_append: q, q_out [B, N, H, D]")
         H = qs[2]
     st, dev = _launch_on("paged_append", kv, stream), kv.device
-    pn, pp = _tree_args("paged_append", kv, N, n_tok, parent)
-    return (ctypes.byref(kv), _arg(k, _F16, dev, "k"), _arg(v, _F16, dev, "v"), N, pn, pp, _arg(inv_freq, _F32, dev, "inv_freq"),
-            0 if inv_freq is None else 2 * inv_freq.numel(), rot_off, 1 if interleaved else 0,
-            _arg(q, _F16, dev, "q"), H, _arg(q_out, _F16, dev, "q_out"), st)
+    pn, pp = _tree_args("paged_append", kv, B, N, n_tok, parent)
+    return (ctypes.byref(kv), _arg(k, _F16, dev, "k"), _arg(v, _F16, dev, "v"), N, pn, pp,
+            _arg(inv_freq, _F32, dev, "inv_freq"), 0 if inv_freq is None else 2 * inv_freq.numel(), rot_off,
+            1 if interleaved else 0, _arg(q, _F16, dev, "q"), H, _arg(q_out, _F16, dev, "q_out"), st)
 
 
 def ds4a_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, rot_off: int = 0,
@@ -610,7 +606,7 @@ def _marshal_compress_tree(kv: PagedKVDesc, n_node, parent, score_w, ratio: int,
     if state.shape != (kv.B, 2 + 2 * kv.D) or score_w.numel() != kv.D:
         raise ValueError("compress_tree: state [B, 2 + 2D], score_w [D]")
     st, dev = _launch_on("compress_tree", kv, stream), kv.device
-    pn, pp = _tree_args("compress_tree", kv, N, n_node, parent)
+    pn, pp = _tree_args("compress_tree", kv, kv.B, N, n_node, parent)
     ck, cv, cap = _draft_rows("compress_tree", kv, comp_k, comp_v)
     return (ctypes.byref(kv), N, pn, pp, _arg(score_w, _F32, dev, "score_w"), ratio, _arg(state, _F32, dev, "state"), ck, cv, cap,
             st)
@@ -641,7 +637,7 @@ def _marshal_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, 
             raise ValueError("attn_tree: sel [B, N, n_sel]")
         n_sel = ss[2]
     st, dev = _launch_on("attn_tree", kv, stream), kv.device
-    pn, pp = _tree_args("attn_tree", kv, N, n_node, parent)
+    pn, pp = _tree_args("attn_tree", kv, kv.B, N, n_node, parent)
     ck, cv, cap = _draft_rows("attn_tree", kv, comp_k, comp_v) if ratio else (None, None, 0)
     return (ctypes.byref(kv), _arg(q, _F16, dev, "q"), N, H, pn, pp, window, ck, cv, cap, ratio, _arg(sel, _I32, dev, "sel"), n_sel,
             scale, _arg(out, _F16, dev, "out"), _arg(ws, _U8, dev, "ws"), 0 if ws is None else ws.numel(), st)
@@ -659,27 +655,29 @@ def ds4a_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, comp
 
 def _marshal_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w=None, ratio: int = 0, state=None,
                          state_out=None, comp_k=None, comp_v=None, k_idx=None, N=None, stream=None):
-    N = _nodes("commit_tree", parent, N)
-    if leaf.shape != (kv.B,) or len_out.shape != (kv.B,):
+    N, B = _nodes("commit_tree", parent, N), kv.B
+    if leaf.shape != (B,) or len_out.shape != (B,):
         raise ValueError("commit_tree: leaf, len_out [B]")
     st, dev = _launch_on("commit_tree", kv, stream), kv.device
-    pn, pp = _tree_args("commit_tree", kv, N, n_node, parent)
-    ck = cv = None
+    pn, pp = _tree_args("commit_tree", kv, B, N, n_node, parent)
+    pw = ps = po = ck = cv = None
     cap = d_idx = 0
     if ratio:
-        _required("commit_tree", score_w=score_w, state=state, state_out=state_out, comp_k=comp_k, comp_v=comp_v)
-        if state.shape != (kv.B, 2 + 2 * kv.D) or state_out.shape != state.shape or score_w.numel() != kv.D:
+        if score_w is None or state is None or state_out is None:
+            raise ValueError("commit_tree: score_w, state and state_out are required")
+        shape = state.shape
+        if shape != (B, 2 + 2 * kv.D) or state_out.shape != shape or score_w.numel() != kv.D:
             raise ValueError("commit_tree: state, state_out [B, 2 + 2D], score_w [D]")
         ck, cv, cap = _draft_rows("commit_tree", kv, comp_k, comp_v)
-    else:
-        score_w = state = state_out = None
+        pw, ps = _arg(score_w, _F32, dev, "score_w"), _arg(state, _F32, dev, "state")
+        po = _arg(state_out, _F32, dev, "state_out")
     if k_idx is not None:
-        if k_idx.dim() != 3 or k_idx.shape[:2] != (kv.B, cap):
+        shape = k_idx.shape
+        if len(shape) != 3 or shape[0] != B or shape[1] != cap:
             raise ValueError("commit_tree: k_idx [B, cap, d_idx], rows as comp_k")
-        d_idx = k_idx.shape[2]
-    return (ctypes.byref(kv), N, pn, pp, _arg(leaf, _I32, dev, "leaf"), _arg(len_out, _I64, dev, "len_out"),
-            _arg(score_w, _F32, dev, "score_w"), ratio, _arg(state, _F32, dev, "state"),
-            _arg(state_out, _F32, dev, "state_out"), ck, cv, cap, _arg(k_idx, _F16, dev, "k_idx"), d_idx, st)
+        d_idx = shape[2]
+    return (ctypes.byref(kv), N, pn, pp, _arg(leaf, _I32, dev, "leaf"), _arg(len_out, _I64, dev, "len_out"), pw, ratio, ps,
+            po, ck, cv, cap, _arg(k_idx, _F16, dev, "k_idx"), d_idx, st)
 
 
 def ds4a_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w=None, ratio: int = 0, state=None,
