@@ -24,7 +24,9 @@ constexpr int kMaxPairs = 64;   // rotated pairs: head_dim / 2
 // key and its value; a row is D / 16 items of 32 bytes: unit u of the rotated dims holds the 8
 // pairs 8u .. 8u+7 (two adjacent 16-byte chunks when interleaved, chunks u and u + rot/16
 // otherwise), the other items two of the remaining chunks.  Bound by memory: a 2048-token
-// chunk with 64 heads moves 69 MB.  The inputs do not depend on the session's counts, so a
+// chunk with 64 heads moves 69 MB in 13.8 us (5.0 TB/s; 17 us = 4.0 TB/s with inputs from DRAM); one
+// token takes 3.4 us, a launch and three dependent loads.  Two or six items a thread instead of
+// three: 14.3 and 19 us.  The inputs do not depend on the session's counts, so a
 // thread's loads are in flight while length, angle and page are looked up.
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs a, int t_cta, int d_shift) {
