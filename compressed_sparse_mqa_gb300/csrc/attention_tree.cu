@@ -970,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     const int chunks = tile_chunks(n_runs, tile0 + t);
                     for (int c = 0; c < chunks && ok; ++c, ++n_c) {
                         const uint32_t buf = n_c & 1u;
-                        // all this round's waits at once, so that nothing stands between its products
+                        // all waits at once, so that nothing stands between the two products
                         bool good = wait_k();
                         if (c == 0) {
                             // The item before has been read: the accumulator is free, and every earlier V tile has

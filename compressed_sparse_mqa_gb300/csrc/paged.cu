@@ -5,7 +5,7 @@
 // rotated to its position p (len + i, or len + depth in a tree).  Rotation of the pair
 // (x1, x2) with frequency f_j: (x1 c - x2 s, x1 s + x2 c), c = cos(p f_j), s = sin(p f_j).
 //
-// The angle is taken in turns as a 64-bit fraction: p times round(f_j / 2 pi * 2^64),
+// The angle is taken in turns as a 64-bit fraction: p times floor(f_j / 2 pi * 2^64),
 // modulo 2^64, is the angle modulo one turn, so whole turns drop out of the integer
 // product exactly.  f_j / 2 pi is computed in double (2^-53 relative), so at position
 // 2^31 and f = 1 the angle is within 2^-24 turns of the true one and at 2^20 within 2^-35;
@@ -20,11 +20,24 @@ constexpr int kItems = 3;       // work items a thread, all loaded before the fi
 constexpr int kMaxTokens = 16;  // tokens of one CTA
 constexpr int kMaxPairs = 64;   // rotated pairs: head_dim / 2
 
+// x modulo 1 as a fraction of 2^64: the significand shifted to its place, whole turns and what is
+// below 2^-64 dropped.  (binary64 units are few: floor, subtraction, product and conversion in
+// binary64 took 0.4 us of a 2048-token chunk.)
+DS4A_DEVINL unsigned long long turn_fraction(double x) {
+    const long long b = __double_as_longlong(x);
+    const int shift = static_cast<int>((b >> 52) & 0x7ff) - 1075 + 64;      // x = significand * 2^(shift - 64)
+    const unsigned long long m = (static_cast<unsigned long long>(b) & 0xfffffffffffffull) | 0x10000000000000ull;
+    unsigned long long f = 0;
+    if (shift >= 0 && shift < 64) f = m << shift;
+    else if (shift < 0 && shift > -64) f = m >> -shift;
+    return b < 0 ? 0ull - f : f;
+}
+
 // A CTA takes t_cta consecutive tokens of a session.  A token's rows are its query heads, its
 // key and its value; a row is D / 16 items of 32 bytes: unit u of the rotated dims holds the 8
 // pairs 8u .. 8u+7 (two adjacent 16-byte chunks when interleaved, chunks u and u + rot/16
 // otherwise), the other items two of the remaining chunks.  Bound by memory: a 2048-token
-// chunk with 64 heads moves 69 MB in 13.8 us (5.0 TB/s; 17 us = 4.0 TB/s with inputs from DRAM); one
+// chunk with 64 heads moves 69 MB in 13.4 us (5.2 TB/s; 17 us = 4.0 TB/s with inputs from DRAM); one
 // token takes 3.4 us, a launch and three dependent loads.  Two or six items a thread instead of
 // three: 14.3 and 19 us.  The inputs do not depend on the session's counts, so a
 // thread's loads are in flight while length, angle and page are looked up.
@@ -86,9 +99,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs
     for (int w = tid; w < count * (rot / 2); w += blockDim.x) {
         const int tt = w / (rot / 2), j = w - tt * (rot / 2);
         const long long pos = ses.len + (a.parent ? __popcll(s_mask[i0 + tt]) - 1 : i0 + tt);
-        const double turns = static_cast<double>(a.inv_freq[j]) * 0.15915494309189533577;   // 1 / (2 pi)
-        const double frac = turns - floor(turns);
-        const unsigned long long step = __double2ull_rn(frac * 18446744073709551616.0);
+        const unsigned long long step = turn_fraction(static_cast<double>(a.inv_freq[j]) * 0.15915494309189533577);   // 1 / (2 pi)
         const int ang = static_cast<int>((step * static_cast<unsigned long long>(pos)) >> 32);
         float sn, cs;
         sincospif(static_cast<float>(ang) * 4.656612873077392578125e-10f, &sn, &cs);   // half-turns: 2^-31

@@ -131,6 +131,31 @@ def test_append_far_position():
     assert (np.abs(got - want) <= 2.0 ** -11 * np.abs(want) + 8 * 2.0 ** -20).all()
 
 
+@pytest.mark.parametrize("ln", [0, 1, (1 << 24) + 12345])
+@pytest.mark.parametrize("inv", [
+    [-3.5, -1.0, -1e-3, -100.25],       # turns backwards
+    [0.0, -0.0, 1e-30, 1e-42],          # no turn at all: zeros, below 2^-64 of a turn, a denormal
+    [100.25, 6.5, 2.0 ** -40, 1.0],     # more than a turn a token, and next to none
+])
+def test_append_unusual_frequencies(ln, inv):
+    """The angle, in radians: two roundings of f / 2 pi <= 16 to 2^-53 each, times 2^24 positions
+    (2^-21.3); what falls below 2^-64 and 2^-32 turns (2^-29); float(angle) (2^-23.3); the sine's
+    own error (2^-23); the oracle's product (2^-22.4): below 2^-20.  The products and their sum add
+    2^-23 of |x1| + |x2| < 8: in all below 8 * 2^-19, beside the rounding to 16 bits."""
+    page, D = 65536, 64
+    mp = ln // page + 1
+    table = torch.zeros(1, mp, dtype=torch.int32, device="cuda")    # every page is page 0: only one slot is written
+    pk = torch.zeros(1, page, D, dtype=torch.float16, device="cuda")
+    kv = ds4a.paged_kv_desc(pk, torch.zeros_like(pk), table, torch.tensor([ln], device="cuda"))
+    inv = np.array(inv * 2, np.float32)
+    k = np.random.default_rng(1).uniform(-3, 3, (1, 1, D)).astype(np.float16)
+    ds4a.ds4a_paged_append(kv, dev(k), dev(k), torch.ones(1, dtype=torch.int32, device="cuda"), None, dev(inv), 16, True)
+    no_error()
+    want = R.rotate(k[0, 0].astype(np.float64), ln, inv, 16, True)
+    got = pk[0, ln % page].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - want) <= 2.0 ** -11 * np.abs(want) + 8 * 2.0 ** -19).all()
+
+
 # ---- rows completed in the draft, commit --------------------------------------------------------
 
 def comp_setup(rng, c, ratio, D, room=2):
