@@ -42,7 +42,7 @@ DS4A_DEVINL Session load_session(const PagedKV &kv, const int32_t *n_node, int N
     if (r.n < 0 || r.n > N || r.len < 0) {
         record_error(err, DS4A_ERR_DEVICE_INDEX);
         r.ok = false;
-    } else if (r.len + r.n > static_cast<long long>(kv.max_pages) * kv.page) {
+    } else if (r.len > static_cast<long long>(kv.max_pages) * kv.page - r.n) {   // len + n may not fit 64 bits
         record_error(err, DS4A_ERR_CAPACITY);
         r.ok = false;
     }
