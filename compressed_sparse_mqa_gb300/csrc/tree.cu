@@ -101,6 +101,10 @@ __global__ void __launch_bounds__(kTreeThreads) compress_tree_kernel(CompressTre
     pdl_trigger();
     const Session ses = load_session(a.kv, a.n_node, a.N, s, tid == 0 ? a.err : nullptr);
     if (!ses.ok) return;
+    if (ses.len >= (a.cap - a.N + 1) * a.ratio) {   // len / ratio > cap - N: the draft's rows would be committed ones
+        if (tid == 0) record_error(a.err, DS4A_ERR_CAPACITY);
+        return;
+    }
     if (!tree_masks(a.parent ? a.parent + static_cast<long long>(s) * a.N : nullptr, ses.n, s_mask, s_ptr, a.err))
         return;
     if (tid < kMaxNodes) {

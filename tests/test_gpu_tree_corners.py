@@ -48,3 +48,23 @@ def test_lengths_near_the_end_of_int64_are_refused(call, ln):
         check_attn(c, par, q, None, None, None, 64, 0, 0.1, out)
     if call == "commit":
         assert lo.tolist() == [21 + len(R.paths_of(par[0], 4)[3]), -9, 15 + len(R.paths_of(par[2], 3)[2])]
+
+
+def test_compress_tree_leaves_committed_rows_past_the_capacity_alone():
+    """Session 0 has more committed rows than lie before the draft's: those rows keep their bits."""
+    rng = np.random.default_rng(8)
+    N, D = 4, 64
+    c = Cache(rng, [6, 3], [4, 4], D, 16, N)
+    c.draft()
+    ck, cv, w, state, dck, dcv, dw = comp_setup(rng, c, 1, D)
+    keep = 4 + N                                     # rows 0 .. 3 before the draft's; session 0 has six
+    dck, dcv = dck[:, :keep].contiguous(), dcv[:, :keep].contiguous()
+    before = dck.clone(), dcv.clone()
+    ds4a.ds4a_compress_tree(c.upload(), c.dn, None, dw, 1, state, dck, dcv, N=N)
+    torch.cuda.synchronize()
+    assert ds4a.ds4a_last_device_error() == ds4a.DS4A_ERR_CAPACITY
+    for b, a in zip(before, (dck, dcv)):
+        assert torch.equal(b[0].view(torch.int16), a[0].view(torch.int16))
+        assert torch.isfinite(a[1, 4:]).all()        # session 1's four rows (a row of one token is the token)
+    at = c.rows(1, range(3, 7))
+    assert np.array_equal(dck[1, 4:].cpu().numpy(), c.k[at]) and np.array_equal(dcv[1, 4:].cpu().numpy(), c.v[at])
