@@ -195,14 +195,15 @@ DS4A_DEVINL uint32_t run_bits(const WorkInfo &w, int v, int lo, unsigned long lo
     v -= w.comp_runs;
     return v * kRun < kMaxNodes ? static_cast<uint32_t>(cmp >> (v * kRun)) & 0xffffu : 0u;
 }
-// every key of tile t is valid for every row (with readable pages)
+// every key of tile t is valid for every row (with readable pages).  Slots and rows go up to 2^31 - 16, so
+// nothing is added to one: the room behind it is compared.
 DS4A_DEVINL bool tile_full(const WorkInfo &w, int t) {
     const int v = t * kRuns;
     if (v < w.raw_runs) {
         const int slot = w.t0 + v * kRun;
-        return slot >= w.lo_max && slot + kTK <= w.len;
+        return slot >= w.lo_max && w.len - slot >= kTK;
     }
-    return (v - w.raw_runs + kRuns) * kRun <= w.n_vis0;
+    return v - w.raw_runs + kRuns <= w.n_vis0 / kRun;
 }
 
 // some row masks keys of tile t whose V rows are read (not the list's: a skipped entry loads zeros)
@@ -236,7 +237,7 @@ DS4A_DEVINL int session_t0(const AttnTreeArgs &a, int len) {
     const long long lo = static_cast<long long>(len) - a.window + 1;
     return (lo < 0 ? 0 : min(static_cast<int>(lo), len)) & ~(kRun - 1);
 }
-DS4A_DEVINL int runs_of(int rows) { return (rows + kRun - 1) / kRun; }
+DS4A_DEVINL int runs_of(int rows) { return rows / kRun + (rows % kRun != 0); }   // rows + kRun may not fit 32 bits
 
 // The set-up warp's walk over the sessions, 32 at a time.  A session counts its row tiles that
 // have nodes (64 sessions of 16 .. 32 nodes, 406 of 512 row tiles in use: 3 items a CTA at
@@ -468,9 +469,9 @@ __device__ void make_work(const Args &g, const Item id, W &w, int lane) {
         w.len = len;
         w.n = n;
         w.t0 = t0;
-        w.raw_runs = (len + n - t0 + kRun - 1) / kRun;
+        w.raw_runs = runs_of(len + n - t0);
         w.n_vis0 = kSel ? a.n_sel : n_done;
-        w.comp_runs = (w.n_vis0 + kRun - 1) / kRun;
+        w.comp_runs = runs_of(w.n_vis0);
         w.n_runs = w.raw_runs + w.comp_runs;
         // the draft's rows (stream: the session's all, as in the walk), as far as one of the item's nodes attends any
         if (!kSel && a.ratio > 0 && g.mode == kStream) w.n_runs += runs_of(n);
@@ -538,7 +539,7 @@ __device__ __noinline__ uint3 poison_bits(const Work &w, int node, int word) {
         bool hit;
         if (key < kMaxNodes) hit = (raw >> key) & 1ull;
         else if (key < kEdge) hit = (cmp >> (key - kMaxNodes)) & 1ull;
-        else hit = w.lo_min + key - kEdge >= lo;
+        else hit = static_cast<unsigned>(w.lo_min) + (key - kEdge) >= static_cast<unsigned>(lo);
         if (!hit) continue;
         nan |= w.poison[key][word];
         pi |= w.poison[key][4 + word];
@@ -1046,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                                     if ((any >> key) & 1u) {
                                         if (v < w.raw_runs) {
                                             const int tk = w.t0 + v * kRun + key;
-                                            slot = tk >= w.len ? tk - w.len : kEdge + tk - w.lo_min;
+                                            slot = tk >= w.len ? tk - w.len : kEdge + (tk - w.lo_min);
                                         } else {
                                             slot = kMaxNodes + (v - w.raw_runs - w.comp_runs) * kRun + key;
                                         }

@@ -68,3 +68,74 @@ def test_compress_tree_leaves_committed_rows_past_the_capacity_alone():
         assert torch.isfinite(a[1, 4:]).all()        # session 1's four rows (a row of one token is the token)
     at = c.rows(1, range(3, 7))
     assert np.array_equal(dck[1, 4:].cpu().numpy(), c.k[at]) and np.array_equal(dcv[1, 4:].cpu().numpy(), c.v[at])
+
+
+# page * max_pages = 2^31 - 16, the most slots that pages of multiples of 16 can hold
+FAR_PAGE, FAR_PAGES = 8176, 262657
+
+
+@pytest.mark.parametrize("window,ln", [(128, 2147483600), (200, 2147483611), (128, 2147483628), (64, 2147483568)])
+def test_attn_tree_at_the_last_positions(window, ln):
+    """Slots up to 2^31 - 17: a node attends its own tokens, and what was never written or is another
+    branch's (NaN there) stays out."""
+    rng = np.random.default_rng(ln % 97)
+    N, H, D = 4, 16, 64
+    table = np.zeros((1, FAR_PAGES), np.int32)       # page 0: NaN, nobody reads it
+    table[0, -1] = 1
+    k, v = np.full((2 * FAR_PAGE, D), NAN16), np.full((2 * FAR_PAGE, D), NAN16)
+    rows = R.slot_rows(table[0], FAR_PAGE, range(ln - window, ln + N))
+    k[rows], v[rows] = (rng.standard_normal((len(rows), D)).astype(np.float16) for _ in range(2))
+    par, n = np.array([[-1, 0, 0, 1]], np.int32), 4
+    v[R.slot_rows(table[0], FAR_PAGE, [ln + 2])] = NAN16
+    q = rng.standard_normal((1, N, H, D)).astype(np.float16)
+    pool = lambda a: dev(a.reshape(2, FAR_PAGE, D))
+    kv = ds4a.paged_kv_desc(pool(k), pool(v), dev(table), torch.tensor([ln], device="cuda"))
+    out = torch.full(q.shape, 7.0, dtype=torch.float16, device="cuda")
+    ws = torch.zeros(ds4a.ds4a_attn_tree_workspace_bytes(1, N, H, D), dtype=torch.uint8, device="cuda")
+    ds4a.ds4a_attn_tree(kv, dev(q), torch.tensor([n], dtype=torch.int32, device="cuda"), dev(par), window, None, None, 0,
+                        None, 0.125, out, ws)
+    no_error()
+    for i, path in enumerate(R.paths_of(par[0], n)):
+        if i == 2:
+            assert torch.isnan(out[0, i]).all()
+            continue
+        kk, vv = R.node_keys(k, v, None, None, table[0], FAR_PAGE, ln, path, N, window, 0, None)
+        want, tol = R.attend(q[0, i], kk, vv, 0.125)
+        assert (np.abs(out[0, i].cpu().numpy().astype(np.float64) - want) <= tol).all(), i
+
+
+def test_append_and_commit_at_the_last_positions():
+    """The angle, in radians, at positions below 2^31 with f <= 1: f / 2 pi is off by two roundings of
+    2^-53 each, which is 2^-21 at 2^31 positions; what is dropped below 2^-64 and 2^-32 of a turn 2^-29;
+    float(angle) 2^-23.3; the sine's own error 2^-23: below 2^-20.  The products and their sum add
+    2^-23 of |x1| + |x2| < 8: in all below 8 * 2^-19, beside the rounding to 16 bits.  The oracle
+    takes the angle modulo a turn in integers."""
+    rng = np.random.default_rng(0)
+    D, N, ln = 64, 4, (1 << 31) - 16 - 4
+    turn = int("6283185307179586476925286766559005768394338798750211641949889184615632812572417997256069650684234135")  # 2 pi * 10^99
+    table = np.zeros((1, FAR_PAGES), np.int32)
+    table[0, -1] = 1
+    pk = torch.zeros(2, FAR_PAGE, D, dtype=torch.float16, device="cuda")
+    pv, length = torch.zeros_like(pk), torch.tensor([ln], device="cuda")
+    kv = ds4a.paged_kv_desc(pk, pv, dev(table), length)
+    k = rng.uniform(-3, 3, (1, N, D)).astype(np.float16)
+    inv = np.array([1.0, 0.7, 2.0 ** -20, 1e-3, 1e-6, 0.5, 0.25, 0.0], np.float32)
+    n = torch.tensor([N], dtype=torch.int32, device="cuda")
+    par = np.array([[-1, 0, 0, 2]], np.int32)
+    ds4a.ds4a_paged_append(kv, dev(k), dev(k), n, dev(par), dev(inv), 16, True)
+    no_error()
+    at = R.slot_rows(table[0], FAR_PAGE, range(ln, ln + N))
+    got = pk.view(-1, D).cpu().numpy()[at].astype(np.float64)
+    for i, path in enumerate(R.paths_of(par[0], N)):
+        pos = ln + len(path) - 1
+        th = []
+        for f in inv:
+            num, den = float(f).as_integer_ratio()
+            th.append((pos * num * 10 ** 99 // den) % turn / 10 ** 99)
+        want = R.rotate(k[0, i].astype(np.float64), 1, np.array(th), 16, True)
+        assert (np.abs(got[i] - want) <= 2.0 ** -11 * np.abs(want) + 8 * 2.0 ** -19).all(), i
+    ds4a.ds4a_commit_tree(kv, n, dev(par), torch.tensor([3], dtype=torch.int32, device="cuda"), length)
+    no_error()
+    assert length.item() == ln + 3
+    moved = pk.view(-1, D).cpu().numpy()[at].astype(np.float64)
+    assert np.array_equal(moved[:3], got[[0, 2, 3]])
