@@ -529,8 +529,8 @@ __device__ __noinline__ void clean_chunk(Work *w, unsigned char *at, int slot, i
     w->dirty = 1;
 }
 
-// Values that are not finite, of the keys that `node` attends: into columns col .. col+31 of
-// its accumulator.
+// Values that are not finite, of the keys that `node` attends: added to columns col .. col+31 of
+// its accumulator, which holds those of the keys that every row attends.
 __device__ __noinline__ uint3 poison_bits(const Work &w, int node, int word) {
     const int lo = w.lo[node];
     const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
@@ -552,8 +552,8 @@ DS4A_DEVINL void add_poison(const Work &w, int node, int col, uint32_t (&o)[32])
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
         if ((p.x >> e) & 1u) o[e] = 0x7fffffffu;
-        else if ((p.y >> e) & 1u) o[e] = 0x7f800000u;
-        else if ((p.z >> e) & 1u) o[e] = 0xff800000u;
+        else if ((p.y >> e) & 1u) o[e] = __float_as_uint(__uint_as_float(o[e]) + INFINITY);
+        else if ((p.z >> e) & 1u) o[e] = __float_as_uint(__uint_as_float(o[e]) - INFINITY);
     }
 }
 

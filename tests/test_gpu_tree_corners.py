@@ -139,3 +139,33 @@ def test_append_and_commit_at_the_last_positions():
     assert length.item() == ln + 3
     moved = pk.view(-1, D).cpu().numpy()[at].astype(np.float64)
     assert np.array_equal(moved[:3], got[[0, 2, 3]])
+
+
+# ways of cutting the work: two row blocks, one (its sides joined), one line of key tiles (its pieces joined)
+CUTS = [(40, 10, 64, 96, 4, lambda s: 130 + 11 * s), (3, 6, 16, 200, 0, lambda s: 300 + s),
+        (2, 6, 64, 1 << 30, 16, lambda s: 6000 - 900 * s)]
+
+
+@pytest.mark.parametrize("B,N,H,window,ratio,lens", CUTS)
+@pytest.mark.parametrize("common,own", [(np.nan, np.inf), (-np.inf, np.inf), (np.inf, -np.inf), (np.nan, -np.inf),
+                                        (np.inf, np.inf)])
+def test_attn_tree_adds_values_that_are_not_finite(B, N, H, window, ratio, lens, common, own):
+    """A token that every node attends and a drafted one that some do, both with a value that is not
+    finite in one column: the nodes that attend both get their sum."""
+    rng = np.random.default_rng(B + N)
+    ln, n = [lens(s) for s in range(B)], [N - s % 2 for s in range(B)]
+    c, par, q, ck, cv, _ = attn_setup(rng, ln, n, N, H, 128, 16, window, ratio, 0, "tree")
+    for s in range(B):
+        c.v[c.rows(s, [ln[s] - 30]), 5] = common
+        c.v[c.rows(s, [ln[s] + 1]), 5] = own
+    out = run_attn(c, par, q, ck, cv, None, window, ratio, 0.09)
+    no_error()
+    o = out.float().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        both = common + own
+    for s in range(B):
+        for i, path in enumerate(R.paths_of(par[s], n[s])):
+            want = both if 1 in path else common
+            got = o[s, i, :, 5]
+            assert np.isnan(got).all() if np.isnan(want) else (got == want).all(), (s, i)
+            assert np.isfinite(np.delete(o[s, i], 5, 1)).all()
