@@ -1268,7 +1268,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
             for (int u = 0; u < kBatch; ++u) {
                 const int k = k0 + u * kPerRow;
                 const float wk = __shfl_sync(0xffffffffu, w, k & 31);
-                if (k < 32 && c + k < pieces && wk != 0.f) {
+                if (k < 32 && c + k < pieces) {   // weight 0 too: 0 * NaN is NaN
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) o[e] += wk * x[u][e];
                 }

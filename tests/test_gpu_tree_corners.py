@@ -169,3 +169,21 @@ def test_attn_tree_adds_values_that_are_not_finite(B, N, H, window, ratio, lens,
             got = o[s, i, :, 5]
             assert np.isnan(got).all() if np.isnan(want) else (got == want).all(), (s, i)
             assert np.isfinite(np.delete(o[s, i], 5, 1)).all()
+
+
+def test_attn_tree_keeps_nan_of_far_smaller_weights():
+    """One node over a long cache, cut into pieces: a NaN in V whose weight underflows beside the
+    others' is still a term of the sum."""
+    rng = np.random.default_rng(3)
+    ln = 9000
+    c, par, q, _, _, _ = attn_setup(rng, [ln], [1], 1, 8, 128, 64, 1 << 30, 0, 0, "chain")
+    q[0, 0] = np.abs(q[0, 0]) + np.float16(0.5)
+    c.k[c.rows(0, range(ln))] = np.float16(-2.0)     # scores below -64: 2^-160 beside the newest token's
+    c.k[c.rows(0, [ln])] = np.float16(1.0)
+    c.v[c.rows(0, [100]), 7] = NAN16
+    out = run_attn(c, par, q, None, None, None, 1 << 30, 0, 1.0)
+    no_error()
+    assert torch.isnan(out[0, 0, :, 7]).all()
+    rest = torch.cat([out[0, 0, :, :7], out[0, 0, :, 8:]], 1)
+    v = dev(c.v[c.rows(0, [ln])])[0]
+    assert torch.equal(rest, torch.cat([v[:7], v[8:]]).expand_as(rest))
