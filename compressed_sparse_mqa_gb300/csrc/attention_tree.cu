@@ -79,6 +79,7 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr uint64_t kWaitNs = 10000000000ull;   // some waits last an item, which over a cache of 10^8 tokens is a second
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.f;            // lazy rescale threshold (log2 units)
+constexpr float kLowest = -3.402823466e38f;   // reference of a row whose scores are all -inf
 constexpr int kEdge = 2 * kMaxNodes;       // first window-edge entry of the poison table
 constexpr int kPoison = 3 * kMaxNodes;     // keys that only some rows attend: nodes, their rows, the window's edge
 
@@ -174,6 +175,10 @@ DS4A_DEVINL float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
+}
+// 1 / sum of a row's weights: 0 for a row without keys, NaN for scores that are all -inf
+DS4A_DEVINL float inverse(float m, float l) {
+    return l != 0.f ? 1.f / l : (m == -INFINITY ? 0.f : __uint_as_float(0x7fffffffu));
 }
 DS4A_DEVINL int clamp16(int x) { return x < 0 ? 0 : (x > kRun ? kRun : x); }
 
@@ -655,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             const int row = (sides2 ? side * kTK : 0) + r;        // row in the item
             const int node = min(kMaxNodes - 1, node_of(g, w.row0 + row));
             float m = -INFINITY, l = 0.f;
+            uint32_t seen = 0;                       // not 0: the row attends a key
             bool first = true;
             for (int t = sides2 ? t0 : t0 + side; t < t1; t += sides2 ? 1 : 2) {
                 const uint16_t *inf = info + ((n_t + t - t0) & (kInfo - 1)) * kRuns;
@@ -669,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     tc::ld_x32(col + 32, x[1]);
                     const uint32_t full = *reinterpret_cast<const uint32_t *>(wh + c * kChunkRuns);   // a byte per run
                     tc::wait_ld();
+                    seen |= full;
                     if (full != 0x01010101u) {
                         const int lo = w.lo[node];
                         const unsigned long long raw = w.raw[node], cmp = w.cmp[node];
@@ -677,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                             if ((full >> (8 * u)) & 1u) continue;
                             const uint32_t bits =
                                 run_bits<kSel>(w, t * kRuns + c * kChunkRuns + u, lo, raw, cmp, inf);
+                            seen |= bits;
 #pragma unroll
                             for (int e = 0; e < kRun; ++e)
                                 if (!((bits >> e) & 1u)) x[u / 2][(u & 1) * kRun + e] = 0xff800000u;   // -inf
@@ -739,6 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             }
             n_t += t1 - t0;
             // ---- end of the item ----
+            // l is 0 with m = -inf for a row without keys (its output is 0), with m = kLowest for one whose scores
+            // are all -inf (NaN, unless another side or piece has a finite score: kLowest weighs nothing beside it)
+            if (m == -INFINITY && seen) m = kLowest;
             const bool have = !first;                              // this side has tiles
             const bool joined = !sides2 && t1 - t0 > 1;            // side 1 holds part of the same rows
             if (have) {
@@ -767,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     wait(&bar.chk[it & 1], it >> 1);
                     const bool valid = row < w.rows, direct = w.pieces == 1;
                     const int dirty = w.dirty;
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    const float inv = inverse(m, l);
                     const long long qrow = (static_cast<long long>(w.s) * a.N) * a.H + w.row0 + row;
                     const long long prow = static_cast<long long>(w.part) * g.tile_rows + row;
                     if (!direct && valid && c0 == 0) g.part_ml[prow] = make_float2(m, l);
@@ -1287,7 +1298,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
             for (int x = 1; x < kPerRow; ++x) o[e] += s_o[x][lane * kPer + e];
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = inverse(m, l);
     uint32_t h[kPer / 2];
 #pragma unroll
     for (int e = 0; e < kPer / 2; ++e) h[e] = pack_half2(o[2 * e] * inv, o[2 * e + 1] * inv);

@@ -187,3 +187,44 @@ def test_attn_tree_keeps_nan_of_far_smaller_weights():
     rest = torch.cat([out[0, 0, :, :7], out[0, 0, :, 8:]], 1)
     v = dev(c.v[c.rows(0, [ln])])[0]
     assert torch.equal(rest, torch.cat([v[:7], v[8:]]).expand_as(rest))
+
+
+@pytest.mark.parametrize("B,N,H,window,ratio,lens", CUTS)
+def test_attn_tree_over_scores_that_are_all_minus_infinity(B, N, H, window, ratio, lens):
+    """A softmax without a finite score is NaN, as by its definition; with one finite score it is
+    that row's value."""
+    rng = np.random.default_rng(7)
+    ln, n = [lens(s) for s in range(B)], [N] * B
+    c, par, q, ck, cv, _ = attn_setup(rng, ln, n, N, H, 128, 16, window, ratio, 0, "roots")
+    q[..., 0] = np.float16(1.0)
+    q[:, :, 1, 0] = np.float16(-1.0)                 # head 1: +inf scores, NaN in any case
+    for s in range(B):
+        c.k[c.rows(s, range(ln[s] + n[s])), 0] = np.float16(-np.inf)
+    if ratio:
+        ck[:, :, 0] = np.where(np.isnan(ck[:, :, 0]), NAN16, np.float16(-np.inf))
+    k2 = [c.rows(s, [ln[s] + 2])[0] for s in range(B)]
+    for s in range(0, B, 2):                         # even sessions: node 2 has a finite score for itself
+        c.k[k2[s], 0] = np.float16(0.25)
+    out = run_attn(c, par, q, ck, cv, None, window, ratio, 0.09)
+    no_error()
+    for s in range(B):
+        for i in range(N):
+            if s % 2 == 0 and i == 2:
+                o = torch.cat([out[s, i, :1], out[s, i, 2:]])
+                assert torch.equal(o, dev(c.v[k2[s]]).expand_as(o)), s
+                assert torch.isnan(out[s, i, 1]).all()
+            else:
+                assert torch.isnan(out[s, i]).all(), (s, i)
+
+
+def test_attn_tree_one_key_of_minus_infinity():
+    """A window of one token, whose score is -inf."""
+    rng = np.random.default_rng(2)
+    c, par, q, _, _, _ = attn_setup(rng, [20], [2], 2, 8, 64, 16, 1, 0, 0, "roots")
+    q[..., 3] = np.float16(2.0)
+    c.k[c.rows(0, [20]), 3] = np.float16(-np.inf)
+    out = run_attn(c, par, q, None, None, None, 1, 0, 0.1)
+    no_error()
+    assert torch.isnan(out[0, 0]).all()
+    v = dev(c.v[c.rows(0, [21])])[0]
+    assert torch.equal(out[0, 1], v.expand_as(out[0, 1]))
