@@ -42,8 +42,12 @@
 // of 128 keys per side the two sides fell into step, both in their softmax, then both waiting
 // for products: 4200 cycles a 256-row tile, of which the tensor core worked 2050).  The price is
 // that a product with N = 64 is bound by reading Q from shared memory, 48 cycles instead of 32.
-// The softmax reference of a row is raised (and O rescaled) only when a score exceeds it
-// by 2^8; p <= 256 fits 16 bits, sums are binary32.
+// The softmax reference of a row is raised (and O rescaled) only when a score is 2^15 above it, to 2^7
+// below that score: the largest weight is 2^7 .. 2^15, which fits 16 bits, and half a step of the
+// smallest ones is 2^-32 of it (with weights of 2^0 .. 2^8 it was 2^-25: of 2^18 keys of weight 2^-25
+// beside one of 1 all were lost or rounded to 2^-24).  Sums are binary32, of the weights before they
+// are rounded to 16 bits for the product with V; the accumulator drops what is below about 2^-25 of
+// what it holds.
 //
 // Measured (device time): 4 sessions of up to 64 nodes x 64 heads over 32768 tokens 172 us =
 // 1354 TFLOP/s, bound by the tensor pipe and the shared memory that feeds it; 64 sessions of up
@@ -78,7 +82,7 @@ static_assert(kWarps == 16, "128 registers a thread");
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr uint64_t kWaitNs = 10000000000ull;   // some waits last an item, which over a cache of 10^8 tokens is a second
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescale = 8.f;            // lazy rescale threshold (log2 units)
+constexpr float kLift = 7.f, kRescale = 15.f;   // log2 units: a reference is kLift below the score that set it, kept up to kRescale above
 constexpr float kLowest = -3.402823466e38f;   // reference of a row whose scores are all -inf
 constexpr int kEdge = 2 * kMaxNodes;       // first window-edge entry of the poison table
 constexpr int kPoison = 3 * kMaxNodes;     // keys that only some rows attend: nodes, their rows, the window's edge
@@ -701,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     // raise the reference: at the first finite score, then only past the threshold
                     float alpha = 1.f;
                     if (top > m + kRescale || (m == -INFINITY && top > m)) {
-                        alpha = ex2(m - top);
-                        m = top;
+                        alpha = ex2(m - (top - kLift));
+                        m = top - kLift;
                         l *= alpha;
                     }
                     if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {

@@ -228,3 +228,40 @@ def test_attn_tree_one_key_of_minus_infinity():
     assert torch.isnan(out[0, 0]).all()
     v = dev(c.v[c.rows(0, [21])])[0]
     assert torch.equal(out[0, 1], v.expand_as(out[0, 1]))
+
+
+@pytest.mark.parametrize("first", [True, False])
+def test_attn_tree_one_dominant_key_over_a_long_tail(first):
+    """2^18 keys of weight e^-17 .. e^-21 and V = 1 beside one of weight 1 and V = 0: 1e-2 .. 2e-4 in all.
+
+    A weight is rounded to 16 bits beside a reference of 2^7 or more, half a step being 2^-11 of it, or
+    2^-25 below the smallest normal, 2^-32 of the largest weight: 2^-11 of the result and n 2^-32.  The
+    scores have one product, exact; log2(e), its product with the score and the difference are off by
+    2^-24 of at most 32 each, and 2^x by 2^-22: 2^-17 in a weight.  The sum: parts of 64 (64 2^-24) and
+    at most 4096 of those (2^-12).  The accumulator, of binary32, holds only what these keys gave; each
+    product may lose 2^-24 of it: for 2^17 keys a side, the accumulator half full on average, 2^-8.  The
+    result's own rounding: 2^-11 of it, or 2^-25."""
+    B = torch.cuda.get_device_properties(0).multi_processor_count     # a whole row tile a CTA
+    N, H, D, page, ln = 2, 64, 128, 4096, 1 << 18
+    pages = ln // page + 1
+    k, v = np.zeros((pages, page, D), np.float16), np.ones((pages, page, D), np.float16)
+    at = 5 if first else ln - 1
+    k.reshape(-1, D)[at, 0] = 17.0
+    v.reshape(-1, D)[at] = 0.0
+    k.reshape(-1, D)[ln:ln + 2, 0] = -50.0           # the drafted tokens themselves: nothing
+    q = np.zeros((B, N, H, D), np.float16)
+    q[:, :, :, 0] = (1 + np.arange(H) / 256).astype(np.float16)
+    table = np.tile(np.arange(pages, dtype=np.int32), (B, 1))         # the sessions share their pages
+    kv = ds4a.paged_kv_desc(dev(k), dev(v), dev(table), torch.full((B,), ln, device="cuda"))
+    n = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    out = torch.zeros(B, N, H, D, dtype=torch.float16, device="cuda")
+    ws = torch.zeros(ds4a.ds4a_attn_tree_workspace_bytes(B, N, H, D), dtype=torch.uint8, device="cuda")
+    ds4a.ds4a_attn_tree(kv, dev(q), n, None, 1 << 30, None, None, 0, None, 1.0, out, ws)
+    no_error()
+    got = out.cpu().numpy().astype(np.float64)
+    gap = q[0, 0, :, 0].astype(np.float64) * 17.0
+    tail = (ln - 1) * np.exp(-gap)
+    want = (tail / (1 + tail))[:, None]
+    tol = want * (2.0 ** -8 + 2 * 2.0 ** -11 + 2.0 ** -12 + 2.0 ** -16) + ln * 2.0 ** -32 + 2.0 ** -25
+    err = np.abs(got - want)
+    assert (err <= tol).all(), float((err / tol).max())
