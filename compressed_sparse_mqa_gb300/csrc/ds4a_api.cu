@@ -4,6 +4,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <thread>
 
 #include "ds4a_common.cuh"
 #include "ds4a_internal.h"
@@ -33,7 +34,59 @@ bool pdl_enabled() {
     return on;
 }
 
-int make_ctx(void *stream, ds4a::Ctx &c) {
+// Some kernels read tokens, queries and key rows before their dependency wait (the header lists each
+// call's early reads).  Programmatic dependence orders those reads behind nothing, so a call that
+// may make them is launched without it directly behind a call that wrote such arrays.
+enum class Early { kReads, kNone, kWrites };
+
+// The streams whose last call wrote them; a capture's calls come behind the capture's own, the others behind
+// the others.
+struct Written {
+    int dev = 0;
+    void *stream = nullptr;
+    std::thread::id thread;            // the per-thread default stream is one stream a thread
+    bool now = false;                  // outside captures
+    unsigned long long capture = 0;    // in this one
+};
+constexpr int kMaxWritten = 1024;
+Written g_written[kMaxWritten];
+std::atomic<int> g_n_written{0};       // kMaxWritten + 1: there were more, and every stream counts as one of them
+std::mutex g_written_mu;
+
+// Notes a call on a stream; whether the call before it there wrote what may be read early.
+bool behind_written(int dev, void *stream, Early e) {
+    if (e != Early::kWrites && g_n_written.load(std::memory_order_acquire) == 0) return false;
+    Written w;
+    w.dev = dev;
+    w.stream = stream == cudaStreamLegacy ? nullptr : stream;
+    if (stream == cudaStreamPerThread) w.thread = std::this_thread::get_id();
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long capture = 0;
+    if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &capture) != cudaSuccess) {
+        cudaGetLastError();            // the legacy stream beside another one's capture
+        status = cudaStreamCaptureStatusNone;
+    }
+    if (status == cudaStreamCaptureStatusNone) capture = 0;
+    std::lock_guard<std::mutex> lock(g_written_mu);
+    int n = g_n_written.load(std::memory_order_relaxed), at = 0;
+    if (n > kMaxWritten) return true;
+    while (at < n && !(g_written[at].dev == w.dev && g_written[at].stream == w.stream && g_written[at].thread == w.thread)) ++at;
+    if (at < n) w = g_written[at];
+    if (capture == 0) w.capture = 0;   // the stream's capture is over
+    const bool found = capture ? w.capture == capture : w.now;
+    if (capture) w.capture = e == Early::kWrites ? capture : (found ? 0 : w.capture);
+    else w.now = e == Early::kWrites;
+    if (w.now || w.capture) {
+        if (at < kMaxWritten) g_written[at] = w;
+        if (at == n) ++n;
+    } else if (at < n) {
+        g_written[at] = g_written[--n];
+    }
+    g_n_written.store(n, std::memory_order_release);
+    return found;
+}
+
+int make_ctx(void *stream, ds4a::Ctx &c, Early early = Early::kReads) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DS4A_ERR_CUDA;
     DeviceInfo &d = g_dev[dev];
@@ -54,6 +107,7 @@ int make_ctx(void *stream, ds4a::Ctx &c) {
     c.err = d.err;
     c.num_sms = d.num_sms;
     c.pdl = pdl_enabled();
+    if (behind_written(dev, stream, early) && early == Early::kReads) c.pdl = false;
     return DS4A_OK;
 }
 
@@ -457,7 +511,7 @@ int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16
     // queries in place, or apart
     if (q && q_out != q && overlap(q, q_out, static_cast<size_t>(kv->B) * N * H * kv->D * 2)) return DS4A_ERR_ARG;
     ds4a::Ctx c;
-    rc = make_ctx(stream, c);
+    rc = make_ctx(stream, c, Early::kWrites);
     if (rc != DS4A_OK) return rc;
     const ds4a::AppendArgs a{paged_view(kv), k, v, q, q_out, n_tok, parent, inv_freq, c.err, N, q ? H : 0, rot, rot_off,
                              interleaved != 0};
@@ -478,7 +532,7 @@ int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, 
     if (!aligned(score_w, 4) || !aligned(state, 4) || !aligned(comp_k, 16) || !aligned(comp_v, 16)) return DS4A_ERR_ARG;
     if (cap < N) return DS4A_ERR_CAPACITY;
     ds4a::Ctx c;
-    rc = make_ctx(stream, c);
+    rc = make_ctx(stream, c, Early::kNone);
     if (rc != DS4A_OK) return rc;
     const ds4a::CompressTreeArgs a{paged_view(kv), n_node, parent, score_w, state, comp_k, comp_v, cap, c.err, N, ratio};
     return from_cuda(ds4a::launch_compress_tree(a, kv->B, c));
@@ -512,7 +566,7 @@ int ds4a_attn_tree(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, c
     if (!ws || !aligned(ws, 256) || ws_bytes < ds4a_attn_tree_workspace_bytes(kv->B, N, H, kv->D))
         return DS4A_ERR_WORKSPACE;
     ds4a::Ctx c;
-    rc = make_ctx(stream, c);
+    rc = make_ctx(stream, c, Early::kNone);
     if (rc != DS4A_OK) return rc;
     const ds4a::AttnTreeArgs a{paged_view(kv), q, comp_k, comp_v, n_node, parent, sel, out, ws, c.err,
                                window, cap, N, H, ratio, sel ? n_sel : 0, scale, 0.f};
@@ -540,7 +594,7 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
         if (cap < N) return DS4A_ERR_CAPACITY;
     }
     ds4a::Ctx c;
-    rc = make_ctx(stream, c);
+    rc = make_ctx(stream, c, Early::kWrites);
     if (rc != DS4A_OK) return rc;
     const ds4a::CommitTreeArgs a{paged_view(kv), n_node, parent, leaf, len_out, score_w, state, state_out, comp_k, comp_v,
                                  k_idx, cap, c.err, N, ratio, k_idx ? d_idx : 0};

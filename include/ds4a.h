@@ -40,10 +40,11 @@
  *     them: cache state such as key rows and window rows, and its queries), and
  *     waits for the kernel ahead to finish before it reads anything else or
  *     writes anything.  So the kernel directly ahead on the stream must not
- *     write those early inputs.  The calls of this library never write another
- *     call's early inputs (the drafted-token calls below excepted: they say which
- *     arrays that concerns); a kernel that does not use programmatic launch
- *     finishes before the next call starts.  With the environment variable
+ *     write those early inputs.  The calls of this library may: directly behind
+ *     one that writes arrays of that kind (ds4a_paged_append, ds4a_commit_tree) a
+ *     call with early reads is launched without programmatic dependence and
+ *     starts once they are written.  A kernel that does not use programmatic
+ *     launch finishes before the next call starts.  With the environment variable
  *     DS4A_PDL=0 (read once per process) every kernel waits for the kernel
  *     ahead before it starts.
  */
@@ -523,9 +524,7 @@ int ds4a_decode_layer_step(const ds4a_decode_layer_t *layer, long long pos, cons
  * cap - N (DS4A_ERR_CAPACITY).  A page id outside the pool (DS4A_ERR_DEVICE_INDEX): the
  * token is not written and not attended, a row that would pool it is not written, and a
  * commit leaves the session alone.
- * Early reads: none.  These calls write arrays that other calls read early when the
- * caller passes them there (q_out as a query, committed key rows as k_idx): do not
- * put such a call directly behind the call that writes them.
+ * Early reads: none.
  */
 typedef struct ds4a_paged_kv {
     int B;                       /* sessions, 0 .. 65535 */

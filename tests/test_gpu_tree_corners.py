@@ -265,3 +265,85 @@ def test_attn_tree_one_dominant_key_over_a_long_tail(first):
     tol = want * (2.0 ** -8 + 2 * 2.0 ** -11 + 2.0 ** -12 + 2.0 ** -16) + ln * 2.0 ** -32 + 2.0 ** -25
     err = np.abs(got - want)
     assert (err <= tol).all(), float((err / tol).max())
+
+
+def captured(*calls):
+    """The calls directly behind one another in a graph."""
+    for call in calls:
+        call()                                       # once on the stream: set-up is done
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call in calls:
+            call()
+    return graph
+
+
+@pytest.mark.parametrize("N", [1, 700])
+def test_decode_attention_directly_behind_an_append(N):
+    """ds4a_attn_decode reads queries and window rows before its dependency wait: an append directly
+    ahead of it that writes them has finished by then."""
+    rng = np.random.default_rng(N)
+    D, H, page, ln = 128, 64, 64, 40
+    mp = (ln + N) // page + 1
+    pk, pv = (torch.randn(mp, page, D, device="cuda").half() for _ in range(2))
+    kv = ds4a.paged_kv_desc(pk, pv, torch.arange(mp, dtype=torch.int32, device="cuda")[None], torch.tensor([ln], device="cuda"))
+    k, v = (dev(rng.standard_normal((1, N, D)).astype(np.float16)) for _ in range(2))
+    q = dev(rng.standard_normal((1, N, H, D)).astype(np.float16))
+    qo, n = torch.zeros_like(q), torch.tensor([N], dtype=torch.int32, device="cuda")
+    inv = dev((10000.0 ** (-np.arange(32) / 32)).astype(np.float32))
+    w0 = ln + N - 33                                 # the newest 33 tokens as the window
+    fk, fv = pk.view(-1, D), pv.view(-1, D)
+    out = torch.zeros(H, D, dtype=torch.float16, device="cuda")
+    append = lambda: ds4a.ds4a_paged_append(kv, k, v, n, None, inv, 64, True, q, qo)
+    decode = lambda: ds4a.ds4a_attn_decode(qo[0, N - 1], fk[w0:ln + N], fv[w0:ln + N], None, None, None, 0, 0.088, out)
+    graph = captured(append, decode)
+    torch.cuda.synchronize()
+    append()
+    torch.cuda.synchronize()
+    decode()
+    torch.cuda.synchronize()
+    want = out.clone()
+    for _ in range(50):
+        qo.fill_(math.nan)
+        fk[ln:ln + N] = math.nan
+        fv[ln:ln + N] = math.nan
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        no_error()
+        assert torch.equal(out, want)
+
+
+def test_indexer_directly_behind_a_commit():
+    """ds4a_indexer_topk reads key rows before its dependency wait: a commit directly ahead of it that
+    moves them into place has finished by then."""
+    rng = np.random.default_rng(4)
+    D, N, ratio, ln, topk = 128, 64, 1, 70, 32
+    c = Cache(rng, [ln], [N], D, 16, N)
+    c.draft()
+    ck, cv, w, state, dck, dcv, dw = comp_setup(rng, c, ratio, D)
+    cap = ck.shape[1]
+    kidx = torch.randn(1, cap, D, device="cuda").half()
+    kidx[0, cap - N:] *= 4                           # the path's rows rank first
+    kv, leaf, lo = c.upload(), torch.tensor([N - 1], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    qi = torch.randn(1, D, device="cuda").half()
+    sel = torch.zeros(1, topk, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(ds4a.ds4a_indexer_workspace_bytes(1, cap, topk), dtype=torch.uint8, device="cuda")
+    so = state.clone()
+    commit = lambda: ds4a.ds4a_commit_tree(kv, c.dn, None, leaf, lo, dw, ratio, state, so, dck, dcv, kidx, N=N)
+    rank = lambda: ds4a.ds4a_indexer_topk(qi, kidx[0], ln + N, ratio, topk, sel, None, ws, n_rows=ln + N)
+    graph = captured(commit, rank)
+    commit()
+    torch.cuda.synchronize()
+    rank()
+    torch.cuda.synchronize()
+    want = sel.clone()
+    assert (want >= ln).sum() > topk // 2
+    for _ in range(50):
+        kidx[0, ln:ln + N] = 0
+        sel.fill_(-7)
+        torch.cuda.synchronize()
+        graph.replay()
+        no_error()
+        assert torch.equal(sel, want)
