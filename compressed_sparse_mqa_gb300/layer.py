@@ -572,7 +572,8 @@ class TreeDecodeLayer:
         tokens; parent [B, N] (int array-like on the host: an earlier node or -1) and n_node [B]
         its shape; on an indexer layer q_idx [B, N, d_idx], and kidx [B, N, d_idx] holding the
         indexer key of the row that each node completes (other nodes' are ignored).  Returns
-        out [B, N, H, D].  Replaces an earlier draft that was not accepted."""
+        out [B, N, H, D].  Replaces an earlier draft that was not accepted.  Arguments that do not
+        fit raise before anything changes; if a call fails behind that, there is no draft."""
         par = np.ascontiguousarray(parent, dtype=np.int32)
         n_host = [int(n) for n in n_node]
         if par.shape != (self.B, self.N) or len(n_host) != self.B:
@@ -584,7 +585,8 @@ class TreeDecodeLayer:
                 raise ValueError(f"verify: session {s} has no room for {n} more tokens")
         if self.topk and (q_idx is None or kidx is None):
             raise ValueError("verify: an indexer layer needs the nodes' indexer queries and keys")
-        self.parent_host, self.n_host = par, n_host
+        self._check_tensors(k, v, q, q_idx, kidx)
+        self.n_host = [0] * self.B       # nothing to accept until every call is enqueued: the cache changes from here on
         self.parent.copy_(torch.from_numpy(par))
         self.n_node.copy_(torch.tensor(n_host, dtype=torch.int32))
         inv, off, inter = self.rope if self.rope is not None else (None, 0, True)
@@ -596,23 +598,38 @@ class TreeDecodeLayer:
                                     self.comp_v)
         if self.topk:
             self.kidx[:, self.cap - self.N:] = kidx
-            self._select(q_idx)
+            self._select(q_idx, par, n_host)
         ds4a.ds4a_attn_tree(self.kv, qr, self.n_node, self.parent, self.W, self.comp_k, self.comp_v, self.ratio, self.sel,
                             self.scale, self.out, self.ws)
+        self.parent_host, self.n_host = par, n_host
         return self.out
 
-    def _select(self, q_idx):
+    def _check_tensors(self, k, v, q, q_idx, kidx):
+        """Raises for tensors of a draft that a call would refuse or read past, before anything changes."""
+        B, N, dev = self.B, self.N, self.kv.device
+        for name, t, shape in (("k", k, (B, N, self.D)), ("v", v, (B, N, self.D)), ("q", q, (B, N, self.H, self.D))):
+            if ds4a._arg(t, torch.float16, dev, f"verify: {name}") is None or t.shape != shape:
+                raise ValueError(f"verify: {name} {list(shape)}")
+        if self.topk:
+            shape = (B, N, self.kidx.shape[2])
+            for name, t in (("q_idx", q_idx), ("kidx", kidx)):
+                if not isinstance(t, torch.Tensor) or t.shape != shape:
+                    raise ValueError(f"verify: {name} {list(shape)}")
+            if q_idx.dtype != torch.float16 or q_idx.get_device() != dev:
+                raise ValueError("verify: q_idx is fp16, on the cache's device")
+
+    def _select(self, q_idx, parent, n_node):
         """Every node's kept rows.  The indexer ranks rows by position, so the nodes of one
         root-to-leaf path are one call over the committed keys and that path's own (laid out
         behind them, in rows that are free until the commit)."""
-        par, dev = self.parent_host, self.kidx.device
+        dev = self.kidx.device
         for s in range(self.B):
-            n, ln = self.n_host[s], self.len_host[s]
+            n, ln = n_node[s], self.len_host[s]
             done = set()
-            for leaf in [i for i in range(n) if i not in set(par[s, :n])]:
+            for leaf in [i for i in range(n) if i not in set(parent[s, :n])]:
                 path = [leaf]
-                while par[s, path[0]] >= 0:
-                    path.insert(0, int(par[s, path[0]]))
+                while parent[s, path[0]] >= 0:
+                    path.insert(0, int(parent[s, path[0]]))
                 rows = [i for d, i in enumerate(path) if (ln + d + 1) % self.ratio == 0]
                 n_vis = ln // self.ratio
                 if rows:
