@@ -574,7 +574,7 @@ class TreeDecodeLayer:
         indexer key of the row that each node completes (other nodes' are ignored).  Returns
         out [B, N, H, D].  Replaces an earlier draft that was not accepted.  Arguments that do not
         fit raise before anything changes; if a call fails behind that, there is no draft."""
-        par = np.ascontiguousarray(parent, dtype=np.int32)
+        par = np.array(parent, dtype=np.int32)      # a copy: accept walks it, and the caller may use its array again
         n_host = [int(n) for n in n_node]
         if par.shape != (self.B, self.N) or len(n_host) != self.B:
             raise ValueError("verify: parent [B, N], n_node [B]")

@@ -85,3 +85,17 @@ def test_a_draft_whose_calls_fail_cannot_be_accepted(call, monkeypatch):
         L.accept([3])
     for a, b in zip(state_of(T), state_of(C)):
         assert torch.equal(a, b)
+
+
+def test_parents_are_the_layers_own_copy():
+    """The caller's array of parents may be used again between verify and accept."""
+    T, C = make(), make()
+    d = draft(1, [-1, 0, 1, 2, 3])
+    C.verify(**draft(1, [-1, 0, 1, 2, 3]))
+    T.verify(**d)
+    d["parent"][:] = -1
+    T.accept([4])
+    C.accept([4])
+    assert T.len_host == C.len_host == [101 + 5]
+    for a, b in zip(state_of(T), state_of(C)):
+        assert torch.equal(a, b)
