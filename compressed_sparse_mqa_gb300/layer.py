@@ -498,7 +498,9 @@ class TreeDecodeLayer:
     instance's position is committed, so a session starts with p + 1 tokens.  Every node's
     output is that of decoding its path token by token.  `room` is how many tokens beyond the
     longest session the pages and the compressed rows have place for (a draft counts
-    until it is committed or dropped).  rope = (inv_freq [rot/2] float32 tensor, first rotated
+    until it is committed or dropped); both are laid out once, pages that left the window are not
+    used again, and a draft past the room is refused.  Layers that pool their indexer keys from
+    per-token ones are refused.  rope = (inv_freq [rot/2] float32 tensor, first rotated
     dim, interleaved) rotates keys and queries to their positions on the way in; None takes
     them as already encoded.
     """
@@ -512,7 +514,10 @@ class TreeDecodeLayer:
         singles = [DecodeLayer(inst, device=device, cap_extra=1) for inst in instances]
         L0 = singles[0]
         for L in singles:
-            if (L.H, L.D, L.W, L.ratio, L.topk) != (L0.H, L0.D, L0.W, L0.ratio, L0.topk) or L.pooled_keys:
+            if L.pooled_keys:
+                raise ValueError("TreeDecodeLayer: layers that pool their indexer keys are not supported (verify takes "
+                                 "the keys of completed rows)")
+            if (L.H, L.D, L.W, L.ratio, L.topk) != (L0.H, L0.D, L0.W, L0.ratio, L0.topk):
                 raise ValueError("TreeDecodeLayer: sessions must share the layer's shape and schedule")
         self.B, self.N, self.page, self.rope = len(singles), max_nodes, page, rope
         self.H, self.D, self.W, self.ratio, self.topk, self.scale = L0.H, L0.D, L0.W, L0.ratio, L0.topk, L0.scale

@@ -1,4 +1,6 @@
 """TreeDecodeLayer when a call on it fails, and when the caller's arrays change after one."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -99,3 +101,10 @@ def test_parents_are_the_layers_own_copy():
     assert T.len_host == C.len_host == [101 + 5]
     for a, b in zip(state_of(T), state_of(C)):
         assert torch.equal(a, b)
+
+
+def test_layers_that_pool_their_indexer_keys_are_refused_by_name():
+    inst = instances(2, [100])[0]
+    inst = dataclasses.replace(inst, kidx_tok=np.zeros((inst.raw_k.shape[0], 128), np.float16))
+    with pytest.raises(ValueError, match="pool their indexer keys"):
+        TreeDecodeLayer([inst], max_nodes=N, room=32, page=16)
