@@ -586,11 +586,15 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
     if (k_idx && (d_idx < 8 || d_idx > 256 || d_idx % 8 != 0)) return DS4A_ERR_UNSUPPORTED;
     if (kv->B == 0) return DS4A_OK;
     if (!leaf || !len_out || !aligned(leaf, 4) || !aligned(len_out, 8)) return DS4A_ERR_ARG;
+    // in place, or apart: a session's outputs may not be what another session's CTA reads
+    const size_t len_bytes = static_cast<size_t>(kv->B) * 8, state_bytes = static_cast<size_t>(kv->B) * (2 + 2 * kv->D) * 4;
+    if (len_out != kv->len && overlap(len_out, kv->len, len_bytes)) return DS4A_ERR_ARG;
     if (ratio > 0) {
         if (!score_w || !state || !state_out || !comp_k || !comp_v) return DS4A_ERR_ARG;
         if (!aligned(score_w, 4) || !aligned(state, 4) || !aligned(state_out, 4) || !aligned(comp_k, 16) ||
             !aligned(comp_v, 16) || !aligned(k_idx, 16))
             return DS4A_ERR_ARG;
+        if (state_out != state && overlap(state_out, state, state_bytes)) return DS4A_ERR_ARG;
         if (cap < N) return DS4A_ERR_CAPACITY;
     }
     ds4a::Ctx c;

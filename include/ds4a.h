@@ -610,9 +610,10 @@ size_t ds4a_attn_tree_workspace_bytes(int B, int N, int H, int D);
  * len[s] + a.  A path token's state update and rows are those of ds4a_compress_append fed
  * one token at a time.
  *   leaf       [B] int32.
- *   len_out    [B] int64; may be kv->len's array.
+ *   len_out    [B] int64; may be kv->len's array, and may not overlap it otherwise.
  *   score_w, state, state_out, comp_k, comp_v, cap: as ds4a_compress_tree (state_out may be
- *              state; it is written when (len + a) % ratio != 0); all NULL with ratio = 0.
+ *              state, and may not overlap it otherwise; it is written when (len + a) % ratio
+ *              != 0); all NULL with ratio = 0.
  *   k_idx      [B, cap, d_idx] fp16, 16-byte aligned, d_idx multiple of 8, 8 .. 256; or NULL.
  */
 int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, const int32_t *parent,
