@@ -347,3 +347,62 @@ def test_indexer_directly_behind_a_commit():
         graph.replay()
         no_error()
         assert torch.equal(sel, want)
+
+
+@pytest.mark.parametrize("ratio", [4, 128])
+def test_three_drafts_one_after_the_other(ratio):
+    """Drafts checked and committed three times over one cache: every node's output is what
+    ds4a_attn_decode gives over its path, rows completed in a draft among what the next attends."""
+    rng = np.random.default_rng(ratio)
+    N, H, D, room = 12, 64, 128, 40
+    c = Cache(rng, [300, 118, 0], [11, 9, 6], D, 16, N + room)
+    c.N = N
+    ck0, cv0, w, state, ck, cv, dw = comp_setup(rng, c, ratio, D, room=N + room)
+    kv = c.upload()
+    out = torch.zeros(3, N, H, D, dtype=torch.float16, device="cuda")
+    qr = torch.zeros_like(out)
+    inv = dev((10000.0 ** (-np.arange(32) / 32)).astype(np.float32))
+    ws = torch.zeros(ds4a.ds4a_attn_tree_workspace_bytes(3, N, H, D), dtype=torch.uint8, device="cuda")
+    pk, pv = c.dk.view(-1, D), c.dv.view(-1, D)
+    drafts = 0
+    for _ in range(3):
+        lens = c.dlen.tolist()
+        par = R.random_parents(rng, 3, N)
+        dpar, leaf = dev(par), [n - 1 for n in c.n]
+        k, v = (dev(rng.standard_normal((3, N, D)).astype(np.float16)) for _ in range(2))
+        q = dev(rng.standard_normal((3, N, H, D)).astype(np.float16))
+        ds4a.ds4a_paged_append(kv, k, v, c.dn, dpar, inv, 64, True, q, qr)
+        ds4a.ds4a_compress_tree(kv, c.dn, dpar, dw, ratio, state, ck, cv)
+        ds4a.ds4a_attn_tree(kv, qr, c.dn, dpar, 128, ck, cv, ratio, None, 0.088, out, ws)
+        no_error()
+        after = []
+        for s in range(3):
+            for i, path in enumerate(R.paths_of(par[s], c.n[s])):
+                st, tk, tv = state[s].clone(), ck[s].clone(), cv[s].clone()
+                slots = [lens[s] + j for j in path]
+                for d, t in enumerate(slots):
+                    r = c.rows(s, [t])[0]
+                    ds4a.ds4a_compress_append(pk[r:r + 1], pv[r:r + 1], dw, ratio, lens[s] + d, st, tk, tv)
+                p = lens[s] + len(path) - 1
+                win = [t if t < lens[s] else slots[t - lens[s]] for t in range(max(0, p - 127), p + 1)]
+                at = torch.from_numpy(c.rows(s, win)).cuda()
+                ref = torch.empty(H, D, dtype=torch.float16, device="cuda")
+                wk, wv = pk[at], pv[at]
+                torch.cuda.synchronize()
+                ds4a.ds4a_attn_decode(qr[s, i], wk, wv, tk, tv, None, (p + 1) // ratio, 0.088, ref)
+                torch.cuda.synchronize()
+                # two 16-bit results of one value: both are within the repository's 2e-3 of it
+                assert float((ref.float() - out[s, i].float()).abs().max()) <= 4e-3, (drafts, s, i)
+                if i == leaf[s]:
+                    after.append((lens[s] + len(path), st, tk, tv))
+        ds4a.ds4a_commit_tree(kv, c.dn, dpar, dev(np.array(leaf, np.int32)), c.dlen, dw, ratio, state, state, ck, cv)
+        no_error()
+        for s, (ln, st, tk, tv) in enumerate(after):
+            assert c.dlen[s].item() == ln
+            m = ln // ratio
+            assert torch.equal(ck[s, :m].view(torch.int16), tk[:m].view(torch.int16))
+            assert torch.equal(cv[s, :m].view(torch.int16), tv[:m].view(torch.int16))
+            if ln % ratio:
+                assert torch.equal(state[s].view(torch.int32), st.view(torch.int32))
+        drafts += 1
+    assert drafts == 3 and c.dlen.max().item() <= c.mp * c.page
