@@ -94,7 +94,7 @@ struct alignas(16) WorkInfo {
     int lo[kMaxNodes];                     // first committed slot that node i attends
     unsigned long long any_raw, all_raw, any_cmp, all_cmp;   // over the item's nodes
     int lo_min, lo_max;
-    int s, len, n, t0;                     // session; first slot of the key runs
+    int s, len, t0;                        // session; committed tokens; first slot of the key runs
     int raw_runs, comp_runs, n_runs;       // runs of raw slots, of committed compressed rows (sel: of the list), in all
     int n_vis0;                            // committed compressed rows (sel: list entries)
     int node;                              // sel: the node
@@ -476,7 +476,6 @@ __device__ void make_work(const Args &g, const Item id, W &w, int lane) {
         w.lo_max = lo_max;
         w.s = s;
         w.len = len;
-        w.n = n;
         w.t0 = t0;
         w.raw_runs = runs_of(len + n - t0);
         w.n_vis0 = kSel ? a.n_sel : n_done;

@@ -1,5 +1,4 @@
-// paged.cu -- the paged token cache: appending tokens with their position rotation, and
-// committing the accepted path of a draft.
+// paged.cu -- the paged token cache: appending tokens with their position rotation.
 //
 // Append: token i of session s goes to slot len + i; its key and its query heads are
 // rotated to its position p (len + i, or len + depth in a tree).  Rotation of the pair

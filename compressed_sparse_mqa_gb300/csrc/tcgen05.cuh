@@ -33,10 +33,6 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, bool a_mn_maj
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// byte offset of fp16 element c (0..63) of row r inside a 128-byte-swizzled atom column
-DS4A_DEVINL uint32_t sw128(int r, int c) {
-    return static_cast<uint32_t>(r * 128 + ((((c >> 3) ^ (r & 7)) << 4) | ((c & 7) * 2)));
-}
 // byte offset of 16-byte chunk ch (0..7) of row r inside a 128-byte-swizzled atom column
 DS4A_DEVINL uint32_t sw128_chunk(int r, int ch) { return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4)); }
 
@@ -110,19 +106,6 @@ DS4A_DEVINL bool mbar_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns = 1
 
 template <int N> DS4A_DEVINL void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N> DS4A_DEVINL void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
-
-// named barriers over n threads (whole warps)
-DS4A_DEVINL void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
-// the same barrier, returning whether any of the threads passed pred = true
-DS4A_DEVINL bool bar_any(int id, int n, bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(n)
-        : "memory");
-    return r != 0;
-}
 
 // two binary32 values in one 64-bit register: one instruction for both
 DS4A_DEVINL uint64_t pack2(float a, float b) {
