@@ -554,7 +554,7 @@ int ds4a_attn_tree(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, c
     rc = check_tree(N, n_node, parent);
     if (rc != DS4A_OK) return rc;
     if (window < 1 || ratio < 0 || cap < 0 || n_sel < 0 || (sel && (ratio == 0 || n_sel < 1))) return DS4A_ERR_ARG;
-    if (!(scale > 0.f) || scale > 3.0e38f) return DS4A_ERR_ARG;
+    if (!(scale > 0.f) || scale > 2.3e38f) return DS4A_ERR_ARG;   // scale * log2(e) is finite
     if (ratio > 1024 || cap > 0x7fffffffLL || n_sel > 0x3fffffff) return DS4A_ERR_UNSUPPORTED;
     if (kv->B == 0) return DS4A_OK;
     if (!q || !out || (ratio > 0 && (!comp_k || !comp_v))) return DS4A_ERR_ARG;

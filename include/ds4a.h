@@ -586,7 +586,7 @@ int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, 
  *   sel        [B, N, n_sel] int32 (as ds4a_indexer_topk writes them: negative entries are
  *              skipped; entries not yet complete at p are skipped and recorded as
  *              DS4A_ERR_DEVICE_INDEX), or NULL.
- *   scale      softmax scale, > 0 and finite.
+ *   scale      softmax scale, > 0, at most 2.3e38.
  *   out        [B, N, H, D] fp16, not overlapping q (DS4A_ERR_ARG).
  *   ws         ds4a_attn_tree_workspace_bytes(B, N, H, D) bytes, 256-byte aligned; its contents
  *              need not be set or kept.  Calls that share one workspace must be
