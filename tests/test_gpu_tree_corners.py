@@ -406,3 +406,35 @@ def test_three_drafts_one_after_the_other(ratio):
                 assert torch.equal(state[s].view(torch.int32), st.view(torch.int32))
         drafts += 1
     assert drafts == 3 and c.dlen.max().item() <= c.mp * c.page
+
+
+def test_bound_calls_repeat_the_calls():
+    """ds4a.bind marshals each of the four calls once: the same bits as the calls themselves."""
+    def setup():
+        rng = np.random.default_rng(6)
+        N, H, D, ratio = 5, 16, 64, 3
+        c, par, q, _, _, _ = attn_setup(rng, [50, 13], [5, 4], N, H, D, 16, 32, 0, 0, "tree")
+        _, _, _, state, ck, cv, dw = comp_setup(rng, c, ratio, D)
+        kv = c.upload()
+        k, v = (dev(rng.standard_normal((2, N, D)).astype(np.float16)) for _ in range(2))
+        t = dict(q=dev(q), qo=torch.zeros(2, N, H, D, dtype=torch.float16, device="cuda"), par=dev(par), lo=torch.zeros_like(c.dlen),
+                 out=torch.zeros(2, N, H, D, dtype=torch.float16, device="cuda"), so=state.clone(), state=state, ck=ck, cv=cv,
+                 leaf=torch.tensor([4, 2], dtype=torch.int32, device="cuda"), k=k, v=v, w=dw,
+                 inv=dev((10000.0 ** (-np.arange(16) / 16)).astype(np.float32)),
+                 ws=torch.zeros(ds4a.ds4a_attn_tree_workspace_bytes(2, N, H, D), dtype=torch.uint8, device="cuda"))
+        calls = [("ds4a_paged_append", (kv, k, v, c.dn, t["par"], t["inv"], 16, False, t["q"], t["qo"])),
+                 ("ds4a_compress_tree", (kv, c.dn, t["par"], dw, ratio, state, ck, cv)),
+                 ("ds4a_attn_tree", (kv, t["qo"], c.dn, t["par"], 32, ck, cv, ratio, None, 0.125, t["out"], t["ws"])),
+                 ("ds4a_commit_tree", (kv, c.dn, t["par"], t["leaf"], t["lo"], dw, ratio, state, t["so"], ck, cv))]
+        return c, t, calls
+    a, b = setup(), setup()
+    for name, args in a[2]:
+        getattr(ds4a, name)(*args)
+    for call in [ds4a.bind(name, *args) for name, args in b[2]]:
+        call()
+    no_error()
+    for x, y in zip((a[0].dk, a[0].dv) + tuple(a[1][n] for n in ("qo", "out", "lo", "so", "ck", "cv")),
+                    (b[0].dk, b[0].dv) + tuple(b[1][n] for n in ("qo", "out", "lo", "so", "ck", "cv"))):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert torch.isfinite(a[1]["out"][0].float()).all() and a[1]["lo"].tolist() == [50 + len(R.paths_of(a[1]["par"][0].tolist(), 5)[4]),
+                                                                                  13 + len(R.paths_of(a[1]["par"][1].tolist(), 4)[2])]
