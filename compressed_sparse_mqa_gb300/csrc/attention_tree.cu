@@ -49,11 +49,13 @@
 // are rounded to 16 bits for the product with V; the accumulator drops what is below about 2^-25 of
 // what it holds.
 //
-// Measured (device time): 4 sessions of up to 64 nodes x 64 heads over 32768 tokens 172 us =
-// 1354 TFLOP/s, bound by the tensor pipe and the shared memory that feeds it; 64 sessions of up
-// to 32 nodes over 128 + 512 rows 52 us, bound by six-tile items (their start and output);
-// 16 sessions of up to 16 nodes with 512 listed rows each 29 us, bound by the gathers; 4 nodes over the
-// window 9.7 us, latency.
+// Measured (device time, inputs in L2): 4 sessions of up to 64 nodes x 64 heads over 32768 tokens
+// 172 us = 1354 TFLOP/s, bound by the tensor pipe and the shared memory that feeds it; 64 sessions of
+// up to 32 nodes over 128 + 512 rows 52 us: 406 six-tile items on 152 SMs are three rounds, the last
+// two thirds full, and a third of an item is its output and the next one's start; 16 sessions of up to 16
+// nodes with 512 listed rows each 28 us: 192 items are two rounds, the second a quarter full, of which
+// the gathers (about 20 B a cycle and SM) take some 16 us and the items' start and output the rest; 4
+// nodes over the window 9.9 us, latency.
 //
 // Masked keys get weight 0, but 0 * V is not 0 where V is infinite or NaN: slots never
 // written, or another branch's values.  The checker scans the V rows of runs that some row
@@ -123,7 +125,7 @@ struct Bars {
 // With sel the query block is 64 rows (the products read 128: the other 64 are what follows in
 // shared memory, rows that nobody reads) and there is no poison table, which leaves room for two V
 // stages a side: listed rows come slowly, and a V stage is held until its product is done
-// (attn_sel_16x16 29.7 us, 32 with one a side).
+// (attn_sel_16x16 29.7 us against 32 with one a side).
 template <int D, bool kSel>
 struct Layout {
     using W = std::conditional_t<kSel, WorkInfo, Work>;
@@ -1319,7 +1321,9 @@ struct Plan {
 
 size_t header_bytes(long long slots) { return (static_cast<size_t>(slots) * 8 + 255) / 256 * 256; }
 
-// How a call is cut, from the sizes that the host knows (the most keys and nodes there may be).
+// How a call is cut, from the sizes that the host knows: the most keys and nodes there may be.  Where page
+// table and compressed rows hold far more than the sessions do, the choice is that of the larger size
+// (attn_r128_64x32 with room for eight times its tokens: the stream, 97 us against 52).
 // Two row blocks per item (each K and V tile read once for 256 rows) when that leaves at least four
 // key tiles per SM; else one, with its two sides on alternate tiles.  Stream or not: the smaller of
 // the two costs, in key tiles: an item's fixed part counts 4, in a stream 6 (its pieces start and end

@@ -36,8 +36,10 @@ DS4A_DEVINL unsigned long long turn_fraction(double x) {
 // key and its value; a row is D / 16 items of 32 bytes: unit u of the rotated dims holds the 8
 // pairs 8u .. 8u+7 (two adjacent 16-byte chunks when interleaved, chunks u and u + rot/16
 // otherwise), the other items two of the remaining chunks.  Bound by memory: a 2048-token
-// chunk with 64 heads moves 69 MB in 13.4 us (5.2 TB/s; 17 us = 4.0 TB/s with inputs from DRAM); one
-// token takes 3.4 us, a launch and three dependent loads.  Two or six items a thread instead of
+// chunk with 64 heads moves 69 MB in 13.4 us with its inputs in L2 (5.2 TB/s) and in 17 us with inputs
+// from DRAM (4.0 TB/s: 2048 CTAs of one token, about five to an SM, are 2.7 waves, and inside a CTA
+// loads, look-ups and stores follow one another); one token takes 3.4 us, a launch and three dependent
+// loads.  Two or six items a thread instead of
 // three: 14.3 and 19 us.  The inputs do not depend on the session's counts, so a
 // thread's loads are in flight while length, angle and page are looked up.
 template <bool kInterleaved>

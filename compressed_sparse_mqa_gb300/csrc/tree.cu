@@ -8,10 +8,13 @@
 // arithmetic of the one-token compressor update, so a row completed in a tree, and the
 // state after a commit, have the bits that decoding the path token by token gives.
 //
-// Both are bound by latency: a chain of loads (counts, parents, page numbers, tokens) and of up to
-// 64 dependent updates.  The tokens' loads are all in flight at once and only the sums are a chain.
-// Measured: 64 sessions of up to 64 nodes at ratio 128 7.8 us (12.8 with a CTA per node and one load
-// at a time), 16 of up to 16 nodes at ratio 4 4.7 us; committing 64 paths of up to 32 nodes about 4 us.
+// Both are bound by latency: counts, parents, page numbers and tokens are loads one behind the other.  The
+// keys' loads for the scores are all in flight at once; the weighted sums then load the path eight
+// tokens at a time, up to eight load latencies in a row, beside the search for each token's node
+// among the path's bits and a loop for each running maximum.  The up to 64 dependent updates
+// themselves are the smaller part.
+// Measured: 64 sessions of up to 64 nodes at ratio 128 7.9 us (12.8 with a CTA per node and one load
+// at a time), 16 of up to 16 nodes at ratio 4 4.9 us; committing 64 paths of up to 32 nodes about 4 us.
 #include "compress_dev.cuh"
 #include "paged_dev.cuh"
 

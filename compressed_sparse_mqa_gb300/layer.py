@@ -496,7 +496,8 @@ class TreeDecodeLayer:
 
     Built from one DecodeInstance per session, as BatchedDecodeLayer; the token at the
     instance's position is committed, so a session starts with p + 1 tokens.  Every node's
-    output is that of decoding its path token by token.  `room` is how many tokens beyond the
+    rows are those of decoding its path token by token, bit for bit, and its output is within the
+    tolerance of one.  `room` is how many tokens beyond the
     longest session the pages and the compressed rows have place for (a draft counts
     until it is committed or dropped); both are laid out once, pages that left the window are not
     used again, and a draft past the room is refused.  Layers that pool their indexer keys from

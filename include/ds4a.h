@@ -494,8 +494,10 @@ int ds4a_decode_layer_step(const ds4a_decode_layer_t *layer, long long pos, cons
  * ("ds4 antirez DeepSeek V4 Flash local engine 2026 guide" and "DwarfStar (ds4)
  * Deep Dive" name speculative decoding with a draft; the pages give no cache layout
  * for it.)  A draft proposes a tree of tokens per session; one pass scores every node,
- * and the accepted path is committed.  For each node the results are those of
- * decoding its path token by token, so checking a draft loses nothing.
+ * and the accepted path is committed.  For each node the compressed rows, states and
+ * kept rows have the bits of decoding its path token by token; attention outputs are the
+ * same sums in another order (for values of unit scale within 2e-3 of the exact one,
+ * as ds4a_attn_decode's are), so a choice between nearly equal tokens can differ.
  *
  * One step of a layer is ds4a_paged_append (the drafted tokens into the pages, keys and
  * queries rotated), ds4a_compress_tree (the compressed rows that nodes complete; layers
@@ -593,7 +595,9 @@ int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, 
  *              stream-ordered (two captured graphs that may replay at the same time need
  *              one each).
  * q, comp_k, comp_v, out and the pools are 16-byte aligned.  A node none of whose rows can be
- * read (bad page ids) gets zeros.
+ * read (bad page ids) gets zeros; one whose scores are all -inf gets NaN.  Scores, maxima and sums
+ * are binary32; a weight is rounded to fp16 for its product with V (the largest to 2^-11 of it, the
+ * smallest to 2^-32 of the largest), not in the sum that divides; an output is rounded once.
  */
 int ds4a_attn_tree(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, const int32_t *n_node,
                    const int32_t *parent, long long window, const uint16_t *comp_k, const uint16_t *comp_v,
