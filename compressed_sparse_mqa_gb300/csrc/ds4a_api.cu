@@ -53,11 +53,13 @@ Written g_written[kMaxWritten];
 std::atomic<int> g_n_written{0};       // kMaxWritten + 1: there were more, and every stream counts as one of them
 std::mutex g_written_mu;
 
-// Notes a call on a stream; whether the call before it there wrote what may be read early.
-bool behind_written(int dev, void *stream, Early e) {
-    if (e != Early::kWrites && g_n_written.load(std::memory_order_acquire) == 0) return false;
+// Whether the call before on this stream wrote what may be read early; notes (kSet) that this one does or
+// (kClear) that another kernel is on the stream now.
+enum class Note { kAsk, kSet, kClear };
+bool behind_written(void *stream, Note note) {
+    if (note != Note::kSet && g_n_written.load(std::memory_order_acquire) == 0) return false;
     Written w;
-    w.dev = dev;
+    if (cudaGetDevice(&w.dev) != cudaSuccess) cudaGetLastError();
     w.stream = stream == cudaStreamLegacy ? nullptr : stream;
     if (stream == cudaStreamPerThread) w.thread = std::this_thread::get_id();
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
@@ -72,10 +74,12 @@ bool behind_written(int dev, void *stream, Early e) {
     if (n > kMaxWritten) return true;
     while (at < n && !(g_written[at].dev == w.dev && g_written[at].stream == w.stream && g_written[at].thread == w.thread)) ++at;
     if (at < n) w = g_written[at];
-    if (capture == 0) w.capture = 0;   // the stream's capture is over
     const bool found = capture ? w.capture == capture : w.now;
-    if (capture) w.capture = e == Early::kWrites ? capture : (found ? 0 : w.capture);
-    else w.now = e == Early::kWrites;
+    if (note == Note::kAsk) return found;
+    if (capture == 0) w.capture = 0;   // the stream's capture is over
+    if (capture == 0) w.now = note == Note::kSet;
+    else if (note == Note::kSet) w.capture = capture;
+    else if (found) w.capture = 0;
     if (w.now || w.capture) {
         if (at < kMaxWritten) g_written[at] = w;
         if (at == n) ++n;
@@ -107,7 +111,8 @@ int make_ctx(void *stream, ds4a::Ctx &c, Early early = Early::kReads) {
     c.err = d.err;
     c.num_sms = d.num_sms;
     c.pdl = pdl_enabled();
-    if (behind_written(dev, stream, early) && early == Early::kReads) c.pdl = false;
+    if (early == Early::kReads && behind_written(stream, Note::kAsk)) c.pdl = false;
+    if (early == Early::kWrites) behind_written(stream, Note::kSet);
     return DS4A_OK;
 }
 
@@ -119,6 +124,12 @@ int from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return DS4A_OK;
     cudaGetLastError();   // clear the sticky-free launch error
     return e == cudaErrorInvalidValue ? DS4A_ERR_UNSUPPORTED : DS4A_ERR_CUDA;
+}
+
+// the same for a call that writes nothing that is read early: once launched, it is what the next call is behind
+int from_cuda(cudaError_t e, const ds4a::Ctx &c) {
+    if (e == cudaSuccess) behind_written(c.stream, Note::kClear);
+    return from_cuda(e);
 }
 
 }  // namespace
@@ -176,7 +187,7 @@ int ds4a_compress_append(const uint16_t *k, const uint16_t *v, int n_new, int he
     int rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_compress(k, v, n_new, head_dim, score_w, ratio, pos, state, comp_k,
-                                           comp_v, c));
+                                           comp_v, c), c);
 }
 
 int ds4a_compress_append_keys(const uint16_t *k, const uint16_t *v, const uint16_t *k_idx_tok, int n_new,
@@ -195,7 +206,7 @@ int ds4a_compress_append_keys(const uint16_t *k, const uint16_t *v, const uint16
     int rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_compress(k, v, n_new, head_dim, score_w, ratio, pos, state, comp_k, comp_v, c,
-                                           k_idx_tok, comp_kidx, d_idx));
+                                           k_idx_tok, comp_kidx, d_idx), c);
 }
 
 size_t ds4a_indexer_workspace_bytes(int n_q, long long n_rows, int k) {
@@ -218,7 +229,7 @@ int ds4a_indexer_topk(const uint16_t *q_idx, int n_q, const uint16_t *k_idx, lon
     int rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_indexer(q_idx, n_q, k_idx, n_rows, d_idx, q_pos0, ratio, k, out_idx,
-                                          out_n, ws, c));
+                                          out_n, ws, c), c);
 }
 
 int ds4a_indexer_topk_compress(const uint16_t *q_idx, const uint16_t *k_idx, long long n_rows, int d_idx,
@@ -244,7 +255,7 @@ int ds4a_indexer_topk_compress(const uint16_t *q_idx, const uint16_t *k_idx, lon
     int rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_indexer_compress(q_idx, k_idx, n_rows, d_idx, q_pos, ratio, k, out_idx, out_n, ws,
-                                                   k_new, v_new, head_dim, score_w, state, comp_k, comp_v, c));
+                                                   k_new, v_new, head_dim, score_w, state, comp_k, comp_v, c), c);
 }
 
 int ds4a_indexer_topk_compress_keys(const uint16_t *q_idx, uint16_t *k_idx, long long n_rows, int d_idx,
@@ -272,7 +283,7 @@ int ds4a_indexer_topk_compress_keys(const uint16_t *q_idx, uint16_t *k_idx, long
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_indexer_compress(q_idx, k_idx, n_rows, d_idx, q_pos, ratio, k, out_idx, out_n, ws,
                                                    k_new, v_new, head_dim, score_w, state, comp_k, comp_v, c,
-                                                   k_idx_tok));
+                                                   k_idx_tok), c);
 }
 
 static int check_heads(int H, int D) {
@@ -301,7 +312,7 @@ int ds4a_attn_decode(const uint16_t *q, int H, int D, const uint16_t *win_k,
     rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_attn_decode(q, H, D, win_k, win_v, n_win, comp_k, comp_v, n_comp, sel,
-                                              n_sel, scale, out, c));
+                                              n_sel, scale, out, c), c);
 }
 
 int ds4a_compress_attn_decode(const uint16_t *k_new, const uint16_t *v_new, const float *score_w, int ratio,
@@ -327,7 +338,7 @@ int ds4a_compress_attn_decode(const uint16_t *k_new, const uint16_t *v_new, cons
     rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_compress_attn_decode(k_new, v_new, score_w, ratio, pos, state, q, H, D, win_k,
-                                                       win_v, n_win, comp_k, comp_v, scale, out, c));
+                                                       win_v, n_win, comp_k, comp_v, scale, out, c), c);
 }
 
 int ds4a_attn_prefill(const uint16_t *q, int T, int H, int D, const uint16_t *raw_k,
@@ -355,7 +366,7 @@ int ds4a_attn_prefill(const uint16_t *q, int T, int H, int D, const uint16_t *ra
     rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_attn_prefill(q, T, H, D, raw_k, raw_v, n_prior, window, comp_k, comp_v,
-                                               n_comp, sel, k_stride, q_pos0, ratio, scale, out, c));
+                                               n_comp, sel, k_stride, q_pos0, ratio, scale, out, c), c);
 }
 
 int ds4a_probe_gather(const uint16_t *table, long long n_table, int D, const int32_t *idx, long long n_idx,
@@ -366,7 +377,7 @@ int ds4a_probe_gather(const uint16_t *table, long long n_table, int D, const int
     ds4a::Ctx c;
     int rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
-    return from_cuda(ds4a::launch_gather_probe(table, n_table, D, idx, n_idx, sink, c));
+    return from_cuda(ds4a::launch_gather_probe(table, n_table, D, idx, n_idx, sink, c), c);
 }
 
 // ---- batched decode: B independent sessions per call ------------------------------------
@@ -407,7 +418,7 @@ int ds4a_indexer_topk_compress_batched(int B, const uint16_t *q_idx, const uint1
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_indexer_compress_batched(B, q_idx, k_idx, cap, d_idx, pos, ratio, k, out_idx, out_n,
                                                            ws, ring_k, ring_v, W, head_dim, score_w, state, comp_k,
-                                                           comp_v, c));
+                                                           comp_v, c), c);
 }
 
 static int attn_batched_common(int B, const uint16_t *q, int H, int D, const uint16_t *ring_k, const uint16_t *ring_v,
@@ -441,7 +452,7 @@ int ds4a_attn_decode_batched(int B, const uint16_t *q, int H, int D, const uint1
     rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_attn_decode_batched(B, q, H, D, ring_k, ring_v, W, pos, comp_k, comp_v, cap, sel,
-                                                      n_sel, ratio, scale, out, nullptr, nullptr, c));
+                                                      n_sel, ratio, scale, out, nullptr, nullptr, c), c);
 }
 
 int ds4a_compress_attn_decode_batched(int B, const float *score_w, int ratio, float *state, uint16_t *comp_k,
@@ -458,7 +469,7 @@ int ds4a_compress_attn_decode_batched(int B, const float *score_w, int ratio, fl
     rc = make_ctx(stream, c);
     if (rc != DS4A_OK) return rc;
     return from_cuda(ds4a::launch_attn_decode_batched(B, q, H, D, ring_k, ring_v, W, pos, comp_k, comp_v, cap,
-                                                      nullptr, 0, ratio, scale, out, score_w, state, c));
+                                                      nullptr, 0, ratio, scale, out, score_w, state, c), c);
 }
 
 // ---- paged token cache and drafted-token trees ---------------------------------------------
@@ -535,7 +546,7 @@ int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, 
     rc = make_ctx(stream, c, Early::kNone);
     if (rc != DS4A_OK) return rc;
     const ds4a::CompressTreeArgs a{paged_view(kv), n_node, parent, score_w, state, comp_k, comp_v, cap, c.err, N, ratio};
-    return from_cuda(ds4a::launch_compress_tree(a, kv->B, c));
+    return from_cuda(ds4a::launch_compress_tree(a, kv->B, c), c);
 }
 
 size_t ds4a_attn_tree_workspace_bytes(int B, int N, int H, int D) {
@@ -570,7 +581,7 @@ int ds4a_attn_tree(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, c
     if (rc != DS4A_OK) return rc;
     const ds4a::AttnTreeArgs a{paged_view(kv), q, comp_k, comp_v, n_node, parent, sel, out, ws, c.err,
                                window, cap, N, H, ratio, sel ? n_sel : 0, scale, 0.f};
-    return from_cuda(ds4a::launch_attn_tree(a, kv->B, c));
+    return from_cuda(ds4a::launch_attn_tree(a, kv->B, c), c);
 }
 
 int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, const int32_t *parent,
@@ -743,7 +754,8 @@ int ds4a_decode_layer_step(const ds4a_decode_layer_t *L, long long pos, const ds
         e = ds4a::launch_attn_decode(L->q, H, D, L->ring_k, L->ring_v, n_win, nullptr, nullptr, 0, nullptr, 0,
                                      L->scale, out, c_first);
     }
-    if (e != cudaSuccess) return from_cuda(e);
+    rc = from_cuda(e, c);
+    if (rc != DS4A_OK) return rc;
     if (out_host) {
         if ((!out_direct && cudaMemcpyAsync(out_host, L->out, static_cast<size_t>(H) * row, cudaMemcpyDeviceToHost,
                                             c.stream) != cudaSuccess) ||
@@ -818,5 +830,5 @@ extern "C" int ds4a_indexer_topk_noalloc(const uint16_t *q_idx, const uint16_t *
     }
     // rows past n_vis are never read: the call is the same as one over the visible rows
     return from_cuda(ds4a::launch_indexer(q_idx, 1, k_idx, n_vis, d_idx, q_pos, ratio, k, out_idx, out_n,
-                                          slot.addr, c));
+                                          slot.addr, c), c);
 }
