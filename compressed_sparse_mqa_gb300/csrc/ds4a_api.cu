@@ -502,9 +502,12 @@ static ds4a::PagedKV paged_view(const ds4a_paged_kv_t *kv) {
     return ds4a::PagedKV{kv->k, kv->v, kv->table, kv->len, kv->n_pages, kv->page, kv->max_pages, kv->D};
 }
 
-int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16_t *v, int N, const int32_t *n_tok,
-                      const int32_t *parent, const float *inv_freq, int rot, int rot_off, int interleaved,
-                      const uint16_t *q, int H, uint16_t *q_out, void *stream) {
+// What the two appends share: the checks, and the arguments of the kernel (norm: false).  `run` is false
+// where there is nothing to do.
+static int append_args(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16_t *v, int N, const int32_t *n_tok,
+                       const int32_t *parent, const float *inv_freq, int rot, int rot_off, int interleaved,
+                       const uint16_t *q, int H, uint16_t *q_out, ds4a::AppendArgs &a, bool &run) {
+    run = false;
     int rc = check_paged(kv);
     if (rc != DS4A_OK) return rc;
     if (N < 0 || rot < 0 || rot_off < 0 || (q == nullptr) != (q_out == nullptr)) return DS4A_ERR_ARG;
@@ -521,11 +524,48 @@ int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16
         return DS4A_ERR_ARG;
     // queries in place, or apart
     if (q && q_out != q && overlap(q, q_out, static_cast<size_t>(kv->B) * N * H * kv->D * 2)) return DS4A_ERR_ARG;
+    a = ds4a::AppendArgs{paged_view(kv), k, v, q, q_out, n_tok, parent, inv_freq, nullptr, N, q ? H : 0, rot, rot_off,
+                         interleaved != 0, 0, nullptr, nullptr, 0.f, nullptr, nullptr, 0};
+    run = true;
+    return DS4A_OK;
+}
+
+int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16_t *v, int N, const int32_t *n_tok,
+                      const int32_t *parent, const float *inv_freq, int rot, int rot_off, int interleaved,
+                      const uint16_t *q, int H, uint16_t *q_out, void *stream) {
+    ds4a::AppendArgs a;
+    bool run;
+    int rc = append_args(kv, k, v, N, n_tok, parent, inv_freq, rot, rot_off, interleaved, q, H, q_out, a, run);
+    if (rc != DS4A_OK || !run) return rc;
     ds4a::Ctx c;
     rc = make_ctx(stream, c, Early::kWrites);
     if (rc != DS4A_OK) return rc;
-    const ds4a::AppendArgs a{paged_view(kv), k, v, q, q_out, n_tok, parent, inv_freq, c.err, N, q ? H : 0, rot, rot_off,
-                             interleaved != 0};
+    a.err = c.err;
+    return from_cuda(ds4a::launch_paged_append(a, kv->B, c));
+}
+
+int ds4a_paged_append_norm(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16_t *v, int N, const int32_t *n_tok,
+                           const int32_t *parent, const float *k_w, const float *q_w, float eps, const float *inv_freq,
+                           int rot, int rot_off, int interleaved, const uint16_t *q, int H, uint16_t *q_out,
+                           const long long *pos0, int32_t *slot_pos, int slots, void *stream) {
+    ds4a::AppendArgs a;
+    bool run;
+    int rc = append_args(kv, k, v, N, n_tok, parent, inv_freq, rot, rot_off, interleaved, q, H, q_out, a, run);
+    if (rc != DS4A_OK) return rc;
+    if (!(eps > 0.f) || eps > 3.4e38f || (slot_pos && slots < 1)) return DS4A_ERR_ARG;
+    if (!aligned(k_w, 4) || !aligned(q_w, 4) || !aligned(pos0, 8) || !aligned(slot_pos, 4)) return DS4A_ERR_ARG;
+    if (!run) return rc;
+    ds4a::Ctx c;
+    rc = make_ctx(stream, c, Early::kWrites);
+    if (rc != DS4A_OK) return rc;
+    a.err = c.err;
+    a.norm = 1;
+    a.k_w = k_w;
+    a.q_w = q_w;
+    a.eps = eps;
+    a.pos0 = pos0;
+    a.slot_pos = slot_pos;
+    a.slots = slots;
     return from_cuda(ds4a::launch_paged_append(a, kv->B, c));
 }
 
@@ -614,6 +654,58 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
     const ds4a::CommitTreeArgs a{paged_view(kv), n_node, parent, leaf, len_out, score_w, state, state_out, comp_k, comp_v,
                                  k_idx, cap, c.err, N, ratio, k_idx ? d_idx : 0};
     return from_cuda(ds4a::launch_commit_tree(a, kv->B, c));
+}
+
+// ---- caches held to a budget of tokens -----------------------------------------------------
+
+int ds4a_attn_weights(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, const int32_t *n_tok, const float *lse,
+                      float scale, float decay, float *acc, int slots, void *stream) {
+    int rc = check_paged(kv);
+    if (rc != DS4A_OK) return rc;
+    rc = check_heads(H, kv->D);
+    if (rc != DS4A_OK) return rc;
+    rc = check_tree(N, n_tok, nullptr);
+    if (rc != DS4A_OK) return rc;
+    if (slots < 1 || !(scale > 0.f) || scale > 2.3e38f || !(decay >= 0.f) || decay > 1.f) return DS4A_ERR_ARG;
+    if (kv->B == 0) return DS4A_OK;
+    if (!q || !lse || !acc || !aligned(q, 16) || !aligned(lse, 4) || !aligned(acc, 4)) return DS4A_ERR_ARG;
+    ds4a::Ctx c;
+    rc = make_ctx(stream, c, Early::kNone);
+    if (rc != DS4A_OK) return rc;
+    const ds4a::AttnWeightsArgs a{paged_view(kv), q, n_tok, lse, acc, c.err, scale, decay, N, H, slots};
+    return from_cuda(ds4a::launch_attn_weights(a, kv->B, c), c);
+}
+
+size_t ds4a_evict_workspace_bytes(int B, int slots, int budget) {
+    if (B < 0 || slots < 1 || slots > ds4a::kMaxEvictSlots || budget < 1) return 0;
+    return ds4a::evict_ws_bytes(B, slots, budget);
+}
+
+int ds4a_evict(const ds4a_paged_kv_t *kv, const float *acc, const int32_t *pos, int slots, const long long *next, int budget,
+               int n_sink, int n_recent, float *acc_out, int32_t *pos_out, long long *len_out, void *ws, size_t ws_bytes,
+               void *stream) {
+    int rc = check_paged(kv);
+    if (rc != DS4A_OK) return rc;
+    if (slots < 1 || budget < 1 || n_sink < 0 || n_recent < 0 || static_cast<long long>(n_sink) + n_recent > budget)
+        return DS4A_ERR_ARG;
+    if (slots > ds4a::kMaxEvictSlots) return DS4A_ERR_UNSUPPORTED;
+    if (kv->B == 0) return DS4A_OK;
+    if (!acc || !pos || !next || !acc_out || !pos_out || !len_out || !aligned(acc, 4) || !aligned(pos, 4) ||
+        !aligned(next, 8) || !aligned(acc_out, 4) || !aligned(pos_out, 4) || !aligned(len_out, 8))
+        return DS4A_ERR_ARG;
+    // in place, or apart, both arrays alike: a session's outputs may not be what it still reads
+    const size_t bytes = static_cast<size_t>(kv->B) * slots * 4, len_bytes = static_cast<size_t>(kv->B) * 8;
+    if ((acc_out == acc) != (pos_out == pos)) return DS4A_ERR_ARG;
+    if (acc_out != acc && (overlap(acc_out, acc, bytes) || overlap(pos_out, pos, bytes))) return DS4A_ERR_ARG;
+    if (overlap(acc_out, pos, bytes) || overlap(pos_out, acc, bytes) || overlap(acc_out, pos_out, bytes)) return DS4A_ERR_ARG;
+    if ((len_out != kv->len && overlap(len_out, kv->len, len_bytes)) || overlap(len_out, next, len_bytes)) return DS4A_ERR_ARG;
+    if (!ws || !aligned(ws, 256) || ws_bytes < ds4a::evict_ws_bytes(kv->B, slots, budget)) return DS4A_ERR_WORKSPACE;
+    ds4a::Ctx c;
+    rc = make_ctx(stream, c, Early::kWrites);
+    if (rc != DS4A_OK) return rc;
+    const ds4a::EvictArgs a{paged_view(kv), acc, pos, next, acc_out, pos_out, len_out, ws, c.err, slots, budget, n_sink,
+                            n_recent, 0, 0, 0};
+    return from_cuda(ds4a::launch_evict(a, kv->B, c));
 }
 
 // ---- one decode step of one layer from host memory ------------------------------------------

@@ -120,6 +120,13 @@ struct AppendArgs {
     const float *inv_freq;
     unsigned int *err;
     int N, H, rot, rot_off, interleaved;
+    // with norms
+    int norm;
+    const float *k_w, *q_w;      // [D], or nullptr: ones
+    float eps;
+    const long long *pos0;       // [B], or nullptr: len
+    int32_t *slot_pos;           // [B, slots], or nullptr
+    int slots;
 };
 struct CompressTreeArgs {
     PagedKV kv;
@@ -152,9 +159,36 @@ struct AttnTreeArgs {
     int N, H, ratio, n_sel;
     float scale, scale_log2;
 };
+struct AttnWeightsArgs {
+    PagedKV kv;
+    const uint16_t *q;           // [B, N, H, D]
+    const int32_t *n_tok;
+    const float *lse;            // [B, N, H]
+    float *acc;                  // [B, slots]
+    unsigned int *err;
+    float scale, decay;
+    int N, H, slots;
+};
+constexpr int kMaxEvictSlots = 1 << 23;
+struct EvictArgs {
+    PagedKV kv;
+    const float *acc;            // [B, slots]
+    const int32_t *pos;
+    const long long *next;       // [B]
+    float *acc_out;              // acc, or apart from it; pos_out likewise
+    int32_t *pos_out;
+    long long *len_out;
+    void *ws;                    // int32: moves per session, then [B][2][most] dropped slots and kept tokens
+    unsigned int *err;
+    int slots, budget, n_sink, n_recent, slice_cap;
+    long long most, list0;
+};
 cudaError_t launch_paged_append(const AppendArgs &a, int B, const Ctx &c);
 cudaError_t launch_compress_tree(const CompressTreeArgs &a, int B, const Ctx &c);
 cudaError_t launch_commit_tree(const CommitTreeArgs &a, int B, const Ctx &c);
+cudaError_t launch_attn_weights(const AttnWeightsArgs &a, int B, const Ctx &c);
+size_t evict_ws_bytes(int B, int slots, int budget);
+cudaError_t launch_evict(const EvictArgs &a, int B, const Ctx &c);
 size_t attn_tree_ws_bytes(int B, int N, int H, int D);
 cudaError_t launch_attn_tree(const AttnTreeArgs &a, int B, const Ctx &c);
 

@@ -33,7 +33,8 @@ EXPORTED = ["ds4a_status_str", "ds4a_last_device_error", "ds4a_compress_append",
             "ds4a_decode_batched_workspace_bytes", "ds4a_indexer_topk_compress_batched", "ds4a_attn_decode_batched",
             "ds4a_compress_attn_decode_batched", "ds4a_probe_gather", "ds4a_decode_layer_step",
             "ds4a_indexer_topk_compress_keys", "ds4a_paged_append", "ds4a_compress_tree", "ds4a_attn_tree",
-            "ds4a_attn_tree_workspace_bytes", "ds4a_commit_tree"]
+            "ds4a_attn_tree_workspace_bytes", "ds4a_commit_tree", "ds4a_paged_append_norm",
+            "ds4a_attn_weights", "ds4a_evict", "ds4a_evict_workspace_bytes"]
 
 
 class Ds4aError(RuntimeError):
@@ -74,14 +75,19 @@ def lib() -> ctypes.CDLL:
                                              P, P]
         KV = ctypes.POINTER(PagedKVDesc)
         L.ds4a_paged_append.argtypes = [KV, P, P, I, P, P, P, I, I, I, P, I, P, P]
+        L.ds4a_paged_append_norm.argtypes = [KV, P, P, I, P, P, P, P, F, P, I, I, I, P, I, P, P, P, I, P]
         L.ds4a_compress_tree.argtypes = [KV, I, P, P, P, I, P, P, P, LL, P]
         L.ds4a_attn_tree.argtypes = [KV, P, I, I, P, P, LL, P, P, LL, I, P, I, F, P, P, SZ, P]
         L.ds4a_attn_tree_workspace_bytes.argtypes = [I, I, I, I]
         L.ds4a_attn_tree_workspace_bytes.restype = SZ
+        L.ds4a_attn_weights.argtypes = [KV, P, I, I, P, P, F, F, P, I, P]
+        L.ds4a_evict.argtypes = [KV, P, P, I, P, I, I, I, P, P, P, P, SZ, P]
+        L.ds4a_evict_workspace_bytes.argtypes = [I, I, I]
+        L.ds4a_evict_workspace_bytes.restype = SZ
         L.ds4a_commit_tree.argtypes = [KV, I, P, P, P, P, P, I, P, P, P, P, LL, P, I, P]
         for name in EXPORTED:
             if name not in ("ds4a_status_str", "ds4a_indexer_workspace_bytes", "ds4a_decode_batched_workspace_bytes",
-                            "ds4a_attn_tree_workspace_bytes"):
+                            "ds4a_attn_tree_workspace_bytes", "ds4a_evict_workspace_bytes"):
                 getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -571,19 +577,24 @@ def _nodes(where, parent, N):
     return N
 
 
-def _marshal_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, rot_off: int = 0,
-                          interleaved: bool = True, q=None, q_out=None, stream=None):
+def _append_sizes(where, kv, k, v, q, q_out):
     shape, B, D = k.shape, kv.B, kv.D
     if len(shape) != 3 or shape[0] != B or shape[2] != D or v.shape != shape:
-        raise ValueError("paged_append: k, v [B, N, D]")
+        raise ValueError(f"{where}: k, v [B, N, D]")
     N, H = shape[1], 0
     if (q is None) != (q_out is None):
-        raise ValueError("paged_append: q and q_out come together")
+        raise ValueError(f"{where}: q and q_out come together")
     if q is not None:
         qs = q.shape
         if len(qs) != 4 or qs[0] != B or qs[1] != N or qs[3] != D or q_out.shape != qs:
-            raise ValueError("paged_append: q, q_out [B, N, H, D]")
+            raise ValueError(f"{where}: q, q_out [B, N, H, D]")
         H = qs[2]
+    return B, N, H
+
+
+def _marshal_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, rot_off: int = 0,
+                          interleaved: bool = True, q=None, q_out=None, stream=None):
+    B, N, H = _append_sizes("paged_append", kv, k, v, q, q_out)
     st, dev = _launch_on("paged_append", kv, stream), kv.device
     pn, pp = _tree_args("paged_append", kv, B, N, n_tok, parent)
     return (ctypes.byref(kv), _arg(k, _F16, dev, "k"), _arg(v, _F16, dev, "v"), N, pn, pp,
@@ -598,6 +609,43 @@ def ds4a_paged_append(kv: PagedKVDesc, k, v, n_tok, parent=None, inv_freq=None, 
     inv_freq [rot/2] (None: as they are).  parent [B, N] int32 or None (a chain)."""
     args = _marshal_paged_append(kv, k, v, n_tok, parent, inv_freq, rot_off, interleaved, q, q_out, stream)
     _check(lib().ds4a_paged_append(*args), "ds4a_paged_append")
+
+
+def _slot_rows(where, kv, t, dtype, name):
+    """The address and row length of a [B, slots] array of the cache (None: NULL, 0)."""
+    if t is None:
+        return None, 0
+    if len(t.shape) != 2 or t.shape[0] != kv.B:
+        raise ValueError(f"{where}: {name} [B, slots]")
+    return _arg(t, dtype, kv.device, name), t.shape[1]
+
+
+def _marshal_paged_append_norm(kv: PagedKVDesc, k, v, n_tok, k_w, q_w, eps: float, parent=None, inv_freq=None,
+                               rot_off: int = 0, interleaved: bool = True, q=None, q_out=None, pos0=None,
+                               slot_pos=None, stream=None):
+    B, N, H = _append_sizes("paged_append_norm", kv, k, v, q, q_out)
+    if any(w is not None and w.shape != (kv.D,) for w in (k_w, q_w)):
+        raise ValueError("paged_append_norm: k_w, q_w [D] (or None)")
+    if pos0 is not None and pos0.shape != (B,):
+        raise ValueError("paged_append_norm: pos0 [B] (or None)")
+    st, dev = _launch_on("paged_append_norm", kv, stream), kv.device
+    pn, pp = _tree_args("paged_append_norm", kv, B, N, n_tok, parent)
+    sp, slots = _slot_rows("paged_append_norm", kv, slot_pos, _I32, "slot_pos")
+    return (ctypes.byref(kv), _arg(k, _F16, dev, "k"), _arg(v, _F16, dev, "v"), N, pn, pp, _arg(k_w, _F32, dev, "k_w"),
+            _arg(q_w, _F32, dev, "q_w"), eps, _arg(inv_freq, _F32, dev, "inv_freq"),
+            0 if inv_freq is None else 2 * inv_freq.numel(), rot_off, 1 if interleaved else 0, _arg(q, _F16, dev, "q"), H,
+            _arg(q_out, _F16, dev, "q_out"), _arg(pos0, _I64, dev, "pos0"), sp, slots, st)
+
+
+def ds4a_paged_append_norm(kv: PagedKVDesc, k, v, n_tok, k_w, q_w, eps: float, parent=None, inv_freq=None,
+                           rot_off: int = 0, interleaved: bool = True, q=None, q_out=None, pos0=None, slot_pos=None,
+                           stream=None):
+    """ds4a_paged_append with the RMS norm of each key (weights k_w [D], None: ones) and query head
+    (q_w) in the same pass; pos0 [B] int64: the position of each session's first new token (None:
+    its slot); slot_pos [B, slots] int32 receives the tokens' positions (None: not kept)."""
+    args = _marshal_paged_append_norm(kv, k, v, n_tok, k_w, q_w, eps, parent, inv_freq, rot_off, interleaved, q, q_out,
+                                      pos0, slot_pos, stream)
+    _check(lib().ds4a_paged_append_norm(*args), "ds4a_paged_append_norm")
 
 
 def _marshal_compress_tree(kv: PagedKVDesc, n_node, parent, score_w, ratio: int, state, comp_k, comp_v, N=None,
@@ -691,6 +739,59 @@ def ds4a_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w=Non
     _check(lib().ds4a_commit_tree(*args), "ds4a_commit_tree")
 
 
+# ---- caches held to a budget of tokens -----------------------------------------------------------
+
+def _marshal_attn_weights(kv: PagedKVDesc, q, n_tok, lse, scale: float, decay: float, acc, stream=None):
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != kv.B or shape[3] != kv.D:
+        raise ValueError("attn_weights: q [B, N, H, D]")
+    N, H = shape[1], shape[2]
+    if lse is None or lse.shape != shape[:3]:
+        raise ValueError("attn_weights: lse [B, N, H]")
+    if n_tok.shape != (kv.B,):
+        raise ValueError("attn_weights: n_tok [B]")
+    st, dev = _launch_on("attn_weights", kv, stream), kv.device
+    pa, slots = _slot_rows("attn_weights", kv, acc, _F32, "acc")
+    return (ctypes.byref(kv), _arg(q, _F16, dev, "q"), N, H, _arg(n_tok, _I32, dev, "n_tok"), _arg(lse, _F32, dev, "lse"),
+            scale, decay, pa, slots, st)
+
+
+def ds4a_attn_weights(kv: PagedKVDesc, q, n_tok, lse, scale: float, decay: float, acc, stream=None):
+    """Adds to acc [B, slots] float32 the attention weight that each cached token gets from the
+    n_tok[s] new tokens in slots len and up, summed over heads and tokens, the sums before times
+    decay: q [B, N, H, D] as attended, lse [B, N, H] float32 as the attention call left it."""
+    args = _marshal_attn_weights(kv, q, n_tok, lse, scale, decay, acc, stream)
+    _check(lib().ds4a_attn_weights(*args), "ds4a_attn_weights")
+
+
+def ds4a_evict_workspace_bytes(B: int, slots: int, budget: int) -> int:
+    return int(lib().ds4a_evict_workspace_bytes(B, slots, budget))
+
+
+def _marshal_evict(kv: PagedKVDesc, acc, pos, next_pos, budget: int, n_sink: int, n_recent: int, acc_out, pos_out, len_out,
+                   ws, stream=None):
+    if acc is None or any(t is None or t.shape != acc.shape for t in (pos, acc_out, pos_out)):
+        raise ValueError("evict: acc, pos, acc_out, pos_out [B, slots]")
+    if any(t is None or t.shape != (kv.B,) for t in (next_pos, len_out)):
+        raise ValueError("evict: next_pos, len_out [B]")
+    st, dev = _launch_on("evict", kv, stream), kv.device
+    pa, slots = _slot_rows("evict", kv, acc, _F32, "acc")
+    return (ctypes.byref(kv), pa, _arg(pos, _I32, dev, "pos"), slots, _arg(next_pos, _I64, dev, "next_pos"), budget, n_sink,
+            n_recent, _arg(acc_out, _F32, dev, "acc_out"), _arg(pos_out, _I32, dev, "pos_out"),
+            _arg(len_out, _I64, dev, "len_out"), _arg(ws, _U8, dev, "ws"), 0 if ws is None else ws.numel(), st)
+
+
+def ds4a_evict(kv: PagedKVDesc, acc, pos, next_pos, budget: int, n_sink: int, n_recent: int, acc_out, pos_out, len_out, ws,
+               stream=None):
+    """Cuts every session to `budget` tokens: positions below n_sink, from next_pos - n_recent on, and
+    the largest acc [B, slots]; kept tokens from slots budget and up move into the dropped slots below
+    it, with their sums and positions (pos [B, slots] int32).  acc_out, pos_out: acc and pos, or
+    arrays apart; len_out [B] int64 (or the cache's lengths).  ws: uint8,
+    ds4a_evict_workspace_bytes(B, slots, budget) bytes."""
+    args = _marshal_evict(kv, acc, pos, next_pos, budget, n_sink, n_recent, acc_out, pos_out, len_out, ws, stream)
+    _check(lib().ds4a_evict(*args), "ds4a_evict")
+
+
 _MARSHAL = {"ds4a_attn_decode": _marshal_attn_decode,
             "ds4a_indexer_topk_compress_batched": _marshal_indexer_topk_compress_batched,
             "ds4a_attn_decode_batched": _marshal_attn_decode_batched,
@@ -702,7 +803,9 @@ _MARSHAL = {"ds4a_attn_decode": _marshal_attn_decode,
             "ds4a_decode_layer_step": _marshal_decode_layer_step,
             "ds4a_indexer_topk_compress_keys": _marshal_indexer_topk_compress_keys,
             "ds4a_paged_append": _marshal_paged_append, "ds4a_compress_tree": _marshal_compress_tree,
-            "ds4a_attn_tree": _marshal_attn_tree, "ds4a_commit_tree": _marshal_commit_tree}
+            "ds4a_attn_tree": _marshal_attn_tree, "ds4a_commit_tree": _marshal_commit_tree,
+            "ds4a_paged_append_norm": _marshal_paged_append_norm, "ds4a_attn_weights": _marshal_attn_weights,
+            "ds4a_evict": _marshal_evict}
 
 
 def bind(name: str, *args, **kwargs):

@@ -562,6 +562,28 @@ int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16
                       const uint16_t *q, int H, uint16_t *q_out, void *stream);
 
 /*
+ * ds4a_paged_append_norm -- ds4a_paged_append with the RMS norm of every key and every query
+ * head in the same pass, and positions that may run ahead of the slots (a cache that
+ * dropped tokens: ds4a_evict).
+ *
+ * A row x of D values becomes x / sqrt(mean(x^2) + eps) * w, is then rotated to its token's
+ * position, and is rounded to fp16 once, behind both.  Values are copied.
+ *   k, v, N, n_tok, parent, inv_freq .. q_out   as ds4a_paged_append.
+ *   k_w, q_w   [D] float weights of keys and of query heads; NULL: ones.
+ *   eps        > 0, finite.
+ *   pos0       [B] int64: the position of the token in slot len (tokens are at pos0 + i, nodes
+ *              at pos0 + depth), 0 .. 2^31-1 - n; NULL: len.
+ *   slot_pos   [B, slots] int32, or NULL: entry len + i receives the position of token i.
+ *              The other entries are left as they were.
+ * A session whose pos0 is out of range (DS4A_ERR_DEVICE_INDEX) or whose tokens pass `slots`
+ * (DS4A_ERR_CAPACITY) is left alone.  Sums and products are binary32.
+ */
+int ds4a_paged_append_norm(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16_t *v, int N, const int32_t *n_tok,
+                           const int32_t *parent, const float *k_w, const float *q_w, float eps, const float *inv_freq,
+                           int rot, int rot_off, int interleaved, const uint16_t *q, int H, uint16_t *q_out,
+                           const long long *pos0, int32_t *slot_pos, int slots, void *stream);
+
+/*
  * ds4a_compress_tree -- the compressed row of every drafted node whose position p ends a
  * block ((p+1) % ratio == 0), over the block's tokens on the node's own path, into row
  * cap - N + node of comp_k and comp_v (rows of other nodes are left as they were).  The
@@ -624,6 +646,71 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
                      const int32_t *leaf, long long *len_out, const float *score_w, int ratio, const float *state,
                      float *state_out, uint16_t *comp_k, uint16_t *comp_v, long long cap, uint16_t *k_idx, int d_idx,
                      void *stream);
+
+/*
+ * Caches held to a budget of tokens.
+ * ("DwarfStar (ds4) Deep Dive" bounds a session's memory by its context length; the pages give
+ * no rule for dropping tokens.)  A session of the paged cache that attends all its tokens
+ * can be cut to the ones that matter: the step's attention call leaves each row's log of
+ * the sum of exp, ds4a_attn_weights adds up what weight every cached token got, and
+ * ds4a_evict keeps the first and newest tokens and those with the most weight.  A cut cache
+ * has positions that differ from its slots: ds4a_paged_append_norm takes and records them,
+ * and they go with the tokens.  Attention without a window takes slots in any order, so the
+ * calls on the paged cache work on it as before as long as no window is shorter than it.
+ *
+ * Sums and positions are [B, slots] arrays beside the pages: entry t belongs to slot t.
+ */
+
+/*
+ * ds4a_attn_weights -- for every session and slot t < len + n,
+ *   acc[t] = (t < len ? decay * acc[t] : 0) + sum_i sum_h exp(scale * q_ih . K_t - lse_ih)
+ * over the new tokens i that attend it (i >= t - len; they sit in slots len .. len+n-1, and token i
+ * attends slots 0 .. len+i).
+ *
+ *   q          [B, N, H, D] fp16: the queries as the attention call had them; N 1 .. 64.
+ *   n_tok      [B] int32: n.  A session with n = 0 is left as it is.
+ *   lse        [B, N, H] float: log of the sum of exp of each row's scaled scores.  A row whose
+ *              lse is -inf (no key, or none but scores of -inf) adds nothing.
+ *   scale      softmax scale, > 0, at most 2.3e38.
+ *   decay      0 .. 1; with 0 the sums before are not read.
+ *   acc        [B, slots] float.  Entries of slots >= len + n, and of tokens whose page id is
+ *              outside the pool, are left as they were.
+ * A session whose tokens pass `slots` is left alone (DS4A_ERR_CAPACITY).  Scores, exponentials and
+ * sums are binary32; a slot's sum is taken in a fixed order (no atomics).
+ */
+int ds4a_attn_weights(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, const int32_t *n_tok, const float *lse,
+                      float scale, float decay, float *acc, int slots, void *stream);
+
+/*
+ * ds4a_evict -- cuts every session of more than `budget` tokens to exactly `budget`.
+ *
+ * Kept: tokens at positions below n_sink or at next - n_recent and above; then those with the
+ * largest acc, equal ones by the lower slot (NaN counts as less than any number, -0 as 0).  If
+ * positions repeat and more than `budget` are always kept, the lower slots of those stay.
+ * The j-th dropped slot below `budget`, in slot order, receives the j-th kept token from slots
+ * budget and up: its K and V rows, sum and position.  All other kept tokens stay where they are.
+ *
+ *   acc, pos   [B, slots] float / int32 (pos >= 0): entries of slots 0 .. len-1 are read.
+ *   slots      1 .. 2^23.
+ *   next       [B] int64: the position of the session's next token.
+ *   budget     >= 1, n_sink >= 0, n_recent >= 0, n_sink + n_recent <= budget.
+ *   acc_out, pos_out  [B, slots]: entries 0 .. len_out-1 are the kept tokens'; those behind are left as
+ *              they were.  Both are acc and pos themselves, or both overlap neither.
+ *   len_out    [B] int64: min(len, budget); may be kv->len's array, and may not overlap it otherwise.
+ *   ws         ds4a_evict_workspace_bytes(B, slots, budget) bytes, 256-byte aligned; its contents need
+ *              not be set or kept.  Calls that share one workspace must be stream-ordered (two
+ *              captured graphs that may replay at the same time need one each).
+ * Pages of slots below `budget` that hold a token to drop are written, so they may not be shared:
+ * a shared prefix stays whole when its positions are below n_sink.  Pages behind the budget are free
+ * afterwards.  A session that is not cut keeps its pages as they are.  A session with len < 0 or a page
+ * id outside the pool among its tokens' (DS4A_ERR_DEVICE_INDEX), or with len past `slots` or its pages
+ * (DS4A_ERR_CAPACITY), is left alone.
+ */
+int ds4a_evict(const ds4a_paged_kv_t *kv, const float *acc, const int32_t *pos, int slots, const long long *next, int budget,
+               int n_sink, int n_recent, float *acc_out, int32_t *pos_out, long long *len_out, void *ws, size_t ws_bytes,
+               void *stream);
+
+size_t ds4a_evict_workspace_bytes(int B, int slots, int budget);
 
 /*
  * ds4a_probe_gather -- MEASUREMENT CALL, not a step of the attention path; the
