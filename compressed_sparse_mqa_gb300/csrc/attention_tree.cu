@@ -63,6 +63,7 @@
 // rows, noted, so that exactly those rows get them in the end.
 #include <type_traits>
 
+#include "line.cuh"
 #include "paged_dev.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"
@@ -159,6 +160,9 @@ struct Args {
     int B, mode, min_tiles, row_tiles, tile_rows, item_rows, n_work;
     int pool_oob, comp_oob;                        // rows of the maps: the zero-fill rows
     uint32_t h_mul;                                // node_of
+    PrefixArgs pre;                                // shared prefixes
+    int *pre_ok;                                   // the groups were well formed
+    int g_tile_rows, g_slots, part_s;              // a group's row tiles; their places; first partial row of the sessions' own
 };
 
 enum { kDirect, kWalk, kStream };
@@ -172,6 +176,9 @@ struct JoinArgs {
     uint16_t *out;
     long long cap;
     int B, N, H, ratio, row_tiles, tile_rows, item_rows;
+    PrefixArgs pre;
+    const int *pre_ok;
+    int g_tile_rows, g_slots, part_s;
 };
 
 // row / H of a session's row (below 64 * 64 + 256) without a division: h_mul = ceil(2^20 / H)
@@ -186,6 +193,9 @@ DS4A_DEVINL float ex2(float x) {
 DS4A_DEVINL float inverse(float m, float l) {
     return l != 0.f ? 1.f / l : (m == -INFINITY ? 0.f : __uint_as_float(0x7fffffffu));
 }
+// log of the sum of exp of a row's scores, from its reference and sum in powers of two: -inf for a row without keys
+// or with scores that are all -inf
+DS4A_DEVINL float log_sum(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
 DS4A_DEVINL int clamp16(int x) { return x < 0 ? 0 : (x > kRun ? kRun : x); }
 
 // Valid keys of run v for a row with first committed slot lo, drafted tokens raw and
@@ -232,9 +242,10 @@ DS4A_DEVINL unsigned long long shfl64(unsigned long long v, int src) { return __
 // stream: how many CTAs share the row tile, the first of them, this one's place.
 struct Item {
     int s, rt, t0, t1, pieces, first, part;
+    int shared, slot, rows;          // shared prefixes: its length; the row tile's place in the table; a group's rows (0: a session)
 };
 DS4A_DEVINL Item direct_item(const Args &g) {
-    Item id{-1, 0, 0, 0x7fffffff, 1, 0, 0};
+    Item id{-1, 0, 0, 0x7fffffff, 1, 0, 0, 0, 0, 0};
     if (static_cast<int>(blockIdx.x) < g.n_work) {
         const unsigned x = blockIdx.x;
         id.rt = g.B > 1 ? x / static_cast<unsigned>(g.B) : x;
@@ -300,7 +311,7 @@ DS4A_DEVINL int walk_to(const Args &g, Walk &k, long long t, int lane) {
 }
 template <bool kSel>
 DS4A_DEVINL Item walk_item(const Args &g, Walk &k, int number, int lane) {
-    Item id{-1, 0, 0, 0x7fffffff, 1, 0, 0};
+    Item id{-1, 0, 0, 0x7fffffff, 1, 0, 0, 0, 0, 0};
     const int l = walk_to<kSel>(g, k, number, lane);
     if (l >= 0) {
         id.s = k.first + l;
@@ -334,7 +345,7 @@ DS4A_DEVINL Share stream_share(const Args &g, Walk &k, int lane) {
 }
 template <bool kSel>
 DS4A_DEVINL Item stream_item(const Args &g, Walk &k, Share &h, int lane) {
-    Item id{-1, 0, 0, 0, 1, 0, 0};
+    Item id{-1, 0, 0, 0, 1, 0, 0, 0, 0, 0};
     if (h.u >= h.end) return id;
     const int l = walk_to<kSel>(g, k, h.u, lane);
     if (l < 0) return id;
@@ -354,6 +365,127 @@ DS4A_DEVINL Item stream_item(const Args &g, Walk &k, Share &h, int lane) {
     return id;
 }
 
+// ---- shared prefixes ----
+// The line then has two kinds of entries: first the groups, whose rows are those of all their sessions
+// (consecutive in q) and whose keys are the prefix, slots 0 .. shared-1 of the first session's
+// pages; then the sessions, whose keys are what follows.  A row's result is joined from both.
+
+// The groups are in order and inside the batch (every lane gets the answer).
+DS4A_DEVINL bool groups_ok(const PrefixArgs &p, int B, int lane) {
+    bool bad = false;
+    for (int i = lane; i <= p.n_groups && p.n_groups > 0; i += 32) {
+        const int a0 = __ldg(p.start + i);
+        bad |= a0 < 0 || a0 > B || (i > 0 && a0 < __ldg(p.start + i - 1));
+    }
+    return !__any_sync(0xffffffffu, bad);
+}
+// The group of session s, or -1
+DS4A_DEVINL int group_of(const PrefixArgs &p, int s) {
+    int lo = 0, hi = p.n_groups + 1;                  // the first entry above s
+    if (p.n_groups == 0) return -1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.start + mid) > s) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo == 0 || lo > p.n_groups ? -1 : lo - 1;
+}
+// Length of session s's shared prefix: 0 without one, -1 if the session must be left alone (the reason is recorded).
+DS4A_DEVINL int shared_of(const PrefixArgs &p, const PagedKV &kv, int s, int group, long long len, unsigned int *err) {
+    if (group < 0) return 0;
+    const long long sh = __ldg(p.shared + group);
+    if (sh < 0 || sh > len) {                         // (len fits the session's pages)
+        record_error(err, DS4A_ERR_DEVICE_INDEX);
+        return -1;
+    }
+    return static_cast<int>(sh);
+}
+struct Entry {
+    int s, rows, shared, tiles, row_tiles;            // first session, rows, prefix, key tiles, row tiles
+};
+DS4A_DEVINL Entry prefix_entry(const Args &g, int x, unsigned int *err) {
+    const AttnTreeArgs &a = g.a;
+    const PrefixArgs &p = g.pre;
+    Entry e{0, 0, 0, 0, 0};
+    if (x < p.n_groups) {
+        const int a0 = __ldg(p.start + x), a1 = __ldg(p.start + x + 1);
+        const long long sh = __ldg(p.shared + x);
+        if (a0 >= a1 || sh <= 0 || sh > static_cast<long long>(a.kv.max_pages) * a.kv.page) return e;
+        e.s = a0;
+        e.rows = (a1 - a0) * a.N * a.H;
+        e.shared = static_cast<int>(sh);
+        e.tiles = (runs_of(e.shared) + kRuns - 1) / kRuns;
+        e.row_tiles = (e.rows + g.g_tile_rows - 1) / g.g_tile_rows;
+        return e;
+    }
+    e.s = x - p.n_groups;
+    const Session ses = load_session(a.kv, a.n_node, a.N, e.s, err);
+    if (!ses.ok || ses.n == 0) return e;
+    e.shared = shared_of(p, a.kv, e.s, group_of(p, e.s), ses.len, err);
+    if (e.shared < 0) return e;
+    e.rows = ses.n * a.H;
+    e.tiles = (runs_of(static_cast<int>(ses.len) + ses.n - (e.shared & ~(kRun - 1))) + kRuns - 1) / kRuns;
+    e.row_tiles = (e.rows + g.tile_rows - 1) / g.tile_rows;
+    return e;
+}
+DS4A_DEVINL long long entry_units(const Args &g, int x, unsigned int *err) {
+    const Entry e = prefix_entry(g, x, err);
+    return static_cast<long long>(e.tiles) * e.row_tiles;
+}
+// A row tile's place in the table; along the line it grows, so with the CTA added it is also a place of its own for
+// each piece (the next piece is another row tile's or another CTA's).
+DS4A_DEVINL int group_slot(const PrefixArgs &p, int group, long long session_rows, int tile_rows) {
+    return static_cast<int>(__ldg(p.start + group) * session_rows / tile_rows) + group;
+}
+DS4A_DEVINL Share prefix_share(const Args &g, Line &k, int lane) {
+    Share h{0, 0, 0, 0};
+    const bool ok = groups_ok(g.pre, g.B, lane);
+    if (blockIdx.x == 0 && lane == 0) *g.pre_ok = ok;
+    if (!ok) {
+        if (lane == 0) record_error(g.a.err, DS4A_ERR_DEVICE_INDEX);
+        return h;
+    }
+    auto units = [&](int x) { return entry_units(g, x, g.a.err); };
+    h.units = line_total(k, g.pre.n_groups + g.B, units);
+    const long long most = line_quot(h.units + g.min_tiles - 1, g.min_tiles);
+    h.ctas = most < static_cast<long long>(gridDim.x) ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+    const int c = blockIdx.x;
+    h.u = c < h.ctas ? line_quot(h.units * c, h.ctas) : 0;
+    h.end = c < h.ctas ? line_quot(h.units * (c + 1), h.ctas) : 0;
+    return h;
+}
+DS4A_DEVINL Item prefix_item(const Args &g, Line &k, Share &h) {
+    Item id{-1, 0, 0, 0, 1, 0, 0, 0, 0, 0};
+    if (h.u >= h.end) return id;
+    auto units = [&](int x) { return entry_units(g, x, nullptr); };
+    const int n = g.pre.n_groups + g.B, l = line_to(k, n, h.u, units);
+    if (l < 0) return id;
+    const int x = k.first + l;
+    const long long at = k.before + __shfl_sync(0xffffffffu, k.incl - k.mine, l);   // the entry's first unit
+    const Entry e = prefix_entry(g, x, nullptr);
+    const bool group = x < g.pre.n_groups;
+    id.s = e.s;
+    id.shared = e.shared;
+    id.rows = group ? e.rows : 0;
+    id.rt = static_cast<int>(line_quot(h.u - at, e.tiles));
+    const long long lo = at + static_cast<long long>(id.rt) * e.tiles, hi = lo + e.tiles;
+    id.t0 = static_cast<int>(h.u - lo);
+    const long long end = hi < h.end ? hi : h.end;
+    id.t1 = static_cast<int>(end - lo);
+    id.first = static_cast<int>(line_quot((lo + 1) * h.ctas - 1, h.units));
+    id.pieces = static_cast<int>(line_quot(hi * h.ctas - 1, h.units)) - id.first + 1;
+    const int c = blockIdx.x;
+    if (group) {
+        id.slot = group_slot(g.pre, x, static_cast<long long>(g.a.N) * g.a.H, g.g_tile_rows) + id.rt;
+        id.part = (id.slot + c) * g.g_tile_rows;
+    } else {
+        id.slot = g.g_slots + e.s * g.row_tiles + id.rt;
+        id.part = g.part_s + (id.slot - g.g_slots + c) * g.tile_rows;
+    }
+    h.u = end;
+    return id;
+}
+
 // or / and over the warp
 template <bool kOr>
 DS4A_DEVINL unsigned long long reduce64(unsigned long long v) {
@@ -364,13 +496,44 @@ DS4A_DEVINL unsigned long long reduce64(unsigned long long v) {
 }
 
 // The set-up warp's item: lane holds nodes lane and lane + 32.
-template <bool kSel, typename W>
+template <bool kSel, bool kPre, typename W>
 __device__ void make_work(const Args &g, const Item id, W &w, int lane) {
     const AttnTreeArgs &a = g.a;
     if (lane == 0) w.stop = id.s < 0;
     if (id.s < 0) {
         __syncwarp();
         return;
+    }
+    if constexpr (kPre) {
+        if (id.rows > 0) {                            // a group: its prefix, which every row attends
+            for (int x = lane; x < kMaxNodes; x += 32) {
+                w.raw[x] = w.cmp[x] = 0;
+                w.lo[x] = 0;
+            }
+            if (w.dirty)
+                for (int x = lane; x < kPoison * 12; x += 32) (&w.poison[0][0])[x] = 0;
+            __syncwarp();
+            if (lane == 0) {
+                w.any_raw = w.all_raw = w.any_cmp = w.all_cmp = 0;
+                w.lo_min = w.lo_max = 0;
+                w.s = id.s;
+                w.len = id.shared;
+                w.t0 = 0;
+                w.raw_runs = w.n_runs = runs_of(id.shared);
+                w.comp_runs = w.n_vis0 = w.node = 0;
+                w.row0 = id.rt * g.g_tile_rows;
+                w.rows = min(g.g_tile_rows, id.rows - w.row0);
+                w.sides2 = w.rows > kTK;
+                w.tile0 = id.t0;
+                w.tile1 = id.t1;
+                w.pieces = 2;                         // joined with the sessions' own
+                w.part = id.part;
+                w.dirty = 0;
+                if (id.first == static_cast<int>(blockIdx.x)) g.pieces[id.slot] = make_int2(id.pieces, id.first);
+            }
+            __syncwarp();
+            return;
+        }
     }
     const int rt = id.rt, s = id.s;
     int p[2];                                         // parents, loaded beside the session's counts
@@ -444,7 +607,7 @@ __device__ void make_work(const Args &g, const Item id, W &w, int lane) {
         unsigned long long raw = m[x];
         for (long long c = depth + 1; c > a.window; --c) raw &= raw - 1;   // the shallowest fall out of the window
         const long long lo64 = static_cast<long long>(len) + depth - a.window + 1;
-        const int lo = lo64 < 0 ? 0 : static_cast<int>(lo64);
+        const int lo = kPre ? id.shared : (lo64 < 0 ? 0 : static_cast<int>(lo64));
         const unsigned long long cmp = kSel ? m[x] : m[x] & done;
         w.raw[i] = raw;
         w.cmp[i] = cmp;
@@ -469,7 +632,7 @@ __device__ void make_work(const Args &g, const Item id, W &w, int lane) {
             for (int x = lane; x < kPoison * 12; x += 32) (&w.poison[0][0])[x] = 0;
     __syncwarp();   // w.cmp is read below
     if (lane == 0) {
-        const int t0 = g.mode == kStream ? session_t0(a, len) : min(lo_min, len) & ~(kRun - 1);
+        const int t0 = kPre ? id.shared & ~(kRun - 1) : (g.mode == kStream ? session_t0(a, len) : min(lo_min, len) & ~(kRun - 1));
         w.any_raw = any_raw;
         w.all_raw = all_raw;
         w.any_cmp = any_cmp;
@@ -498,11 +661,11 @@ __device__ void make_work(const Args &g, const Item id, W &w, int lane) {
         const int tiles = rows > 0 ? (w.n_runs + kRuns - 1) / kRuns : 0;
         w.tile0 = min(tiles, id.t0);
         w.tile1 = min(tiles, id.t1);
-        w.pieces = id.pieces;
+        w.pieces = kPre && id.shared > 0 ? 2 : id.pieces;
         w.part = id.part;
         w.dirty = 0;
         if (g.mode == kStream && id.first == static_cast<int>(blockIdx.x))
-            g.pieces[s * g.row_tiles + rt] = make_int2(rows > 0 ? id.pieces : 0, id.first);
+            g.pieces[kPre ? id.slot : s * g.row_tiles + rt] = make_int2(rows > 0 ? id.pieces : 0, id.first);
     }
     __syncwarp();
 }
@@ -587,7 +750,7 @@ DS4A_DEVINL void transpose4(uint4 (&u)[4], int lane) {
     }
 }
 
-template <int D, bool kSel>
+template <int D, bool kSel, bool kPre>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_constant__ Args g) {
     using L = Layout<D, kSel>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -785,8 +948,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                     const int dirty = w.dirty;
                     const float inv = inverse(m, l);
                     const long long qrow = (static_cast<long long>(w.s) * a.N) * a.H + w.row0 + row;
-                    const long long prow = static_cast<long long>(w.part) * g.tile_rows + row;
+                    const long long prow = kPre ? static_cast<long long>(w.part) + row
+                                                : static_cast<long long>(w.part) * g.tile_rows + row;
                     if (!direct && valid && c0 == 0) g.part_ml[prow] = make_float2(m, l);
+                    if (kPre && direct && valid && c0 == 0 && g.pre.lse) g.pre.lse[qrow] = log_sum(m, l);
 #pragma unroll 1
                     for (int c = c0; c < c1; ++c) {                // 32 columns at a time
                         uint32_t o[32];
@@ -871,10 +1036,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
         };
         if (warp == kSetupWarp) {
             uint32_t n_q = 0;
-            auto load_q = [&](int s, int row0) {
+            auto load_q = [&](int s, int row0, bool two) {
                 if (n_q > 0 && !warp_wait(&bar.q_empty, n_q - 1)) return false;
                 if (lane == 0) {
-                    const int blocks = !kSel && g.tile_rows > kTK ? 2 : 1;
+                    const int blocks = two ? 2 : 1;
                     const int qrow = s * a.N * a.H + row0;
                     constexpr int kBlock = L::q_rows * D * 2;
                     tc::expect_tx(&bar.q_full, blocks * kBlock);
@@ -892,24 +1057,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             if (lane == 0) tc::prefetch_map(&g.map_q);
             if (g.mode == kDirect) {   // the query rows are known from the CTA's number
                 const Item id = direct_item(g);
-                if (id.s >= 0) load_q(id.s, id.rt * g.item_rows);
+                if (id.s >= 0) load_q(id.s, id.rt * g.item_rows, !kSel && g.tile_rows > kTK);
             }
-            if (g.mode == kWalk) walk_load<kSel>(g, walk, 0, 0, lane);
-            if (g.mode == kStream) share = stream_share<kSel>(g, walk, lane);
+            Line line{};
+            if constexpr (kPre) {
+                share = prefix_share(g, line, lane);
+            } else {
+                if (g.mode == kWalk) walk_load<kSel>(g, walk, 0, 0, lane);
+                if (g.mode == kStream) share = stream_share<kSel>(g, walk, lane);
+            }
             for (int it = 0;; ++it) {
                 if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
                 W &w = works[it & 1];
-                Item id{-1, 0, 0, 0, 0, 0, 0};
-                if (g.mode == kWalk) id = walk_item<kSel>(g, walk, blockIdx.x + it * gridDim.x, lane);
+                Item id{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                if (kPre) id = prefix_item(g, line, share);
+                else if (g.mode == kWalk) id = walk_item<kSel>(g, walk, blockIdx.x + it * gridDim.x, lane);
                 else if (g.mode == kStream) id = stream_item<kSel>(g, walk, share, lane);
                 else if (it == 0) id = direct_item(g);
-                make_work<kSel>(g, id, w, lane);
+                make_work<kSel, kPre>(g, id, w, lane);
                 if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
                 __syncwarp();
                 if (id.s < 0) break;
                 // the queries, when the item before has made its last scores (its output, which frees the
                 // Work after next, comes later; the K producers do not wait here)
-                if (g.mode != kDirect && w.tile1 > w.tile0 && !load_q(w.s, w.row0)) break;
+                if (g.mode != kDirect && w.tile1 > w.tile0 &&
+                    !load_q(w.s, w.row0, kPre ? w.sides2 != 0 : !kSel && g.tile_rows > kTK))
+                    break;
             }
             if (!ok && lane == 0 && n_q > 0) tc::mbar_wait(&bar.q_full, (n_q - 1) & 1u);   // a wait gave up
             __syncwarp();
@@ -1227,7 +1400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
 // 128; with one warp going through them one by one the join took 40 us).  Rows of a row tile that
 // one CTA had are already written.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-template <int D, int kPerRow>
+template <int D, int kPerRow, bool kPre>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
     constexpr int kPer = D / 32, kBatch = 8;
     __shared__ float s_o[kPerRow > 1 ? kPerRow : 1][D];
@@ -1238,15 +1411,35 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
     pdl_trigger();
     if (row >= g.B * per) return;                    // (with kPerRow > 1 a block has one row: it leaves as a whole)
     const int s = row / per, r = row - s * per, rt = static_cast<unsigned>(r) / static_cast<unsigned>(g.item_rows);
-    const int2 p = g.pieces[s * g.row_tiles + rt];   // set if the session is in the line
+    const int2 p = g.pieces[(kPre ? g.g_slots : 0) + s * g.row_tiles + rt];   // set if the session is in the line
     const Session ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
     if (!ses.ok || r >= ses.n * g.H) return;
     if (g.ratio > 0 && static_cast<unsigned>(ses.len) / static_cast<unsigned>(g.ratio) > g.cap - g.N) return;
-    const int pieces = p.x, first = p.y;
+    const int first = p.y, in_tile = r - rt * g.item_rows;
+    int pieces = p.x, shared_pieces = 0;
+    long long shared_at = 0;                         // the first piece of the shared prefix
+    if constexpr (kPre) {
+        if (!*g.pre_ok) return;
+        const int group = group_of(g.pre, s), sh = shared_of(g.pre, g.kv, s, group, ses.len, nullptr);
+        if (sh < 0 || pieces <= 0) return;           // left alone
+        if (sh > 0) {
+            const int gr = (s - __ldg(g.pre.start + group)) * static_cast<int>(per) + r, grt = gr / g.g_tile_rows;
+            const int slot = group_slot(g.pre, group, per, g.g_tile_rows) + grt;
+            const int2 gp = g.pieces[slot];
+            shared_pieces = gp.x;
+            shared_at = static_cast<long long>(slot + gp.y) * g.g_tile_rows + gr - grt * g.g_tile_rows;
+            pieces += shared_pieces;
+        }
+    }
     if (pieces <= 1) return;
-    const int in_tile = r - rt * g.item_rows;
-    // the first CTA has the row tile as its tail, the others as their head
-    auto at = [&](int i) { return static_cast<long long>(2 * (first + i) + (i == 0)) * g.tile_rows + in_tile; };
+    // stream: the first CTA has the row tile as its tail, the others as their head
+    auto at = [&](int i) -> long long {
+        if constexpr (kPre) {
+            if (i < shared_pieces) return shared_at + static_cast<long long>(i) * g.g_tile_rows;
+            return g.part_s + static_cast<long long>(s * g.row_tiles + rt + first + i - shared_pieces) * g.tile_rows + in_tile;
+        }
+        return static_cast<long long>(2 * (first + i) + (i == 0)) * g.tile_rows + in_tile;
+    };
     float m = -INFINITY;
     for (int i = lane; i < pieces; i += 32) m = fmaxf(m, g.part_ml[at(i)].x);
     m = warp_max(m);
@@ -1303,6 +1496,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
             for (int x = 1; x < kPerRow; ++x) o[e] += s_o[x][lane * kPer + e];
         }
     }
+    if (kPre && g.pre.lse && lane == 0) g.pre.lse[row] = log_sum(m, l);
     const float inv = inverse(m, l);
     uint32_t h[kPer / 2];
 #pragma unroll
@@ -1361,18 +1555,18 @@ Plan make_plan(const AttnTreeArgs &a, int B, int num_sms) {
     return p;
 }
 
-template <int D, bool kSel>
+template <int D, bool kSel, bool kPre = false>
 cudaError_t launch_one(Args &g, int ctas, const Ctx &c) {
     static thread_local int configured_device = -1;
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_device != dev) {
-        cudaError_t e = cudaFuncSetAttribute(attn_tree_kernel<D, kSel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(attn_tree_kernel<D, kSel, kPre>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(Layout<D, kSel>::bytes));
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
-    return launch(attn_tree_kernel<D, kSel>, dim3(ctas), dim3(kThreads), (Layout<D, kSel>::bytes), c, 1, g);
+    return launch(attn_tree_kernel<D, kSel, kPre>, dim3(ctas), dim3(kThreads), (Layout<D, kSel>::bytes), c, 1, g);
 }
 
 }  // namespace
@@ -1418,16 +1612,95 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
                              : (a.sel ? launch_one<64, true>(g, p.ctas, c) : launch_one<64, false>(g, p.ctas, c));
     if (e != cudaSuccess || p.mode != kStream) return e;
     const JoinArgs j{g.part, g.part_ml, g.pieces, a.kv, a.n_node, a.out, a.cap, B, a.N, a.H, a.ratio, p.row_tiles,
-                     p.tile_rows, p.item_rows};
+                     p.tile_rows, p.item_rows, {}, nullptr, 0, 0, 0};
     const long long rows = static_cast<long long>(B) * a.N * a.H;
     if (p.ctas >= 8 * slots) {                           // eight pieces a row tile or more
         const dim3 grid(static_cast<unsigned>(rows));
-        return D == 128 ? launch(combine_kernel<128, kJoinWarps>, grid, dim3(kJoinThreads), 0, c, 1, j)
-                        : launch(combine_kernel<64, kJoinWarps>, grid, dim3(kJoinThreads), 0, c, 1, j);
+        return D == 128 ? launch(combine_kernel<128, kJoinWarps, false>, grid, dim3(kJoinThreads), 0, c, 1, j)
+                        : launch(combine_kernel<64, kJoinWarps, false>, grid, dim3(kJoinThreads), 0, c, 1, j);
     }
     const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
-    return D == 128 ? launch(combine_kernel<128, 1>, grid, dim3(kJoinThreads), 0, c, 1, j)
-                    : launch(combine_kernel<64, 1>, grid, dim3(kJoinThreads), 0, c, 1, j);
+    return D == 128 ? launch(combine_kernel<128, 1, false>, grid, dim3(kJoinThreads), 0, c, 1, j)
+                    : launch(combine_kernel<64, 1, false>, grid, dim3(kJoinThreads), 0, c, 1, j);
+}
+
+namespace {
+
+// How a call with shared prefixes is cut, from the sizes that the host knows.
+struct PrefixPlan {
+    int g_tile_rows, tile_rows, row_tiles, g_slots, part_s, min_tiles, ctas;
+    size_t part_rows;
+};
+PrefixPlan prefix_plan(int B, int N, int H, int n_groups, long long tokens, int num_sms) {
+    PrefixPlan p{};
+    const long long per = static_cast<long long>(N) * H, tiles = (tokens + kTK - 1) / kTK;
+    const long long group = n_groups > 0 ? (B + n_groups - 1) / n_groups * per : 0;   // rows of a group, were they alike
+    auto two = [&](long long rows, long long n) { return rows > kTK && (rows + 2 * kTK - 1) / (2 * kTK) * n * tiles >= 4LL * num_sms; };
+    p.g_tile_rows = two(group, n_groups) ? 2 * kTK : kTK;
+    p.tile_rows = two(per, B) ? 2 * kTK : kTK;
+    p.row_tiles = static_cast<int>((per + p.tile_rows - 1) / p.tile_rows);
+    p.min_tiles = p.tile_rows == kTK && p.g_tile_rows == kTK ? 2 : 1;
+    p.ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+    p.g_slots = n_groups > 0 ? static_cast<int>(B * per / p.g_tile_rows) + n_groups + 1 : 0;
+    p.part_s = n_groups > 0 ? (p.g_slots + p.ctas) * p.g_tile_rows : 0;
+    p.part_rows = static_cast<size_t>(p.part_s) + (static_cast<size_t>(B) * p.row_tiles + p.ctas) * p.tile_rows;
+    return p;
+}
+size_t prefix_header(const PrefixPlan &p, int B) { return 256 + header_bytes(p.g_slots + static_cast<long long>(B) * p.row_tiles); }
+
+}  // namespace
+
+// No less than any way a call of these sizes may be cut (tiles of one or two blocks, for groups and sessions).
+size_t attn_prefix_ws_bytes(int B, int N, int H, int D, int n_groups) {
+    const size_t per = static_cast<size_t>(N) * H, two = 2 * kTK, b = B, g = n_groups, ctas = kMaxCtas;
+    const size_t slots = (g > 0 ? b * per / kTK + g + 1 : 0) + b * ((per + kTK - 1) / kTK);
+    const size_t rows = (g > 0 ? b * per + (g + 1 + ctas) * two : 0) + b * ((per + two - 1) / two * two) + ctas * two;
+    return 256 + header_bytes(static_cast<long long>(slots)) + rows * (static_cast<size_t>(D) * 4 + 8);
+}
+
+cudaError_t launch_attn_prefix(const AttnTreeArgs &args, const PrefixArgs &pre, int B, const Ctx &c) {
+    Args g{};
+    g.a = args;
+    g.pre = pre;
+    AttnTreeArgs &a = g.a;
+    a.scale_log2 = a.scale * kLog2e;
+    a.window = 1LL << 62;
+    const int D = a.kv.D;
+    const long long tokens = static_cast<long long>(a.kv.max_pages) * a.kv.page, pool_rows = a.kv.n_pages * a.kv.page;
+    const PrefixPlan p = prefix_plan(B, a.N, a.H, pre.n_groups, tokens, c.num_sms);
+    if (!tc::encode_map(&g.map_q, a.q, D, static_cast<long long>(B) * a.N * a.H, kTK) ||
+        !tc::encode_map(&g.map_k, a.kv.k, D, pool_rows, kRun) || !tc::encode_map(&g.map_v, a.kv.v, D, pool_rows, kRun))
+        return cudaErrorInvalidValue;
+    g.B = B;
+    g.mode = kStream;
+    g.min_tiles = p.min_tiles;
+    g.row_tiles = p.row_tiles;
+    g.tile_rows = g.item_rows = p.tile_rows;
+    g.g_tile_rows = p.g_tile_rows;
+    g.g_slots = p.g_slots;
+    g.part_s = p.part_s;
+    g.h_mul = ((1u << 20) + static_cast<uint32_t>(a.H) - 1) / static_cast<uint32_t>(a.H);
+    g.pool_oob = static_cast<int>(pool_rows);
+    unsigned char *ws = static_cast<unsigned char *>(a.ws);
+    const size_t head = prefix_header(p, B);
+    g.pre_ok = reinterpret_cast<int *>(ws);
+    g.pieces = reinterpret_cast<int2 *>(ws + 256);
+    g.part = reinterpret_cast<float *>(ws + head);
+    g.part_ml = reinterpret_cast<float2 *>(ws + head + p.part_rows * D * 4);
+    cudaError_t e = D == 128 ? launch_one<128, false, true>(g, p.ctas, c) : launch_one<64, false, true>(g, p.ctas, c);
+    if (e != cudaSuccess) return e;
+    const JoinArgs j{g.part, g.part_ml, g.pieces, a.kv, a.n_node, a.out, 0, B, a.N, a.H, 0, p.row_tiles, p.tile_rows, p.tile_rows,
+                     pre, g.pre_ok, p.g_tile_rows, p.g_slots, p.part_s};
+    const long long rows = static_cast<long long>(B) * a.N * a.H;
+    // many pieces a row where there are eight CTAs or more for every 128 rows
+    if (p.ctas >= 8 * ((rows + kTK - 1) / kTK)) {
+        const dim3 grid(static_cast<unsigned>(rows));
+        return D == 128 ? launch(combine_kernel<128, kJoinWarps, true>, grid, dim3(kJoinThreads), 0, c, 1, j)
+                        : launch(combine_kernel<64, kJoinWarps, true>, grid, dim3(kJoinThreads), 0, c, 1, j);
+    }
+    const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+    return D == 128 ? launch(combine_kernel<128, 1, true>, grid, dim3(kJoinThreads), 0, c, 1, j)
+                    : launch(combine_kernel<64, 1, true>, grid, dim3(kJoinThreads), 0, c, 1, j);
 }
 
 }  // namespace ds4a

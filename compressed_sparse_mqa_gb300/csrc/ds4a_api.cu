@@ -656,6 +656,37 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
     return from_cuda(ds4a::launch_commit_tree(a, kv->B, c));
 }
 
+size_t ds4a_attn_prefix_workspace_bytes(int B, int N, int H, int D, int n_groups) {
+    if (B < 0 || B > 65535 || N < 1 || N > 64 || n_groups < 0 || n_groups > 65535 || check_heads(H, D) != DS4A_OK) return 0;
+    return ds4a::attn_prefix_ws_bytes(B, N, H, D, n_groups);
+}
+
+int ds4a_attn_prefix(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, const int32_t *n_node, const int32_t *parent,
+                     const int32_t *start, const long long *shared, int n_groups, float scale, uint16_t *out, float *lse,
+                     void *ws, size_t ws_bytes, void *stream) {
+    int rc = check_paged(kv);
+    if (rc != DS4A_OK) return rc;
+    rc = check_heads(H, kv->D);
+    if (rc != DS4A_OK) return rc;
+    rc = check_tree(N, n_node, parent);
+    if (rc != DS4A_OK) return rc;
+    if (n_groups < 0 || !(scale > 0.f) || scale > 2.3e38f) return DS4A_ERR_ARG;   // scale * log2(e) is finite
+    if (n_groups > 65535) return DS4A_ERR_UNSUPPORTED;
+    if (kv->B == 0) return DS4A_OK;
+    if (!q || !out || (n_groups > 0 && (!start || !shared))) return DS4A_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(start, 4) || !aligned(shared, 8)) return DS4A_ERR_ARG;
+    if (overlap(q, out, static_cast<size_t>(kv->B) * N * H * kv->D * 2)) return DS4A_ERR_ARG;
+    if (!ws || !aligned(ws, 256) || ws_bytes < ds4a_attn_prefix_workspace_bytes(kv->B, N, H, kv->D, n_groups))
+        return DS4A_ERR_WORKSPACE;
+    ds4a::Ctx c;
+    rc = make_ctx(stream, c, Early::kNone);
+    if (rc != DS4A_OK) return rc;
+    const ds4a::AttnTreeArgs a{paged_view(kv), q, nullptr, nullptr, n_node, parent, nullptr, out, ws, c.err, 0, 0, N, H, 0, 0,
+                               scale, 0.f};
+    const ds4a::PrefixArgs p{start, shared, lse, n_groups};
+    return from_cuda(ds4a::launch_attn_prefix(a, p, kv->B, c), c);
+}
+
 // ---- caches held to a budget of tokens -----------------------------------------------------
 
 int ds4a_attn_weights(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, const int32_t *n_tok, const float *lse,

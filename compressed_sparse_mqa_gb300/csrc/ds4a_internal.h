@@ -159,6 +159,12 @@ struct AttnTreeArgs {
     int N, H, ratio, n_sel;
     float scale, scale_log2;
 };
+struct PrefixArgs {
+    const int32_t *start;        // [n_groups + 1]
+    const long long *shared;     // [n_groups]
+    float *lse;                  // [B, N, H], or nullptr
+    int n_groups;
+};
 struct AttnWeightsArgs {
     PagedKV kv;
     const uint16_t *q;           // [B, N, H, D]
@@ -186,6 +192,8 @@ struct EvictArgs {
 cudaError_t launch_paged_append(const AppendArgs &a, int B, const Ctx &c);
 cudaError_t launch_compress_tree(const CompressTreeArgs &a, int B, const Ctx &c);
 cudaError_t launch_commit_tree(const CommitTreeArgs &a, int B, const Ctx &c);
+size_t attn_prefix_ws_bytes(int B, int N, int H, int D, int n_groups);
+cudaError_t launch_attn_prefix(const AttnTreeArgs &a, const PrefixArgs &p, int B, const Ctx &c);
 cudaError_t launch_attn_weights(const AttnWeightsArgs &a, int B, const Ctx &c);
 size_t evict_ws_bytes(int B, int slots, int budget);
 cudaError_t launch_evict(const EvictArgs &a, int B, const Ctx &c);

@@ -34,7 +34,8 @@ EXPORTED = ["ds4a_status_str", "ds4a_last_device_error", "ds4a_compress_append",
             "ds4a_compress_attn_decode_batched", "ds4a_probe_gather", "ds4a_decode_layer_step",
             "ds4a_indexer_topk_compress_keys", "ds4a_paged_append", "ds4a_compress_tree", "ds4a_attn_tree",
             "ds4a_attn_tree_workspace_bytes", "ds4a_commit_tree", "ds4a_paged_append_norm",
-            "ds4a_attn_weights", "ds4a_evict", "ds4a_evict_workspace_bytes"]
+            "ds4a_attn_weights", "ds4a_evict", "ds4a_evict_workspace_bytes", "ds4a_attn_prefix",
+            "ds4a_attn_prefix_workspace_bytes"]
 
 
 class Ds4aError(RuntimeError):
@@ -80,6 +81,9 @@ def lib() -> ctypes.CDLL:
         L.ds4a_attn_tree.argtypes = [KV, P, I, I, P, P, LL, P, P, LL, I, P, I, F, P, P, SZ, P]
         L.ds4a_attn_tree_workspace_bytes.argtypes = [I, I, I, I]
         L.ds4a_attn_tree_workspace_bytes.restype = SZ
+        L.ds4a_attn_prefix.argtypes = [KV, P, I, I, P, P, P, P, I, F, P, P, P, SZ, P]
+        L.ds4a_attn_prefix_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.ds4a_attn_prefix_workspace_bytes.restype = SZ
         L.ds4a_attn_weights.argtypes = [KV, P, I, I, P, P, F, F, P, I, P]
         L.ds4a_evict.argtypes = [KV, P, P, I, P, I, I, I, P, P, P, P, SZ, P]
         L.ds4a_evict_workspace_bytes.argtypes = [I, I, I]
@@ -87,7 +91,8 @@ def lib() -> ctypes.CDLL:
         L.ds4a_commit_tree.argtypes = [KV, I, P, P, P, P, P, I, P, P, P, P, LL, P, I, P]
         for name in EXPORTED:
             if name not in ("ds4a_status_str", "ds4a_indexer_workspace_bytes", "ds4a_decode_batched_workspace_bytes",
-                            "ds4a_attn_tree_workspace_bytes", "ds4a_evict_workspace_bytes"):
+                            "ds4a_attn_tree_workspace_bytes", "ds4a_evict_workspace_bytes",
+                            "ds4a_attn_prefix_workspace_bytes"):
                 getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -701,6 +706,40 @@ def ds4a_attn_tree(kv: PagedKVDesc, q, n_node, parent, window: int, comp_k, comp
     _check(lib().ds4a_attn_tree(*args), "ds4a_attn_tree")
 
 
+def ds4a_attn_prefix_workspace_bytes(B: int, N: int, H: int, D: int, n_groups: int) -> int:
+    return int(lib().ds4a_attn_prefix_workspace_bytes(B, N, H, D, n_groups))
+
+
+def _marshal_attn_prefix(kv: PagedKVDesc, q, n_node, parent, start, shared, scale: float, out, lse, ws, stream=None):
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != kv.B or shape[3] != kv.D or out.shape != shape:
+        raise ValueError("attn_prefix: q, out [B, N, H, D]")
+    N, H, G = shape[1], shape[2], 0
+    if (start is None) != (shared is None):
+        raise ValueError("attn_prefix: start and shared come together")
+    if start is not None:
+        if shared.dim() != 1 or start.shape != (shared.shape[0] + 1,):
+            raise ValueError("attn_prefix: start [G + 1], shared [G]")
+        G = shared.shape[0]
+    if lse is not None and lse.shape != shape[:3]:
+        raise ValueError("attn_prefix: lse [B, N, H] (or None)")
+    st, dev = _launch_on("attn_prefix", kv, stream), kv.device
+    pn, pp = _tree_args("attn_prefix", kv, kv.B, N, n_node, parent)
+    return (ctypes.byref(kv), _arg(q, _F16, dev, "q"), N, H, pn, pp, _arg(start, _I32, dev, "start"),
+            _arg(shared, _I64, dev, "shared"), G, scale, _arg(out, _F16, dev, "out"), _arg(lse, _F32, dev, "lse"),
+            _arg(ws, _U8, dev, "ws"), 0 if ws is None else ws.numel(), st)
+
+
+def ds4a_attn_prefix(kv: PagedKVDesc, q, n_node, parent, start, shared, scale: float, out, lse, ws, stream=None):
+    """Attention of every node over its session's whole cache, where sessions start[g] .. start[g+1]-1
+    share their first shared[g] tokens (the first session's pages), which are read and multiplied once
+    for all of them: q, out [B, N, H, D], start [G + 1] int32, shared [G] int64 (both None: nothing is
+    shared), lse [B, N, H] float32 or None: the log of the sum of exp.  ws: uint8,
+    ds4a_attn_prefix_workspace_bytes(B, N, H, D, G) bytes."""
+    args = _marshal_attn_prefix(kv, q, n_node, parent, start, shared, scale, out, lse, ws, stream)
+    _check(lib().ds4a_attn_prefix(*args), "ds4a_attn_prefix")
+
+
 def _marshal_commit_tree(kv: PagedKVDesc, n_node, parent, leaf, len_out, score_w=None, ratio: int = 0, state=None,
                          state_out=None, comp_k=None, comp_v=None, k_idx=None, N=None, stream=None):
     N, B = _nodes("commit_tree", parent, N), kv.B
@@ -805,7 +844,7 @@ _MARSHAL = {"ds4a_attn_decode": _marshal_attn_decode,
             "ds4a_paged_append": _marshal_paged_append, "ds4a_compress_tree": _marshal_compress_tree,
             "ds4a_attn_tree": _marshal_attn_tree, "ds4a_commit_tree": _marshal_commit_tree,
             "ds4a_paged_append_norm": _marshal_paged_append_norm, "ds4a_attn_weights": _marshal_attn_weights,
-            "ds4a_evict": _marshal_evict}
+            "ds4a_evict": _marshal_evict, "ds4a_attn_prefix": _marshal_attn_prefix}
 
 
 def bind(name: str, *args, **kwargs):

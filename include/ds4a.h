@@ -629,6 +629,35 @@ int ds4a_attn_tree(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, c
 size_t ds4a_attn_tree_workspace_bytes(int B, int N, int H, int D);
 
 /*
+ * ds4a_attn_prefix -- attention over the whole cache for a batch whose sessions share long
+ * prefixes, the prefix computed once for all rows of a group: for every node and head one softmax over
+ * the session's len committed tokens, the node's ancestors and itself (ds4a_attn_tree with a window past
+ * every length and no compressed rows).
+ *
+ * Group g is the sessions start[g] .. start[g+1]-1.  Its sessions' first shared[g] tokens are
+ * slots 0 .. shared[g]-1 of its FIRST session's pages; the other sessions' page entries of slots
+ * that lie before shared[g] are not read, except that of the page that slot shared[g] is in.  A prefix
+ * need not end with a page.  Sessions before start[0] and from start[n_groups] on share nothing.
+ *
+ *   q, N, H, n_node, parent, scale, out   as ds4a_attn_tree.
+ *   start      [n_groups + 1] int32, 0 .. B, in ascending order (equal neighbours: an empty group).
+ *   shared     [n_groups] int64, 0 .. len of each of the group's sessions.
+ *   n_groups   0 .. 65535 (0: start and shared may be NULL).
+ *   lse        [B, N, H] float, or NULL: the log of the sum of exp of the row's scaled scores, -inf
+ *              for a row without readable keys or with scores that are all -inf.
+ *   ws         ds4a_attn_prefix_workspace_bytes(B, N, H, D, n_groups) bytes, 256-byte aligned, as
+ *              ds4a_attn_tree's.
+ * Rows behind a session's last node are left as they were in out and lse.  A session that is shorter
+ * than its group's prefix, or whose group's length is negative, is left alone
+ * (DS4A_ERR_DEVICE_INDEX); with start not in order all are.  Precision as ds4a_attn_tree's.
+ */
+int ds4a_attn_prefix(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H, const int32_t *n_node, const int32_t *parent,
+                     const int32_t *start, const long long *shared, int n_groups, float scale, uint16_t *out, float *lse,
+                     void *ws, size_t ws_bytes, void *stream);
+
+size_t ds4a_attn_prefix_workspace_bytes(int B, int N, int H, int D, int n_groups);
+
+/*
  * ds4a_commit_tree -- accepts the path that ends in node leaf[s] (-1: nothing): its tokens
  * move to slots len .. len+a-1 in path order, the compressed rows they completed move
  * from the draft's rows to rows len/ratio and up (with k_idx, their indexer keys too, laid

@@ -24,6 +24,15 @@ def weights(L, cache, **kw):
                                ctypes.c_float(a["decay"]), a["acc"], a["slots"], None)
 
 
+def prefix(L, cache, **kw):
+    a = dict(q=FAKE, N=4, H=64, n=FAKE, parent=FAKE, start=FAKE, shared=FAKE, G=3, scale=0.1, out=FAKE + APART, lse=FAKE, ws=FAKE,
+             nb=None)
+    a.update(kw)
+    nb = L.ds4a_attn_prefix_workspace_bytes(2, 4, 64, 128, 3) if a["nb"] is None else a["nb"]
+    return L.ds4a_attn_prefix(cache, a["q"], a["N"], a["H"], a["n"], a["parent"], a["start"], a["shared"], a["G"],
+                              ctypes.c_float(a["scale"]), a["out"], a["lse"], a["ws"], nb, None)
+
+
 def evict(L, cache, **kw):
     a = dict(acc=FAKE, pos=FAKE + APART, slots=100, next=FAKE, budget=50, sink=4, recent=8, ao=FAKE, po=FAKE + APART,
              lo=FAKE + 2 * APART, ws=FAKE, nb=None)
@@ -33,7 +42,7 @@ def evict(L, cache, **kw):
                         a["lo"], a["ws"], nb, None)
 
 
-@pytest.mark.parametrize("call", [append, weights, evict])
+@pytest.mark.parametrize("call", [append, weights, evict, prefix])
 def test_bad_caches_are_refused(ds4a_lib, call):
     L = ds4a_lib.lib()
     assert call(L, None) == ARG
@@ -61,6 +70,22 @@ def test_weights_refusals(ds4a_lib):
                      (dict(acc=FAKE + 2), ARG), (dict(slots=0), ARG), (dict(scale=0.0), ARG), (dict(scale=float("nan")), ARG),
                      (dict(scale=2.5e38), ARG), (dict(decay=-0.1), ARG), (dict(decay=1.5), ARG), (dict(decay=float("nan")), ARG)]:
         assert weights(L, c, **kw) == code, kw
+
+
+def test_prefix_refusals(ds4a_lib):
+    L, c = ds4a_lib.lib(), kv(ds4a_lib)
+    nb = L.ds4a_attn_prefix_workspace_bytes(2, 4, 64, 128, 3)
+    assert nb > 0
+    for kw, code in [(dict(q=None), ARG), (dict(out=None), ARG), (dict(n=None), ARG), (dict(N=0), ARG), (dict(N=65), UNSUP),
+                     (dict(H=12), UNSUP), (dict(q=FAKE + 8), ARG), (dict(out=FAKE + APART + 8), ARG), (dict(parent=FAKE + 2), ARG),
+                     (dict(start=None), ARG), (dict(shared=None), ARG), (dict(start=FAKE + 2), ARG), (dict(shared=FAKE + 4), ARG),
+                     (dict(G=-1), ARG), (dict(G=65536), UNSUP), (dict(lse=FAKE + 2), ARG), (dict(out=FAKE), ARG), (dict(out=FAKE + 16), ARG),
+                     (dict(scale=0.0), ARG), (dict(scale=float("nan")), ARG), (dict(scale=2.5e38), ARG), (dict(ws=None), WS),
+                     (dict(ws=FAKE + 128), WS), (dict(nb=nb - 1), WS)]:
+        assert prefix(L, c, **kw) == code, kw
+    for bad in [(-1, 4, 64, 128, 1), (65536, 4, 64, 128, 1), (2, 0, 64, 128, 1), (2, 65, 64, 128, 1), (2, 4, 12, 128, 1),
+                (2, 4, 64, 96, 1), (2, 4, 64, 128, -1), (2, 4, 64, 128, 65536)]:
+        assert L.ds4a_attn_prefix_workspace_bytes(*bad) == 0
 
 
 def test_evict_refusals(ds4a_lib):
@@ -94,6 +119,14 @@ def test_binding_refuses_shapes(ds4a_lib):
         ds4a_lib.ds4a_paged_append_norm(desc, q[:, :, 0], q[:, :, 0], n, f, None, 1e-6)
     with pytest.raises(ValueError, match="paged_append_norm: pos0"):
         ds4a_lib.ds4a_paged_append_norm(desc, q[:, :, 0], q[:, :, 0], n, None, None, 1e-6, pos0=f)
+    with pytest.raises(ValueError, match="attn_prefix: q, out"):
+        ds4a_lib.ds4a_attn_prefix(desc, q[0], n, None, None, None, 0.1, q, None, q)
+    with pytest.raises(ValueError, match="come together"):
+        ds4a_lib.ds4a_attn_prefix(desc, q, n, None, n, None, 0.1, q, None, q)
+    with pytest.raises(ValueError, match="attn_prefix: start"):
+        ds4a_lib.ds4a_attn_prefix(desc, q, n, None, n, n, 0.1, q, None, q)
+    with pytest.raises(ValueError, match="attn_prefix: lse"):
+        ds4a_lib.ds4a_attn_prefix(desc, q, n, None, None, None, 0.1, q, f, q)
     with pytest.raises(ValueError, match="attn_weights: q"):
         ds4a_lib.ds4a_attn_weights(desc, q[0], n, f, 0.1, 1.0, f)
     with pytest.raises(ValueError, match="attn_weights: lse"):
