@@ -502,8 +502,8 @@ static ds4a::PagedKV paged_view(const ds4a_paged_kv_t *kv) {
     return ds4a::PagedKV{kv->k, kv->v, kv->table, kv->len, kv->n_pages, kv->page, kv->max_pages, kv->D};
 }
 
-// What the two appends share: the checks, and the arguments of the kernel (norm: false).  `run` is false
-// where there is nothing to do.
+// What the two appends share: the checks, and their kernels' common arguments.  `run` is false where there is
+// nothing to do.
 static int append_args(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16_t *v, int N, const int32_t *n_tok,
                        const int32_t *parent, const float *inv_freq, int rot, int rot_off, int interleaved,
                        const uint16_t *q, int H, uint16_t *q_out, ds4a::AppendArgs &a, bool &run) {
@@ -559,14 +559,14 @@ int ds4a_paged_append_norm(const ds4a_paged_kv_t *kv, const uint16_t *k, const u
     rc = make_ctx(stream, c, Early::kWrites);
     if (rc != DS4A_OK) return rc;
     a.err = c.err;
-    a.norm = 1;
+    a.B = kv->B;
     a.k_w = k_w;
     a.q_w = q_w;
     a.eps = eps;
     a.pos0 = pos0;
     a.slot_pos = slot_pos;
     a.slots = slots;
-    return from_cuda(ds4a::launch_paged_append(a, kv->B, c));
+    return from_cuda(ds4a::launch_norm_append(a, kv->B, c));
 }
 
 int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, const int32_t *parent,

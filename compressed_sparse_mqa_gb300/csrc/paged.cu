@@ -9,10 +9,6 @@
 // product exactly.  f_j / 2 pi is computed in double (2^-53 relative), so at position
 // 2^31 and f = 1 the angle is within 2^-24 turns of the true one and at 2^20 within 2^-35;
 // sine and cosine are then taken in binary32 of the half-turns.
-//
-// With norms (ds4a_paged_append_norm) a key or query row is first x / sqrt(mean(x^2) + eps) * w.  A row
-// is 8 (D = 64: 4) neighbouring lanes, 16 values each, so its sum of squares is three (two) shuffles of
-// values that the rotation has in registers anyway; nothing is rounded between norm and rotation.
 #include "paged_dev.cuh"
 
 namespace ds4a {
@@ -36,21 +32,6 @@ DS4A_DEVINL unsigned long long turn_fraction(double x) {
     return b < 0 ? 0ull - f : f;
 }
 
-DS4A_DEVINL void unpack8(const uint4 x, float *f) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 p = unpack_half2(w[e]);
-        f[2 * e] = p.x;
-        f[2 * e + 1] = p.y;
-    }
-}
-DS4A_DEVINL void turn(float &x, float &y, float c, float s) {
-    const float x0 = x, y0 = y;
-    x = x0 * c - y0 * s;
-    y = x0 * s + y0 * c;
-}
-
 // A CTA takes t_cta consecutive tokens of a session.  A token's rows are its query heads, its
 // key and its value; a row is D / 16 items of 32 bytes: unit u of the rotated dims holds the 8
 // pairs 8u .. 8u+7 (two adjacent 16-byte chunks when interleaved, chunks u and u + rot/16
@@ -61,7 +42,7 @@ DS4A_DEVINL void turn(float &x, float &y, float c, float s) {
 // loads.  Two or six items a thread instead of
 // three: 14.3 and 19 us.  The inputs do not depend on the session's counts, so a
 // thread's loads are in flight while length, angle and page are looked up.
-template <bool kInterleaved, bool kNorm>
+template <bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs a, int t_cta, int d_shift) {
     __shared__ __align__(16) float2 s_cs[kMaxTokens][kMaxPairs];
     __shared__ unsigned long long s_mask[kMaxNodes];
@@ -103,7 +84,6 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const Item t = item(k);
-        if (kNorm) x1[k] = x2[k] = make_uint4(0, 0, 0, 0);
         if (t.tt < 0) continue;
         const long long tok = tok0 + t.tt;
         const uint16_t *src = t.row < a.H ? a.q + (tok * a.H + t.row) * D : (t.row == a.H ? a.k : a.v) + tok * D;
@@ -112,27 +92,14 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs
     }
     const Session ses = load_session(a.kv, a.n_tok, a.N, s, tid == 0 ? a.err : nullptr);
     if (!ses.ok || i0 >= ses.n) return;
-    long long pos0 = ses.len;
-    if (kNorm) {
-        if (a.pos0) pos0 = a.pos0[s];
-        if (pos0 < 0 || pos0 > 0x7fffffffLL - ses.n || (a.slot_pos && ses.len > a.slots - ses.n)) {
-            if (tid == 0)
-                record_error(a.err, pos0 < 0 || pos0 > 0x7fffffffLL - ses.n ? DS4A_ERR_DEVICE_INDEX : DS4A_ERR_CAPACITY);
-            return;
-        }
-    }
     if (a.parent && !tree_masks(a.parent + static_cast<long long>(s) * a.N, ses.n, s_mask, s_ptr, a.err)) return;
     const int count = min(t_cta, ses.n - i0);
-    if (tid < count) {
+    if (tid < count)
         s_row[tid] = pool_row(a.kv, a.kv.table + static_cast<long long>(s) * a.kv.max_pages,
                               static_cast<unsigned>(ses.len + i0 + tid), a.err);
-        if (kNorm && a.slot_pos && s_row[tid] >= 0)
-            a.slot_pos[static_cast<long long>(s) * a.slots + ses.len + i0 + tid] =
-                static_cast<int>(pos0 + (a.parent ? __popcll(s_mask[i0 + tid]) - 1 : i0 + tid));
-    }
     for (int w = tid; w < count * (rot / 2); w += blockDim.x) {
         const int tt = w / (rot / 2), j = w - tt * (rot / 2);
-        const long long pos = pos0 + (a.parent ? __popcll(s_mask[i0 + tt]) - 1 : i0 + tt);
+        const long long pos = ses.len + (a.parent ? __popcll(s_mask[i0 + tt]) - 1 : i0 + tt);
         const unsigned long long step = turn_fraction(static_cast<double>(a.inv_freq[j]) * 0.15915494309189533577);   // 1 / (2 pi)
         const int ang = static_cast<int>((step * static_cast<unsigned long long>(pos)) >> 32);
         float sn, cs;
@@ -140,23 +107,6 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs
         s_cs[tt][j] = make_float2(cs, sn);
     }
     __syncthreads();
-    float r[kItems];                 // 1 / sqrt(mean(x^2) + eps) of the item's row
-    if (kNorm) {
-#pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            float ss = 0.f;
-            const uint32_t w[8] = {x1[k].x, x1[k].y, x1[k].z, x1[k].w, x2[k].x, x2[k].y, x2[k].z, x2[k].w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 p = unpack_half2(w[e]);
-                ss += p.x * p.x + p.y * p.y;
-            }
-            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-            if (d_shift == 3) ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-            r[k] = rsqrtf(ss / static_cast<float>(D) + a.eps);
-        }
-    }
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const Item t = item(k);
@@ -169,40 +119,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs
             if (s_row[t.tt] < 0) continue;
             dst = (t.row == a.H ? a.kv.k : a.kv.v) + s_row[t.tt] * D;
         }
-        if (kNorm && t.row <= a.H) {
-            const float *w = t.row < a.H ? a.q_w : a.k_w;
-            float f[16];
-            unpack8(x1[k], f);
-            unpack8(x2[k], f + 8);
-            if (w) {
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float *we = w + (e < 8 ? t.o1 + e : t.o2 + e - 8);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f[e + i] = f[e + i] * r[k] * __ldg(we + i);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) f[e] *= r[k];
-            }
-            if (t.u >= 0) {
-                const float4 *cs4 = reinterpret_cast<const float4 *>(&s_cs[t.tt][t.u * 8]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 cs = cs4[e];   // cos, sin of pairs 2e and 2e + 1
-                    if (kInterleaved) {
-                        turn(f[4 * e], f[4 * e + 1], cs.x, cs.y);
-                        turn(f[4 * e + 2], f[4 * e + 3], cs.z, cs.w);
-                    } else {
-                        turn(f[2 * e], f[2 * e + 8], cs.x, cs.y);
-                        turn(f[2 * e + 1], f[2 * e + 9], cs.z, cs.w);
-                    }
-                }
-            }
-            x1[k] = make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
-            x2[k] = make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]),
-                               pack_half2(f[14], f[15]));
-        } else if (!kNorm && t.u >= 0) {
+        if (t.u >= 0) {
             const float4 *cs4 = reinterpret_cast<const float4 *>(&s_cs[t.tt][t.u * 8]);
             uint32_t w[8] = {x1[k].x, x1[k].y, x1[k].z, x1[k].w, x2[k].x, x2[k].y, x2[k].z, x2[k].w};
 #pragma unroll
@@ -226,7 +143,198 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(AppendArgs
     }
 }
 
+// ---- append with norms ------------------------------------------------------------------------
+
+DS4A_DEVINL void unpack8(const uint4 x, float *f) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 p = unpack_half2(w[e]);
+        f[2 * e] = p.x;
+        f[2 * e + 1] = p.y;
+    }
+}
+DS4A_DEVINL uint4 pack8(const float *f) {
+    return make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+}
+DS4A_DEVINL void turn(float &x, float &y, const float2 cs) {
+    const float x0 = x, y0 = y;
+    x = x0 * cs.x - y0 * cs.y;
+    y = x0 * cs.y + y0 * cs.x;
+}
+
+// Depth of node i in a session's tree of n <= 64 nodes, by one warp (two nodes a lane, pointer jumping over
+// shuffles); -1 (recorded) if a parent is not an earlier node or -1.
+DS4A_DEVINL int node_depth(const int32_t *parent, int n, int i, int lane, unsigned int *err) {
+    int p[2], d[2];
+    bool bad = false;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int j = lane + 32 * x;
+        p[x] = j < n ? __ldg(parent + j) : -1;
+        bad |= p[x] < -1 || p[x] >= j;
+        d[x] = p[x] >= 0;                                        // ancestors counted so far; p: the next one
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+        record_error(err, DS4A_ERR_DEVICE_INDEX);
+        return -1;
+    }
+    for (int span = 1; span < n; span *= 2) {
+        int np[2], nd[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int src = p[x] & 31;
+            const int p0 = __shfl_sync(0xffffffffu, p[0], src), p1 = __shfl_sync(0xffffffffu, p[1], src);
+            const int d0 = __shfl_sync(0xffffffffu, d[0], src), d1 = __shfl_sync(0xffffffffu, d[1], src);
+            np[x] = p[x] < 0 ? -1 : (p[x] < 32 ? p0 : p1);
+            nd[x] = p[x] < 0 ? d[x] : d[x] + (p[x] < 32 ? d0 : d1);
+        }
+        p[0] = np[0];
+        p[1] = np[1];
+        d[0] = nd[0];
+        d[1] = nd[1];
+    }
+    const int a = __shfl_sync(0xffffffffu, d[0], i & 31), b = __shfl_sync(0xffffffffu, d[1], i & 31);
+    return i < 32 ? a : b;
+}
+
+// A warp takes up to kNormIt x 4 (D = 64: x 8) rows of one token: its query heads, its key, its value.
+// A row is D / 16 neighbouring lanes of 16 values each, the two chunks of the items above, so a lane has
+// the same pairs in every row: their sines, cosines (each taken by one of the lanes that need it) and
+// weights stay in registers, a row's sum of squares is three (two) shuffles, and no warp waits for another.  The norm is applied to what the
+// rotation reads, and nothing is rounded between them.
+constexpr int kNormIt = 3;
+constexpr int kNormThreads = 128;
+constexpr int kNormBlocks = 5;
+template <int D, bool kInterleaved>
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_append_kernel(const AppendArgs a, int warps_tok, int rows_warp) {
+    constexpr int kLanes = D / 16, kRowsIt = 32 / kLanes;
+    const int lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
+    const long long gw = static_cast<long long>(blockIdx.x) * (kNormThreads / 32) + (threadIdx.x >> 5);
+    const long long tok = gw / warps_tok;
+    const int part = static_cast<int>(gw - tok * warps_tok), row0 = part * rows_warp;
+    const int rot = a.rot, units = rot / 16, rows = min(row0 + rows_warp, a.H + 2);
+    pdl_wait();
+    pdl_trigger();
+    const int s = static_cast<int>(tok / a.N), i = static_cast<int>(tok - static_cast<long long>(s) * a.N);
+    if (s >= a.B) return;
+    // this lane's two chunks of 8 values: a unit of the rotated dims, or two of the others
+    int o1, o2;
+    if (c < units) {
+        o1 = a.rot_off + (kInterleaved ? c * 16 : c * 8);
+        o2 = kInterleaved ? o1 + 8 : o1 + rot / 2;
+    } else {
+        o1 = (c - units) * 16;
+        o2 = o1 + 8;
+        if (o1 >= a.rot_off) o1 += rot;
+        if (o2 >= a.rot_off) o2 += rot;
+    }
+    uint4 x1[kNormIt], x2[kNormIt];
+#pragma unroll
+    for (int it = 0; it < kNormIt; ++it) {
+        const int row = row0 + it * kRowsIt + sub;
+        x1[it] = x2[it] = make_uint4(0, 0, 0, 0);
+        if (row >= rows) continue;
+        const uint16_t *src = row < a.H ? a.q + (tok * a.H + row) * D : (row == a.H ? a.k : a.v) + tok * D;
+        x1[it] = *reinterpret_cast<const uint4 *>(src + o1);
+        x2[it] = *reinterpret_cast<const uint4 *>(src + o2);
+    }
+    // everything else that does not depend on the session's counts, so that one round of loads covers it
+    const long long len = a.kv.len[s], pos0 = *(a.pos0 ? a.pos0 + s : a.kv.len + s);
+    const int n = a.n_tok[s];
+    constexpr int kPairs = 8 / kRowsIt > 0 ? 8 / kRowsIt : 1;   // pairs whose angle a lane takes; its row's lanes share them
+    float freq[kPairs];
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) freq[e] = c < units ? __ldg(a.inv_freq + c * 8 + sub * kPairs + e) : 0.f;
+    float wq[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) wq[e] = a.q_w && row0 < a.H ? __ldg(a.q_w + (e < 8 ? o1 + e : o2 + e - 8)) : 1.f;
+    const Session ses = check_session(a.kv, len, n, a.N, lane == 0 ? a.err : nullptr);
+    if (!ses.ok || i >= ses.n) return;
+    if (pos0 < 0 || pos0 > 0x7fffffffLL - ses.n) {
+        if (lane == 0) record_error(a.err, DS4A_ERR_DEVICE_INDEX);
+        return;
+    }
+    if (a.slot_pos && ses.len > a.slots - ses.n) {
+        if (lane == 0) record_error(a.err, DS4A_ERR_CAPACITY);
+        return;
+    }
+    const int depth = a.parent ? node_depth(a.parent + static_cast<long long>(s) * a.N, ses.n, i, lane, a.err) : i;
+    if (depth < 0) return;
+    const long long pos = pos0 + depth;
+    long long dst_row = -1;                                      // of the key and the value
+    if (rows > a.H) {
+        dst_row = pool_row(a.kv, a.kv.table + static_cast<long long>(s) * a.kv.max_pages, static_cast<unsigned>(ses.len + i),
+                           lane == 0 ? a.err : nullptr);
+        if (row0 <= a.H && lane == 0 && dst_row >= 0 && a.slot_pos)
+            a.slot_pos[static_cast<long long>(s) * a.slots + ses.len + i] = static_cast<int>(pos);
+    }
+    float2 cs[8], own[kPairs];
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+        const unsigned long long step = turn_fraction(static_cast<double>(freq[e]) * 0.15915494309189533577);   // 1 / (2 pi)
+        const int ang = static_cast<int>((step * static_cast<unsigned long long>(pos)) >> 32);
+        sincospif(static_cast<float>(ang) * 4.656612873077392578125e-10f, &own[e].y, &own[e].x);   // half-turns: 2^-31
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        cs[e].x = __shfl_sync(0xffffffffu, own[e % kPairs].x, e / kPairs * kLanes + c);
+        cs[e].y = __shfl_sync(0xffffffffu, own[e % kPairs].y, e / kPairs * kLanes + c);
+    }
+#pragma unroll
+    for (int it = 0; it < kNormIt; ++it) {
+        const int row = row0 + it * kRowsIt + sub;
+        float f[16];
+        unpack8(x1[it], f);
+        unpack8(x2[it], f + 8);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ss += f[e] * f[e];
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (row >= rows) continue;
+        if (row <= a.H) {
+            const float r = rsqrtf(ss * (1.f / D) + a.eps);
+            if (row < a.H) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) f[e] = f[e] * r * wq[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) f[e] = f[e] * r * (a.k_w ? __ldg(a.k_w + (e < 8 ? o1 + e : o2 + e - 8)) : 1.f);
+            }
+            if (c < units) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {                    // pairs 8c + e
+                    if (kInterleaved) turn(f[2 * e], f[2 * e + 1], cs[e]);
+                    else turn(f[e], f[e + 8], cs[e]);
+                }
+            }
+            x1[it] = pack8(f);
+            x2[it] = pack8(f + 8);
+        }
+        uint16_t *dst;
+        if (row < a.H) {
+            dst = a.q_out + (tok * a.H + row) * D;
+        } else {
+            if (dst_row < 0) continue;
+            dst = (row == a.H ? a.kv.k : a.kv.v) + dst_row * D;
+        }
+        *reinterpret_cast<uint4 *>(dst + o1) = x1[it];
+        *reinterpret_cast<uint4 *>(dst + o2) = x2[it];
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_norm_append(const AppendArgs &a, int B, const Ctx &c) {
+    const int rows = a.H + 2, it = a.kv.D == 128 ? 4 : 8;        // rows an iteration
+    const int warps = (rows + kNormIt * it - 1) / (kNormIt * it), per = ((rows + warps - 1) / warps + it - 1) / it * it;
+    const long long total = static_cast<long long>(B) * a.N * warps;
+    const dim3 grid(static_cast<unsigned>((total + kNormThreads / 32 - 1) / (kNormThreads / 32))), block(kNormThreads);
+    const auto kernel = a.kv.D == 128 ? (a.interleaved ? norm_append_kernel<128, true> : norm_append_kernel<128, false>)
+                                      : (a.interleaved ? norm_append_kernel<64, true> : norm_append_kernel<64, false>);
+    return launch(kernel, grid, block, 0, c, 1, a, warps, per);
+}
 
 cudaError_t launch_paged_append(const AppendArgs &a, int B, const Ctx &c) {
     // as many tokens a CTA as its threads have items for, but no fewer CTAs than SMs
@@ -240,9 +348,8 @@ cudaError_t launch_paged_append(const AppendArgs &a, int B, const Ctx &c) {
     long long threads = ((t * (a.H + 2) << d_shift) + kItems - 1) / kItems;
     threads = threads <= 64 ? 64 : (threads + 31) / 32 * 32;
     const dim3 block(static_cast<unsigned>(threads));
-    const auto kernel = a.norm ? (a.interleaved ? paged_append_kernel<true, true> : paged_append_kernel<false, true>)
-                               : (a.interleaved ? paged_append_kernel<true, false> : paged_append_kernel<false, false>);
-    return launch(kernel, grid, block, 0, c, 1, a, static_cast<int>(t), d_shift);
+    return a.interleaved ? launch(paged_append_kernel<true>, grid, block, 0, c, 1, a, static_cast<int>(t), d_shift)
+                         : launch(paged_append_kernel<false>, grid, block, 0, c, 1, a, static_cast<int>(t), d_shift);
 }
 
 }  // namespace ds4a

@@ -34,10 +34,10 @@ struct Session {
     int n;
     bool ok;
 };
-DS4A_DEVINL Session load_session(const PagedKV &kv, const int32_t *n_node, int N, int s, unsigned int *err) {
+DS4A_DEVINL Session check_session(const PagedKV &kv, long long len, int n, int N, unsigned int *err) {
     Session r;
-    r.len = kv.len[s];
-    r.n = n_node[s];
+    r.len = len;
+    r.n = n;
     r.ok = true;
     if (r.n < 0 || r.n > N || r.len < 0) {
         record_error(err, DS4A_ERR_DEVICE_INDEX);
@@ -47,6 +47,9 @@ DS4A_DEVINL Session load_session(const PagedKV &kv, const int32_t *n_node, int N
         r.ok = false;
     }
     return r;
+}
+DS4A_DEVINL Session load_session(const PagedKV &kv, const int32_t *n_node, int N, int s, unsigned int *err) {
+    return check_session(kv, kv.len[s], n_node[s], N, err);
 }
 
 // Ancestor masks of a session's n nodes into mask[kMaxNodes] (shared memory), each node
