@@ -87,6 +87,7 @@ constexpr uint64_t kWaitNs = 10000000000ull;   // some waits last an item, which
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLift = 7.f, kRescale = 15.f;   // log2 units: a reference is kLift below the score that set it, kept up to kRescale above
 constexpr float kLowest = -3.402823466e38f;   // reference of a row whose scores are all -inf
+constexpr int kItemUnits = 8;              // shared prefixes: the fixed part of a row tile's time, in one-block tiles
 constexpr int kEdge = 2 * kMaxNodes;       // first window-edge entry of the poison table
 constexpr int kPoison = 3 * kMaxNodes;     // keys that only some rows attend: nodes, their rows, the window's edge
 
@@ -401,88 +402,112 @@ DS4A_DEVINL int shared_of(const PrefixArgs &p, const PagedKV &kv, int s, int gro
     return static_cast<int>(sh);
 }
 struct Entry {
-    int s, rows, shared, tiles, row_tiles;            // first session, rows, prefix, key tiles, row tiles
+    int s, rows, shared, tiles, row_tiles, group;     // first session, rows, prefix, key tiles, row tiles; a group or not
 };
+// Entry x of the line (groups that are out of order give nothing that is used).  The loads of both kinds go out together.
 DS4A_DEVINL Entry prefix_entry(const Args &g, int x, unsigned int *err) {
     const AttnTreeArgs &a = g.a;
     const PrefixArgs &p = g.pre;
-    Entry e{0, 0, 0, 0, 0};
-    if (x < p.n_groups) {
-        const int a0 = __ldg(p.start + x), a1 = __ldg(p.start + x + 1);
-        const long long sh = __ldg(p.shared + x);
-        if (a0 >= a1 || sh <= 0 || sh > static_cast<long long>(a.kv.max_pages) * a.kv.page) return e;
+    Entry e{0, 0, 0, 0, 0, x < p.n_groups};
+    const int s = x - p.n_groups;
+    const int32_t *first = e.group ? p.start + x : a.n_node + s;
+    const int a0 = first[0], a1 = first[e.group];
+    const long long len = *(e.group ? p.shared + x : a.kv.len + s), most = static_cast<long long>(a.kv.max_pages) * a.kv.page;
+    if (e.group) {
+        if (a0 >= a1 || len <= 0 || len > most) return e;
         e.s = a0;
         e.rows = (a1 - a0) * a.N * a.H;
-        e.shared = static_cast<int>(sh);
+        e.shared = static_cast<int>(len);
         e.tiles = (runs_of(e.shared) + kRuns - 1) / kRuns;
         e.row_tiles = (e.rows + g.g_tile_rows - 1) / g.g_tile_rows;
         return e;
     }
-    e.s = x - p.n_groups;
-    const Session ses = load_session(a.kv, a.n_node, a.N, e.s, err);
+    e.s = s;
+    const Session ses = check_session(a.kv, len, a0, a.N, err);
     if (!ses.ok || ses.n == 0) return e;
-    e.shared = shared_of(p, a.kv, e.s, group_of(p, e.s), ses.len, err);
+    e.shared = shared_of(p, a.kv, s, group_of(p, s), ses.len, err);
     if (e.shared < 0) return e;
     e.rows = ses.n * a.H;
     e.tiles = (runs_of(static_cast<int>(ses.len) + ses.n - (e.shared & ~(kRun - 1))) + kRuns - 1) / kRuns;
     e.row_tiles = (e.rows + g.tile_rows - 1) / g.tile_rows;
     return e;
 }
-DS4A_DEVINL long long entry_units(const Args &g, int x, unsigned int *err) {
-    const Entry e = prefix_entry(g, x, err);
-    return static_cast<long long>(e.tiles) * e.row_tiles;
+// A row tile is its fixed part, then its key tiles: units of the time of a one-block tile.  A cut of the line inside
+// the fixed part cuts before the first tile.
+DS4A_DEVINL int tile_units(const Args &g, const Entry &e) { return (e.group ? g.g_tile_rows : g.tile_rows) > kTK ? 2 : 1; }
+DS4A_DEVINL long long row_tile_units(const Args &g, const Entry &e) {
+    return e.tiles > 0 ? kItemUnits + static_cast<long long>(tile_units(g, e)) * e.tiles : 0;
+}
+// Tiles of a row tile that start before unit x of it
+DS4A_DEVINL int tiles_before(long long x, int tiles, int w) {
+    const long long n = x <= kItemUnits ? 0 : (x - kItemUnits + w - 1) / w;
+    return n < tiles ? static_cast<int>(n) : tiles;
 }
 // A row tile's place in the table; along the line it grows, so with the CTA added it is also a place of its own for
 // each piece (the next piece is another row tile's or another CTA's).
 DS4A_DEVINL int group_slot(const PrefixArgs &p, int group, long long session_rows, int tile_rows) {
     return static_cast<int>(__ldg(p.start + group) * session_rows / tile_rows) + group;
 }
-DS4A_DEVINL Share prefix_share(const Args &g, Line &k, int lane) {
+// This CTA's share of the line; mine: this lane's entry of the walk's 32.
+DS4A_DEVINL Share prefix_share(const Args &g, Line &k, Entry &mine, int lane) {
     Share h{0, 0, 0, 0};
+    h.units = line_total(k, g.pre.n_groups + g.B, [&](int x) {
+        mine = prefix_entry(g, x, g.a.err);
+        return row_tile_units(g, mine) * mine.row_tiles;
+    });
     const bool ok = groups_ok(g.pre, g.B, lane);
     if (blockIdx.x == 0 && lane == 0) *g.pre_ok = ok;
     if (!ok) {
         if (lane == 0) record_error(g.a.err, DS4A_ERR_DEVICE_INDEX);
         return h;
     }
-    auto units = [&](int x) { return entry_units(g, x, g.a.err); };
-    h.units = line_total(k, g.pre.n_groups + g.B, units);
-    const long long most = line_quot(h.units + g.min_tiles - 1, g.min_tiles);
-    h.ctas = most < static_cast<long long>(gridDim.x) ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+    // every CTA's share holds the start of a tile, wherever it is cut
+    const long long most = line_quot(h.units, g.min_tiles);
+    h.ctas = most < static_cast<long long>(gridDim.x) ? (most > 0 ? static_cast<int>(most) : 1) : static_cast<int>(gridDim.x);
     const int c = blockIdx.x;
     h.u = c < h.ctas ? line_quot(h.units * c, h.ctas) : 0;
     h.end = c < h.ctas ? line_quot(h.units * (c + 1), h.ctas) : 0;
     return h;
 }
-DS4A_DEVINL Item prefix_item(const Args &g, Line &k, Share &h) {
+DS4A_DEVINL Item prefix_item(const Args &g, Line &k, Entry &mine, Share &h) {
     Item id{-1, 0, 0, 0, 1, 0, 0, 0, 0, 0};
-    if (h.u >= h.end) return id;
-    auto units = [&](int x) { return entry_units(g, x, nullptr); };
-    const int n = g.pre.n_groups + g.B, l = line_to(k, n, h.u, units);
-    if (l < 0) return id;
-    const int x = k.first + l;
-    const long long at = k.before + __shfl_sync(0xffffffffu, k.incl - k.mine, l);   // the entry's first unit
-    const Entry e = prefix_entry(g, x, nullptr);
-    const bool group = x < g.pre.n_groups;
-    id.s = e.s;
-    id.shared = e.shared;
-    id.rows = group ? e.rows : 0;
-    id.rt = static_cast<int>(line_quot(h.u - at, e.tiles));
-    const long long lo = at + static_cast<long long>(id.rt) * e.tiles, hi = lo + e.tiles;
-    id.t0 = static_cast<int>(h.u - lo);
-    const long long end = hi < h.end ? hi : h.end;
-    id.t1 = static_cast<int>(end - lo);
-    id.first = static_cast<int>(line_quot((lo + 1) * h.ctas - 1, h.units));
-    id.pieces = static_cast<int>(line_quot(hi * h.ctas - 1, h.units)) - id.first + 1;
-    const int c = blockIdx.x;
-    if (group) {
-        id.slot = group_slot(g.pre, x, static_cast<long long>(g.a.N) * g.a.H, g.g_tile_rows) + id.rt;
-        id.part = (id.slot + c) * g.g_tile_rows;
-    } else {
-        id.slot = g.g_slots + e.s * g.row_tiles + id.rt;
-        id.part = g.part_s + (id.slot - g.g_slots + c) * g.tile_rows;
+    const int n = g.pre.n_groups + g.B;
+    while (h.u < h.end) {
+        const int l = line_to(k, n, h.u, [&](int x) {
+            mine = prefix_entry(g, x, nullptr);
+            return row_tile_units(g, mine) * mine.row_tiles;
+        });
+        if (l < 0) return id;
+        const long long at = k.before + __shfl_sync(0xffffffffu, k.incl - k.mine, l);   // the entry's first unit
+        const Entry e{__shfl_sync(0xffffffffu, mine.s, l),     __shfl_sync(0xffffffffu, mine.rows, l),
+                      __shfl_sync(0xffffffffu, mine.shared, l), __shfl_sync(0xffffffffu, mine.tiles, l),
+                      __shfl_sync(0xffffffffu, mine.row_tiles, l), __shfl_sync(0xffffffffu, mine.group, l)};
+        const long long span = row_tile_units(g, e);
+        const int w = tile_units(g, e), rt = static_cast<int>(line_quot(h.u - at, span));
+        const long long lo = at + rt * span, end = lo + span < h.end ? lo + span : h.end;
+        const int t0 = tiles_before(h.u - lo, e.tiles, w), t1 = tiles_before(end - lo, e.tiles, w);
+        h.u = end;
+        if (t0 >= t1) continue;                       // the fixed part alone
+        id.s = e.s;
+        id.shared = e.shared;
+        id.rows = e.group ? e.rows : 0;
+        id.rt = rt;
+        id.t0 = t0;
+        id.t1 = t1;
+        // the CTAs that have the first and the last tile's first unit: the largest c with units * c / ctas <= x
+        const long long x0 = lo + kItemUnits, x1 = x0 + static_cast<long long>(w) * (e.tiles - 1);
+        id.first = static_cast<int>(line_quot((x0 + 1) * h.ctas - 1, h.units));
+        id.pieces = static_cast<int>(line_quot((x1 + 1) * h.ctas - 1, h.units)) - id.first + 1;
+        const int c = blockIdx.x;
+        if (e.group) {
+            id.slot = group_slot(g.pre, k.first + l, static_cast<long long>(g.a.N) * g.a.H, g.g_tile_rows) + rt;
+            id.part = (id.slot + c) * g.g_tile_rows;
+        } else {
+            id.slot = g.g_slots + e.s * g.row_tiles + rt;
+            id.part = g.part_s + (id.slot - g.g_slots + c) * g.tile_rows;
+        }
+        return id;
     }
-    h.u = end;
     return id;
 }
 
@@ -1060,8 +1085,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 if (id.s >= 0) load_q(id.s, id.rt * g.item_rows, !kSel && g.tile_rows > kTK);
             }
             Line line{};
+            Entry entry{};
             if constexpr (kPre) {
-                share = prefix_share(g, line, lane);
+                share = prefix_share(g, line, entry, lane);
             } else {
                 if (g.mode == kWalk) walk_load<kSel>(g, walk, 0, 0, lane);
                 if (g.mode == kStream) share = stream_share<kSel>(g, walk, lane);
@@ -1070,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
                 W &w = works[it & 1];
                 Item id{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                if (kPre) id = prefix_item(g, line, share);
+                if (kPre) id = prefix_item(g, line, entry, share);
                 else if (g.mode == kWalk) id = walk_item<kSel>(g, walk, blockIdx.x + it * gridDim.x, lane);
                 else if (g.mode == kStream) id = stream_item<kSel>(g, walk, share, lane);
                 else if (it == 0) id = direct_item(g);
@@ -1407,24 +1433,36 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kPerRow;
     const unsigned row = blockIdx.x * (kJoinWarps / kPerRow) + warp / kPerRow;   // below 2^31: a row is 128 bytes or more
     const unsigned per = g.N * g.H;
-    pdl_wait();
+    if (!kPre) pdl_wait();
     pdl_trigger();
     if (row >= g.B * per) return;                    // (with kPerRow > 1 a block has one row: it leaves as a whole)
     const int s = row / per, r = row - s * per, rt = static_cast<unsigned>(r) / static_cast<unsigned>(g.item_rows);
+    // Shared prefixes: this kernel starts when every CTA of the one ahead has passed its own wait, so what that one
+    // only reads is there: counts and groups are looked up while it runs.
+    int group = -1, sh = 0, grt = 0, gr = 0, slot = 0;
+    Session ses;
+    if constexpr (kPre) {
+        ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
+        if (!ses.ok || r >= ses.n * g.H) return;
+        group = group_of(g.pre, s);
+        sh = shared_of(g.pre, g.kv, s, group, ses.len, nullptr);
+        if (sh > 0) {
+            gr = (s - __ldg(g.pre.start + group)) * static_cast<int>(per) + r;
+            grt = gr / g.g_tile_rows;
+            slot = group_slot(g.pre, group, per, g.g_tile_rows) + grt;
+        }
+        pdl_wait();
+    }
     const int2 p = g.pieces[(kPre ? g.g_slots : 0) + s * g.row_tiles + rt];   // set if the session is in the line
-    const Session ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
+    if (!kPre) ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
     if (!ses.ok || r >= ses.n * g.H) return;
     if (g.ratio > 0 && static_cast<unsigned>(ses.len) / static_cast<unsigned>(g.ratio) > g.cap - g.N) return;
     const int first = p.y, in_tile = r - rt * g.item_rows;
     int pieces = p.x, shared_pieces = 0;
     long long shared_at = 0;                         // the first piece of the shared prefix
     if constexpr (kPre) {
-        if (!*g.pre_ok) return;
-        const int group = group_of(g.pre, s), sh = shared_of(g.pre, g.kv, s, group, ses.len, nullptr);
-        if (sh < 0 || pieces <= 0) return;           // left alone
+        if (!*g.pre_ok || sh < 0 || pieces <= 0) return;   // left alone
         if (sh > 0) {
-            const int gr = (s - __ldg(g.pre.start + group)) * static_cast<int>(per) + r, grt = gr / g.g_tile_rows;
-            const int slot = group_slot(g.pre, group, per, g.g_tile_rows) + grt;
             const int2 gp = g.pieces[slot];
             shared_pieces = gp.x;
             shared_at = static_cast<long long>(slot + gp.y) * g.g_tile_rows + gr - grt * g.g_tile_rows;
@@ -1627,6 +1665,8 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &args, int B, const Ctx &c) {
 namespace {
 
 // How a call with shared prefixes is cut, from the sizes that the host knows.
+constexpr int kMinShare = 2;   // units of a CTA: a tile of two blocks, or two of one (prefix_4x1 15.0 us, with 4 16.2, with 8 20.5)
+constexpr int kManyPieces = 8;
 struct PrefixPlan {
     int g_tile_rows, tile_rows, row_tiles, g_slots, part_s, min_tiles, ctas;
     size_t part_rows;
@@ -1639,7 +1679,7 @@ PrefixPlan prefix_plan(int B, int N, int H, int n_groups, long long tokens, int 
     p.g_tile_rows = two(group, n_groups) ? 2 * kTK : kTK;
     p.tile_rows = two(per, B) ? 2 * kTK : kTK;
     p.row_tiles = static_cast<int>((per + p.tile_rows - 1) / p.tile_rows);
-    p.min_tiles = p.tile_rows == kTK && p.g_tile_rows == kTK ? 2 : 1;
+    p.min_tiles = kMinShare;
     p.ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
     p.g_slots = n_groups > 0 ? static_cast<int>(B * per / p.g_tile_rows) + n_groups + 1 : 0;
     p.part_s = n_groups > 0 ? (p.g_slots + p.ctas) * p.g_tile_rows : 0;
@@ -1693,7 +1733,7 @@ cudaError_t launch_attn_prefix(const AttnTreeArgs &args, const PrefixArgs &pre, 
                      pre, g.pre_ok, p.g_tile_rows, p.g_slots, p.part_s};
     const long long rows = static_cast<long long>(B) * a.N * a.H;
     // many pieces a row where there are eight CTAs or more for every 128 rows
-    if (p.ctas >= 8 * ((rows + kTK - 1) / kTK)) {
+    if (p.ctas >= kManyPieces * ((rows + kTK - 1) / kTK)) {
         const dim3 grid(static_cast<unsigned>(rows));
         return D == 128 ? launch(combine_kernel<128, kJoinWarps, true>, grid, dim3(kJoinThreads), 0, c, 1, j)
                         : launch(combine_kernel<64, kJoinWarps, true>, grid, dim3(kJoinThreads), 0, c, 1, j);
