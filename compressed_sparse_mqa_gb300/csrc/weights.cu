@@ -8,8 +8,8 @@
 // nothing is reduced across threads.  A key belongs to one thread of one CTA, which takes the rows in
 // order: no atomics, the same sums every time.
 //
-// Work: all sessions' 128-key tiles in one line, cut evenly over the CTAs (one per SM).  A CTA takes
-// two tiles at a time, one a side, and goes through the rows in chunks of 64.
+// Work: all sessions' pairs of 128-key tiles in one line, cut evenly over the CTAs (one per SM).  A CTA
+// takes the two tiles at a time, one a side, and goes through the rows in chunks of 128, 64 in registers at a time.
 // Roles:
 //   warps 0-3, 4-7  side 0 / 1: thread = key.
 //   warp 8       set-up: the CTA's pieces of the line; query chunks (TMA) and their lse.
@@ -26,15 +26,17 @@ namespace ds4a {
 namespace {
 
 constexpr int kTK = 128;                   // keys per tile
-constexpr int kRows = 64;                  // rows per chunk
-constexpr int kNS = 4, kQS = 3;            // K stages (a tile each), query stages (a chunk each)
+constexpr int kRows = 128;                 // rows per chunk
+constexpr int kHalf = 64;                  // rows that a thread has in its registers at a time
+constexpr int kNS = 4;                     // K stages, a tile each
+constexpr int kQS = 2;                     // query stages, a chunk each
 constexpr int kSideWarps = 4, kSoftWarps = 2 * kSideWarps;
 constexpr int kSetupWarp = kSoftWarps, kMmaWarp = kSetupWarp + 1, kProdWarp = kMmaWarp + 1;
 constexpr int kWarps = kProdWarp + 1, kThreads = 32 * kWarps;
-constexpr uint32_t kTmemCols = 256;        // [side][buffer][64]
+constexpr uint32_t kTmemCols = 512;        // [side][buffer][kRows]
 constexpr uint64_t kWaitNs = 10000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kInfo = 8;                   // tiles whose box information is kept
+constexpr int kInfo = 16;                  // tiles whose box information is kept: four and the K stages, and a power of two
 
 struct Piece {
     int s, len, n, rows;                   // session; cached and new tokens; rows (n * H)
@@ -55,16 +57,17 @@ struct Layout {
     static constexpr int q = k + kNS * tile;
     static constexpr int lse = q + kQS * chunk;              // float [kQS][kRows], in log2 units, negative
     static constexpr int info = lse + kQS * kRows * 4;       // uint8 [kInfo]: readable eighths (16 keys) of a tile
-    static constexpr int work = info + 16;
+    static constexpr int work = info + kInfo;
     static constexpr int bars = work + 64;
     static constexpr int end = bars + static_cast<int>(sizeof(Bars));
     static constexpr size_t bytes = end + 1024;
+    static_assert(kInfo >= 4 + kNS && (kInfo & (kInfo - 1)) == 0, "box information");
     static_assert(2 * sizeof(Piece) <= 64 && work % 8 == 0 && bars % 8 == 0 && lse % 16 == 0, "layout");
     static_assert(bytes <= 227 * 1024, "shared memory");
 };
 
 struct Args {
-    CUtensorMap map_q, map_k;              // 64-row boxes; `box`-row boxes over the pool
+    CUtensorMap map_q, map_k;              // kRows-row boxes; `box`-row boxes over the pool
     AttnWeightsArgs a;
     float scale_log2;
     int B, box, pool_oob;
@@ -74,6 +77,27 @@ DS4A_DEVINL float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Adds a key's weights from half a chunk's rows: 2^(score * c2 + l4[row]); kMask: of rows lo .. hi-1 alone.
+template <bool kMask>
+DS4A_DEVINL void add_weights(const uint32_t (&x)[2][32], const float4 *l4, uint64_t c2, int lo, int hi, uint64_t (&sum)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            const float4 m = l4[(h * 32 + e) / 4];
+            float p[4];
+            tc::unpack2(tc::fma2(tc::pack2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1])), c2, tc::pack2(m.x, m.y)), p[0], p[1]);
+            tc::unpack2(tc::fma2(tc::pack2(__uint_as_float(x[h][e + 2]), __uint_as_float(x[h][e + 3])), c2, tc::pack2(m.z, m.w)), p[2], p[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[i] = ex2(p[i]);
+                if (kMask && (h * 32 + e + i < lo || h * 32 + e + i >= hi)) p[i] = 0.f;
+            }
+            sum[(e / 4) & 1] = tc::add2(sum[(e / 4) & 1], tc::pack2(p[0], p[1]));
+            sum[2 + ((e / 4) & 1)] = tc::add2(sum[2 + ((e / 4) & 1)], tc::pack2(p[2], p[3]));
+        }
 }
 
 // A session's tokens and key tiles; a session that must be left alone has none.
@@ -115,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
             tc::mbar_init(&bar.k_empty[x], 1);
         }
         for (int x = 0; x < kQS; ++x) {
-            tc::mbar_init(&bar.q_full[x], 1);
+            tc::mbar_init(&bar.q_full[x], 2);                     // the queries, their lse
             tc::mbar_init(&bar.q_empty[x], kSoftWarps + 1);
         }
         for (int x = 0; x < 2; ++x) {
@@ -157,15 +181,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
             const int tiles = w.tile1 - w.tile0, rows = w.rows, len = w.len;
             const int chunks = (rows + kRows - 1) / kRows;
             float *acc = a.acc + static_cast<long long>(w.s) * a.slots;
+            // the sums before, loaded two tiles ahead of their use (under a full memory system a load takes longer
+            // than the two tiles)
+            auto old_sum = [&](int b) {
+                const unsigned key = static_cast<unsigned>(w.tile0 + b + side) * kTK + quad * 32 + lane;
+                return b + side < tiles && key < static_cast<unsigned>(len) && a.decay != 0.f ? acc[key] : 0.f;
+            };
+            float old_next = old_sum(0);
             for (int b = 0; b < tiles; b += 2) {
                 const bool mine = b + side < tiles;
                 const unsigned key = static_cast<unsigned>(w.tile0 + b + side) * kTK + quad * 32 + lane;   // below 2^31 + 2^9
                 const unsigned end = static_cast<unsigned>(len) + w.n;
                 const int behind = static_cast<int>(key) - len;                     // its new token's number, or negative
                 const int row0 = behind > 0 && key < end ? behind * a.H : 0;        // first row that attends the key
-                float old = 0.f;
+                const float old = old_next;
+                old_next = old_sum(b + 2);
                 bool readable = false;
-                if (mine && key < static_cast<unsigned>(len) && a.decay != 0.f) old = a.decay * acc[key];
                 uint64_t sum[4] = {0, 0, 0, 0};
                 for (int c = 0; c < chunks; ++c) {
                     const bool loaded = chunks > 1 || b == 0, last_use = chunks > 1 || b + 2 >= tiles;
@@ -175,40 +206,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
                         const uint32_t sb = n_c & 1u;
                         wait(&bar.s_full[side][sb], n_c >> 1);
                         tc::fence_after_sync();
-                        uint32_t x[2][32];
-                        tc::ld_x32(col0 + sb * kRows, x[0]);
-                        tc::ld_x32(col0 + sb * kRows + 32, x[1]);
-                        // read before the scores are given back: the slot is written again eight tiles on, which
-                        // the products of the tile four on come before, and those wait for these scores
+                        // read before the scores are given back: the slot is written again kInfo tiles on, when the
+                        // products of the tile four on are done, and those wait for these scores to be given back
                         if (c == 0) readable = (info[(n_t + b + side) & (kInfo - 1)] >> (quad * 2 + lane / 16)) & 1;
-                        tc::wait_ld();
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&bar.s_empty[side][sb]);
-                        ++n_c;
-                        const float4 *l4 = reinterpret_cast<const float4 *>(s_lse + st * kRows);
-                        const int lo = row0 - c * kRows, hi = rows - c * kRows;   // rows lo .. hi-1 of the chunk
-                        const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= kRows);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 m = l4[(h * 32 + e) / 4];
-                                float p[4];
-                                tc::unpack2(tc::fma2(tc::pack2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1])), c2,
-                                                     tc::pack2(m.x, m.y)), p[0], p[1]);
-                                tc::unpack2(tc::fma2(tc::pack2(__uint_as_float(x[h][e + 2]), __uint_as_float(x[h][e + 3])), c2,
-                                                     tc::pack2(m.z, m.w)), p[2], p[3]);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) p[i] = ex2(p[i]);
-                                if (!whole) {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        if (h * 32 + e + i < lo || h * 32 + e + i >= hi) p[i] = 0.f;
-                                }
-                                sum[(e / 4) & 1] = tc::add2(sum[(e / 4) & 1], tc::pack2(p[0], p[1]));
-                                sum[2 + ((e / 4) & 1)] = tc::add2(sum[2 + ((e / 4) & 1)], tc::pack2(p[2], p[3]));
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            const int lo = row0 - c * kRows - h * kHalf, hi = rows - c * kRows - h * kHalf;   // rows lo .. hi-1 of the half
+                            uint32_t x[2][32];
+                            if (hi > 0) {
+                                tc::ld_x32(col0 + sb * kRows + h * kHalf, x[0]);
+                                tc::ld_x32(col0 + sb * kRows + h * kHalf + 32, x[1]);
+                                tc::wait_ld();
                             }
+                            if (h == 1) {
+                                tc::fence_before_sync();
+                                __syncwarp();
+                                if (lane == 0) tc::mbar_arrive(&bar.s_empty[side][sb]);
+                            }
+                            if (hi <= 0) break;
+                            const float4 *l4 = reinterpret_cast<const float4 *>(s_lse + st * kRows + h * kHalf);
+                            if (__all_sync(0xffffffffu, lo <= 0 && hi >= kHalf)) add_weights<false>(x, l4, c2, lo, hi, sum);
+                            else add_weights<true>(x, l4, c2, lo, hi, sum);
+                        }
+                        ++n_c;
                     }
                     __syncwarp();
                     if (last_use) {
@@ -219,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
                 if (readable && key < end) {
                     float p0, p1;
                     tc::unpack2(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), p0, p1);
-                    acc[key] = old + (p0 + p1);
+                    acc[key] = a.decay * old + (p0 + p1);
                 }
             }
             n_t += tiles;
@@ -228,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
         }
     } else if (warp == kSetupWarp) {
         Line line{};
-        auto units = [&](int s) { return static_cast<long long>(session_tiles(a, s).tiles); };
+        auto units = [&](int s) { return static_cast<long long>((session_tiles(a, s).tiles + 1) / 2); };   // two tiles take the time of one
         if (lane == 0) tc::prefetch_map(&g.map_q);
         const long long total = line_total(line, g.B, units);
         const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x), c = blockIdx.x;
@@ -242,30 +262,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
             const int s = line.first + l;
             const Tiles t = l >= 0 ? session_tiles(a, s) : Tiles{0, 0, 0};
             const long long at = l >= 0 ? line.before + __shfl_sync(0xffffffffu, line.incl - line.mine, l) : 0;
-            const int tile0 = static_cast<int>(u - at);
-            const int tile1 = static_cast<int>(at + t.tiles < u_end ? t.tiles : u_end - at);
+            const int blocks = (t.tiles + 1) / 2;
+            const long long end = at + blocks < u_end ? at + blocks : u_end;
+            const int tile0 = 2 * static_cast<int>(u - at), tile1 = min(2 * static_cast<int>(end - at), t.tiles);
             const int rows = t.n * a.H, chunks = (rows + kRows - 1) / kRows;
             if (lane == 0) w = Piece{s, t.len, t.n, rows, tile0, tile1, l < 0};
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
             if (l < 0) break;
-            u = at + tile1;
-            const int blocks = chunks > 1 ? (tile1 - tile0 + 1) / 2 : 1;
+            u = end;
+            const int loads = chunks > 1 ? (tile1 - tile0 + 1) / 2 : 1;
             const long long row0 = static_cast<long long>(s) * a.N * a.H;
-            for (int x = 0; x < blocks && ok; ++x)
+            // a row without a key: weight 0; rows behind the last are masked
+            auto lse_of = [&](int r) { return r < rows ? __ldg(a.lse + row0 + r) : INFINITY; };
+            auto scaled = [](float v) { return v == -INFINITY ? -INFINITY : -v * kLog2e; };
+            float next[kRows / 32];                               // of the next chunk, loaded while this one waits
+#pragma unroll
+            for (int i = 0; i < kRows / 32; ++i) next[i] = lse_of(i * 32 + lane);
+            for (int x = 0; x < loads && ok; ++x)
                 for (int ch = 0; ch < chunks && ok; ++ch, ++n_q) {
                     const uint32_t st = n_q % kQS;
-                    float m[2];                                   // row without a key: weight 0; rows behind the last are masked
+                    float m[kRows / 32];
+                    const int after = ch + 1 < chunks ? (ch + 1) * kRows : 0;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = ch * kRows + i * 32 + lane;
-                        const float v = r < rows ? __ldg(a.lse + row0 + r) : INFINITY;
-                        m[i] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+                    for (int i = 0; i < kRows / 32; ++i) {
+                        m[i] = next[i];
+                        next[i] = lse_of(after + i * 32 + lane);
                     }
                     if (n_q >= kQS && !warp_wait(&bar.q_empty[st], n_q / kQS - 1)) break;
-                    s_lse[st * kRows + lane] = m[0];
-                    s_lse[st * kRows + 32 + lane] = m[1];
-                    __syncwarp();
                     if (lane == 0) {
                         tc::expect_tx(&bar.q_full[st], L::chunk);
                         for (int at_ = 0; at_ < kAtoms; ++at_)
@@ -273,6 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
                                             static_cast<int>(row0 + ch * kRows), &bar.q_full[st]);
                     }
                     __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kRows / 32; ++i) s_lse[st * kRows + i * 32 + lane] = scaled(m[i]);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.q_full[st]);
                 }
         }
         if (!ok && lane == 0) {                                   // a wait gave up: the copies in flight land first
@@ -281,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        constexpr uint32_t kId = tc::idesc_f16_f32(kTK, kRows, false, false);
+        // all of a chunk's rows, or the first half where there are no more
+        constexpr uint32_t kIdAll = tc::idesc_f16_f32(kTK, kRows, false, false), kIdHalf = tc::idesc_f16_f32(kTK, kHalf, false, false);
         const uint64_t k_d = tc::desc_sw128(tc::smem_u32(smem + L::k), 16, 1024);
         const uint64_t q_d = tc::desc_sw128(tc::smem_u32(smem + L::q), 16, 1024);
         uint32_t n_t = 0, n_q = 0, n_c[2] = {0, 0};
@@ -289,9 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
             const Piece &w = pieces[it & 1];
             if (!warp_wait(&bar.w_full[it & 1], it >> 1) || __shfl_sync(0xffffffffu, w.stop, 0)) break;
             const int tiles = __shfl_sync(0xffffffffu, w.tile1 - w.tile0, 0);
-            const int chunks = (__shfl_sync(0xffffffffu, w.rows, 0) + kRows - 1) / kRows;
+            const int rows = __shfl_sync(0xffffffffu, w.rows, 0), chunks = (rows + kRows - 1) / kRows;
             for (int b = 0; b < tiles && ok; b += 2) {
                 for (int c = 0; c < chunks && ok; ++c) {
+                    const uint32_t id = rows - c * kRows > kHalf ? kIdAll : kIdHalf;
                     const uint32_t qs = n_q % kQS;
                     bool good = true;
                     if (chunks > 1 || b == 0) good = wait(&bar.q_full[qs], n_q / kQS);
@@ -310,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
 #pragma unroll
                             for (int x = 0; x < D / 16; ++x)
                                 tc::mma_f16(d, kd + (x / 4) * (kAtomBytes / 16) + (x % 4) * 2,
-                                            qd + (x / 4) * (kRows * 128 / 16) + (x % 4) * 2, kId, x > 0);
+                                            qd + (x / 4) * (kRows * 128 / 16) + (x % 4) * 2, id, x > 0);
                             tc::commit(&bar.s_full[side][sb]);
                             if (c + 1 == chunks) tc::commit(&bar.k_empty[ks]);
                             if ((chunks > 1 || b + 2 >= tiles) && (side == 1 || b + 1 >= tiles)) tc::commit(&bar.q_empty[qs]);
