@@ -333,6 +333,10 @@ def test_evict_longer_than_shared_memory():
     check_evict(np.random.default_rng(2), [400001, 330000], 200000, 4, 1000, page=4096)
 
 
+def test_evict_the_longest_that_shared_memory_holds():
+    check_evict(np.random.default_rng(5), [327680, 300000], 250000, 64, 100, page=1024)
+
+
 def test_evict_leaves_bad_sessions_alone():
     rng = np.random.default_rng(3)
     S, budget = 100, 40

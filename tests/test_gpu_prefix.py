@@ -160,6 +160,21 @@ def test_prefix_values_that_are_not_finite():
     assert (out[0, 1, :, 9] == -np.inf).all() and np.isfinite(out[0, [0, 2], :, 9]).all() and np.isfinite(out[1, :, :, 9]).all()
 
 
+def test_prefix_ends_beside_another_sessions_tokens():
+    """The first session's own tokens sit in the same page and run as the prefix's end; their NaN reach that session alone."""
+    rng = np.random.default_rng(9)
+    c = Shared(rng, [85, 84, 90], [1, 1, 1], [0, 3], [83], 64, 16, 1)
+    r = c.rows(0, [83, 84, 85])
+    c.k[r] = c.v[r] = np.nan
+    q = rng.standard_normal((3, 1, 8, 64)).astype(np.float16)
+    out, lse = run(c, q, None, 0.125)
+    no_error()
+    assert np.isnan(out[0]).all() and np.isnan(lse[0]).all()
+    want, tol, wl, lt = reference(c, q, R.random_parents(rng, 3, 1), 0.125)
+    for s in (1, 2):
+        assert (np.abs(out[s].astype(np.float64) - want[s]) <= tol[s]).all() and (np.abs(lse[s] - wl[s]) <= lt[s]).all()
+
+
 def test_prefix_scores_of_minus_infinity():
     rng = np.random.default_rng(5)
     c = Shared(rng, [40, 44], [1, 1], [0, 2], [40], 64, 16, 1)
