@@ -392,7 +392,7 @@ DS4A_DEVINL int group_of(const PrefixArgs &p, int s) {
     return lo == 0 || lo > p.n_groups ? -1 : lo - 1;
 }
 // Length of session s's shared prefix: 0 without one, -1 if the session must be left alone (the reason is recorded).
-DS4A_DEVINL int shared_of(const PrefixArgs &p, const PagedKV &kv, int s, int group, long long len, unsigned int *err) {
+DS4A_DEVINL int shared_of(const PrefixArgs &p, int group, long long len, unsigned int *err) {
     if (group < 0) return 0;
     const long long sh = __ldg(p.shared + group);
     if (sh < 0 || sh > len) {                         // (len fits the session's pages)
@@ -401,36 +401,42 @@ DS4A_DEVINL int shared_of(const PrefixArgs &p, const PagedKV &kv, int s, int gro
     }
     return static_cast<int>(sh);
 }
+// tile_rows is kTK or 2 kTK
+DS4A_DEVINL int row_shift(int tile_rows) { return tile_rows > kTK ? 8 : 7; }
+DS4A_DEVINL int row_tiles_of(int rows, int tile_rows) { return (rows + tile_rows - 1) >> row_shift(tile_rows); }
+static_assert(kTK == 128, "row_shift");
 struct Entry {
     int s, rows, shared, tiles, row_tiles, group;     // first session, rows, prefix, key tiles, row tiles; a group or not
 };
-// Entry x of the line (groups that are out of order give nothing that is used).  The loads of both kinds go out together.
-DS4A_DEVINL Entry prefix_entry(const Args &g, int x, unsigned int *err) {
+DS4A_DEVINL Entry group_entry(const Args &g, int a0, int a1, long long shared) {
     const AttnTreeArgs &a = g.a;
-    const PrefixArgs &p = g.pre;
-    Entry e{0, 0, 0, 0, 0, x < p.n_groups};
-    const int s = x - p.n_groups;
-    const int32_t *first = e.group ? p.start + x : a.n_node + s;
-    const int a0 = first[0], a1 = first[e.group];
-    const long long len = *(e.group ? p.shared + x : a.kv.len + s), most = static_cast<long long>(a.kv.max_pages) * a.kv.page;
-    if (e.group) {
-        if (a0 >= a1 || len <= 0 || len > most) return e;
-        e.s = a0;
-        e.rows = (a1 - a0) * a.N * a.H;
-        e.shared = static_cast<int>(len);
-        e.tiles = (runs_of(e.shared) + kRuns - 1) / kRuns;
-        e.row_tiles = (e.rows + g.g_tile_rows - 1) / g.g_tile_rows;
-        return e;
-    }
-    e.s = s;
-    const Session ses = check_session(a.kv, len, a0, a.N, err);
-    if (!ses.ok || ses.n == 0) return e;
-    e.shared = shared_of(p, a.kv, s, group_of(p, s), ses.len, err);
-    if (e.shared < 0) return e;
-    e.rows = ses.n * a.H;
-    e.tiles = (runs_of(static_cast<int>(ses.len) + ses.n - (e.shared & ~(kRun - 1))) + kRuns - 1) / kRuns;
-    e.row_tiles = (e.rows + g.tile_rows - 1) / g.tile_rows;
+    Entry e{0, 0, 0, 0, 0, 1};
+    if (a0 >= a1 || shared <= 0 || shared > static_cast<long long>(a.kv.max_pages) * a.kv.page) return e;
+    e.s = a0;
+    e.rows = (a1 - a0) * a.N * a.H;
+    e.shared = static_cast<int>(shared);
+    e.tiles = (runs_of(e.shared) + kRuns - 1) / kRuns;
+    e.row_tiles = row_tiles_of(e.rows, g.g_tile_rows);
     return e;
+}
+// ok: the session is to be computed; its counts are checked, shared is its prefix's length
+DS4A_DEVINL Entry session_entry(const Args &g, int s, bool ok, int len, int n, int shared) {
+    Entry e{s, 0, 0, 0, 0, 0};
+    if (!ok || n == 0 || shared < 0) return e;
+    e.shared = shared;
+    e.rows = n * g.a.H;
+    e.tiles = (runs_of(len + n - (shared & ~(kRun - 1))) + kRuns - 1) / kRuns;
+    e.row_tiles = row_tiles_of(e.rows, g.tile_rows);
+    return e;
+}
+// Entry x of the line (groups that are out of order give nothing that is used).
+DS4A_DEVINL Entry prefix_entry(const Args &g, int x, unsigned int *err) {
+    const PrefixArgs &p = g.pre;
+    if (x < p.n_groups) return group_entry(g, p.start[x], p.start[x + 1], p.shared[x]);
+    const int s = x - p.n_groups;
+    const Session ses = load_session(g.a.kv, g.a.n_node, g.a.N, s, err);
+    const int shared = ses.ok && ses.n > 0 ? shared_of(p, group_of(p, s), ses.len, err) : -1;
+    return session_entry(g, s, ses.ok, static_cast<int>(ses.len), ses.n, shared);
 }
 // A row tile is its fixed part, then its key tiles: units of the time of a one-block tile.  A cut of the line inside
 // the fixed part cuts before the first tile.
@@ -438,50 +444,164 @@ DS4A_DEVINL int tile_units(const Args &g, const Entry &e) { return (e.group ? g.
 DS4A_DEVINL long long row_tile_units(const Args &g, const Entry &e) {
     return e.tiles > 0 ? kItemUnits + static_cast<long long>(tile_units(g, e)) * e.tiles : 0;
 }
+// The line is cut at units * c / ctas.
+DS4A_DEVINL Share share_of(const Args &g, long long units) {
+    Share h{units, 0, 0, 0};
+    // every CTA's share holds the start of a tile, wherever it is cut
+    const long long most = line_quot(units, g.min_tiles);
+    h.ctas = most < static_cast<long long>(gridDim.x) ? (most > 0 ? static_cast<int>(most) : 1) : static_cast<int>(gridDim.x);
+    const int c = blockIdx.x;
+    h.u = c < h.ctas ? line_quot(units * c, h.ctas) : 0;
+    h.end = c < h.ctas ? line_quot(units * (c + 1), h.ctas) : 0;
+    return h;
+}
+// Up to kTable entries are looked up and laid end to end by all threads at once, before the roles part: one round of
+// loads, where the set-up warp's walk of 65 entries took 12000 cycles.
+constexpr int kTable = 256;
+struct EntryTable {
+    int start[kTable + 1];
+    long long shared[kTable];
+    int4 entry[kTable];                               // session, rows, prefix, key tiles
+    long long incl[kTable];                           // units up to and with the entry
+    long long warp_units[kTable / 32];
+    int used, ok, first;                              // the table holds the line; the groups are in order; this CTA's first entry
+};
+DS4A_DEVINL void fill_table(const Args &g, EntryTable &t) {
+    const PrefixArgs &p = g.pre;
+    const int tid = threadIdx.x, n = p.n_groups + g.B, s = tid - p.n_groups;
+    const bool used = n <= kTable;                    // (then n_groups < kTable: B > 0)
+    if (tid == 0) t.used = used;
+    if (!used) {
+        __syncthreads();
+        return;
+    }
+    const bool session = s >= 0 && tid < n;
+    long long len = 0;
+    int count = 0;
+    if (session) {
+        len = g.a.kv.len[s];
+        count = g.a.n_node[s];
+    }
+    if (p.n_groups > 0 && tid <= p.n_groups) t.start[tid] = p.start[tid];
+    if (tid < p.n_groups) t.shared[tid] = p.shared[tid];
+    __syncthreads();
+    bool bad = false;
+    if (p.n_groups > 0 && tid <= p.n_groups) {
+        const int a0 = t.start[tid];
+        bad = a0 < 0 || a0 > g.B || (tid > 0 && a0 < t.start[tid - 1]);
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) t.ok = 0;
+    } else {
+        Entry e{0, 0, 0, 0, 0, 0};
+        if (tid < p.n_groups) {
+            e = group_entry(g, t.start[tid], t.start[tid + 1], t.shared[tid]);
+        } else if (session) {
+            const Session ses = check_session(g.a.kv, len, count, g.a.N, g.a.err);
+            int shared = ses.ok && ses.n > 0 ? 0 : -1;
+            if (shared == 0 && p.n_groups > 0) {
+                int lo = 0, hi = p.n_groups + 1;      // the first start above s
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (t.start[mid] > s) hi = mid;
+                    else lo = mid + 1;
+                }
+                if (lo > 0 && lo <= p.n_groups) {
+                    const long long sh = t.shared[lo - 1];
+                    if (sh < 0 || sh > ses.len) {
+                        record_error(g.a.err, DS4A_ERR_DEVICE_INDEX);
+                        shared = -1;
+                    } else {
+                        shared = static_cast<int>(sh);
+                    }
+                }
+            }
+            e = session_entry(g, s, ses.ok, static_cast<int>(ses.len), ses.n, shared);
+        }
+        if (tid == 0) t.ok = 1;
+        const int lane = tid & 31, warp = tid >> 5;
+        long long incl = row_tile_units(g, e) * e.row_tiles;
+        const long long own = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31 && warp < kTable / 32) t.warp_units[warp] = incl;
+        __syncthreads();
+        long long units = 0;
+#pragma unroll
+        for (int x = 0; x < kTable / 32; ++x) {
+            if (x == warp) incl += units;
+            units += t.warp_units[x];
+        }
+        if (tid < n) {
+            t.entry[tid] = make_int4(e.s, e.rows, e.shared, e.tiles);
+            t.incl[tid] = incl;
+            const long long u = share_of(g, units).u;
+            if (u >= incl - own && u < incl) t.first = tid;
+        }
+    }
+    __syncthreads();
+}
+DS4A_DEVINL Entry table_entry(const Args &g, const EntryTable &t, int x) {
+    const int4 v = t.entry[x];
+    const bool group = x < g.pre.n_groups;
+    return Entry{v.x, v.y, v.z, v.w, v.w > 0 ? row_tiles_of(v.y, group ? g.g_tile_rows : g.tile_rows) : 0, group};
+}
 // Tiles of a row tile that start before unit x of it
 DS4A_DEVINL int tiles_before(long long x, int tiles, int w) {
-    const long long n = x <= kItemUnits ? 0 : (x - kItemUnits + w - 1) / w;
+    const long long n = x <= kItemUnits ? 0 : (x - kItemUnits + w - 1) >> (w - 1);   // w is 1 or 2
     return n < tiles ? static_cast<int>(n) : tiles;
 }
 // A row tile's place in the table; along the line it grows, so with the CTA added it is also a place of its own for
 // each piece (the next piece is another row tile's or another CTA's).
 DS4A_DEVINL int group_slot(const PrefixArgs &p, int group, long long session_rows, int tile_rows) {
-    return static_cast<int>(__ldg(p.start + group) * session_rows / tile_rows) + group;
+    return static_cast<int>(__ldg(p.start + group) * session_rows >> row_shift(tile_rows)) + group;
 }
 // This CTA's share of the line; mine: this lane's entry of the walk's 32.
-DS4A_DEVINL Share prefix_share(const Args &g, Line &k, Entry &mine, int lane) {
+DS4A_DEVINL Share prefix_share(const Args &g, const EntryTable &t, Line &k, Entry &mine, int lane) {
     Share h{0, 0, 0, 0};
-    h.units = line_total(k, g.pre.n_groups + g.B, [&](int x) {
-        mine = prefix_entry(g, x, g.a.err);
-        return row_tile_units(g, mine) * mine.row_tiles;
-    });
-    const bool ok = groups_ok(g.pre, g.B, lane);
+    const bool ok = t.used ? t.ok != 0 : groups_ok(g.pre, g.B, lane);
     if (blockIdx.x == 0 && lane == 0) *g.pre_ok = ok;
     if (!ok) {
         if (lane == 0) record_error(g.a.err, DS4A_ERR_DEVICE_INDEX);
         return h;
     }
-    // every CTA's share holds the start of a tile, wherever it is cut
-    const long long most = line_quot(h.units, g.min_tiles);
-    h.ctas = most < static_cast<long long>(gridDim.x) ? (most > 0 ? static_cast<int>(most) : 1) : static_cast<int>(gridDim.x);
-    const int c = blockIdx.x;
-    h.u = c < h.ctas ? line_quot(h.units * c, h.ctas) : 0;
-    h.end = c < h.ctas ? line_quot(h.units * (c + 1), h.ctas) : 0;
-    return h;
+    const int n = g.pre.n_groups + g.B;
+    if (t.used) {
+        k.first = t.first;
+        return share_of(g, t.incl[n - 1]);
+    }
+    return share_of(g, line_total(k, n, [&](int x) {
+        mine = prefix_entry(g, x, g.a.err);
+        return row_tile_units(g, mine) * mine.row_tiles;
+    }));
 }
-DS4A_DEVINL Item prefix_item(const Args &g, Line &k, Entry &mine, Share &h) {
+DS4A_DEVINL Item prefix_item(const Args &g, const EntryTable &t, Line &k, Entry &mine, Share &h) {
     Item id{-1, 0, 0, 0, 1, 0, 0, 0, 0, 0};
     const int n = g.pre.n_groups + g.B;
     while (h.u < h.end) {
-        const int l = line_to(k, n, h.u, [&](int x) {
-            mine = prefix_entry(g, x, nullptr);
-            return row_tile_units(g, mine) * mine.row_tiles;
-        });
-        if (l < 0) return id;
-        const long long at = k.before + __shfl_sync(0xffffffffu, k.incl - k.mine, l);   // the entry's first unit
-        const Entry e{__shfl_sync(0xffffffffu, mine.s, l),     __shfl_sync(0xffffffffu, mine.rows, l),
-                      __shfl_sync(0xffffffffu, mine.shared, l), __shfl_sync(0xffffffffu, mine.tiles, l),
+        int x;                                        // the entry of unit u, and its first unit
+        long long at;
+        Entry e;
+        if (t.used) {
+            while (t.incl[k.first] <= h.u) ++k.first;   // (u is below the last one's)
+            x = k.first;
+            at = x > 0 ? t.incl[x - 1] : 0;
+            e = table_entry(g, t, x);
+        } else {
+            const int l = line_to(k, n, h.u, [&](int y) {
+                mine = prefix_entry(g, y, nullptr);
+                return row_tile_units(g, mine) * mine.row_tiles;
+            });
+            if (l < 0) return id;
+            x = k.first + l;
+            at = k.before + __shfl_sync(0xffffffffu, k.incl - k.mine, l);
+            e = Entry{__shfl_sync(0xffffffffu, mine.s, l),         __shfl_sync(0xffffffffu, mine.rows, l),
+                      __shfl_sync(0xffffffffu, mine.shared, l),    __shfl_sync(0xffffffffu, mine.tiles, l),
                       __shfl_sync(0xffffffffu, mine.row_tiles, l), __shfl_sync(0xffffffffu, mine.group, l)};
+        }
         const long long span = row_tile_units(g, e);
         const int w = tile_units(g, e), rt = static_cast<int>(line_quot(h.u - at, span));
         const long long lo = at + rt * span, end = lo + span < h.end ? lo + span : h.end;
@@ -500,7 +620,7 @@ DS4A_DEVINL Item prefix_item(const Args &g, Line &k, Entry &mine, Share &h) {
         id.pieces = static_cast<int>(line_quot((x1 + 1) * h.ctas - 1, h.units)) - id.first + 1;
         const int c = blockIdx.x;
         if (e.group) {
-            id.slot = group_slot(g.pre, k.first + l, static_cast<long long>(g.a.N) * g.a.H, g.g_tile_rows) + rt;
+            id.slot = group_slot(g.pre, x, static_cast<long long>(g.a.N) * g.a.H, g.g_tile_rows) + rt;
             id.part = (id.slot + c) * g.g_tile_rows;
         } else {
             id.slot = g.g_slots + e.s * g.row_tiles + rt;
@@ -778,6 +898,7 @@ DS4A_DEVINL void transpose4(uint4 (&u)[4], int lane) {
 template <int D, bool kSel, bool kPre>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_constant__ Args g) {
     using L = Layout<D, kSel>;
+    static_assert(!kPre || L::bytes + sizeof(EntryTable) + 1024 <= 227 * 1024, "shared memory with the table of entries");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -834,6 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     pdl_wait();
     pdl_trigger();
+    __shared__ std::conditional_t<kPre, EntryTable, char> s_table;
+    if constexpr (kPre) fill_table(g, s_table);
     bool ok = true;
     // a failed wait records the failure; later waits of this thread return at once
     auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -1087,7 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
             Line line{};
             Entry entry{};
             if constexpr (kPre) {
-                share = prefix_share(g, line, entry, lane);
+                share = prefix_share(g, s_table, line, entry, lane);
             } else {
                 if (g.mode == kWalk) walk_load<kSel>(g, walk, 0, 0, lane);
                 if (g.mode == kStream) share = stream_share<kSel>(g, walk, lane);
@@ -1096,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_kernel(const __grid_con
                 if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
                 W &w = works[it & 1];
                 Item id{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                if (kPre) id = prefix_item(g, line, entry, share);
+                if constexpr (kPre) id = prefix_item(g, s_table, line, entry, share);
                 else if (g.mode == kWalk) id = walk_item<kSel>(g, walk, blockIdx.x + it * gridDim.x, lane);
                 else if (g.mode == kStream) id = stream_item<kSel>(g, walk, share, lane);
                 else if (it == 0) id = direct_item(g);
@@ -1445,7 +1568,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
         ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
         if (!ses.ok || r >= ses.n * g.H) return;
         group = group_of(g.pre, s);
-        sh = shared_of(g.pre, g.kv, s, group, ses.len, nullptr);
+        sh = shared_of(g.pre, group, ses.len, nullptr);
         if (sh > 0) {
             gr = (s - __ldg(g.pre.start + group)) * static_cast<int>(per) + r;
             grt = gr / g.g_tile_rows;

@@ -118,6 +118,50 @@ DS4A_DEVINL Tiles session_tiles(const AttnWeightsArgs &a, int s) {
     return t;
 }
 
+DS4A_DEVINL int tile_pairs(const Tiles &t) { return (t.tiles + 1) / 2; }   // two tiles take the time of one
+
+// Up to kTable sessions are looked up and laid end to end by all threads at once, before the roles part: one round of
+// loads, where the set-up warp's walk of 64 sessions took 8000 cycles to the first scores.
+constexpr int kTable = 256;
+static_assert(kTable <= kThreads, "a thread per session");
+struct SessionTable {
+    int4 session[kTable];                  // cached tokens, new tokens, tiles
+    long long incl[kTable];                // tile pairs up to and with the session
+    long long warp_pairs[kTable / 32];
+    int first;                             // session of this CTA's first pair
+};
+DS4A_DEVINL void line_share(long long total, long long &u, long long &end) {
+    const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x), c = blockIdx.x;
+    u = c < ctas ? line_quot(total * c, ctas) : 0;
+    end = c < ctas ? line_quot(total * (c + 1), ctas) : 0;
+}
+DS4A_DEVINL void fill_table(const Args &g, SessionTable &t) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Tiles s = tid < g.B ? session_tiles(g.a, tid) : Tiles{0, 0, 0};
+    const int own = tile_pairs(s);
+    long long incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31 && warp < kTable / 32) t.warp_pairs[warp] = incl;
+    __syncthreads();
+    long long total = 0, u, end;
+#pragma unroll
+    for (int x = 0; x < kTable / 32; ++x) {
+        if (x == warp) incl += total;
+        total += t.warp_pairs[x];
+    }
+    if (tid < g.B) {
+        t.session[tid] = make_int4(s.len, s.n, s.tiles, 0);
+        t.incl[tid] = incl;
+        line_share(total, u, end);
+        if (u >= incl - own && u < incl) t.first = tid;
+    }
+    __syncthreads();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_constant__ Args g) {
     using L = Layout<D>;
@@ -159,6 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     pdl_wait();
     pdl_trigger();
+    __shared__ SessionTable s_table;
+    const bool table = g.B <= kTable;
+    if (table) fill_table(g, s_table);
     bool ok = true;
     // a failed wait records the failure; later waits of this thread return at once
     auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -248,28 +295,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
         }
     } else if (warp == kSetupWarp) {
         Line line{};
-        auto units = [&](int s) { return static_cast<long long>((session_tiles(a, s).tiles + 1) / 2); };   // two tiles take the time of one
+        auto pairs = [&](int s) { return static_cast<long long>(tile_pairs(session_tiles(a, s))); };
         if (lane == 0) tc::prefetch_map(&g.map_q);
-        const long long total = line_total(line, g.B, units);
-        const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x), c = blockIdx.x;
-        long long u = c < ctas ? line_quot(total * c, ctas) : 0;
-        const long long u_end = c < ctas ? line_quot(total * (c + 1), ctas) : 0;
+        long long u, u_end;
+        line_share(table ? s_table.incl[g.B - 1] : line_total(line, g.B, pairs), u, u_end);
+        int cursor = table ? s_table.first : 0;
         uint32_t n_q = 0;
         for (int it = 0;; ++it) {
             if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
             Piece &w = pieces[it & 1];
-            const int l = u < u_end ? line_to(line, g.B, u, units) : -1;
-            const int s = line.first + l;
-            const Tiles t = l >= 0 ? session_tiles(a, s) : Tiles{0, 0, 0};
-            const long long at = l >= 0 ? line.before + __shfl_sync(0xffffffffu, line.incl - line.mine, l) : 0;
-            const int blocks = (t.tiles + 1) / 2;
-            const long long end = at + blocks < u_end ? at + blocks : u_end;
+            int s = -1;                                           // the session of pair u, and its first pair
+            long long at = 0;
+            Tiles t{0, 0, 0};
+            if (u < u_end && table) {
+                while (s_table.incl[cursor] <= u) ++cursor;
+                s = cursor;
+                at = s > 0 ? s_table.incl[s - 1] : 0;
+                t = Tiles{s_table.session[s].x, s_table.session[s].y, s_table.session[s].z};
+            } else if (u < u_end) {
+                const int l = line_to(line, g.B, u, pairs);
+                if (l >= 0) {
+                    s = line.first + l;
+                    at = line.before + __shfl_sync(0xffffffffu, line.incl - line.mine, l);
+                    t = session_tiles(a, s);
+                }
+            }
+            const long long end = at + tile_pairs(t) < u_end ? at + tile_pairs(t) : u_end;
             const int tile0 = 2 * static_cast<int>(u - at), tile1 = min(2 * static_cast<int>(end - at), t.tiles);
             const int rows = t.n * a.H, chunks = (rows + kRows - 1) / kRows;
-            if (lane == 0) w = Piece{s, t.len, t.n, rows, tile0, tile1, l < 0};
+            if (lane == 0) w = Piece{s, t.len, t.n, rows, tile0, tile1, s < 0};
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bar.w_full[it & 1]);
-            if (l < 0) break;
+            if (s < 0) break;
             u = end;
             const int loads = chunks > 1 ? (tile1 - tile0 + 1) / 2 : 1;
             const long long row0 = static_cast<long long>(s) * a.N * a.H;

@@ -181,6 +181,8 @@ def check_weights(c, q, lse, acc, got, scale, decay, lens, n):
     ([5000], [2], 2, 40, 64, 32, 1.0),
     ([90 + 37 * i for i in range(45)], [1 + i % 2 for i in range(45)], 2, 16, 64, 16, 1.0),   # two walks of sessions
     ([40000], [1], 1, 8, 64, 1024, 1.0),                            # more than two tiles an SM
+    ([3 + 17 * i % 601 for i in range(256)], [1 - i % 5 // 4 for i in range(256)], 1, 8, 64, 16, 1.0),   # as many as are looked up at once
+    ([3 + 17 * i % 601 for i in range(300)], [i % 3 for i in range(300)], 2, 8, 64, 16, 1.0),            # and more
 ])
 def test_weights(lens, n, N, H, D, page, decay):
     scale = 1 / math.sqrt(D)

@@ -101,6 +101,8 @@ def check(rng, lens, n, N, H, D, page, start, shared, kind="tree", scale=None, r
     ([5000, 5100, 5003, 5001, 5050, 5000, 5010, 5090], [8] * 8, 8, 64, 128, 64, [0, 8], [4990], "tree"),   # two row blocks
     ([300, 17], [5, 4], 5, 40, 64, 16, [0], [], "tree"),                                   # nothing shared
     ([4000], [1], 1, 64, 128, 80, [0, 1], [4000], "chain"),                                # a group of one
+    ([60 + i % 50 for i in range(250)], [1 + i % 2 for i in range(250)], 2, 8, 64, 16, [0, 9, 9, 40, 100, 100, 249], [60, 7, 33, 1, 5, 48], "tree"),   # 256 entries
+    ([60 + i % 50 for i in range(290)], [i % 3 for i in range(290)], 2, 8, 64, 16, [3, 9, 9, 40, 100, 280], [60, 7, 33, 59, 16], "tree"),   # and more
 ])
 def test_prefix(lens, n, N, H, D, page, start, shared, kind):
     check(np.random.default_rng(len(lens) + N), lens, n, N, H, D, page, start, shared, kind)
@@ -204,6 +206,10 @@ def test_prefix_bad_groups_and_sessions():
         return Shared(np.random.default_rng(7), lens, n, [0, 3], [85], 64, 16, 2)
     good, wl = run(fresh(), q, par, 0.125)
     no_error()
+    many = Shared(rng, [20] * 300, [1] * 300, [0, 300], [18], 64, 16, 1)     # more entries than are looked up at once
+    many.start = np.array([0, 301], np.int32)
+    code, out, lse = error_of(many, rng.standard_normal((300, 1, 8, 64)).astype(np.float16), None, 0.125)
+    assert code == 7 and (out == 7).all() and (lse == 7).all()
     for start in ([0, 5], [-1, 3], [2, 1]):
         c = fresh()
         c.start = np.array(start, np.int32)
