@@ -57,6 +57,13 @@
 // the gathers (about 20 B a cycle and SM) take some 16 us and the items' start and output the rest; 4
 // nodes over the window 9.9 us, latency.
 //
+// Shared prefixes (ds4a_attn_prefix) use the same kernel: a group's prefix is an item whose rows are those of all its
+// sessions, so that 128 or 256 rows are full where a session alone has 64 or fewer, and K and V are read
+// once for them; the sessions' own tokens are items as above; combine_kernel joins a row's pieces of both and
+// leaves the log of its sum of exp.  prefix_64x1 (64 sessions of one token over 32768 shared and up to 512 own) 65 us =
+// 1070 TFLOP/s, with every session for itself (ds4a_attn_tree over the same pages) 126.  Of its 104000 cycles a
+// CTA's start is 6000, its 30 tiles of 256 rows 85000, the output 6000.
+//
 // Masked keys get weight 0, but 0 * V is not 0 where V is infinite or NaN: slots never
 // written, or another branch's values.  The checker scans the V rows of runs that some row
 // masks: values that are not finite are set to 0, and where the key is valid for some
@@ -87,7 +94,9 @@ constexpr uint64_t kWaitNs = 10000000000ull;   // some waits last an item, which
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLift = 7.f, kRescale = 15.f;   // log2 units: a reference is kLift below the score that set it, kept up to kRescale above
 constexpr float kLowest = -3.402823466e38f;   // reference of a row whose scores are all -inf
-constexpr int kItemUnits = 8;              // shared prefixes: the fixed part of a row tile's time, in one-block tiles
+// Shared prefixes: the fixed part of a row tile's time, in one-block tiles (prefix_64x1: 3 91 us, 6 70.4, 10 70.3, 16 71.9;
+// prefix_29x5_d64: 23.4, 23.0, 22.2, 24.0)
+constexpr int kItemUnits = 8;
 constexpr int kEdge = 2 * kMaxNodes;       // first window-edge entry of the poison table
 constexpr int kPoison = 3 * kMaxNodes;     // keys that only some rows attend: nodes, their rows, the window's edge
 
@@ -455,8 +464,8 @@ DS4A_DEVINL Share share_of(const Args &g, long long units) {
     h.end = c < h.ctas ? line_quot(units * (c + 1), h.ctas) : 0;
     return h;
 }
-// Up to kTable entries are looked up and laid end to end by all threads at once, before the roles part: one round of
-// loads, where the set-up warp's walk of 65 entries took 12000 cycles.
+// 33 to kTable entries are looked up and laid end to end by all threads at once, before the roles part: one round of
+// loads, where the set-up warp's walk of 65 entries took 12000 cycles.  (Up to 32 are one round of the walk's.)
 constexpr int kTable = 256;
 struct EntryTable {
     int start[kTable + 1];
@@ -469,7 +478,7 @@ struct EntryTable {
 DS4A_DEVINL void fill_table(const Args &g, EntryTable &t) {
     const PrefixArgs &p = g.pre;
     const int tid = threadIdx.x, n = p.n_groups + g.B, s = tid - p.n_groups;
-    const bool used = n <= kTable;                    // (then n_groups < kTable: B > 0)
+    const bool used = n > 32 && n <= kTable;          // (then n_groups < kTable: B > 0)
     if (tid == 0) t.used = used;
     if (!used) {
         __syncthreads();

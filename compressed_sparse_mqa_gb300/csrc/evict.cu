@@ -11,10 +11,15 @@
 // whose keys (an order-preserving 32-bit number per token) stay in shared memory.  Four rounds of a
 // radix search from the top, 8 bits each: each CTA counts its keys by digit, every CTA adds up all
 // histograms over distributed shared memory and finds the digit that holds the budget's edge (three
-// rounds of 2048 bins spent 2000 - 2900 cycles each on the remote histograms, these 500).  The last
+// rounds of 2048 bins spent 2000 - 2900 cycles each on the remote histograms, these 1000).  The last
 // histograms also tell each CTA how many tokens equal to the edge come before its slice.  Then
-// kept bits by ballots, ranks by prefix counts over warps and CTAs, and two lists (dropped slots, kept
-// tokens) that the second kernel, over the whole GPU, carries out.
+// kept bits by ballots, ranks by prefix counts over warps and CTAs, and the moves: dealt out over the cluster's
+// warps through distributed shared memory, or, where there may be many, as two lists that a second kernel over
+// the whole GPU carries out.
+//
+// Measured: evict_1x4096 12.3 us and evict_64x8192 17.3, latency (some 25000 cycles of dependent steps: two loads, four
+// rounds of count, cluster barrier and search at 1000 - 2300 cycles each, two counts of kept tokens, the moves);
+// evict_24x4000, which moves 33 MB of tokens, 26.5 us, about half of it the moves.
 #include <cooperative_groups.h>
 
 #include "paged_dev.cuh"
@@ -25,11 +30,12 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kSelectBlocks = 1;           // an SM: two would leave 64 registers a thread (evict_24x4000 29.4 against 26.5 us)
 constexpr int kBins = 256, kRounds = 4;
 constexpr int kOwnMoves = 512;            // moves a CTA of the cluster that it carries out itself
 constexpr int kPer = 8;                    // tokens that a warp moves at a time
 constexpr int kMaxCached = 40960;          // keys that a CTA keeps in shared memory; longer slices are read again each round
-constexpr int kSlotsPerCta = 4096;         // a session gets another CTA for every so many slots
+constexpr int kSlotsPerCta = 2048;         // a session gets another CTA for every so many slots
 constexpr int kMaxSlice = 1 << 20;         // slots of a CTA (their kept bits are 128 KB)
 constexpr int kMaxSmem = 200 * 1024;
 constexpr int kMaxCluster = 8;
@@ -121,7 +127,7 @@ DS4A_DEVINL void move_tokens(const EvictArgs &a, int s, int n, int w, int warps,
 
 // One cluster per session.  kCached: the slice's keys fit shared memory; kMoves: the cluster carries out the moves too.
 template <bool kCached, bool kMoves>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, kSelectBlocks) evict_select_kernel(const EvictArgs a) {
     extern __shared__ __align__(16) uint32_t s_keys[];           // keys (kCached), then kept bits, one word per 32 slots
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -457,9 +463,10 @@ cudaError_t launch_evict(const EvictArgs &args, int B, const Ctx &c) {
     EvictArgs a = args;
     a.most = most_moves(a.slots, a.budget);
     a.list0 = header_ints(B);
-    // CTAs a session: one for every 4096 slots, up to eight, and no more in all than the GPU holds at once
+    // CTAs a session: one for every kSlotsPerCta slots, up to eight, and no more in all than SMs (256 CTAs for 64
+    // sessions, two rounds, took 17.6 us against 17.3 for 128)
     int C = 1;
-    while (C < kMaxCluster && ((static_cast<long long>(C) * kSlotsPerCta < a.slots && 2LL * C * B <= 4LL * c.num_sms) ||
+    while (C < kMaxCluster && ((static_cast<long long>(C) * kSlotsPerCta < a.slots && 2LL * C * B <= c.num_sms) ||
                      static_cast<long long>(C) * kMaxSlice < a.slots))
         C *= 2;
     const long long cap = (static_cast<long long>(a.slots) + C * kThreads - 1) / (C * kThreads) * kThreads;   // slots of a slice
@@ -467,7 +474,8 @@ cudaError_t launch_evict(const EvictArgs &args, int B, const Ctx &c) {
     a.slice_cap = cached ? static_cast<int>(cap) : 0;
     const long long bits = (cap + 31) / 32;
     const size_t smem = static_cast<size_t>((cached ? cap : 0) + bits) * 4;
-    // A cluster moves up to kOwnMoves tokens a CTA itself (evict_64x8192 .. us against ..); more are the whole GPU's.
+    // A cluster moves up to kOwnMoves tokens a CTA itself (evict_1x4096 15.5 us against 16.3 with the second kernel, at
+    // the time); more are the whole GPU's (evict_24x4000 in the clusters 50 us a launch, alone, against 28).
     const bool own = a.most <= static_cast<long long>(kOwnMoves) * C;
     cudaError_t e = own ? (cached ? launch_select<true, true>(a, B, C, smem, c) : launch_select<false, true>(a, B, C, smem, c))
                         : (cached ? launch_select<true, false>(a, B, C, smem, c) : launch_select<false, false>(a, B, C, smem, c));

@@ -8,15 +8,17 @@
 // nothing is reduced across threads.  A key belongs to one thread of one CTA, which takes the rows in
 // order: no atomics, the same sums every time.
 //
-// Work: all sessions' pairs of 128-key tiles in one line, cut evenly over the CTAs (one per SM).  A CTA
-// takes the two tiles at a time, one a side, and goes through the rows in chunks of 128, 64 in registers at a time.
+// Work: all sessions' 128-key tiles in one line, cut evenly over the CTAs (one per SM).  A CTA takes two
+// tiles at a time, one a side, and goes through the rows in chunks of 128, 64 in registers at a time.
 // Roles:
 //   warps 0-3, 4-7  side 0 / 1: thread = key.
 //   warp 8       set-up: the CTA's pieces of the line; query chunks (TMA) and their lse.
 //   warp 9       MMA issuer.
 //   warp 10      K producer: a tile is boxes of as many rows as divide a page (16 .. 128).
-// Bound by reading K at a single token per session; with many rows by the exponentials (16 a cycle
-// and SM: 256 keys x 64 rows take 1024 cycles, their products 512).
+// Measured: weights_64x1 (64 sessions of 29 - 33 thousand keys, one token each) 84 us = 6.2 TB/s, bound by reading
+// K from HBM; weights_5x33_d64 (some 790 rows over 200 tiles) 14.5 us, bound by the sides' arithmetic, 600 cycles
+// for 128 keys x 64 rows a side (a fused multiply-add, a power of two and a sum for each); weights_1x1 (one session, 33
+// tiles) 5.0 us, a launch and three dependent loads.  Branches on the mask inside the 64-row loop cost 91 in place of 85 us.
 #include "line.cuh"
 #include "paged_dev.cuh"
 #include "tcgen05.cuh"
@@ -70,7 +72,7 @@ struct Args {
     CUtensorMap map_q, map_k;              // kRows-row boxes; `box`-row boxes over the pool
     AttnWeightsArgs a;
     float scale_log2;
-    int B, box, pool_oob;
+    int B, box, pool_oob, pair;            // pair: 1 where the line's units are two tiles
 };
 
 DS4A_DEVINL float ex2(float x) {
@@ -118,17 +120,20 @@ DS4A_DEVINL Tiles session_tiles(const AttnWeightsArgs &a, int s) {
     return t;
 }
 
-DS4A_DEVINL int tile_pairs(const Tiles &t) { return (t.tiles + 1) / 2; }   // two tiles take the time of one
+// The line's units: pairs of tiles, which take the time of one, where the rows are more than a chunk; single tiles where
+// reading K is all the time (weights_1x1, 33 tiles: 5.0 us in single tiles, 5.4 in pairs).
+DS4A_DEVINL int units_of(const Args &g, const Tiles &t) { return (t.tiles + (1 << g.pair) - 1) >> g.pair; }
 
-// Up to kTable sessions are looked up and laid end to end by all threads at once, before the roles part: one round of
-// loads, where the set-up warp's walk of 64 sessions took 8000 cycles to the first scores.
+// 33 to kTable sessions are looked up and laid end to end by all threads at once, before the roles part: one round of
+// loads, where the set-up warp's walk of 64 sessions took 8000 cycles to the first scores.  (Up to 32 are one round of the
+// walk's, which needs no barriers: 0.4 us less.)
 constexpr int kTable = 256;
 static_assert(kTable <= kThreads, "a thread per session");
 struct SessionTable {
     int4 session[kTable];                  // cached tokens, new tokens, tiles
-    long long incl[kTable];                // tile pairs up to and with the session
-    long long warp_pairs[kTable / 32];
-    int first;                             // session of this CTA's first pair
+    long long incl[kTable];                // units up to and with the session
+    long long warp_units[kTable / 32];
+    int first;                             // session of this CTA's first unit
 };
 DS4A_DEVINL void line_share(long long total, long long &u, long long &end) {
     const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x), c = blockIdx.x;
@@ -138,20 +143,20 @@ DS4A_DEVINL void line_share(long long total, long long &u, long long &end) {
 DS4A_DEVINL void fill_table(const Args &g, SessionTable &t) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Tiles s = tid < g.B ? session_tiles(g.a, tid) : Tiles{0, 0, 0};
-    const int own = tile_pairs(s);
+    const int own = units_of(g, s);
     long long incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
-    if (lane == 31 && warp < kTable / 32) t.warp_pairs[warp] = incl;
+    if (lane == 31 && warp < kTable / 32) t.warp_units[warp] = incl;
     __syncthreads();
     long long total = 0, u, end;
 #pragma unroll
     for (int x = 0; x < kTable / 32; ++x) {
         if (x == warp) incl += total;
-        total += t.warp_pairs[x];
+        total += t.warp_units[x];
     }
     if (tid < g.B) {
         t.session[tid] = make_int4(s.len, s.n, s.tiles, 0);
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
     pdl_wait();
     pdl_trigger();
     __shared__ SessionTable s_table;
-    const bool table = g.B <= kTable;
+    const bool table = g.B > 32 && g.B <= kTable;
     if (table) fill_table(g, s_table);
     bool ok = true;
     // a failed wait records the failure; later waits of this thread return at once
@@ -295,16 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
         }
     } else if (warp == kSetupWarp) {
         Line line{};
-        auto pairs = [&](int s) { return static_cast<long long>(tile_pairs(session_tiles(a, s))); };
+        auto units = [&](int s) { return static_cast<long long>(units_of(g, session_tiles(a, s))); };
         if (lane == 0) tc::prefetch_map(&g.map_q);
         long long u, u_end;
-        line_share(table ? s_table.incl[g.B - 1] : line_total(line, g.B, pairs), u, u_end);
+        line_share(table ? s_table.incl[g.B - 1] : line_total(line, g.B, units), u, u_end);
         int cursor = table ? s_table.first : 0;
         uint32_t n_q = 0;
         for (int it = 0;; ++it) {
             if (it >= 2 && !warp_wait(&bar.w_empty[it & 1], (it >> 1) - 1)) break;
             Piece &w = pieces[it & 1];
-            int s = -1;                                           // the session of pair u, and its first pair
+            int s = -1;                                           // the session of unit u, and its first unit
             long long at = 0;
             Tiles t{0, 0, 0};
             if (u < u_end && table) {
@@ -313,15 +318,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_weights_kernel(const __grid_
                 at = s > 0 ? s_table.incl[s - 1] : 0;
                 t = Tiles{s_table.session[s].x, s_table.session[s].y, s_table.session[s].z};
             } else if (u < u_end) {
-                const int l = line_to(line, g.B, u, pairs);
+                const int l = line_to(line, g.B, u, units);
                 if (l >= 0) {
                     s = line.first + l;
                     at = line.before + __shfl_sync(0xffffffffu, line.incl - line.mine, l);
                     t = session_tiles(a, s);
                 }
             }
-            const long long end = at + tile_pairs(t) < u_end ? at + tile_pairs(t) : u_end;
-            const int tile0 = 2 * static_cast<int>(u - at), tile1 = min(2 * static_cast<int>(end - at), t.tiles);
+            const long long end = at + units_of(g, t) < u_end ? at + units_of(g, t) : u_end;
+            const int tile0 = static_cast<int>(u - at) << g.pair;
+            const int tile1 = static_cast<int>(min((end - at) << g.pair, static_cast<long long>(t.tiles)));
             const int rows = t.n * a.H, chunks = (rows + kRows - 1) / kRows;
             if (lane == 0) w = Piece{s, t.len, t.n, rows, tile0, tile1, s < 0};
             __syncwarp();
@@ -489,6 +495,7 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs &a, int B, const Ctx &c) {
     g.box = a.kv.page & -a.kv.page;                              // rows that are consecutive in the pool wherever a tile is cut
     if (g.box > kTK) g.box = kTK;
     g.pool_oob = static_cast<int>(pool_rows);
+    g.pair = a.N * a.H > kRows;
     if (!tc::encode_map(&g.map_q, a.q, D, static_cast<long long>(B) * a.N * a.H, kRows) ||
         !tc::encode_map(&g.map_k, a.kv.k, D, pool_rows, static_cast<uint32_t>(g.box)))
         return cudaErrorInvalidValue;

@@ -41,7 +41,8 @@
  *     waits for the kernel ahead to finish before it reads anything else or
  *     writes anything.  So the kernel directly ahead on the stream must not
  *     write those early inputs.  The calls of this library may: directly behind
- *     one that writes arrays of that kind (ds4a_paged_append, ds4a_commit_tree) a
+ *     one that writes arrays of that kind (ds4a_paged_append, ds4a_paged_append_norm,
+ *     ds4a_commit_tree, ds4a_evict) a
  *     call with early reads is launched without programmatic dependence and
  *     starts once they are written.  A kernel that does not use programmatic
  *     launch finishes before the next call starts.  With the environment variable
@@ -573,8 +574,8 @@ int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16
  *   eps        > 0, finite.
  *   pos0       [B] int64: the position of the token in slot len (tokens are at pos0 + i, nodes
  *              at pos0 + depth), 0 .. 2^31-1 - n; NULL: len.
- *   slot_pos   [B, slots] int32, or NULL: entry len + i receives the position of token i.
- *              The other entries are left as they were.
+ *   slot_pos   [B, slots] int32, or NULL: entry len + i receives the position of token i (not
+ *              of one whose page id is outside the pool).  The other entries are left as they were.
  * A session whose pos0 is out of range (DS4A_ERR_DEVICE_INDEX) or whose tokens pass `slots`
  * (DS4A_ERR_CAPACITY) is left alone.  Sums and products are binary32.
  */
@@ -677,10 +678,8 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
                      void *stream);
 
 /*
- * Caches held to a budget of tokens.
- * ("DwarfStar (ds4) Deep Dive" bounds a session's memory by its context length; the pages give
- * no rule for dropping tokens.)  A session of the paged cache that attends all its tokens
- * can be cut to the ones that matter: the step's attention call leaves each row's log of
+ * Caches held to a budget of tokens.  (The pages give no rule for dropping tokens.)  A session
+ * of the paged cache that attends all its tokens can be cut to the ones that matter: the step's attention call leaves each row's log of
  * the sum of exp, ds4a_attn_weights adds up what weight every cached token got, and
  * ds4a_evict keeps the first and newest tokens and those with the most weight.  A cut cache
  * has positions that differ from its slots: ds4a_paged_append_norm takes and records them,
@@ -725,7 +724,8 @@ int ds4a_attn_weights(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H
  *   budget     >= 1, n_sink >= 0, n_recent >= 0, n_sink + n_recent <= budget.
  *   acc_out, pos_out  [B, slots]: entries 0 .. len_out-1 are the kept tokens'; those behind are left as
  *              they were.  Both are acc and pos themselves, or both overlap neither.
- *   len_out    [B] int64: min(len, budget); may be kv->len's array, and may not overlap it otherwise.
+ *   len_out    [B] int64: min(len, budget); may be kv->len's array, and may not overlap it otherwise,
+ *              nor next.
  *   ws         ds4a_evict_workspace_bytes(B, slots, budget) bytes, 256-byte aligned; its contents need
  *              not be set or kept.  Calls that share one workspace must be stream-ordered (two
  *              captured graphs that may replay at the same time need one each).
