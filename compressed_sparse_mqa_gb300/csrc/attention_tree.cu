@@ -1565,25 +1565,30 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kPerRow;
     const unsigned row = blockIdx.x * (kJoinWarps / kPerRow) + warp / kPerRow;   // below 2^31: a row is 128 bytes or more
     const unsigned per = g.N * g.H;
-    if (!kPre) pdl_wait();
-    pdl_trigger();
+    if constexpr (!kPre) {
+        pdl_wait();
+        pdl_trigger();
+    }
     if (row >= g.B * per) return;                    // (with kPerRow > 1 a block has one row: it leaves as a whole)
     const int s = row / per, r = row - s * per, rt = static_cast<unsigned>(r) / static_cast<unsigned>(g.item_rows);
     // Shared prefixes: this kernel starts when every CTA of the one ahead has passed its own wait, so what that one
-    // only reads is there: counts and groups are looked up while it runs.
+    // only reads is there: counts and groups are looked up while it runs.  (Rows without a result wait too: a grid that
+    // did not could be complete, and let the next kernel start, before the one ahead is.)
     int group = -1, sh = 0, grt = 0, gr = 0, slot = 0;
     Session ses;
     if constexpr (kPre) {
         ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
-        if (!ses.ok || r >= ses.n * g.H) return;
-        group = group_of(g.pre, s);
-        sh = shared_of(g.pre, group, ses.len, nullptr);
+        if (ses.ok && r < ses.n * g.H) {
+            group = group_of(g.pre, s);
+            sh = shared_of(g.pre, group, ses.len, nullptr);
+        }
         if (sh > 0) {
             gr = (s - __ldg(g.pre.start + group)) * static_cast<int>(per) + r;
             grt = gr / g.g_tile_rows;
             slot = group_slot(g.pre, group, per, g.g_tile_rows) + grt;
         }
         pdl_wait();
+        pdl_trigger();
     }
     const int2 p = g.pieces[(kPre ? g.g_slots : 0) + s * g.row_tiles + rt];   // set if the session is in the line
     if (!kPre) ses = load_session(g.kv, g.n_node, g.N, s, nullptr);

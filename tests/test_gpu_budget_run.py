@@ -166,6 +166,44 @@ def test_bound_calls_give_the_bits_of_the_calls():
         assert torch.equal(a.pos, b.pos) and torch.equal(a.length, b.length)
 
 
+def test_a_call_without_tokens_does_not_let_the_next_one_start():
+    """Sessions without new tokens have no rows to join; what follows waits for the attention all the same: eviction
+    behind it in a captured graph, over many replays, gives the bits of the calls one by one."""
+    rng = np.random.default_rng(21)
+    a, b = Server(22), Server(22)
+    for _ in range(30):                                   # past the budget
+        t = a.token(rng)
+        a.step(*t, False)
+        b.step(*t, False)
+    none = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for srv in (a, b):
+        srv.out.fill_(5)
+        srv.lse.fill_(6)
+
+    def attend_none(srv):
+        ds4a.ds4a_attn_prefix(srv.kv, srv.q, none, None, srv.start, srv.shared, SCALE, srv.out, srv.lse, srv.ws)
+        ds4a.ds4a_attn_weights(srv.kv, srv.q, none, srv.lse, SCALE, 0.875, srv.acc)
+
+    def cut(srv):
+        ds4a.ds4a_evict(srv.kv, srv.acc, srv.pos, srv.next, BUDGET, SINK, RECENT, srv.acc, srv.pos, srv.length, srv.ews)
+    before = [x.clone() for x in (b.acc, b.pos, b.length, b.pk, b.pv)]
+    attend_none(a)
+    torch.cuda.synchronize()
+    assert (a.out == 5).all() and (a.lse == 6).all() and torch.equal(a.acc, before[0])
+    cut(a)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        attend_none(b)
+        cut(b)
+    for _ in range(20):
+        for x, y in zip((b.acc, b.pos, b.length, b.pk, b.pv), before):
+            x.copy_(y)
+        g.replay()
+        no_error()
+        assert (b.out == 5).all() and torch.equal(a.pos, b.pos) and torch.equal(a.acc, b.acc)
+        assert torch.equal(a.pk.view(torch.int16), b.pk.view(torch.int16)) and b.length.tolist() == a.length.tolist()
+
+
 def test_two_streams_at_once():
     """Two servers on two streams, each with workspaces of its own, give what they give alone."""
     rng = np.random.default_rng(17)
