@@ -315,3 +315,77 @@ def test_queries_past_32_bits():
         assert (out[s - 2, m:] == 7).all()
         add, t = E.weights(q[s - 2, :m].cpu().numpy(), pools[0][rows], 0.1, lse[s - 2, :m].cpu().numpy(), ln)
         assert (np.abs(acc[s - 2, :ln + m].cpu().numpy() - add) <= t).all()
+
+
+# ---- calls that read early, directly behind ---------------------------------------------------------------
+
+def replayed(first, then, spoil, out):
+    """`then` directly behind `first` in a graph gives, over 50 replays, what it gives behind a wait."""
+    first()
+    then()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first()
+        then()
+    spoil()
+    torch.cuda.synchronize()
+    first()
+    torch.cuda.synchronize()
+    then()
+    torch.cuda.synchronize()
+    want = out.clone()
+    assert torch.isfinite(want).all()
+    for _ in range(50):
+        spoil()
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        no_error()
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("n", [1, 700])
+def test_decode_attention_directly_behind_a_normed_append(n):
+    """ds4a_attn_decode reads queries and window rows before its dependency wait."""
+    rng = np.random.default_rng(n)
+    d, h, page, ln = 128, 64, 64, 40
+    mp = (ln + n) // page + 1
+    pk, pv = (dev(rng.standard_normal((mp, page, d)).astype(np.float16)) for _ in range(2))
+    kv = ds4a.paged_kv_desc(pk, pv, torch.arange(mp, dtype=torch.int32, device="cuda")[None], torch.tensor([ln], device="cuda"))
+    k, v = (dev(rng.standard_normal((1, n, d)).astype(np.float16)) for _ in range(2))
+    q = dev(rng.standard_normal((1, n, h, d)).astype(np.float16))
+    qo, count = torch.zeros_like(q), torch.tensor([n], dtype=torch.int32, device="cuda")
+    fk, fv, w0 = pk.view(-1, d), pv.view(-1, d), ln + n - 33
+    out = torch.zeros(h, d, dtype=torch.float16, device="cuda")
+
+    def spoil():
+        qo.fill_(math.nan)
+        fk[ln:ln + n] = math.nan
+        fv[ln:ln + n] = math.nan
+    replayed(lambda: ds4a.ds4a_paged_append_norm(kv, k, v, count, None, None, EPS, None, None, 0, True, q, qo),
+             lambda: ds4a.ds4a_attn_decode(qo[0, n - 1], fk[w0:ln + n], fv[w0:ln + n], None, None, None, 0, 0.088, out), spoil, out)
+
+
+@pytest.mark.parametrize("slots,budget", [(200, 100), (20000, 9000)])          # moves in the clusters, and by the second kernel
+def test_decode_attention_directly_behind_an_eviction(slots, budget):
+    rng = np.random.default_rng(slots)
+    d, h, page = 128, 64, 16
+    mp = slots // page + 1
+    pk, pv = (dev(rng.standard_normal((mp, page, d)).astype(np.float16)) for _ in range(2))
+    kv = ds4a.paged_kv_desc(pk, pv, torch.arange(mp, dtype=torch.int32, device="cuda")[None], torch.tensor([slots], device="cuda"))
+    acc = dev(rng.permutation(slots).astype(np.float32)[None])
+    acc[0, :33] = -1.0                                                        # the first 33 are dropped, and filled
+    pos = torch.arange(slots, dtype=torch.int32, device="cuda")[None].contiguous()
+    ao, po, lo = torch.zeros_like(acc), torch.zeros_like(pos), torch.zeros(1, dtype=torch.int64, device="cuda")
+    ws = torch.zeros(ds4a.ds4a_evict_workspace_bytes(1, slots, budget), dtype=torch.uint8, device="cuda")
+    q = dev(rng.standard_normal((h, d)).astype(np.float16))
+    fk, fv = pk.view(-1, d), pv.view(-1, d)
+    nxt = torch.tensor([slots], device="cuda")
+    out = torch.zeros(h, d, dtype=torch.float16, device="cuda")
+
+    def spoil():
+        fk[:33] = math.nan
+        fv[:33] = math.nan
+    replayed(lambda: ds4a.ds4a_evict(kv, acc, pos, nxt, budget, 0, 0, ao, po, lo, ws),
+             lambda: ds4a.ds4a_attn_decode(q, fk[:33], fv[:33], None, None, None, 0, 0.088, out), spoil, out)

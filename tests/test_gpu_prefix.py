@@ -246,6 +246,46 @@ def test_prefix_bad_groups_and_sessions():
     assert np.array_equal(out[3], good[3])
 
 
+@pytest.mark.parametrize("B", [4, 60, 300])          # the walk, the table, more than the table holds
+def test_prefix_and_weights_bad_counts(B):
+    """Counts and lengths that do not fit leave their sessions alone, in both calls, and no other."""
+    rng = np.random.default_rng(B)
+    lens, n = [40 + i % 7 for i in range(B)], [1 + i % 2 for i in range(B)]
+    q = rng.standard_normal((B, 2, 8, 64)).astype(np.float16)
+
+    def call(spoil):
+        c = Shared(np.random.default_rng(7), lens, n, [0, B - 1], [37], 64, 16, 2)
+        for s, (first, m) in c.lead.items():    # the weights call reads the prefix through each session's own entries
+            c.table[s, :m // 16] = c.table[first, :m // 16]
+            c.k[c.rows(s, range(m - m % 16, m))] = c.k[c.rows(first, range(m - m % 16, m))]
+            c.v[c.rows(s, range(m - m % 16, m))] = c.v[c.rows(first, range(m - m % 16, m))]
+        kv = c.upload()
+        spoil(c)
+        out, lse = torch.full(q.shape, 7.0, dtype=torch.float16, device="cuda"), torch.full((B, 2, 8), 7.0, device="cuda")
+        acc = torch.full((B, c.mp * 16), 3.0, device="cuda")
+        ws = torch.zeros(ds4a.ds4a_attn_prefix_workspace_bytes(B, 2, 8, 64, 1), dtype=torch.uint8, device="cuda")
+        ds4a.ds4a_attn_prefix(kv, dev(q), c.dn, None, dev(c.start), dev(c.shared), 0.125, out, lse, ws)
+        torch.cuda.synchronize()
+        code = ds4a.ds4a_last_device_error()
+        ds4a.ds4a_attn_weights(kv, dev(q), c.dn, lse, 0.125, 1.0, acc)
+        torch.cuda.synchronize()
+        return code, ds4a.ds4a_last_device_error(), out.cpu(), lse.cpu(), acc.cpu()
+    good = call(lambda c: None)
+    assert good[:2] == (0, 0)
+
+    def put(name, s, x):
+        return lambda c: getattr(c, name).__setitem__(s, x)
+    cap = Shared(np.random.default_rng(7), lens, n, [0, B - 1], [37], 64, 16, 2).mp * 16
+    for what, s, code in ((put("dn", 1, -1), 1, 7), (put("dn", 2, 3), 2, 7), (put("dlen", B - 1, -5), B - 1, 7),
+                          (put("dlen", 1, cap), 1, 2), (put("dlen", 2, (1 << 63) - 1), 2, 2)):
+        got = call(what)
+        assert got[:2] == (code, code)
+        assert (got[2][s] == 7).all() and (got[3][s] == 7).all() and (got[4][s] == 3).all()
+        keep = [i for i in range(B) if i != s]
+        for x, y in zip(got[2:], good[2:]):
+            assert torch.equal(x[keep], y[keep])
+
+
 def test_prefix_captured_replays_with_other_groups():
     """A captured call with the groups, lengths and counts of another batch."""
     rng = np.random.default_rng(8)
