@@ -17,9 +17,9 @@
 // warps through distributed shared memory, or, where there may be many, as two lists that a second kernel over
 // the whole GPU carries out.
 //
-// Measured: evict_1x4096 12.3 us and evict_64x8192 17.3, latency (some 25000 cycles of dependent steps: two loads, four
-// rounds of count, cluster barrier and search at 1000 - 2300 cycles each, two counts of kept tokens, the moves);
-// evict_24x4000, which moves 33 MB of tokens, 26.5 us, about half of it the moves.
+// Measured: evict_1x4096 11.5 us and evict_64x8192 16.8, latency (some 20000 cycles of dependent steps: two loads, four
+// rounds of count, cluster barrier and search, two counts of kept tokens, the moves); evict_24x4000, which
+// moves 33 MB of tokens, 27 us, about half of it the moves.
 #include <cooperative_groups.h>
 
 #include "paged_dev.cuh"
@@ -29,7 +29,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
 constexpr int kSelectBlocks = 1;           // an SM: two would leave 64 registers a thread (evict_24x4000 29.4 against 26.5 us)
 constexpr int kBins = 256, kRounds = 4;
 constexpr int kOwnMoves = 512;            // moves a CTA of the cluster that it carries out itself
@@ -188,8 +189,9 @@ __global__ void __launch_bounds__(kThreads, kSelectBlocks) evict_select_kernel(c
         const int t = base + w * 32 + lane;
         return t < len ? token_key(acc[t], pos[t], a.n_sink, newest) : 0u;
     };
-    // kAhead words at a time: their loads go out before anything is done with one
-    constexpr int kAhead = 8;
+    // kAhead words at a time: their loads go out before anything is done with one (evict_64x8192 with 8 17.5 us, 6 16.7,
+    // 3 16.7, 1 18.3: what is unrolled past a warp's words is issued all the same)
+    constexpr int kAhead = 3;
     auto keys_at = [&](int w0, uint32_t (&k)[kAhead]) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) k[i] = w0 + i < words ? key_at(w0 + i) : 0u;

@@ -206,7 +206,7 @@ DS4A_DEVINL int node_depth(const int32_t *parent, int n, int i, int lane, unsign
 // between them.  All loads but the page number go out together (with the session's counts ahead of the others a
 // 2048-token chunk took 24 us).
 //
-// Measured: anorm_2048 (64 heads, 69 MB) 15.8 us with inputs in L2 = 4.4 TB/s, 18.3 from HBM; one token 2.9 us.
+// Measured: anorm_2048 (64 heads, 69 MB) 15.8 us with inputs in L2 = 4.4 TB/s, 17.8 from HBM; one token 3.0 us.
 // Bound by issue slots (58% used) beside memory.  With the norm in the block kernel above, its cosines and weights read
 // from shared memory by 8 lanes 64 bytes apart, the chunk took 22.7 us; six iterations a warp at four blocks an
 // SM take 16.7, three at six blocks 16.7.

@@ -536,13 +536,14 @@ def paged_kv_desc(pool_k, pool_v, table, length) -> PagedKVDesc:
 
 
 _F16, _F32, _I32, _I64, _U8 = torch.float16, torch.float32, torch.int32, torch.int64, torch.uint8
+_Tensor = torch.Tensor
 
 
 def _arg(t, dtype, dev, name):
     """The address of a contiguous tensor of this dtype on device dev (None: NULL)."""
     if t is None:
         return None
-    if t.__class__ is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+    if t.__class__ is _Tensor and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     p = _ptr(t, dtype, name)          # raises, unless it is the device that is wrong
     if t.get_device() != dev:
@@ -629,7 +630,7 @@ def _marshal_paged_append_norm(kv: PagedKVDesc, k, v, n_tok, k_w, q_w, eps: floa
                                rot_off: int = 0, interleaved: bool = True, q=None, q_out=None, pos0=None,
                                slot_pos=None, stream=None):
     B, N, H = _append_sizes("paged_append_norm", kv, k, v, q, q_out)
-    if any(w is not None and w.shape != (kv.D,) for w in (k_w, q_w)):
+    if (k_w is not None and k_w.numel() != kv.D) or (q_w is not None and q_w.numel() != kv.D):
         raise ValueError("paged_append_norm: k_w, q_w [D] (or None)")
     if pos0 is not None and pos0.shape != (B,):
         raise ValueError("paged_append_norm: pos0 [B] (or None)")
