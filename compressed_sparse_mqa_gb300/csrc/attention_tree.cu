@@ -1591,6 +1591,12 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
         pdl_trigger();
     }
     const int2 p = g.pieces[(kPre ? g.g_slots : 0) + s * g.row_tiles + rt];   // set if the session is in the line
+    int2 gp = make_int2(0, 0);                       // the group's row tile, looked up beside the session's
+    int groups_good = 1;
+    if constexpr (kPre) {
+        groups_good = *g.pre_ok;
+        if (sh > 0) gp = g.pieces[min(max(slot, 0), g.g_slots - 1)];   // (out of order, the groups' places are not used)
+    }
     if (!kPre) ses = load_session(g.kv, g.n_node, g.N, s, nullptr);
     if (!ses.ok || r >= ses.n * g.H) return;
     if (g.ratio > 0 && static_cast<unsigned>(ses.len) / static_cast<unsigned>(g.ratio) > g.cap - g.N) return;
@@ -1598,9 +1604,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
     int pieces = p.x, shared_pieces = 0;
     long long shared_at = 0;                         // the first piece of the shared prefix
     if constexpr (kPre) {
-        if (!*g.pre_ok || sh < 0 || pieces <= 0) return;   // left alone
+        if (!groups_good || sh < 0 || pieces <= 0) return;   // left alone
         if (sh > 0) {
-            const int2 gp = g.pieces[slot];
             shared_pieces = gp.x;
             shared_at = static_cast<long long>(slot + gp.y) * g.g_tile_rows + gr - grt * g.g_tile_rows;
             pieces += shared_pieces;
@@ -1615,6 +1620,28 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
         }
         return static_cast<long long>(2 * (first + i) + (i == 0)) * g.tile_rows + in_tile;
     };
+    // pieces c + k0, c + k0 + kPerRow, ..: the first batch goes out before the maximum is known
+    float x[kBatch][kPer];
+    auto load_batch = [&](int c, int k0) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int k = k0 + u * kPerRow;
+            const bool in = k < 32 && c + k < pieces;
+            const float *src = g.part + at(c + k) * D + lane * kPer;
+            if (kPer == 4) {
+                const float4 v = in ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[u][0] = v.x;
+                x[u][1] = v.y;
+                x[u][kPer - 2] = v.z;
+                x[u][kPer - 1] = v.w;
+            } else {
+                const float2 v = in ? *reinterpret_cast<const float2 *>(src) : make_float2(0.f, 0.f);
+                x[u][0] = v.x;
+                x[u][1] = v.y;
+            }
+        }
+    };
+    load_batch(0, sub);
     float m = -INFINITY;
     for (int i = lane; i < pieces; i += 32) m = fmaxf(m, g.part_ml[at(i)].x);
     m = warp_max(m);
@@ -1630,24 +1657,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(JoinArgs g) {
             }
         }
         for (int k0 = sub; k0 < 32 && c + k0 < pieces; k0 += kBatch * kPerRow) {
-            float x[kBatch][kPer];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int k = k0 + u * kPerRow;
-                const bool in = k < 32 && c + k < pieces;
-                const float *src = g.part + at(c + k) * D + lane * kPer;
-                if (kPer == 4) {
-                    const float4 v = in ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    x[u][0] = v.x;
-                    x[u][1] = v.y;
-                    x[u][kPer - 2] = v.z;
-                    x[u][kPer - 1] = v.w;
-                } else {
-                    const float2 v = in ? *reinterpret_cast<const float2 *>(src) : make_float2(0.f, 0.f);
-                    x[u][0] = v.x;
-                    x[u][1] = v.y;
-                }
-            }
+            if (c > 0 || k0 != sub) load_batch(c, k0);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int k = k0 + u * kPerRow;
