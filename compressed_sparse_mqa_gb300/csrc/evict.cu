@@ -158,16 +158,33 @@ __global__ void __launch_bounds__(kThreads, kSelectBlocks) evict_select_kernel(c
         return;
     }
     const int len = static_cast<int>(len64);
+    const int pages = len > 0 ? (len - 1) / a.kv.page + 1 : 0;   // of the session's tokens
+    const int32_t *table = a.kv.table + static_cast<long long>(s) * a.kv.max_pages;
+    auto bad_pages = [&](int p) {                                // whether one of this thread's from p on is bad
+        bool off = false;
+        for (; p < pages; p += C * kThreads) {
+            const int id = __ldg(table + p);
+            off |= id < 0 || id >= a.kv.n_pages;
+        }
+        return off;
+    };
     if (len <= a.budget) {                                       // nothing to drop
-        if (apart)
+        bad = __syncthreads_or(bad_pages(rank * kThreads + tid));
+        if (C > 1) {
+            if (tid == 0) sh.bad = bad;
+            cluster.sync();
+            for (int x = 0; x < C; ++x) bad |= *cluster.map_shared_rank(&sh.bad, x) != 0;
+        }
+        if (apart && !bad)
             for (int t = rank * kThreads + tid; t < len; t += C * kThreads) {
                 acc_out[t] = acc[t];
                 pos_out[t] = pos[t];
             }
-        if (C > 1) cluster.sync();                               // every CTA has read len
+        if (C > 1) cluster.sync();                               // every CTA has read len and the others' flags
         if (tid == 0 && rank == 0) {
             *count = 0;
-            a.len_out[s] = len;
+            if (bad) record_error(a.err, DS4A_ERR_DEVICE_INDEX);
+            else a.len_out[s] = len;
         }
         return;
     }
@@ -180,9 +197,7 @@ __global__ void __launch_bounds__(kThreads, kSelectBlocks) evict_select_kernel(c
     for (int x = tid; x < kRounds * kBins; x += kThreads) (&sh.hist[0][0])[x] = 0;
     if (tid == 0) sh.bad = 0;
     __syncthreads();
-    // pages of the session's tokens (the first ones' ids are looked at when the tokens have been counted)
-    const int pages = (len - 1) / a.kv.page + 1;
-    const int32_t *table = a.kv.table + static_cast<long long>(s) * a.kv.max_pages;
+    // (the first pages' ids are looked at when the tokens have been counted)
     const int page0 = rank * kThreads + tid, id0 = page0 < pages ? __ldg(table + page0) : 0;
     auto key_at = [&](int w) {                                   // key of the warp's word w, this lane
         if (kCached) return s_keys[warp * per_warp + w * 32 + lane];
@@ -217,11 +232,7 @@ __global__ void __launch_bounds__(kThreads, kSelectBlocks) evict_select_kernel(c
         }
     }
     {
-        bool off = id0 < 0 || id0 >= a.kv.n_pages;
-        for (int p = page0 + C * kThreads; p < pages; p += C * kThreads) {
-            const int id = __ldg(table + p);
-            off |= id < 0 || id >= a.kv.n_pages;
-        }
+        const bool off = id0 < 0 || id0 >= a.kv.n_pages || bad_pages(page0 + C * kThreads);
         if (off) sh.bad = 1;
     }
     uint32_t want = a.budget, prefix = 0;                        // tokens still to find at or below the prefix
