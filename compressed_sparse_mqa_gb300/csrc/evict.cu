@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, kSelectBlocks) evict_select_kernel(c
         }
         return;
     }
-    const long long newest = a.next[s] - a.n_recent;
+    // (below -2^62 every position is one of the newest; the difference fits)
+    const long long newest = max(a.next[s], -(1LL << 62)) - a.n_recent;
     // slices: a whole number of 32-slot words per warp
     const int per_warp = (len + C * kThreads - 1) / (C * kThreads) * 32, slice = per_warp * kWarps;
     const int base = rank * slice + warp * per_warp;             // the warp's first slot (below 2^31 + 2^17: kept in range below)

@@ -6,7 +6,7 @@ import torch
 import budget_ref as E
 from compressed_sparse_mqa_gb300 import ds4a
 from test_gpu_budget import last_error
-from test_gpu_tree import Cache, dev
+from test_gpu_tree import Cache, dev, no_error
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,22 @@ def test_evict_uncut_session_with_a_bad_page_is_left_alone(ln, other, budget, ba
     assert np.array_equal(ao[2, :ln].cpu().numpy(), acc[2, :ln])
     place, _ = E.evict(acc[1], pos[1], other, other, budget, 2, 5)
     assert np.array_equal(po[1, :budget].cpu().numpy(), pos[1, place])
+
+
+@pytest.mark.parametrize("nxt,always", [(-(1 << 63), True), (3 - (1 << 63), True), (-1, True), (5, True), (6, False),
+                                        ((1 << 63) - 1, False)])
+def test_evict_next_positions_at_the_ends_of_their_range(nxt, always):
+    """Kept: positions of next - 5 and above, in exact arithmetic.  All of them (the lower slots stay), or only position 0's."""
+    rng = np.random.default_rng(3)
+    c = Cache(rng, [50], [0], 64, 16, 0)
+    acc = rng.permutation(50).astype(np.float32)[None]
+    acc[0, 0] = -1                              # the least, at position 0
+    pos = np.arange(50, dtype=np.int32)[None]
+    if not always:
+        pos[0, 1:] = 0                          # 0 >= 6 - 5 is false
+    da, dp, lo = dev(acc), dev(pos), torch.zeros(1, dtype=torch.int64, device="cuda")
+    ws = torch.zeros(ds4a.ds4a_evict_workspace_bytes(1, 50, 20), dtype=torch.uint8, device="cuda")
+    ds4a.ds4a_evict(c.upload(), da, dp, torch.tensor([nxt], device="cuda"), 20, 0, 5, da, dp, lo, ws)
+    no_error()
+    got = np.sort(da[0, :20].cpu().numpy())
+    assert np.array_equal(got, np.sort(acc[0, :20] if always else np.sort(acc[0])[-20:]))
