@@ -5,7 +5,7 @@ import torch
 
 import budget_ref as E
 from compressed_sparse_mqa_gb300 import ds4a
-from test_gpu_budget import last_error
+from test_gpu_budget import last_error, weights_setup
 from test_gpu_tree import Cache, dev, no_error
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +60,34 @@ def test_evict_next_positions_at_the_ends_of_their_range(nxt, always):
     no_error()
     got = np.sort(da[0, :20].cpu().numpy())
     assert np.array_equal(got, np.sort(acc[0, :20] if always else np.sort(acc[0])[-20:]))
+
+
+# ---- attention weights ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens,n,N,H", [([150], [3], 3, 8), ([300, 77], [5, 2], 5, 64), ([200], [33], 33, 24)])
+@pytest.mark.parametrize("what", ["rows", "keys"])
+def test_weights_rows_of_lse_minus_infinity_add_nothing_whatever_their_scores(lens, n, N, H, what):
+    """rows: a padded token among the new ones, whose queries are NaN or infinite and whose lse is -inf.  keys: all rows'
+    lse are -inf and some keys NaN or infinite."""
+    rng = np.random.default_rng(N)
+    scale = 0.125
+    c, q, lse, acc = weights_setup(rng, lens, n, N, H, 64, 16, scale)
+    if what == "rows":
+        q[0, 1, :, 5], q[0, n[0] - 1, ::2] = np.nan, np.inf
+        lse[0, [1, n[0] - 1]] = -np.inf
+    else:
+        lse[0] = -np.inf
+        c.k[c.rows(0, [3, 40])], c.k[c.rows(0, [lens[0]])] = np.nan, -np.inf
+        c.k[c.rows(0, [lens[0] - 1]), ::2] = np.inf
+    da = dev(acc)
+    ds4a.ds4a_attn_weights(c.upload(), dev(q), c.dn, dev(lse), scale, 0.5, da)
+    no_error()
+    got = da.cpu().numpy().astype(np.float64)
+    for s, ln in enumerate(lens):
+        T = ln + n[s]
+        k = c.k[c.rows(s, range(T))]
+        dead = lse[s, :n[s], 0] == -np.inf
+        add, tol = E.weights(np.where(dead[:, None, None], 0, q[s, :n[s]]), np.where(dead.all(), 0, k), scale, lse[s, :n[s]], ln)
+        old = np.where(np.arange(T) < ln, 0.5 * acc[s, :T].astype(np.float64), 0)
+        assert np.isfinite(got[s, :T]).all()
+        assert (np.abs(got[s, :T] - old - add) <= tol + 2.0 ** -23 * old + 2.0 ** -24 * (old + add)).all()
