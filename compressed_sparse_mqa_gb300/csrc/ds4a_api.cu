@@ -491,6 +491,28 @@ static bool overlap(const void *a, const void *b, size_t bytes) {
     return x < y + bytes && y < x + bytes;
 }
 
+// What a call writes shares no byte with what it reads (NULL: not there) nor with what else it writes, so that no
+// CTA's output is what another still reads.
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+static bool apart(const Span *out, int n_out, const Span *in, int n_in) {
+    auto meet = [](const Span &x, const Span &y) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+        return x.p && y.p && a < b + y.bytes && b < a + x.bytes;
+    };
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return false;
+        for (int j = 0; j < n_in; ++j)
+            if (meet(out[i], in[j])) return false;
+    }
+    return true;
+}
+static size_t pool_bytes(const ds4a_paged_kv_t *kv) { return static_cast<size_t>(kv->n_pages) * kv->page * kv->D * 2; }
+static size_t table_bytes(const ds4a_paged_kv_t *kv) { return static_cast<size_t>(kv->B) * kv->max_pages * 4; }
+
 static int check_tree(int N, const int32_t *n_node, const int32_t *parent) {
     if (N < 1) return DS4A_ERR_ARG;
     if (N > 64) return DS4A_ERR_UNSUPPORTED;
@@ -724,13 +746,16 @@ int ds4a_evict(const ds4a_paged_kv_t *kv, const float *acc, const int32_t *pos, 
     if (!acc || !pos || !next || !acc_out || !pos_out || !len_out || !aligned(acc, 4) || !aligned(pos, 4) ||
         !aligned(next, 8) || !aligned(acc_out, 4) || !aligned(pos_out, 4) || !aligned(len_out, 8))
         return DS4A_ERR_ARG;
-    // in place, or apart, both arrays alike: a session's outputs may not be what it still reads
-    const size_t bytes = static_cast<size_t>(kv->B) * slots * 4, len_bytes = static_cast<size_t>(kv->B) * 8;
     if ((acc_out == acc) != (pos_out == pos)) return DS4A_ERR_ARG;
-    if (acc_out != acc && (overlap(acc_out, acc, bytes) || overlap(pos_out, pos, bytes))) return DS4A_ERR_ARG;
-    if (overlap(acc_out, pos, bytes) || overlap(pos_out, acc, bytes) || overlap(acc_out, pos_out, bytes)) return DS4A_ERR_ARG;
-    if ((len_out != kv->len && overlap(len_out, kv->len, len_bytes)) || overlap(len_out, next, len_bytes)) return DS4A_ERR_ARG;
-    if (!ws || !aligned(ws, 256) || ws_bytes < ds4a::evict_ws_bytes(kv->B, slots, budget)) return DS4A_ERR_WORKSPACE;
+    const size_t need = ds4a::evict_ws_bytes(kv->B, slots, budget);
+    if (!ws || !aligned(ws, 256) || ws_bytes < need) return DS4A_ERR_WORKSPACE;
+    // sums and positions in place, or apart, both alike; lengths in place or apart
+    const size_t bytes = static_cast<size_t>(kv->B) * slots * 4, len_bytes = static_cast<size_t>(kv->B) * 8;
+    const Span out[] = {{acc_out, bytes}, {pos_out, bytes}, {len_out, len_bytes}, {ws, need}};
+    const Span in[] = {{acc_out == acc ? nullptr : acc, bytes}, {pos_out == pos ? nullptr : pos, bytes}, {next, len_bytes},
+                       {len_out == kv->len ? nullptr : kv->len, len_bytes}, {kv->table, table_bytes(kv)},
+                       {kv->k, pool_bytes(kv)}, {kv->v, pool_bytes(kv)}};
+    if (!apart(out, 4, in, 7)) return DS4A_ERR_ARG;
     ds4a::Ctx c;
     rc = make_ctx(stream, c, Early::kWrites);
     if (rc != DS4A_OK) return rc;

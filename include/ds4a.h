@@ -725,11 +725,12 @@ int ds4a_attn_weights(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H
  *   budget     >= 1, n_sink >= 0, n_recent >= 0, n_sink + n_recent <= budget.
  *   acc_out, pos_out  [B, slots]: entries 0 .. len_out-1 are the kept tokens'; those behind are left as
  *              they were.  Both are acc and pos themselves, or both overlap neither.
- *   len_out    [B] int64: min(len, budget); may be kv->len's array, and may not overlap it otherwise,
- *              nor next.
+ *   len_out    [B] int64: min(len, budget); may be kv->len's array, and may not overlap it otherwise.
  *   ws         ds4a_evict_workspace_bytes(B, slots, budget) bytes, 256-byte aligned; its contents need
  *              not be set or kept.  Calls that share one workspace must be stream-ordered (two
  *              captured graphs that may replay at the same time need one each).
+ * acc_out, pos_out, len_out and ws overlap nothing else: not one another, nor next, the table or the pools
+ * (DS4A_ERR_ARG).
  * Pages of slots below `budget` that hold a token to drop are written, so they may not be shared:
  * a shared prefix stays whole when its positions are below n_sink.  Pages behind the budget are free
  * afterwards.  A session that is not cut keeps its pages as they are.  A session with len < 0 or a page

@@ -1,0 +1,53 @@
+"""Refusals of the calls on caches held to a budget: arrays that one CTA would write while another reads them.  The
+defaults overlap nothing, so only the checks on overlaps stand between them and a launch: no call here passes them."""
+import ctypes
+
+import pytest
+
+from test_tree_host import ARG, kv
+
+B, N, H, D, PAGE, MAX_PAGES, POOL, SLOTS, G = 2, 4, 64, 128, 64, 100, 300, 100, 3
+STEP = 1 << 28              # farther than any array of these sizes
+NAMES = ["pk", "pv", "table", "len", "k", "v", "n", "parent", "kw", "qw", "inv", "q", "qo", "pos0", "sp", "lse", "acc", "start",
+         "shared", "out", "ws", "pos", "next", "ao", "po", "lo"]
+AT = {name: (1 + i) * STEP for i, name in enumerate(NAMES)}
+BYTES = dict(pk=POOL * PAGE * D * 2, pv=POOL * PAGE * D * 2, table=B * MAX_PAGES * 4, len=B * 8, k=B * N * D * 2, v=B * N * D * 2, n=B * 4,
+             parent=B * N * 4, kw=D * 4, qw=D * 4, inv=32 * 4, q=B * N * H * D * 2, qo=B * N * H * D * 2, pos0=B * 8, sp=B * SLOTS * 4,
+             lse=B * N * H * 4, acc=B * SLOTS * 4, start=(G + 1) * 4, shared=G * 8, out=B * N * H * D * 2, pos=B * SLOTS * 4, next=B * 8,
+             ao=B * SLOTS * 4, po=B * SLOTS * 4, lo=B * 8)
+
+
+def cache(ds4a, a):
+    return kv(ds4a, B=B, D=D, page=PAGE, max_pages=MAX_PAGES, n_pages=POOL, k=a["pk"], v=a["pv"], table=a["table"], len=a["len"])
+
+
+def refused(ds4a, call, pairs, **fixed):
+    """Each pair (out, other): out's start at other's end, on its start, and out's end behind its start."""
+    for out, other in pairs:
+        for where in {max(0, BYTES[other] - 16) // 16 * 16, 0, min(0, 16 - BYTES[out]) // 16 * 16}:
+            a = {**AT, **fixed}
+            a[out] = a[other] + where
+            assert call(ds4a, a) == ARG, (out, other, where)
+
+
+def evict(ds4a, a):
+    L = ds4a.lib()
+    return L.ds4a_evict(cache(ds4a, a), a["acc"], a["pos"], SLOTS, a["next"], 50, 4, 8, a["ao"], a["po"], a["lo"], a["ws"],
+                        L.ds4a_evict_workspace_bytes(B, SLOTS, 50), None)
+
+
+def test_evict_outputs_overlap_nothing(ds4a_lib):
+    BYTES["ws"] = ds4a_lib.lib().ds4a_evict_workspace_bytes(B, SLOTS, 50)
+    outs = ["ao", "po", "lo"]
+    rest = ["table", "next", "pk", "pv", "ws"]
+    refused(ds4a_lib, evict, [(o, r) for o in outs for r in rest + [x for x in outs if x != o] + ["len", "acc", "pos"]
+                              if (o, r) not in (("lo", "len"), ("ao", "acc"), ("po", "pos"))])
+    # in place (acc, pos and the lengths are what is written)
+    for x, y in (("lo", "acc"), ("lo", "pos"), ("acc", "table"), ("acc", "next"), ("acc", "len"), ("pos", "next"), ("pos", "len"),
+                 ("pos", "table"), ("acc", "pk"), ("pos", "pv"), ("acc", "ws")):
+        a = dict(AT)
+        a[x] = a[y]
+        a["ao"], a["po"] = a["acc"], a["pos"]
+        assert evict(ds4a_lib, a) == ARG, (x, y)
+    a = dict(AT, lo=AT["len"], next=AT["len"])          # the length in place is not the next position
+    assert evict(ds4a_lib, a) == ARG
