@@ -697,9 +697,14 @@ int ds4a_attn_prefix(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H,
     if (kv->B == 0) return DS4A_OK;
     if (!q || !out || (n_groups > 0 && (!start || !shared))) return DS4A_ERR_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(start, 4) || !aligned(shared, 8)) return DS4A_ERR_ARG;
-    if (overlap(q, out, static_cast<size_t>(kv->B) * N * H * kv->D * 2)) return DS4A_ERR_ARG;
-    if (!ws || !aligned(ws, 256) || ws_bytes < ds4a_attn_prefix_workspace_bytes(kv->B, N, H, kv->D, n_groups))
-        return DS4A_ERR_WORKSPACE;
+    const size_t need = ds4a_attn_prefix_workspace_bytes(kv->B, N, H, kv->D, n_groups);
+    if (!ws || !aligned(ws, 256) || ws_bytes < need) return DS4A_ERR_WORKSPACE;
+    const size_t B = kv->B, rows = B * N * H;
+    const Span outs[] = {{out, rows * kv->D * 2}, {lse, rows * 4}, {ws, need}};
+    const Span in[] = {{q, rows * kv->D * 2}, {n_node, B * 4}, {parent, B * N * 4}, {n_groups > 0 ? start : nullptr, (n_groups + 1ull) * 4},
+                       {n_groups > 0 ? shared : nullptr, n_groups * 8ull}, {kv->len, B * 8}, {kv->table, table_bytes(kv)},
+                       {kv->k, pool_bytes(kv)}, {kv->v, pool_bytes(kv)}};
+    if (!apart(outs, 3, in, 9)) return DS4A_ERR_ARG;
     ds4a::Ctx c;
     rc = make_ctx(stream, c, Early::kNone);
     if (rc != DS4A_OK) return rc;

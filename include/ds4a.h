@@ -648,7 +648,8 @@ size_t ds4a_attn_tree_workspace_bytes(int B, int N, int H, int D);
  *              for a row without readable keys or with scores that are all -inf.
  *   ws         ds4a_attn_prefix_workspace_bytes(B, N, H, D, n_groups) bytes, 256-byte aligned, as
  *              ds4a_attn_tree's.
- * Rows behind a session's last node are left as they were in out and lse.  A session that is shorter
+ * out, lse and ws overlap nothing else (DS4A_ERR_ARG).  Rows behind a session's last node are left as they
+ * were in out and lse.  A session that is shorter
  * than its group's prefix, or whose group's length is negative, is left alone
  * (DS4A_ERR_DEVICE_INDEX); with start not in order all are.  Precision as ds4a_attn_tree's.
  */

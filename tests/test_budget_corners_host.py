@@ -2,8 +2,6 @@
 defaults overlap nothing, so only the checks on overlaps stand between them and a launch: no call here passes them."""
 import ctypes
 
-import pytest
-
 from test_tree_host import ARG, kv
 
 B, N, H, D, PAGE, MAX_PAGES, POOL, SLOTS, G = 2, 4, 64, 128, 64, 100, 300, 100, 3
@@ -51,3 +49,18 @@ def test_evict_outputs_overlap_nothing(ds4a_lib):
         assert evict(ds4a_lib, a) == ARG, (x, y)
     a = dict(AT, lo=AT["len"], next=AT["len"])          # the length in place is not the next position
     assert evict(ds4a_lib, a) == ARG
+
+
+def prefix(ds4a, a):
+    L = ds4a.lib()
+    return L.ds4a_attn_prefix(cache(ds4a, a), a["q"], N, H, a["n"], a["parent"], a["start"], a["shared"], G, ctypes.c_float(0.1), a["out"],
+                              a["lse"], a["ws"], L.ds4a_attn_prefix_workspace_bytes(B, N, H, D, G), None)
+
+
+def test_prefix_outputs_overlap_nothing(ds4a_lib):
+    BYTES["ws"] = ds4a_lib.lib().ds4a_attn_prefix_workspace_bytes(B, N, H, D, G)
+    assert BYTES["ws"] < STEP
+    refused(ds4a_lib, prefix, [(o, r) for o in ("out", "lse") for r in
+                               ("q", "n", "parent", "start", "shared", "len", "table", "pk", "pv", "ws", "out" if o == "lse" else "lse")])
+    for other in ("q", "n", "parent", "start", "shared", "len", "table", "pk", "pv"):
+        assert prefix(ds4a_lib, dict(AT, ws=AT[other])) == ARG, other
