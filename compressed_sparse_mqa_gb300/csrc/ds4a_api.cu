@@ -727,6 +727,11 @@ int ds4a_attn_weights(const ds4a_paged_kv_t *kv, const uint16_t *q, int N, int H
     if (slots < 1 || !(scale > 0.f) || scale > 2.3e38f || !(decay >= 0.f) || decay > 1.f) return DS4A_ERR_ARG;
     if (kv->B == 0) return DS4A_OK;
     if (!q || !lse || !acc || !aligned(q, 16) || !aligned(lse, 4) || !aligned(acc, 4)) return DS4A_ERR_ARG;
+    const size_t B = kv->B, rows = B * N * H;
+    const Span out{acc, B * slots * 4};
+    const Span in[] = {{q, rows * kv->D * 2}, {lse, rows * 4}, {n_tok, B * 4}, {kv->len, B * 8}, {kv->table, table_bytes(kv)},
+                       {kv->k, pool_bytes(kv)}, {kv->v, pool_bytes(kv)}};
+    if (!apart(&out, 1, in, 7)) return DS4A_ERR_ARG;
     ds4a::Ctx c;
     rc = make_ctx(stream, c, Early::kNone);
     if (rc != DS4A_OK) return rc;

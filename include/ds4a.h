@@ -703,7 +703,7 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
  *   scale      softmax scale, > 0, at most 2.3e38.
  *   decay      0 .. 1; with 0 the sums before are not read.
  *   acc        [B, slots] float.  Entries of slots >= len + n, and of tokens whose page id is
- *              outside the pool, are left as they were.
+ *              outside the pool, are left as they were.  acc overlaps nothing else (DS4A_ERR_ARG).
  * Every token is read through its session's own page entries, those of a shared prefix too.
  * A session whose tokens pass `slots` is left alone (DS4A_ERR_CAPACITY).  Scores, exponentials and
  * sums are binary32; a slot's sum is taken in a fixed order (no atomics).

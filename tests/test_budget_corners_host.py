@@ -64,3 +64,12 @@ def test_prefix_outputs_overlap_nothing(ds4a_lib):
                                ("q", "n", "parent", "start", "shared", "len", "table", "pk", "pv", "ws", "out" if o == "lse" else "lse")])
     for other in ("q", "n", "parent", "start", "shared", "len", "table", "pk", "pv"):
         assert prefix(ds4a_lib, dict(AT, ws=AT[other])) == ARG, other
+
+
+def weights(ds4a, a):
+    return ds4a.lib().ds4a_attn_weights(cache(ds4a, a), a["q"], N, H, a["n"], a["lse"], ctypes.c_float(0.1), ctypes.c_float(1.0), a["acc"],
+                                        SLOTS, None)
+
+
+def test_weights_sums_overlap_nothing(ds4a_lib):
+    refused(ds4a_lib, weights, [("acc", r) for r in ("q", "lse", "n", "len", "table", "pk", "pv")])
