@@ -577,6 +577,13 @@ int ds4a_paged_append_norm(const ds4a_paged_kv_t *kv, const uint16_t *k, const u
     if (!(eps > 0.f) || eps > 3.4e38f || (slot_pos && slots < 1)) return DS4A_ERR_ARG;
     if (!aligned(k_w, 4) || !aligned(q_w, 4) || !aligned(pos0, 8) || !aligned(slot_pos, 4)) return DS4A_ERR_ARG;
     if (!run) return rc;
+    // a token's warps write its query rows and its position while others' inputs are still read
+    const size_t B = kv->B, tokens = B * N, row = static_cast<size_t>(kv->D) * 2, head = static_cast<size_t>(kv->D) * 4;
+    const Span out[] = {{q_out, tokens * a.H * row}, {slot_pos, slot_pos ? B * slots * 4 : 0}};
+    const Span in[] = {{q_out == q ? nullptr : q, tokens * a.H * row}, {k, tokens * row}, {v, tokens * row}, {n_tok, B * 4},
+                       {parent, tokens * 4}, {k_w, head}, {q_w, head}, {rot > 0 ? inv_freq : nullptr, rot * 2ull}, {pos0, B * 8},
+                       {kv->len, B * 8}, {kv->table, table_bytes(kv)}, {kv->k, pool_bytes(kv)}, {kv->v, pool_bytes(kv)}};
+    if (!apart(out, 2, in, 13)) return DS4A_ERR_ARG;
     ds4a::Ctx c;
     rc = make_ctx(stream, c, Early::kWrites);
     if (rc != DS4A_OK) return rc;

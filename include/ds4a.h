@@ -576,6 +576,7 @@ int ds4a_paged_append(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint16
  *              at pos0 + depth), 0 .. 2^31-1 - n; NULL: len.
  *   slot_pos   [B, slots] int32, or NULL: entry len + i receives the position of token i (not
  *              of one whose page id is outside the pool).  The other entries are left as they were.
+ * q_out (which may be q) and slot_pos overlap nothing else (DS4A_ERR_ARG).
  * A session whose pos0 is out of range (DS4A_ERR_DEVICE_INDEX) or whose tokens pass `slots`
  * (DS4A_ERR_CAPACITY) is left alone.  Sums and products are binary32.
  */

@@ -73,3 +73,14 @@ def weights(ds4a, a):
 
 def test_weights_sums_overlap_nothing(ds4a_lib):
     refused(ds4a_lib, weights, [("acc", r) for r in ("q", "lse", "n", "len", "table", "pk", "pv")])
+
+
+def append(ds4a, a):
+    return ds4a.lib().ds4a_paged_append_norm(cache(ds4a, a), a["k"], a["v"], N, a["n"], a["parent"], a["kw"], a["qw"], ctypes.c_float(1e-6),
+                                             a["inv"], 64, 64, 1, a["q"], H, a["qo"], a["pos0"], a["sp"], SLOTS, None)
+
+
+def test_append_norm_outputs_overlap_nothing(ds4a_lib):
+    rest = ("k", "v", "n", "parent", "kw", "qw", "inv", "pos0", "len", "table", "pk", "pv")
+    refused(ds4a_lib, append, [(o, r) for o in ("qo", "sp") for r in rest + ("sp" if o == "qo" else "qo",)] + [("sp", "q")])
+    refused(ds4a_lib, append, [("sp", "q"), ("sp", "k")], qo=AT["q"])           # queries in place
