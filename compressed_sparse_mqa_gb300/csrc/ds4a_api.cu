@@ -574,7 +574,7 @@ int ds4a_paged_append_norm(const ds4a_paged_kv_t *kv, const uint16_t *k, const u
     bool run;
     int rc = append_args(kv, k, v, N, n_tok, parent, inv_freq, rot, rot_off, interleaved, q, H, q_out, a, run);
     if (rc != DS4A_OK) return rc;
-    if (!(eps > 0.f) || eps > 3.4e38f || (slot_pos && slots < 1)) return DS4A_ERR_ARG;
+    if (!(eps > 0.f) || eps > 3.402823466e38f || (slot_pos && slots < 1)) return DS4A_ERR_ARG;
     if (!aligned(k_w, 4) || !aligned(q_w, 4) || !aligned(pos0, 8) || !aligned(slot_pos, 4)) return DS4A_ERR_ARG;
     if (!run) return rc;
     // a token's warps write its query rows and its position while others' inputs are still read

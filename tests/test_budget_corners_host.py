@@ -2,7 +2,10 @@
 defaults overlap nothing, so only the checks on overlaps stand between them and a launch: no call here passes them."""
 import ctypes
 
-from test_tree_host import ARG, kv
+import numpy as np
+import pytest
+
+from test_tree_host import ARG, FAKE, kv
 
 B, N, H, D, PAGE, MAX_PAGES, POOL, SLOTS, G = 2, 4, 64, 128, 64, 100, 300, 100, 3
 STEP = 1 << 28              # farther than any array of these sizes
@@ -84,3 +87,12 @@ def test_append_norm_outputs_overlap_nothing(ds4a_lib):
     rest = ("k", "v", "n", "parent", "kw", "qw", "inv", "pos0", "len", "table", "pk", "pv")
     refused(ds4a_lib, append, [(o, r) for o in ("qo", "sp") for r in rest + ("sp" if o == "qo" else "qo",)] + [("sp", "q")])
     refused(ds4a_lib, append, [("sp", "q"), ("sp", "k")], qo=AT["q"])           # queries in place
+
+
+@pytest.mark.parametrize("eps,code", [(float(np.finfo(np.float32).max), 0), (3.4014e38, 0), (float(np.float32(1e-45)), 0), (float("inf"), ARG),
+                                      (float("nan"), ARG), (0.0, ARG)])
+def test_append_norm_takes_every_finite_eps(ds4a_lib, eps, code):
+    """Without sessions the call ends behind its checks."""
+    none = kv(ds4a_lib, B=0, k=None, v=None, table=None, len=None)
+    assert ds4a_lib.lib().ds4a_paged_append_norm(none, FAKE, FAKE, 1, FAKE, None, None, None, ctypes.c_float(eps), None, 0, 0, 1, None, 0, None,
+                                                 None, None, 0, None) == code
