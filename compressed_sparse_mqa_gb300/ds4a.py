@@ -551,6 +551,13 @@ def _arg(t, dtype, dev, name):
     return p
 
 
+def _int32(x, where, name):
+    """x for a C int (ctypes would drop the bits above)."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{where}: {name} {x} does not fit 32 bits")
+    return x
+
+
 def _launch_on(where, kv, stream):
     """The stream's handle; the cache must be on the current device, where the library launches."""
     dev = torch._C._cuda_getDevice()
@@ -814,6 +821,8 @@ def _marshal_evict(kv: PagedKVDesc, acc, pos, next_pos, budget: int, n_sink: int
         raise ValueError("evict: acc, pos, acc_out, pos_out [B, slots]")
     if any(t is None or t.shape != (kv.B,) for t in (next_pos, len_out)):
         raise ValueError("evict: next_pos, len_out [B]")
+    for name, x in (("budget", budget), ("n_sink", n_sink), ("n_recent", n_recent)):
+        _int32(x, "evict", name)
     st, dev = _launch_on("evict", kv, stream), kv.device
     pa, slots = _slot_rows("evict", kv, acc, _F32, "acc")
     return (ctypes.byref(kv), pa, _arg(pos, _I32, dev, "pos"), slots, _arg(next_pos, _I64, dev, "next_pos"), budget, n_sink,

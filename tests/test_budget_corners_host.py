@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from test_tree_host import ARG, FAKE, kv
 
@@ -96,3 +97,16 @@ def test_append_norm_takes_every_finite_eps(ds4a_lib, eps, code):
     none = kv(ds4a_lib, B=0, k=None, v=None, table=None, len=None)
     assert ds4a_lib.lib().ds4a_paged_append_norm(none, FAKE, FAKE, 1, FAKE, None, None, None, ctypes.c_float(eps), None, 0, 0, 1, None, 0, None,
                                                  None, None, 0, None) == code
+
+
+@pytest.mark.parametrize("name", ["budget", "n_sink", "n_recent"])
+@pytest.mark.parametrize("x", [(1 << 32) + 8, 1 << 31, -(1 << 31) - 1, 1 << 63])
+def test_evict_counts_are_not_cut_to_32_bits(ds4a_lib, name, x):
+    """A budget of 2^32 + 8 is not one of 8."""
+    desc = ds4a_lib.PagedKVDesc(B=1, D=64, page=16, max_pages=3, n_pages=4)
+    desc.tensors, desc.device = (), 0
+    f, n = torch.zeros(1, 40), torch.zeros(1, dtype=torch.int64)
+    counts = {**dict(budget=10, n_sink=0, n_recent=0), name: x}
+    for call in (ds4a_lib.ds4a_evict, lambda *a: ds4a_lib.bind("ds4a_evict", *a)):
+        with pytest.raises(ValueError, match=f"evict: {name} {x} does not fit"):
+            call(desc, f, f, n, counts["budget"], counts["n_sink"], counts["n_recent"], f, f, n, None)
