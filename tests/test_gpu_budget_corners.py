@@ -1,11 +1,13 @@
 """Calls on caches held to a budget that the other tests do not make."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import budget_ref as E
 from compressed_sparse_mqa_gb300 import ds4a
-from test_gpu_budget import last_error, weights_setup
+from test_gpu_budget import check_evict, check_weights, last_error, weights_setup
 from test_gpu_tree import Cache, dev, no_error
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +93,52 @@ def test_weights_rows_of_lse_minus_infinity_add_nothing_whatever_their_scores(le
         old = np.where(np.arange(T) < ln, 0.5 * acc[s, :T].astype(np.float64), 0)
         assert np.isfinite(got[s, :T]).all()
         assert (np.abs(got[s, :T] - old - add) <= tol + 2.0 ** -23 * old + 2.0 ** -24 * (old + add)).all()
+
+
+def bits(t):
+    return t.view(torch.int32)
+
+
+@pytest.mark.parametrize("lens,n,N,H,D,page", [
+    ([12001 + 371 * i for i in range(8)], [4, 1, 3, 2, 4, 4, 1, 3], 4, 64, 128, 64),             # 1 or 2 chunks, two or three blocks a CTA
+    ([1900 + 17 * i for i in range(40)], [1 + i % 3 for i in range(40)], 3, 64, 64, 16),         # the table, pairs, sessions of 1 - 2 chunks
+    ([1000 + 29 * i for i in range(30)] + [40, 3, 0], [20 - i % 7 for i in range(30)] + [20, 0, 20], 20, 24, 64, 48),   # 4 chunks
+    ([30000, 10500], [64, 33], 64, 16, 128, 128),                                                 # 8 chunks, two sessions
+])
+def test_weights_of_many_rows_over_more_tiles_than_ctas(lens, n, N, H, D, page):
+    """Query chunks are loaded again for every block of two tiles, over several pieces of a CTA; each session gets the bits that
+    it gets alone."""
+    scale = 1 / math.sqrt(D)
+    c, q, lse, acc = weights_setup(np.random.default_rng(N), lens, n, N, H, D, page, scale)
+    kv = c.upload()
+    da, dq, dl = dev(acc), dev(q), dev(lse)
+    ds4a.ds4a_attn_weights(kv, dq, c.dn, dl, scale, 0.75, da)
+    no_error()
+    check_weights(c, q, lse, acc, da.cpu().numpy(), scale, 0.75, lens, n)
+    for s in (0, len(lens) // 2):
+        one = dev(acc[s:s + 1])
+        ds4a.ds4a_attn_weights(ds4a.paged_kv_desc(c.dk, c.dv, c.dtab[s:s + 1].contiguous(), c.dlen[s:s + 1].contiguous()),
+                               dq[s:s + 1].contiguous(), c.dn[s:s + 1].contiguous(), dl[s:s + 1].contiguous(), scale, 0.75, one)
+        no_error()
+        assert torch.equal(bits(one), bits(da[s:s + 1]))
+
+
+# ---- eviction: clusters of two, and slices whose keys are read again each round ---------------------
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,budget,sink,recent,extra", [
+    ([2600, 3000, 2100, 1400], 1500, 4, 100, 50),                                # two CTAs a session by its slots
+    ([4000] * 3, 2100, 0, 0, 90),                                                # the same, moves by the second kernel
+    ([8448 - 3 * i for i in range(64)], 8192, 4, 256, 0),                        # by the batch
+    ([700 - i for i in range(76)] + [3], 250, 4, 60, 41000),                     # one, not in shared memory
+    ([500 + i for i in range(40)], 400, 8, 0, 90000),                            # two, not in shared memory
+])
+def test_evict_two_ctas_a_session_and_long_rows(lens, budget, sink, recent, extra, in_place):
+    check_evict(np.random.default_rng(budget), lens, budget, sink, recent, extra=extra, in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("budget", [4000, 397000])
+def test_evict_few_moves_in_sessions_longer_than_shared_memory(budget, in_place):
+    """Eight CTAs that read their keys again each round, and carry out the moves themselves over what they read."""
+    check_evict(np.random.default_rng(6), [400001, 399000, 17], budget, 4, 1000, page=4096, in_place=in_place)
