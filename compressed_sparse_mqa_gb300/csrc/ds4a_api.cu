@@ -547,7 +547,7 @@ static int append_args(const ds4a_paged_kv_t *kv, const uint16_t *k, const uint1
     // queries in place, or apart
     if (q && q_out != q && overlap(q, q_out, static_cast<size_t>(kv->B) * N * H * kv->D * 2)) return DS4A_ERR_ARG;
     a = ds4a::AppendArgs{paged_view(kv), k, v, q, q_out, n_tok, parent, inv_freq, nullptr, N, q ? H : 0, rot, rot_off,
-                         interleaved != 0, 0, nullptr, nullptr, 0.f, nullptr, nullptr, 0};
+                         interleaved != 0};
     run = true;
     return DS4A_OK;
 }
@@ -588,14 +588,8 @@ int ds4a_paged_append_norm(const ds4a_paged_kv_t *kv, const uint16_t *k, const u
     rc = make_ctx(stream, c, Early::kWrites);
     if (rc != DS4A_OK) return rc;
     a.err = c.err;
-    a.B = kv->B;
-    a.k_w = k_w;
-    a.q_w = q_w;
-    a.eps = eps;
-    a.pos0 = pos0;
-    a.slot_pos = slot_pos;
-    a.slots = slots;
-    return from_cuda(ds4a::launch_norm_append(a, kv->B, c));
+    const ds4a::NormAppendArgs norm{a, k_w, q_w, eps, pos0, slot_pos, slots};
+    return from_cuda(ds4a::launch_norm_append(norm, kv->B, c));
 }
 
 int ds4a_compress_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, const int32_t *parent,

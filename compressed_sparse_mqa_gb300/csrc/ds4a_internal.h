@@ -120,8 +120,8 @@ struct AppendArgs {
     const float *inv_freq;
     unsigned int *err;
     int N, H, rot, rot_off, interleaved;
-    // with norms
-    int B;
+};
+struct NormAppendArgs : AppendArgs {
     const float *k_w, *q_w;      // [D], or nullptr: ones
     float eps;
     const long long *pos0;       // [B], or nullptr: len
@@ -190,7 +190,7 @@ struct EvictArgs {
     long long most, list0;
 };
 cudaError_t launch_paged_append(const AppendArgs &a, int B, const Ctx &c);
-cudaError_t launch_norm_append(const AppendArgs &a, int B, const Ctx &c);
+cudaError_t launch_norm_append(const NormAppendArgs &a, int B, const Ctx &c);
 cudaError_t launch_compress_tree(const CompressTreeArgs &a, int B, const Ctx &c);
 cudaError_t launch_commit_tree(const CommitTreeArgs &a, int B, const Ctx &c);
 size_t attn_prefix_ws_bytes(int B, int N, int H, int D, int n_groups);

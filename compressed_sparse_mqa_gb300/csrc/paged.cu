@@ -214,7 +214,7 @@ constexpr int kNormIt = 3;
 constexpr int kNormThreads = 128;
 constexpr int kNormBlocks = 5;             // an SM: 96 registers a thread
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_append_kernel(const AppendArgs a, int warps_tok, int rows_warp) {
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_append_kernel(const NormAppendArgs a, int warps_tok, int rows_warp) {
     constexpr int kLanes = D / 16, kRowsIt = 32 / kLanes;
     const int lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
     const unsigned gw = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5), ui = gw / static_cast<unsigned>(warps_tok);
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_append_kernel(
 
 }  // namespace
 
-cudaError_t launch_norm_append(const AppendArgs &a, int B, const Ctx &c) {
+cudaError_t launch_norm_append(const NormAppendArgs &a, int B, const Ctx &c) {
     const int rows = a.H + 2, it = a.kv.D == 128 ? 4 : 8;        // rows an iteration
     const int warps = (rows + kNormIt * it - 1) / (kNormIt * it), per = ((rows + warps - 1) / warps + it - 1) / it * it;
     const long long total = static_cast<long long>(a.N) * warps;   // of a session: below 2^31 (its tokens fit its pages)
