@@ -206,8 +206,10 @@ DS4A_DEVINL int node_depth(const int32_t *parent, int n, int i, int lane, unsign
 // between them.  All loads but the page number go out together (with the session's counts ahead of the others a
 // 2048-token chunk took 24 us).
 //
-// Measured: anorm_2048 (64 heads, 69 MB) 15.8 us with inputs in L2 = 4.4 TB/s, 17.8 from HBM; one token 3.0 us.
-// Bound by issue slots (58% used) beside memory.  With the norm in the block kernel above, its cosines and weights read
+// Measured: anorm_2048 (64 heads, 69 MB) 15.7 us with inputs in L2 = 4.4 TB/s, 17.7 from HBM; one token 2.9 us.
+// No unit is used up (issue slots 60%, 17 of 20 warps resident): a warp loads once, waits, and stores, and the time is
+// linear in the tokens, without a step where a round of blocks is full (1520 tokens 11.6 us, 1900 14.0, 2026, four
+// rounds, 14.9, 2028 14.9, 2200 16.2).  With the norm in the block kernel above, its cosines and weights read
 // from shared memory by 8 lanes 64 bytes apart, the chunk took 22.7 us; six iterations a warp at four blocks an
 // SM take 16.7, three at six blocks 16.7.
 constexpr int kNormIt = 3;

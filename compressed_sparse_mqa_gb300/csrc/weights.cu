@@ -16,9 +16,11 @@
 //   warp 9       MMA issuer.
 //   warp 10      K producer: a tile is boxes of as many rows as divide a page (16 .. 128).
 // Measured: weights_64x1 (64 sessions of 29 - 33 thousand keys, one token each) 84 us = 6.2 TB/s, bound by reading
-// K from HBM; weights_5x33_d64 (some 790 rows over 200 tiles) 14.5 us, bound by the sides' arithmetic, 600 cycles
-// for 128 keys x 64 rows a side (a fused multiply-add, a power of two and a sum for each); weights_1x1 (one session, 33
-// tiles) 5.0 us, a launch and three dependent loads.  Branches on the mask inside the 64-row loop cost 91 in place of 85 us.
+// K from HBM; weights_5x33_d64 (some 790 rows over 200 tiles) 14.8 us: a CTA with seven chunks takes 23000 cycles, 5900 to its
+// first scores, 1600 waiting for later scores, at most 1900 for queries, and the rest, some 2000 a chunk, in the sides'
+// loads and sums of scores (a fused multiply-add, a power of two and a sum for each, two warps a scheduler); a third of
+// the SMs have no tiles.  weights_1x1 (one session, 33 tiles) 4.9 us, a launch and three dependent loads.  Branches on
+// the mask inside the 64-row loop cost 91 in place of 85 us.
 #include "line.cuh"
 #include "paged_dev.cuh"
 #include "tcgen05.cuh"

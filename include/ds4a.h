@@ -689,6 +689,9 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
  * calls on the paged cache work on it as before as long as no window is shorter than it.
  *
  * Sums and positions are [B, slots] arrays beside the pages: entry t belongs to slot t.
+ *
+ * Both calls take every token through its session's own page entries: before a session that shares a prefix
+ * (ds4a_attn_prefix) is scored or cut, its entries of the prefix's pages are set, to the first session's.
  */
 
 /*
@@ -702,7 +705,7 @@ int ds4a_commit_tree(const ds4a_paged_kv_t *kv, int N, const int32_t *n_node, co
  *   lse        [B, N, H] float: log of the sum of exp of each row's scaled scores.  A row whose
  *              lse is -inf (no key, or none but scores of -inf) adds nothing.
  *   scale      softmax scale, > 0, at most 2.3e38.
- *   decay      0 .. 1; with 0 the sums before are not read.
+ *   decay      0 .. 1, once a call; with 0 the sums before are not read.
  *   acc        [B, slots] float.  Entries of slots >= len + n, and of tokens whose page id is
  *              outside the pool, are left as they were.  acc overlaps nothing else (DS4A_ERR_ARG).
  * Every token is read through its session's own page entries, those of a shared prefix too.
