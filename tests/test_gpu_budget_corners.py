@@ -142,3 +142,30 @@ def test_evict_two_ctas_a_session_and_long_rows(lens, budget, sink, recent, extr
 def test_evict_few_moves_in_sessions_longer_than_shared_memory(budget, in_place):
     """Eight CTAs that read their keys again each round, and carry out the moves themselves over what they read."""
     check_evict(np.random.default_rng(6), [400001, 399000, 17], budget, 4, 1000, page=4096, in_place=in_place)
+
+
+# ---- shared prefixes ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,ln", [(2, 40), (3, 5000), (40, 300)])
+def test_prefix_sessions_without_a_readable_page(B, ln):
+    """Zeros and an lse of -inf, joined from one piece or from many; then the weights call adds nothing."""
+    rng = np.random.default_rng(B)
+    c = Cache(rng, [ln + i % 7 for i in range(B)], [1 + i % 2 for i in range(B)], 64, 16, 2)
+    c.draft()
+    c.table[:] = np.where(np.arange(c.mp) % 2, -1, c.n_pages)
+    q = rng.standard_normal((B, 2, 8, 64)).astype(np.float16)
+    kv, dq = c.upload(), dev(q)
+    out, lse = torch.full_like(dq, 7), torch.full((B, 2, 8), 7.0, device="cuda")
+    ws = torch.full((ds4a.ds4a_attn_prefix_workspace_bytes(B, 2, 8, 64, 1),), 255, dtype=torch.uint8, device="cuda")
+    ds4a.ds4a_attn_prefix(kv, dq, c.dn, None, dev(np.array([0, B - 1], np.int32)), torch.tensor([ln - 3], device="cuda"), 0.125, out, lse, ws)
+    assert last_error() == 7
+    for s in range(B):
+        assert (out[s, :c.n[s]] == 0).all() and (lse[s, :c.n[s]] == -math.inf).all()
+        assert (out[s, c.n[s]:] == 7).all() and (lse[s, c.n[s]:] == 7).all()
+    c.table[:] = np.arange(B * c.mp).reshape(B, c.mp)       # readable again, over tokens that are NaN and numbers
+    kv = c.upload()
+    acc = torch.full((B, c.mp * 16), 2.0, device="cuda")
+    ds4a.ds4a_attn_weights(kv, dq, c.dn, lse, 0.125, 0.5, acc)
+    no_error()
+    for s in range(B):
+        assert (acc[s, :c.lens[s]] == 1).all() and (acc[s, c.lens[s]:c.lens[s] + c.n[s]] == 0).all() and (acc[s, c.lens[s] + c.n[s]:] == 2).all()
